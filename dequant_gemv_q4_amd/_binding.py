@@ -17,7 +17,10 @@ HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "qgemv.h")
 
 Q4_0, Q5_0, Q8_0, Q4_K, Q5_K, Q6_K = 2, 6, 8, 12, 13, 14
 IQ4_NL, IQ4_XS, Q1_0, AQ4 = 20, 23, 40, 41
+F16, BF16 = 1, 30
 OP_GEMV, OP_NRM, OP_GUS_NRM, OP_RES, OP_ARGMAX, OP_MOE, OP_NRM_BIAS = range(7)
+OP_KV_APPEND, OP_ATTN, OP_ATTN_PROMPT = 7, 8, 9
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 ACT_SILU, ACT_GELU_TANH = 0, 1
 STATUS = {0: "QG_OK", 1: "QG_ERR_NULL", 2: "QG_ERR_FORMAT", 3: "QG_ERR_SHAPE", 4: "QG_ERR_ALIGN",
           5: "QG_ERR_WORKSPACE", 6: "QG_ERR_LAUNCH", 7: "QG_ERR_ALIAS"}
@@ -52,6 +55,16 @@ _SIGS = {
     "qgemm_workspace_bytes": (_i64, [_i32, _i64, _i64, _i64]),
     "qgemm": (_i32, [_i32, _vp, _i64, _i64, _vp, _i64, _vp, _vp, _sz, _vp]),
     "qgemv_moe_error": (_i32, [_vp, _i64, _i64, _i64, _i32, ctypes.POINTER(ctypes.c_int), _vp]),
+    "qgemv_attn_workspace_bytes": (_i64, [_i32, _i32, _i32, _i32, _i32]),
+    "qgemv_kv_append": (_i32, [_i32, _vp, _vp, _i64, _i32, _i64, _i32, _i32, _vp, _i32, _vp, _vp,
+                               _i32, _vp, _vp, _i64, _i64, _vp, _sz, _vp]),
+    "qgemv_attn": (_i32, [_i32, _vp, _vp, _i64, _i32, _i64, _i32, _i32, _vp, _i32, _vp, _i32, _vp,
+                          _i64, _i32, _f32, _vp, _vp, _sz, _vp]),
+    "qgemv_attn_prompt": (_i32, [_i32, _vp, _vp, _i64, _i32, _i64, _i32, _i32, _vp, _i32, _vp, _vp,
+                                 _i32, _vp, _i64, _i64, _i32, _f32, _vp, _vp, _sz, _vp]),
+    "qgemv_attn_error": (_i32, [_vp, ctypes.POINTER(ctypes.c_int), _vp]),
+    "qgemv_route": (_i32, [_vp, _i64, _i32, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _f32, _vp,
+                           _vp, _vp]),
     "qgemv_status_str": (ctypes.c_char_p, [_i32]),
     "qgemv_layout_version": (_i32, []),
 }
@@ -225,3 +238,53 @@ def qgemv_moe_error(ws, n_exp, N, K, fmt, stream=None) -> int:
     _check("qgemv_moe_error", lib().qgemv_moe_error(_p(ws), n_exp, N, K, fmt, ctypes.byref(flag),
                                                     _stream(stream)))
     return flag.value
+
+
+def qgemv_attn_workspace_bytes(op: int, n_seq: int, n_q_heads: int, n_kv_heads: int,
+                               head_dim: int) -> int:
+    return lib().qgemv_attn_workspace_bytes(op, n_seq, n_q_heads, n_kv_heads, head_dim)
+
+
+def qgemv_kv_append(kv_type, k_pages, v_pages, n_pages, page_size, page_stride, n_kv_heads,
+                    head_dim, table, max_pages, q_start, kv_len, n_seq, k, v, kv_stride, n_rows, ws,
+                    ws_bytes=None, stream=None):
+    _check("qgemv_kv_append",
+           lib().qgemv_kv_append(kv_type, _p(k_pages), _p(v_pages), n_pages, page_size, page_stride,
+                                 n_kv_heads, head_dim, _p(table), max_pages, _p(q_start),
+                                 _p(kv_len), n_seq, _p(k), _p(v), kv_stride, n_rows, _p(ws),
+                                 _nbytes(ws) if ws_bytes is None else ws_bytes, _stream(stream)))
+
+
+def qgemv_attn(kv_type, k_pages, v_pages, n_pages, page_size, page_stride, n_kv_heads, head_dim,
+               table, max_pages, kv_len, n_seq, q, q_stride, n_q_heads, scale, o, ws,
+               ws_bytes=None, stream=None):
+    _check("qgemv_attn",
+           lib().qgemv_attn(kv_type, _p(k_pages), _p(v_pages), n_pages, page_size, page_stride,
+                            n_kv_heads, head_dim, _p(table), max_pages, _p(kv_len), n_seq, _p(q),
+                            q_stride, n_q_heads, scale, _p(o), _p(ws),
+                            _nbytes(ws) if ws_bytes is None else ws_bytes, _stream(stream)))
+
+
+def qgemv_attn_prompt(kv_type, k_pages, v_pages, n_pages, page_size, page_stride, n_kv_heads,
+                      head_dim, table, max_pages, q_start, kv_len, n_seq, q, q_stride, n_rows,
+                      n_q_heads, scale, o, ws, ws_bytes=None, stream=None):
+    _check("qgemv_attn_prompt",
+           lib().qgemv_attn_prompt(kv_type, _p(k_pages), _p(v_pages), n_pages, page_size,
+                                   page_stride, n_kv_heads, head_dim, _p(table), max_pages,
+                                   _p(q_start), _p(kv_len), n_seq, _p(q), q_stride, n_rows,
+                                   n_q_heads, scale, _p(o), _p(ws),
+                                   _nbytes(ws) if ws_bytes is None else ws_bytes, _stream(stream)))
+
+
+def qgemv_attn_error(ws, stream=None) -> int:
+    flag = ctypes.c_int(0)
+    _check("qgemv_attn_error", lib().qgemv_attn_error(_p(ws), ctypes.byref(flag), _stream(stream)))
+    return flag.value
+
+
+def qgemv_route(logits, n_rows, n_exp, score, bias, n_group, group_top, topk_group, topk, renorm,
+                scale, ids, wts, stream=None):
+    _check("qgemv_route",
+           lib().qgemv_route(_p(logits), n_rows, n_exp, score, _p(bias), n_group, group_top,
+                             topk_group, topk, 1 if renorm else 0, scale, _p(ids), _p(wts),
+                             _stream(stream)))

@@ -45,3 +45,23 @@ def workspace(op: int, fmt: int, N: int, K: int, nb: int, n_exp: int = 0, topk: 
     if n == 0:
         return None
     return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def kv_pages(kv_type: int, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int,
+             device="cuda") -> tuple[torch.Tensor, torch.Tensor]:
+    """Uninitialised page arrays of a key-value cache, packed (page_stride = n_kv_heads *
+    page_size * head_dim): K [n_pages][n_kv_heads][page_size][head_dim] and V
+    [n_pages][n_kv_heads][head_dim][page_size]."""
+    dt = {B.F16: torch.float16, B.BF16: torch.bfloat16}[kv_type]
+    return (torch.empty((n_pages, n_kv_heads, page_size, head_dim), dtype=dt, device=device),
+            torch.empty((n_pages, n_kv_heads, head_dim, page_size), dtype=dt, device=device))
+
+
+def attn_workspace(op: int, n_seq: int, n_q_heads: int, n_kv_heads: int, head_dim: int,
+                   device="cuda") -> torch.Tensor:
+    """Zero-filled workspace of an attention-side operation (OP_KV_APPEND, OP_ATTN,
+    OP_ATTN_PROMPT)."""
+    n = B.qgemv_attn_workspace_bytes(op, n_seq, n_q_heads, n_kv_heads, head_dim)
+    if n < 0:
+        raise ValueError("invalid sizes for the workspace query")
+    return torch.zeros(n, dtype=torch.uint8, device=device)

@@ -73,18 +73,22 @@
 extern "C" {
 #endif
 
+/* Weight formats, and the two element types of a key-value cache. */
 enum { QG_Q4_0 = 2, QG_Q5_0 = 6, QG_Q8_0 = 8, QG_Q4_K = 12, QG_Q5_K = 13, QG_Q6_K = 14,
        QG_IQ4_NL = 20, QG_IQ4_XS = 23, QG_Q1_0 = 40, QG_AQ4 = 41 };
+enum { QG_F16 = 1, QG_BF16 = 30 };
 
 enum {
     QG_OK = 0,
     QG_ERR_NULL = 1,       /* a required pointer is NULL */
     QG_ERR_FORMAT = 2,     /* unknown format id, or a format the entry point does not take */
     QG_ERR_SHAPE = 3,      /* N < 1, nb outside [1, 16], K not a positive multiple of the block,
-                              topk outside [1, 8], n_exp < 1, or a size beyond the limits */
-    QG_ERR_ALIGN = 4,      /* W or a workspace not 256-B aligned, x or gamma not 16-B aligned, or
-                              an output, residual, id or weight array not 4-B aligned */
-    QG_ERR_WORKSPACE = 5,  /* ws smaller than qgemv_workspace_bytes() */
+                              topk outside [1, 8], n_exp < 1, or a size beyond the limits (of the
+                              attention side: those stated there) */
+    QG_ERR_ALIGN = 4,      /* W or a workspace not 256-B aligned, x, gamma or an attention-side
+                              float or page array not 16-B aligned (or a row stride of one not a
+                              multiple of 4), or another array not 4-B aligned */
+    QG_ERR_WORKSPACE = 5,  /* ws smaller than the operation's workspace query says */
     QG_ERR_LAUNCH = 6,     /* the HIP launch reported an error */
     QG_ERR_ALIAS = 7       /* an output overlaps an input in a way the call does not allow */
 };
@@ -93,6 +97,12 @@ enum {
 enum { QG_OP_GEMV = 0, QG_OP_NRM = 1, QG_OP_GUS_NRM = 2, QG_OP_RES = 3, QG_OP_ARGMAX = 4,
        QG_OP_MOE = 5, QG_OP_NRM_BIAS = 6 };
 
+/* Operation ids for qgemv_attn_workspace_bytes. */
+enum { QG_OP_KV_APPEND = 7, QG_OP_ATTN = 8, QG_OP_ATTN_PROMPT = 9 };
+
+/* Scores of qgemv_route. */
+enum { QG_SCORE_SOFTMAX = 0, QG_SCORE_SIGMOID = 1 };
+
 /* Activations of the gated product (qgemv_gus_act_nrm). */
 enum { QG_ACT_SILU = 0, QG_ACT_GELU_TANH = 1 };
 
@@ -100,6 +110,8 @@ enum { QG_ACT_SILU = 0, QG_ACT_GELU_TANH = 1 };
 #define QG_MAX_NB 16
 #define QG_MAX_TOPK 8
 #define QG_MAX_K 65536
+#define QG_ATTN_MAX_SEQ 1024
+#define QG_ROUTE_MAX_EXP 1024
 
 /* Bytes of the packed device layout of an N x K matrix, or -1 if (fmt, N, K) is invalid.
  * Equal to the GGUF byte count rounded up to 256 B per plane (two planes: quants and scales; the
@@ -237,6 +249,106 @@ int qgemm(int fmt, const void *W, int64_t N, int64_t K, const float *x, int64_t 
  * workspace was sized for. */
 int qgemv_moe_error(const void *ws, int64_t n_exp, int64_t N, int64_t K, int fmt, int *flag,
                     void *stream);
+
+/* Paged key-value cache and the attention that reads it
+ * -----------------------------------------------------
+ * The cache is a pool of pages of page_size consecutive positions, in two arrays of one element
+ * type (kv_type QG_F16 or QG_BF16).  Page p, head h (64-bit offsets, in elements):
+ *   k_pages + p * page_stride + h * page_size * head_dim   holds K as [page_size][head_dim],
+ *   v_pages + p * page_stride + h * page_size * head_dim   holds V as [head_dim][page_size]
+ * (V transposed inside the page: eight consecutive positions of one channel are one 16-byte load,
+ * as eight consecutive channels of one position are for K).  page_stride, at least
+ * n_kv_heads * page_size * head_dim and a multiple of 8, lets one pool hold several layers or K
+ * and V side by side.  table is int32 [n_seq][max_pages]: position t of sequence b lies in slot
+ * t % page_size of page table[b][t / page_size].  Entries behind a sequence's last position are
+ * never read.  kv_len, int32 [n_seq], counts a sequence's cached positions WITH the new ones of
+ * this step.
+ *
+ * New rows (of K and V for qgemv_kv_append, of queries for qgemv_attn_prompt) are packed:
+ * sequence b owns rows q_start[b] .. q_start[b + 1] - 1 (int32 [n_seq + 1], not decreasing,
+ * q_start[n_seq] <= n_rows) and its row r is at position
+ *   kv_len[b] - (q_start[b + 1] - q_start[b]) + (r - q_start[b]).
+ * Rows outside every sequence (behind the last one) are neither read nor written.  Sequences may
+ * be empty.  q_start NULL (qgemv_kv_append) means one new row per sequence, row b, with n_rows =
+ * n_seq, as qgemv_attn has it.
+ *
+ * The metadata is on the device, so a captured graph replays with new lengths.  It is checked
+ * there: a table entry outside [0, n_pages) that a position would use, or a position at or behind
+ * max_pages * page_size, leaves that position out (nothing is stored; attention treats it as
+ * masked) and sets the sticky flag in the workspace that qgemv_attn_error reports.  A row at a
+ * negative position (kv_len[b] less than the sequence's new rows: a padded batch) stores nothing
+ * and attends to nothing; its attention output is 0, as is that of kv_len[b] <= 0.
+ *
+ * Order: append the step's K and V first, then attend, on one stream.  Two sequences may share
+ * pages that neither appends to; appending to one page position from two rows is a race.
+ * page_size is 16, 32, 64, 128 or 256; head_dim 64, 96, 128, 192 or 256; n_kv_heads divides
+ * n_q_heads (query head h reads KV head h / (n_q_heads / n_kv_heads)); n_seq in
+ * [1, QG_ATTN_MAX_SEQ]; max_pages * page_size <= 2^30; n_rows in [1, QG_GEMM_MAX_M].  All float
+ * pointers and both page arrays are 16-byte aligned, row strides are multiples of 4 floats. */
+
+/* Workspace bytes of an attention-side operation (QG_OP_KV_APPEND, QG_OP_ATTN,
+ * QG_OP_ATTN_PROMPT), or -1 on invalid sizes.  It holds the sticky flag and the partial results of
+ * a split over the cache's length, so, like qgemv_moe's, it must be zero-filled once after
+ * allocation; a larger one (of another operation or more sequences) also serves.  Host-only. */
+int64_t qgemv_attn_workspace_bytes(int op, int n_seq, int n_q_heads, int n_kv_heads,
+                                   int head_dim);
+
+/* Store the new K and V rows in the cache, rounded to nearest-even.  k and v point at the first K
+ * and V value of row 0, f32, kv_stride floats apart from row to row (the fused QKV output: qkv +
+ * n_q_heads * head_dim, qkv + (n_q_heads + n_kv_heads) * head_dim, stride (n_q_heads +
+ * 2 n_kv_heads) * head_dim), heads back to back. */
+int qgemv_kv_append(int kv_type, void *k_pages, void *v_pages, int64_t n_pages, int page_size,
+                    int64_t page_stride, int n_kv_heads, int head_dim, const int32_t *table,
+                    int max_pages, const int32_t *q_start, const int32_t *kv_len, int n_seq,
+                    const float *k, const float *v, int64_t kv_stride, int64_t n_rows, void *ws,
+                    size_t ws_bytes, void *stream);
+
+/* Attention of one new token per sequence: o[b][h] = sum_t p_t V_t over the positions
+ * t < kv_len[b], p = softmax_t(scale q[b][h] . K_t).  q is f32, row b at q + b * q_stride, heads
+ * back to back (the fused QKV output itself); o is f32 [n_seq][n_q_heads * head_dim], the x of
+ * the output projection's qgemv_res.  Long caches are split over workgroups by the lengths found
+ * on the device and joined by a second, small launch on `stream`. */
+int qgemv_attn(int kv_type, const void *k_pages, const void *v_pages, int64_t n_pages,
+               int page_size, int64_t page_stride, int n_kv_heads, int head_dim,
+               const int32_t *table, int max_pages, const int32_t *kv_len, int n_seq,
+               const float *q, int64_t q_stride, int n_q_heads, float scale, float *o, void *ws,
+               size_t ws_bytes, void *stream);
+
+/* Causal attention of packed sequences of new rows (a prompt, a prefill chunk behind cached
+ * positions, or several tokens to verify): row r at position t attends to the positions <= t of
+ * its sequence.  q as in qgemv_attn, one row per new row; o is f32 [n_rows][n_q_heads *
+ * head_dim], rows outside every sequence left as they were.  Few rows over a long cache are split
+ * over its length and joined by a second launch.
+ * Accuracy of both: scores, softmax statistics and sums in f32; q and the probabilities enter the
+ * f16 / bf16 products as the sum of two halves of that type (2^-17 relative for bf16, 2^-21 for
+ * f16), K and V exactly as stored. */
+int qgemv_attn_prompt(int kv_type, const void *k_pages, const void *v_pages, int64_t n_pages,
+                      int page_size, int64_t page_stride, int n_kv_heads, int head_dim,
+                      const int32_t *table, int max_pages, const int32_t *q_start,
+                      const int32_t *kv_len, int n_seq, const float *q, int64_t q_stride,
+                      int64_t n_rows, int n_q_heads, float scale, float *o, void *ws,
+                      size_t ws_bytes, void *stream);
+
+/* Reads and clears the flag that the three calls above leave in their workspace (*flag = 1 if any
+ * position of an earlier call on this workspace had no valid page).  Like qgemv_moe_error it
+ * SYNCHRONIZES `stream`. */
+int qgemv_attn_error(const void *ws, int *flag, void *stream);
+
+/* Routing of rows to experts: the ids and weights qgemv_moe takes.  logits f32 [n_rows][n_exp].
+ * Scores s = softmax over the row's experts (QG_SCORE_SOFTMAX) or 1 / (1 + e^-z)
+ * (QG_SCORE_SIGMOID); choice c = s + bias (bias f32 [n_exp], balances the load; NULL: 0).  With
+ * n_group > 1 the experts form n_group equal consecutive groups, a group's score is the sum of
+ * its group_top largest c, and only the topk_group best groups stay.  ids[r] = the topk largest c
+ * left, in falling order; equal ones (of groups and of experts) go to the lower index, NaN counts
+ * as -inf.  wts[r] = s at ids[r] (without the bias), divided by their sum if renorm (0 if the sum
+ * is 0), times scale.  The choice is made in f64, so it does not depend on f32 rounding.  ids
+ * int32 and wts f32 [n_rows][topk].
+ * Limits: 1 <= n_rows <= QG_GEMM_MAX_M, 1 <= n_exp <= QG_ROUTE_MAX_EXP, 1 <= topk <= QG_MAX_TOPK,
+ * n_group divides n_exp, 1 <= group_top <= 2 and <= n_exp / n_group, 1 <= topk_group <= n_group,
+ * topk <= topk_group * (n_exp / n_group). */
+int qgemv_route(const float *logits, int64_t n_rows, int n_exp, int score, const float *bias,
+                int n_group, int group_top, int topk_group, int topk, int renorm, float scale,
+                int32_t *ids, float *wts, void *stream);
 
 /* Static, human-readable text of a status code. */
 const char *qgemv_status_str(int status);
