@@ -28,16 +28,25 @@ static bool heads_ok(int nq, int nkv, int hd)
     return nkv >= 1 && nq >= nkv && nq % nkv == 0 && head_dim_ok(hd) && nq <= 4096;
 }
 
-// Workspace: the sticky flag, then the partial results.
-static int64_t ws_bytes_of(int op, int n_seq, int nq, int nkv, int hd)
+// Workspace: the sticky flag (256 bytes), then of the split over a cache's length the (first slot,
+// chunks) records and the partial results.
+struct WsLayout {
+    int64_t rec, part, total;
+};
+
+static WsLayout ws_layout(int op, int nq, int nkv, int hd)
 {
-    (void)n_seq;
-    (void)nq;
-    (void)nkv;
-    (void)hd;
-    (void)op;
-    return 256;
+    WsLayout w = {256, 256, 256};
+    if (op == QG_OP_ATTN) {
+        const int group = nq / nkv;
+        w.part = w.rec + ATTN_SLOTS * 8;     // fewer (sequence, pair)s than slots, or no split
+        w.total = w.part + (int64_t)ATTN_SLOTS * (group < 16 ? group : 16) * (hd + 2) * 4;
+    }
+    w.total = (w.total + 255) / 256 * 256;
+    return w;
 }
+
+static int64_t ws_bytes_of(int op, int nq, int nkv, int hd) { return ws_layout(op, nq, nkv, hd).total; }
 
 struct Span {
     const void *p;
@@ -60,9 +69,9 @@ static int check_cache(int kv_type, const void *k_pages, const void *v_pages, in
         ++lg;
     if ((1 << lg) != page_size || !heads_ok(nq, nkv, hd) || n_seq < 1 || n_seq > QG_ATTN_MAX_SEQ ||
         n_rows < 1 || n_rows > QG_GEMM_MAX_M || max_pages < 1 ||
-        (int64_t)max_pages * page_size > (1 << 30) || n_pages < 1 || n_pages > (1 << 28) ||
+        (int64_t)max_pages * page_size > (1 << 24) || n_pages < 1 || n_pages > (1 << 28) ||
         page_stride % 8 || page_stride < (int64_t)nkv * page_size * hd ||
-        page_stride > ((int64_t)1 << 32) || (int64_t)nkv * page_size * hd > (1 << 28))
+        page_stride >= ((int64_t)1 << 32) || (int64_t)nkv * page_size * hd > (1 << 28))
         return QG_ERR_SHAPE;
     if (!al(k_pages, 16) || !al(v_pages, 16) || !al(table, 4) || !al(kv_len, 4) ||
         (q_start && !al(q_start, 4)))
@@ -118,7 +127,7 @@ static int run_attn(bool prompt, int kv_type, const void *k_pages, const void *v
         return QG_ERR_WORKSPACE;
     if (!al(ws, 256))
         return QG_ERR_ALIGN;
-    if ((int64_t)ws_bytes < ws_bytes_of(prompt ? QG_OP_ATTN_PROMPT : QG_OP_ATTN, n_seq, nq, nkv, hd))
+    if ((int64_t)ws_bytes < ws_bytes_of(prompt ? QG_OP_ATTN_PROMPT : QG_OP_ATTN, nq, nkv, hd))
         return QG_ERR_WORKSPACE;
     const Span in[] = {{q, ((n_rows - 1) * q_stride + width) * 4},
                        {k_pages, span},
@@ -130,7 +139,9 @@ static int run_attn(bool prompt, int kv_type, const void *k_pages, const void *v
         overlap(o, n_rows * width * 4, ws, (int64_t)ws_bytes))
         return QG_ERR_ALIAS;
     a.c.err = static_cast<unsigned int *>(ws);
-    a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + 256);
+    const WsLayout w = ws_layout(prompt ? QG_OP_ATTN_PROMPT : QG_OP_ATTN, nq, nkv, hd);
+    a.rec = static_cast<uint8_t *>(ws) + w.rec;
+    a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + w.part);
     a.q = q;
     a.q_stride = q_stride;
     a.o = o;
@@ -148,7 +159,7 @@ int64_t qgemv_attn_workspace_bytes(int op, int n_seq, int n_q_heads, int n_kv_he
     if ((op != QG_OP_KV_APPEND && op != QG_OP_ATTN && op != QG_OP_ATTN_PROMPT) || n_seq < 1 ||
         n_seq > QG_ATTN_MAX_SEQ || !heads_ok(n_q_heads, n_kv_heads, head_dim))
         return -1;
-    return ws_bytes_of(op, n_seq, n_q_heads, n_kv_heads, head_dim);
+    return ws_bytes_of(op, n_q_heads, n_kv_heads, head_dim);
 }
 
 int qgemv_kv_append(int kv_type, void *k_pages, void *v_pages, int64_t n_pages, int page_size,
@@ -175,7 +186,7 @@ int qgemv_kv_append(int kv_type, void *k_pages, void *v_pages, int64_t n_pages, 
         return QG_ERR_WORKSPACE;
     if (!al(ws, 256))
         return QG_ERR_ALIGN;
-    if ((int64_t)ws_bytes < ws_bytes_of(QG_OP_KV_APPEND, n_seq, n_kv_heads, n_kv_heads, head_dim))
+    if ((int64_t)ws_bytes < ws_bytes_of(QG_OP_KV_APPEND, n_kv_heads, n_kv_heads, head_dim))
         return QG_ERR_WORKSPACE;
     const int64_t rows = ((n_rows - 1) * kv_stride + width) * 4;
     const Span in[] = {{k, rows},

@@ -8,6 +8,9 @@
 
 namespace qg {
 
+// Workgroup slots of the split over a cache's length (qgemv_attn): two per compute unit.
+#define ATTN_SLOTS 512
+
 enum KvType { KV_F16 = 1, KV_BF16 = 30 };
 
 // The paged cache and the step's metadata, as the public header describes them.
@@ -37,6 +40,7 @@ struct AttnArgs {
     int64_t q_stride;
     float *o;                   // [n_rows][nq * hd]
     float *part;                // workspace: partial results of a split
+    void *rec;                  // workspace: (first slot, chunks) of each (sequence, pair)
     int nq, group;              // query heads; query heads per KV head
     float scale;
 };

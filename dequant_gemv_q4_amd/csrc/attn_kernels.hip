@@ -1,7 +1,8 @@
-// attn_kernels.hip -- the paged key-value cache and attention over it.
+// attn_kernels.hip -- the paged key-value cache: storing new rows, and attention of one new token per
+// sequence over it.
 #include <hip/hip_runtime.h>
 
-#include "attn_internal.h"
+#include "attn_common.h"
 
 namespace qg {
 
@@ -76,64 +77,421 @@ __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a)
     }
 }
 
-// One workgroup per (row, query head): strips of 256 positions, a thread's score each, running
-// maximum and sum, then each channel's weighted sum.
-template <int T>
-__global__ __launch_bounds__(256) void k_attn_plain(AttnArgs a)
+// ---------------------------------------------------------------------- one new token per sequence
+//
+// o = sum_t softmax(scale q . K_t) V_t for the query heads of one KV head: a workgroup takes up to
+// 16 of them against one run (chunk) of positions.  Both products run on the matrix cores with the
+// positions in the rows and the query heads in the columns, S^T = K Q^T and O^T = V^T P^T
+// (v_mfma_f32_16x16x32), so that
+//  - K, and V as the cache holds it (transposed inside the page), are the A operands: eight
+//    consecutive halves each, loaded from the cache straight into registers by 16-byte loads;
+//  - a lane's scores all belong to one query head (column l % 16), its running maximum, sum and
+//    factors are per-lane scalars, and the scores it holds are exactly the probabilities it must
+//    supply to the second product: row i of score tile tt is position 8 (i / 4) + 4 tt + i % 4 of a
+//    32-position step, so lane group g = l / 16 holds positions 8 g .. 8 g + 7.
+// The queries (times scale log2 e) and the probabilities are split into two or three f16 / bf16
+// pieces whose products add up in f32 (PIECES); the matrix cores are idle otherwise.
+//
+// Each of the four waves takes every fourth 32-position step, loads one step ahead (K, V) and two
+// ahead (page numbers), and keeps its own maximum, sum and O^T; they are joined in LDS at the end.
+// The reference of the exponentials moves only when a score exceeds it by 2^9 (a wave vote), so the
+// accumulators are hardly ever rescaled; probabilities are held times 2^6 (f16: 2^-30 of the
+// reference still has its first piece's bits, 2^15 does not overflow).
+//
+// Split over the length: the lengths are on the device, so every workgroup derives the same plan
+// from them: the smallest chunk (whole 128-position units) for which the chunks of all sequences
+// fit the ATTN_SLOTS workgroups of the grid; a sequence's chunks are equal to one unit.  One chunk:
+// the workgroup writes o; several: partial O, maximum and sum go to the workspace and k_attn_join
+// adds them in chunk order (no atomics: results do not depend on the order of execution).
+
+constexpr int ATTN_UNIT_LOG2 = 7;
+
+struct AttnPlan {
+    int b, pair, chunk, n_chunk;   // this workgroup's sequence, (KV head, 16-head tile), chunk
+    int64_t len;                   // the sequence's positions
+};
+
+// Positions of sequence b that have a place in its table.
+__device__ __forceinline__ int64_t seq_len(const KvArgs &c, int b)
 {
-    const KvArgs &c = a.c;
-    __shared__ float sq[256], sp[256], red[4];
-    __shared__ int64_t soff[256];
-    const int64_t r = blockIdx.x;
-    const int h = blockIdx.y, tid = threadIdx.x, hkv = h / a.group;
-    int64_t start, end;
-    const int b = seq_of_row(c, r, start, end);
-    if (b < 0)
-        return;
-    const int64_t last = c.kv_len[b] - (end - r);       // the row's position
-    for (int d = tid; d < c.hd; d += 256)
-        sq[d] = a.q[r * a.q_stride + (int64_t)h * c.hd + d] * a.scale;
-    float m = -INFINITY, l = 0.f, o = 0.f;
-    __syncthreads();
-    for (int64_t t0 = 0; t0 <= last && (t0 >> c.ps_log2) < c.max_pages; t0 += 256) {
-        const int64_t t = t0 + tid;
-        float s = -INFINITY;
-        int64_t off = -1;
-        if (t <= last)
-            off = page_at(c, b, t);
-        if (off >= 0) {
-            off += ((int64_t)hkv * c.hd << c.ps_log2);
-            const int slot = (int)(t & ((1 << c.ps_log2) - 1));
-            s = 0.f;
-            for (int d = 0; d < c.hd; ++d)
-                s = fmaf(sq[d], kv_float<T>(c.k[off + (int64_t)slot * c.hd + d]), s);
-            off += slot;
+    const int64_t n = c.kv_len[b], cap = (int64_t)c.max_pages << c.ps_log2;
+    if (n > cap)
+        atomicOr(c.err, 1u);
+    return n < 0 ? 0 : n < cap ? n : cap;
+}
+
+__device__ __forceinline__ int wave_sum(int v)
+{
+#pragma unroll
+    for (int x = 32; x; x >>= 1)
+        v += __shfl_xor(v, x);
+    return v;
+}
+
+// Chunks of a sequence of n positions when a chunk has u units (at least one, so that an empty
+// sequence's rows are written).
+__device__ __forceinline__ int chunks_of(int64_t n, int u)
+{
+    const int units = (int)((n + (1 << ATTN_UNIT_LOG2) - 1) >> ATTN_UNIT_LOG2);
+    return units <= u ? 1 : (units + u - 1) / u;
+}
+
+// Workgroup id -> its place in the plan; false if the plan has fewer workgroups.  Runs in every
+// wave (no barrier); lane l looks at sequences l, l + 64, ...
+__device__ bool attn_plan(const KvArgs &c, int pairs, int id, AttnPlan &p)
+{
+    const int lane = threadIdx.x & 63;
+    int u = 0x3fffffff;
+    if (c.n_seq * pairs < ATTN_SLOTS) {
+        // total chunks <= units / u + n_seq: u_hi is enough, u_lo is the least that could be
+        int units = 0;
+        for (int b = lane; b < c.n_seq; b += 64)
+            units += (int)((seq_len(c, b) + (1 << ATTN_UNIT_LOG2) - 1) >> ATTN_UNIT_LOG2);
+        units = wave_sum(units);
+        const int room = ATTN_SLOTS / pairs;              // workgroups per pair
+        int lo = (units + room - 1) / room;
+        lo = lo > 1 ? lo : 1;
+        int hi = (units + room - c.n_seq - 1) / (room - c.n_seq > 0 ? room - c.n_seq : 1);
+        hi = room > c.n_seq ? (hi > lo ? hi : lo) : 0x3fffffff;
+        while (lo < hi) {
+            const int mid = lo + (hi - lo) / 2;
+            int n = 0;
+            for (int b = lane; b < c.n_seq; b += 64)
+                n += chunks_of(seq_len(c, b), mid);
+            if (wave_sum(n) * pairs <= ATTN_SLOTS)
+                hi = mid;
+            else
+                lo = mid + 1;
         }
-        float mx = s;
-        for (int x = 32; x; x >>= 1)
-            mx = fmaxf(mx, __shfl_xor(mx, x));
-        if ((tid & 63) == 0)
-            red[tid >> 6] = mx;
-        __syncthreads();
-        mx = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-        const float mn = fmaxf(m, mx);
-        const float p = off >= 0 ? expf(s - mn) : 0.f;
-        const float f = m == -INFINITY ? 0.f : expf(m - mn);
-        sp[tid] = p;
-        soff[tid] = off;
-        __syncthreads();
-        o *= f;
-        l *= f;
-        m = mn;
-        for (int j = 0; j < 256; ++j) {
-            l += sp[j];
-            if (soff[j] >= 0 && tid < c.hd)
-                o = fmaf(sp[j], kv_float<T>(c.v[soff[j] + ((int64_t)tid << c.ps_log2)]), o);
-        }
-        __syncthreads();
+        u = lo;
     }
-    if (tid < c.hd)
-        a.o[r * a.nq * c.hd + (int64_t)h * c.hd + tid] = m == -INFINITY ? 0.f : o / l;
+    int base = 0;
+    for (int b0 = 0; b0 < c.n_seq; b0 += 64) {
+        const int b = b0 + lane;
+        const int64_t n = b < c.n_seq ? seq_len(c, b) : 0;
+        const int nc = b < c.n_seq ? chunks_of(n, u) : 0;
+        int end = nc * pairs;                             // inclusive scan over the lanes
+#pragma unroll
+        for (int x = 1; x < 64; x <<= 1) {
+            const int y = __shfl_up(end, x);
+            end += lane >= x ? y : 0;
+        }
+        end += base;
+        const uint64_t in = __ballot(id < end && b < c.n_seq);
+        if (in) {
+            const int l = __ffsll((unsigned long long)in) - 1;
+            p.b = b0 + l;
+            p.n_chunk = __shfl(nc, l);
+            p.len = __shfl((int)n, l);
+            const int rel = id - (__shfl(end, l) - p.n_chunk * pairs);
+            p.pair = rel / p.n_chunk;
+            p.chunk = rel % p.n_chunk;
+            return true;
+        }
+        base = __shfl(end, 63);
+    }
+    return false;
+}
+
+// Workspace of a split: per slot, the tile's O (unnormalised) [cols][hd], then (maximum, sum)
+// [cols]; then per (sequence, pair) its first slot and chunk count.
+__host__ __device__ constexpr int64_t attn_part_floats(int cols, int hd) { return (int64_t)cols * (hd + 2); }
+
+template <int T, int D>
+__global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn(AttnArgs a)
+{
+    constexpr int KB = D / 32, DT = D / 16, NP = PIECES<T>;
+    __shared__ __attribute__((aligned(16))) float s_o[4][16][D];
+    __shared__ float s_m[4][16], s_l[4][16];
+    const KvArgs &c = a.c;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int i = lane & 15, g = lane >> 4;
+    const int tiles = (a.group + 15) / 16, pairs = c.nkv * tiles;
+    AttnPlan p;
+    if (!attn_plan(c, pairs, blockIdx.x, p))
+        return;
+    const int b = __builtin_amdgcn_readfirstlane(p.b), pair = __builtin_amdgcn_readfirstlane(p.pair);
+    const int chunk = __builtin_amdgcn_readfirstlane(p.chunk);
+    const int n_chunk = __builtin_amdgcn_readfirstlane(p.n_chunk);
+    const int len = __builtin_amdgcn_readfirstlane((int)p.len);
+    const int hkv = pair / tiles, h0 = hkv * a.group + (pair % tiles) * 16;
+    const int cols = min(16, a.group - (pair % tiles) * 16);
+
+    // this chunk's 32-position steps, dealt to the waves in turn
+    const int units = (len + (1 << ATTN_UNIT_LOG2) - 1) >> ATTN_UNIT_LOG2;
+    const int per = units / n_chunk, more = units % n_chunk;
+    const int unit0 = chunk * per + min(chunk, more);
+    const int t_begin = unit0 << ATTN_UNIT_LOG2;
+    const int t_end = min(len, (unit0 + per + (chunk < more ? 1 : 0)) << ATTN_UNIT_LOG2);
+    const int n_steps = t_end > t_begin + 32 * wave ? (t_end - t_begin - 32 * wave + 127) / 128 : 0;
+
+    // queries of column i: scaled, split
+    au4 qf[NP][KB];
+    float unscale;
+    {
+        const float *qr = a.q + (int64_t)b * a.q_stride + (int64_t)(h0 + (i < cols ? i : 0)) * D;
+        float v[KB][8], amax = 0.f;
+        const float f = i < cols ? a.scale * LOG2E : 0.f;
+#pragma unroll
+        for (int k = 0; k < KB; ++k) {
+            const float4 x = *reinterpret_cast<const float4 *>(qr + 32 * k + 8 * g);
+            const float4 y = *reinterpret_cast<const float4 *>(qr + 32 * k + 8 * g + 4);
+            const float w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                v[k][e] = i < cols ? w[e] : 0.f;
+                amax = fmaxf(amax, fabsf(v[k][e]));
+            }
+        }
+        const float sc = q_scale<T>(max_x32(max_x16(amax)));
+        unscale = f / sc;
+#pragma unroll
+        for (int k = 0; k < KB; ++k) {
+            float w[8];
+            au4 out[NP];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                w[e] = v[k][e] * sc;
+            split8<T>(w, out);
+#pragma unroll
+            for (int x = 0; x < NP; ++x)
+                qf[x][k] = out[x];
+        }
+    }
+
+    af4 o[DT];
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+        o[d] = af4{0.f, 0.f, 0.f, 0.f};
+    float m = -INFINITY, l = 0.f;
+
+    if (n_steps > 0) {
+        const int last_entry = (len - 1) >> c.ps_log2, ps_mask = (1 << c.ps_log2) - 1;
+        const int32_t *table = c.table + (int64_t)b * c.max_pages;
+        const int64_t head = (int64_t)hkv * D << c.ps_log2;
+        const int tok_k = 8 * (i >> 2) + (i & 3);         // + 4 tt: position of K row i in a step
+        const int64_t np = c.n_pages;
+        struct Ids {
+            int k, v;
+        };
+        struct Buf {
+            au4 k[2][KB], v[DT];
+            bool bad;                                     // this lane's positions have no page
+        };
+        auto step_t = [&](int s) { return t_begin + 32 * wave + 128 * (s < n_steps ? s : n_steps - 1); };
+        auto ids_of = [&](int s) {
+            const int t = step_t(s);
+            Ids r;
+            r.k = table[min((t + tok_k) >> c.ps_log2, last_entry)];
+            r.v = table[min((t + 8 * g) >> c.ps_log2, last_entry)];
+            return r;
+        };
+        auto issue = [&](Buf &x, int s, const Ids &id) {
+            const int t = step_t(s);
+            const bool okk = id.k >= 0 && id.k < np, okv = id.v >= 0 && id.v < np;
+            x.bad = !okv;
+            const uint16_t *kp = c.k + ((okk ? (int64_t)id.k : 0) * c.page_stride + head) + 8 * g;
+            const uint16_t *vp = c.v + ((okv ? (int64_t)id.v : 0) * c.page_stride + head) +
+                                 (i << c.ps_log2) + ((t + 8 * g) & ps_mask);
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+                for (int k = 0; k < KB; ++k)
+                    x.k[tt][k] = *reinterpret_cast<const au4 *>(kp + ((t + tok_k + 4 * tt) & ps_mask) * D + 32 * k);
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+                x.v[d] = *reinterpret_cast<const au4 *>(vp + ((16 * d) << c.ps_log2));
+        };
+        auto compute = [&](Buf &x, int s) {
+            const int t = step_t(s);
+            float sc[8];
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt) {
+                af4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int y = NP - 1; y >= 0; --y)
+#pragma unroll
+                    for (int k = 0; k < KB; ++k)
+                        acc = mm16<T>(x.k[tt][k], qf[y][k], acc);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    sc[4 * tt + r] = acc[r] * unscale;
+            }
+            const uint64_t any_bad = __ballot(x.bad);
+            const bool masked = any_bad != 0 || t + 32 > t_end;
+            if (masked) {
+                if (any_bad && lane == 0)
+                    atomicOr(c.err, 1u);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    sc[e] = x.bad || t + 8 * g + e >= t_end ? -INFINITY : sc[e];
+                // what a masked position holds must not reach the product: 0 x NaN is NaN
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const int tw = t + 8 * g + 2 * w;
+                    const uint32_t keep = x.bad || tw >= t_end ? 0u : tw + 1 >= t_end ? 0xFFFFu : ~0u;
+#pragma unroll
+                    for (int d = 0; d < DT; ++d)
+                        x.v[d][w] &= keep;
+                }
+            }
+            float mx = fmaxf(fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3])),
+                             fmaxf(fmaxf(sc[4], sc[5]), fmaxf(sc[6], sc[7])));
+            if (__any(mx > m + 9.0f)) {
+                mx = max_x32(max_x16(mx));
+                const float mn = fmaxf(m, mx);
+                const float f = m == mn ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+                m = mn;
+                l *= f;
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+                    o[d] *= f;
+            }
+            float pr[8];
+            const float ref = m == -INFINITY ? INFINITY : 6.0f - m;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                pr[e] = __builtin_amdgcn_exp2f(sc[e] + ref);
+                if (masked)
+                    pr[e] = sc[e] == -INFINITY ? 0.f : pr[e];
+                l += pr[e];
+            }
+            au4 pf[NP];
+            split8<T>(pr, pf);
+#pragma unroll
+            for (int y = NP - 1; y >= 0; --y)
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+                    o[d] = mm16<T>(x.v[d], pf[y], o[d]);
+        };
+        Buf A, B;
+        Ids i0 = ids_of(0), i1 = ids_of(1);
+        issue(A, 0, i0);
+        for (int s = 0; s < n_steps; s += 2) {
+            i0 = ids_of(s + 2);
+            issue(B, s + 1, i1);
+            compute(A, s);
+            i1 = ids_of(s + 3);
+            issue(A, s + 2, i0);
+            if (s + 1 < n_steps)
+                compute(B, s + 1);
+        }
+    }
+
+    // join the waves: column i of O^T, rows 16 d + 4 g + r
+    l = sum_x32(sum_x16(l));
+    if (g == 0) {
+        s_m[wave][i] = m;
+        s_l[wave][i] = l;
+    }
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+        *reinterpret_cast<af4 *>(&s_o[wave][i][16 * d + 4 * g]) = o[d];
+    __syncthreads();
+    float *part = nullptr;
+    if (n_chunk > 1) {
+        part = a.part + (int64_t)blockIdx.x * attn_part_floats(min(16, a.group), D);
+        if (chunk == 0 && threadIdx.x == 0) {             // k_attn_join's record of this pair
+            int *rec = reinterpret_cast<int *>(a.rec) + 2 * (b * pairs + pair);
+            rec[0] = blockIdx.x;
+            rec[1] = n_chunk;
+        }
+    } else if (threadIdx.x == 0 && c.n_seq * pairs < ATTN_SLOTS) {
+        reinterpret_cast<int *>(a.rec)[2 * (b * pairs + pair) + 1] = 1;
+    }
+    for (int e = threadIdx.x; e < cols * (D / 4); e += 256) {
+        const int col = e / (D / 4), d4 = e % (D / 4);
+        const float mm = fmaxf(fmaxf(s_m[0][col], s_m[1][col]), fmaxf(s_m[2][col], s_m[3][col]));
+        af4 sum = {0.f, 0.f, 0.f, 0.f};
+        float ls = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const float mw = s_m[w][col];
+            if (mw != -INFINITY) {
+                const float f = mw == mm ? 1.0f : __builtin_amdgcn_exp2f(mw - mm);
+                sum += *reinterpret_cast<const af4 *>(&s_o[w][col][4 * d4]) * f;
+                ls += s_l[w][col] * f;
+            }
+        }
+        if (n_chunk > 1) {
+            *reinterpret_cast<af4 *>(part + col * D + 4 * d4) = sum;
+            if (d4 == 0) {
+                float *ml = part + (int64_t)min(16, a.group) * D + 2 * col;
+                ml[0] = mm;
+                ml[1] = ls;
+            }
+        } else {
+            const float inv = mm == -INFINITY ? 0.f : 1.0f / ls;
+            *reinterpret_cast<af4 *>(a.o + ((int64_t)b * a.nq + h0 + col) * D + 4 * d4) = sum * inv;
+        }
+    }
+}
+
+// o of one (sequence, pair, column) from its chunks' partial results, in chunk order.
+__global__ __launch_bounds__(512) void k_attn_join(AttnArgs a)
+{
+    __shared__ float s_f[ATTN_SLOTS], s_red[8][2];
+    __shared__ __attribute__((aligned(16))) float s_sum[512 * 4];
+    const KvArgs &c = a.c;
+    const int tiles = (a.group + 15) / 16, pairs = c.nkv * tiles, width = min(16, a.group);
+    const int col = blockIdx.x % width, bp = blockIdx.x / width;
+    const int pair = bp % pairs, b = bp / pairs;
+    const int first = reinterpret_cast<const int *>(a.rec)[2 * bp], n = reinterpret_cast<const int *>(a.rec)[2 * bp + 1];
+    const int h = (pair / tiles) * a.group + (pair % tiles) * 16 + col;
+    if (n <= 1 || (pair % tiles) * 16 + col >= a.group)
+        return;
+    const int D = c.hd, tid = threadIdx.x;
+    const int64_t stride = attn_part_floats(width, D);
+    const float *part = a.part + first * stride;
+    float m = -INFINITY;
+    for (int k = tid; k < n; k += 512) {
+        const float v = part[k * stride + (int64_t)width * D + 2 * col];
+        s_f[k] = v;
+        m = fmaxf(m, v);
+    }
+#pragma unroll
+    for (int x = 32; x; x >>= 1)
+        m = fmaxf(m, __shfl_xor(m, x));
+    if ((tid & 63) == 0)
+        s_red[tid >> 6][0] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 8; ++w)
+        m = fmaxf(m, s_red[w][0]);
+    float l = 0.f;
+    for (int k = tid; k < n; k += 512) {
+        const float v = s_f[k];
+        const float f = v == -INFINITY ? 0.f : v == m ? 1.0f : __builtin_amdgcn_exp2f(v - m);
+        s_f[k] = f;
+        l += f == 0.f ? 0.f : f * part[k * stride + (int64_t)width * D + 2 * col + 1];
+    }
+#pragma unroll
+    for (int x = 32; x; x >>= 1)
+        l += __shfl_xor(l, x);
+    if ((tid & 63) == 0)
+        s_red[tid >> 6][1] = l;
+    __syncthreads();
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w)
+        l += s_red[w][1];
+    const int lanes = D / 4, groups = 512 / lanes, d4 = tid % lanes, grp = tid / lanes;
+    af4 sum = {0.f, 0.f, 0.f, 0.f};
+    if (grp < groups)
+#pragma unroll 8
+        for (int k = grp; k < n; k += groups) {
+            const float f = s_f[k];
+            const af4 v = *reinterpret_cast<const af4 *>(part + k * stride + (int64_t)col * D + 4 * d4);
+            sum += f == 0.f ? af4{0.f, 0.f, 0.f, 0.f} : v * f;
+        }
+    *reinterpret_cast<af4 *>(s_sum + 4 * tid) = sum;
+    __syncthreads();
+    if (tid < lanes) {
+        for (int k = 1; k < groups; ++k)
+            sum += *reinterpret_cast<const af4 *>(s_sum + 4 * (tid + k * lanes));
+        *reinterpret_cast<af4 *>(a.o + ((int64_t)b * a.nq + h) * D + 4 * tid) =
+            sum * (m == -INFINITY ? 0.f : 1.0f / l);
+    }
 }
 
 int launch_kv_append(int kv_type, const AppendArgs &a, void *stream)
@@ -146,18 +504,29 @@ int launch_kv_append(int kv_type, const AppendArgs &a, void *stream)
     return (int)hipGetLastError();
 }
 
-static int launch_plain(int kv_type, const AttnArgs &a, void *stream)
+int launch_attn(int kv_type, const AttnArgs &a, void *stream)
 {
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const dim3 grid((unsigned)a.c.n_rows, (unsigned)a.nq);
-    if (kv_type == KV_F16)
-        hipLaunchKernelGGL(k_attn_plain<KV_F16>, grid, dim3(256), 0, s, a);
-    else
-        hipLaunchKernelGGL(k_attn_plain<KV_BF16>, grid, dim3(256), 0, s, a);
+    const int pairs = a.c.nkv * ((a.group + 15) / 16), all = a.c.n_seq * pairs;
+    const int grid = all > ATTN_SLOTS ? all : ATTN_SLOTS;
+    void (*k)(AttnArgs) = nullptr;
+#define QG_ATTN_D(DD) k = kv_type == KV_F16 ? k_attn<KV_F16, DD> : k_attn<KV_BF16, DD>
+    switch (a.c.hd) {
+    case 64: QG_ATTN_D(64); break;
+    case 96: QG_ATTN_D(96); break;
+    case 128: QG_ATTN_D(128); break;
+    case 192: QG_ATTN_D(192); break;
+    default: QG_ATTN_D(256); break;
+    }
+#undef QG_ATTN_D
+    hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(256), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    // no sequence is split when there are as many (sequence, pair)s as workgroup slots
+    if (e != hipSuccess || all >= ATTN_SLOTS)
+        return (int)e;
+    const int cols = a.group < 16 ? a.group : 16;
+    hipLaunchKernelGGL(k_attn_join, dim3((unsigned)(all * cols)), dim3(512), 0, s, a);
     return (int)hipGetLastError();
 }
-
-int launch_attn(int kv_type, const AttnArgs &a, void *stream) { return launch_plain(kv_type, a, stream); }
-int launch_attn_prompt(int kv_type, const AttnArgs &a, void *stream) { return launch_plain(kv_type, a, stream); }
 
 }  // namespace qg

@@ -283,13 +283,13 @@ int qgemv_moe_error(const void *ws, int64_t n_exp, int64_t N, int64_t K, int fmt
  * pages that neither appends to; appending to one page position from two rows is a race.
  * page_size is 16, 32, 64, 128 or 256; head_dim 64, 96, 128, 192 or 256; n_kv_heads divides
  * n_q_heads (query head h reads KV head h / (n_q_heads / n_kv_heads)); n_seq in
- * [1, QG_ATTN_MAX_SEQ]; max_pages * page_size <= 2^30; n_rows in [1, QG_GEMM_MAX_M].  All float
+ * [1, QG_ATTN_MAX_SEQ]; max_pages * page_size <= 2^24; n_rows in [1, QG_GEMM_MAX_M].  All float
  * pointers and both page arrays are 16-byte aligned, row strides are multiples of 4 floats. */
 
 /* Workspace bytes of an attention-side operation (QG_OP_KV_APPEND, QG_OP_ATTN,
  * QG_OP_ATTN_PROMPT), or -1 on invalid sizes.  It holds the sticky flag and the partial results of
  * a split over the cache's length, so, like qgemv_moe's, it must be zero-filled once after
- * allocation; a larger one (of another operation or more sequences) also serves.  Host-only. */
+ * allocation; a larger one also serves.  Host-only. */
 int64_t qgemv_attn_workspace_bytes(int op, int n_seq, int n_q_heads, int n_kv_heads,
                                    int head_dim);
 
