@@ -41,6 +41,8 @@ static WsLayout ws_layout(int op, int nq, int nkv, int hd)
         const int group = nq / nkv;
         w.part = w.rec + ATTN_SLOTS * 8;     // fewer (sequence, pair)s than slots, or no split
         w.total = w.part + (int64_t)ATTN_SLOTS * (group < 16 ? group : 16) * (hd + 2) * 4;
+    } else if (op == QG_OP_ATTN_PROMPT) {
+        w.total = w.part + (int64_t)PROMPT_SLOTS * 128 * (hd + 2) * 4;   // 128 rows a tile
     }
     w.total = (w.total + 255) / 256 * 256;
     return w;
@@ -119,7 +121,10 @@ static int run_attn(bool prompt, int kv_type, const void *k_pages, const void *v
     if (!q || !o || (prompt && !q_start))
         return QG_ERR_NULL;
     const int64_t width = (int64_t)nq * hd;
-    if (q_stride < width || q_stride > ((int64_t)1 << 31) || !isfinite(scale))
+    if (q_stride < width || q_stride > ((int64_t)1 << 31) || n_rows * nq > (1 << 30) ||
+        !isfinite(scale))
+        return QG_ERR_SHAPE;
+    if (prompt && plan_prompt(n_rows, n_seq, nkv, nq / nkv).tiles * nkv > 0x7fffffffLL)
         return QG_ERR_SHAPE;
     if (!al(q, 16) || !al(o, 16) || q_stride % 4)
         return QG_ERR_ALIGN;

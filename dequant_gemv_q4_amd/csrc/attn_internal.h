@@ -10,6 +10,8 @@ namespace qg {
 
 // Workgroup slots of the split over a cache's length (qgemv_attn): two per compute unit.
 #define ATTN_SLOTS 512
+// The same of qgemv_attn_prompt: tile splits, and with them partial results, of a call.
+#define PROMPT_SLOTS 512
 
 enum KvType { KV_F16 = 1, KV_BF16 = 30 };
 
@@ -53,6 +55,12 @@ struct RouteArgs {
     int n_exp, sigmoid, n_group, group_top, topk_group, topk, renorm;
     float scale;
 };
+
+struct PromptPlan {
+    int64_t tiles;              // tile ids per KV head
+    int n_split;                // splits of a tile over the cache's length
+};
+PromptPlan plan_prompt(int64_t n_rows, int n_seq, int nkv, int group);
 
 // Launchers: a hipError_t value (0 = success).
 int launch_kv_append(int kv_type, const AppendArgs &a, void *stream);

@@ -348,12 +348,10 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn(AttnArgs a)
                     o[d] *= f;
             }
             float pr[8];
-            const float ref = m == -INFINITY ? INFINITY : 6.0f - m;
+            const float ref = m == -INFINITY ? 0.f : 6.0f - m;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 pr[e] = __builtin_amdgcn_exp2f(sc[e] + ref);
-                if (masked)
-                    pr[e] = sc[e] == -INFINITY ? 0.f : pr[e];
                 l += pr[e];
             }
             au4 pf[NP];

@@ -1,128 +1,482 @@
-// attn_prompt_kernels.hip -- causal attention of packed rows.
+// attn_prompt_kernels.hip -- causal attention of packed sequences of new rows over the paged cache.
+//
+// A tile is 128 rows of one sequence and one KV head, row rho = token * group + head: the query
+// heads that share a KV head lie side by side, so a tile of any group spans few tokens (little of
+// the diagonal is computed in vain) and every K and V element read serves all of them.  Four waves
+// take 32 rows each against steps of 64 positions held in LDS.  As in the one-token kernel the
+// positions are the rows of both products, S^T = K Q^T and O^T = V^T P^T (v_mfma_f32_32x32x16): a
+// lane's 32 scores of a step belong to one row of the tile (column l % 32), so maximum, sum and
+// factors are per-lane scalars, and they are the probabilities that the lane supplies to the second
+// product (score row i of a 32-position tile is position 16 (i / 16) + 8 (i / 4 % 2) +
+// 4 (i / 8 % 2) + i % 4, which makes a lane's eight values consecutive positions).
+//
+// K and V go from the pages to LDS without registers (global_load_lds, 16 bytes a lane), one step
+// ahead, two buffers, one barrier a step.  The copies land in lane order, so the 16-byte pieces of a
+// row are permuted at the source instead (piece ^ key of the row): eight lanes that read eight rows
+// then use different banks.
 #include <hip/hip_runtime.h>
 
 #include "attn_common.h"
 
 namespace qg {
 
-// Round to nearest-even, as the conversion instructions do.
-template <int T>
-__device__ __forceinline__ uint16_t kv_round(float v)
+constexpr int PT_ROWS = 128;      // rows of a tile
+constexpr int PT_STEP = 64;       // positions of a step
+
+// Global -> LDS copy of 16 bytes per lane to lds_dst + 16 lane.  Written as asm so that the compiler
+// does not wait for it at the next LDS read: the kernel waits with vmcnt itself, once a step.
+__device__ __forceinline__ void pt_copy16(const void *src, uint32_t lds_dst)
 {
-    if constexpr (T == KV_F16)
-        return __builtin_bit_cast(uint16_t, (_Float16)v);
-    else
-        return __builtin_bit_cast(uint16_t, (__bf16)v);
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(src), "{m0}"(lds_dst) : "memory");
 }
-template <int T>
-__device__ __forceinline__ float kv_float(uint16_t b)
+__device__ __forceinline__ void pt_wait_all()
 {
-    if constexpr (T == KV_F16)
-        return (float)__builtin_bit_cast(_Float16, b);
-    else
-        return __builtin_bit_cast(float, (uint32_t)b << 16);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+__device__ __forceinline__ void pt_barrier()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
 }
 
-// Sequence of row r: the last b whose q_start is <= r and whose end is behind r, or -1.
-__device__ __forceinline__ int seq_of_row(const KvArgs &c, int64_t r, int64_t &start, int64_t &end)
+// Bits 15 and 31 set where a half of the pair is an infinity or NaN.
+template <int T>
+__device__ __forceinline__ uint32_t nonfinite2(uint32_t v)
 {
-    if (!c.q_start) {
-        start = r;
-        end = r + 1;
-        return (int)r;
-    }
-    for (int b = 0; b < c.n_seq; ++b) {
-        start = c.q_start[b];
-        end = c.q_start[b + 1];
-        if (r >= start && r < end)
-            return b;
-    }
-    return -1;
+    return T == KV_F16 ? ((v & 0x7C007C00u) + 0x04000400u) & 0x80008000u
+                       : ((v & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
 }
 
-// Element offset of position t's page, or -1 (sticky flag set) if it has no valid one.
-__device__ __forceinline__ int64_t page_at(const KvArgs &c, int b, int64_t t)
+struct TilePlace {
+    int b;                 // sequence
+    int row0, rows;        // first packed row of the sequence, its new rows
+    int rho0;              // first (token, head) row of the tile within the sequence
+    int pos0;              // position of the sequence's first new row (may be negative)
+    int hi;                // positions the tile reads: [0, hi)
+    int chunk0, chunk1;    // steps of this workgroup's split
+};
+
+// Tile id -> sequence.  Sequence b's tiles start at q_start[b] * group / 128 + b: never fewer ids
+// than it has tiles, found without a prefix sum.  Ids without rows return false.
+__device__ bool tile_place(const KvArgs &c, int group, int id, int split, int n_split, TilePlace &p,
+                           int &splits)
 {
-    const int64_t i = t >> c.ps_log2;
-    const int page = i < c.max_pages ? c.table[(int64_t)b * c.max_pages + i] : -1;
-    if (page < 0 || page >= c.n_pages) {
+    const int lane = threadIdx.x & 63;
+    auto start = [&](int b) {
+        const int64_t s = c.q_start[b];
+        return (int)(s < 0 ? 0 : s < c.n_rows ? s : c.n_rows);
+    };
+    int b = -1;
+#pragma unroll 4
+    for (int b0 = 0; b0 < c.n_seq; b0 += 64) {
+        const int i = b0 + lane;
+        const bool in = i < c.n_seq && (int64_t)start(i) * group / PT_ROWS + i <= id;
+        b += __popcll(__ballot(in));
+    }
+    if (b < 0)
+        return false;
+    b = __builtin_amdgcn_readfirstlane(b);
+    const int r0 = start(b), r1 = start(b + 1);
+    const int local = id - (int)((int64_t)r0 * group / PT_ROWS + b);
+    const int64_t cap = (int64_t)c.max_pages << c.ps_log2;
+    const int64_t n = c.kv_len[b];
+    if (local < 0 || r1 <= r0 || (int64_t)local * PT_ROWS >= (int64_t)(r1 - r0) * group)
+        return false;
+    if (n > cap && lane == 0)
         atomicOr(c.err, 1u);
-        return -1;
-    }
-    return page * c.page_stride;
+    p.b = b;
+    p.row0 = r0;
+    p.rows = r1 - r0;
+    p.rho0 = local * PT_ROWS;
+    p.pos0 = (int)(n < -(1 << 30) ? -(1 << 30) : n) - p.rows;
+    const int last = min((p.rho0 + PT_ROWS - 1) / group, p.rows - 1);     // last token of the tile
+    const int64_t hi = (int64_t)p.pos0 + last + 1;
+    p.hi = (int)(hi < 0 ? 0 : hi < cap ? hi : cap);
+    // a split has at least eight steps; all splits of a tile are equal to one step
+    const int steps = (p.hi + PT_STEP - 1) / PT_STEP;
+    splits = min(n_split, max(1, steps / 8));
+    if (split >= splits)
+        return false;
+    const int per = steps / splits, more = steps % splits;
+    p.chunk0 = split * per + min(split, more);
+    p.chunk1 = p.chunk0 + per + (split < more ? 1 : 0);
+    return true;
 }
 
-// One workgroup per (row, query head): strips of 256 positions, a thread's score each, running
-// maximum and sum, then each channel's weighted sum.
-template <int T>
-__global__ __launch_bounds__(256) void k_attn_plain(AttnArgs a)
+__host__ __device__ constexpr int64_t prompt_part_floats(int hd) { return (int64_t)PT_ROWS * (hd + 2); }
+
+template <int T, int D>
+__global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs a, int n_split)
+{
+    constexpr int NP = PIECES<T>, KB = D / 16, DT = D / 32;
+    constexpr int PR = D / 8;                          // 16-byte pieces of a K row
+    constexpr int KEYM = D % 64 == 0 ? 7 : 3;          // bits of the piece number that the key takes
+    constexpr int HALF = PT_STEP * D * 2;              // bytes of a K (or V) buffer
+    constexpr int PASS = HALF / 4096;                  // copies of a thread for either
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * HALF];   // K0 V0 K1 V1
+    const KvArgs &c = a.c;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int col = lane & 31, hf = lane >> 5;
+    const int hkv = blockIdx.x % c.nkv;
+    const int id = gridDim.x / c.nkv - 1 - blockIdx.x / c.nkv;   // the longest rows come first
+    TilePlace p;
+    int splits;
+    if (!tile_place(c, a.group, id, blockIdx.y, n_split, p, splits))
+        return;
+
+    // this lane's row
+    const int rho = p.rho0 + 32 * wave + col;
+    const int tok = rho / a.group, head = hkv * a.group + rho % a.group;
+    const bool live = tok < p.rows;
+    // the wave's least and largest position (rows rise with the column); rows past the sequence
+    // compute along with the last one and are not stored
+    const int wave_tok0 = (p.rho0 + 32 * wave) / a.group;
+    const int wave_tok1 = min((p.rho0 + 32 * wave + 31) / a.group, p.rows - 1);
+    const int wave_min = p.pos0 + wave_tok0;
+    const int wave_max = wave_tok0 < p.rows ? p.pos0 + wave_tok1 : -1;
+    const int pos = live ? p.pos0 + tok : wave_max;    // the row sees positions 0..pos
+
+    au4 qf[NP][KB];
+    float unscale;
+    {
+        const float *qr = a.q + (int64_t)(p.row0 + (live ? tok : 0)) * a.q_stride + (int64_t)head * D;
+        float v[KB][8], amax = 0.f;
+#pragma unroll
+        for (int k = 0; k < KB; ++k) {
+            const float4 x = *reinterpret_cast<const float4 *>(qr + 16 * k + 8 * hf);
+            const float4 y = *reinterpret_cast<const float4 *>(qr + 16 * k + 8 * hf + 4);
+            const float w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                v[k][e] = live ? w[e] : 0.f;
+                amax = fmaxf(amax, fabsf(v[k][e]));
+            }
+        }
+        const float sc = q_scale<T>(max_x32(amax));
+        unscale = a.scale * LOG2E / sc;
+#pragma unroll
+        for (int k = 0; k < KB; ++k) {
+            float w[8];
+            au4 out[NP];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                w[e] = v[k][e] * sc;
+            split8<T>(w, out);
+#pragma unroll
+            for (int x = 0; x < NP; ++x)
+                qf[x][k] = out[x];
+        }
+    }
+
+    // copies: LDS piece idx = 256 pass + tid of a buffer.  K: row idx / PR, source piece
+    // (idx % PR) ^ key(row); V: channel idx / 8, source piece (idx % 8) ^ (channel % 8)
+    const int32_t *table = c.table + (int64_t)p.b * c.max_pages;
+    const int ps_mask = (1 << c.ps_log2) - 1;
+    const int last_entry = p.hi > 0 ? (p.hi - 1) >> c.ps_log2 : 0;
+    const int64_t head_off = (int64_t)hkv * D << c.ps_log2;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)lds + (uint32_t)wave * 1024u;
+    const int vpiece = (tid & 7) ^ ((tid >> 3) & 7);
+    // page number of 16-position block lane % 4 of a step
+    auto ids_of = [&](int s) { return table[min((s * PT_STEP + 16 * (lane & 3)) >> c.ps_log2, last_entry)]; };
+    auto key = [](int row) { return ((row & 3) | ((row >> 1) & 4)) & KEYM; };
+    auto issue = [&](int s, int buf, int ids) -> uint32_t {
+        const bool ok = ids >= 0 && ids < c.n_pages;
+        const uint32_t bad = (uint32_t)__ballot(!ok) & 15u;
+        const int page = ok ? ids : 0;
+        const int t0 = s * PT_STEP;
+        const uint32_t dst = lds0 + (uint32_t)buf * 2 * HALF;
+#pragma unroll
+        for (int x = 0; x < PASS; ++x) {
+            const int idx = 256 * x + tid, row = idx / PR, piece = (idx % PR) ^ key(row);
+            const int pg = __shfl(page, row >> 4);
+            const uint16_t *src = c.k + ((int64_t)pg * c.page_stride + head_off) +
+                                  (((t0 + row) & ps_mask) * D + 8 * piece);
+            pt_copy16(src, __builtin_amdgcn_readfirstlane(dst + 4096 * x));
+        }
+        const int pg = __shfl(page, vpiece >> 1);
+        const uint16_t *vsrc = c.v + ((int64_t)pg * c.page_stride + head_off) + ((t0 + 8 * vpiece) & ps_mask);
+#pragma unroll
+        for (int x = 0; x < PASS; ++x) {
+            const int chan = 32 * x + (tid >> 3);
+            pt_copy16(vsrc + (chan << c.ps_log2), __builtin_amdgcn_readfirstlane(dst + HALF + 4096 * x));
+        }
+        return bad;
+    };
+
+    // operand reads: K row of score row col, pieces 2 k + hf; V channel col of 32, pieces 2 k + hf
+    const int krow = 16 * (col >> 4) + 8 * ((col >> 2) & 1) + 4 * ((col >> 3) & 1) + (col & 3);
+    uint32_t koff[4], voff[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        koff[j] = (uint32_t)(krow * D * 2) + (uint32_t)(((2 * j + hf) ^ key(krow)) << 4);
+        voff[j] = (uint32_t)(col * 128) + (uint32_t)(((2 * j + hf) ^ (col & 7)) << 4);
+    }
+
+    af16 o[DT];
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            o[d][r] = 0.f;
+    float m = -INFINITY, l = 0.f;
+
+    auto compute = [&](int s, int buf, uint32_t bad) {
+        const int t0 = s * PT_STEP;
+        if (t0 > wave_max)
+            return;                                    // nothing of this step is seen by the wave
+        const uint8_t *kb_ = lds + buf * 2 * HALF, *vb_ = kb_ + HALF;
+        af16 sc[2];
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                sc[tt][r] = 0.f;
+#pragma unroll
+        for (int k = 0; k < KB; ++k)
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt) {
+                const au4 kf = *reinterpret_cast<const au4 *>(kb_ + koff[k & 3] + (k >> 2) * 128 + tt * 64 * D);
+#pragma unroll
+                for (int y = NP - 1; y >= 0; --y)
+                    sc[tt] = mm32<T>(kf, qf[y][k], sc[tt]);
+            }
+        const bool masked = bad != 0 || t0 + PT_STEP - 1 > wave_min;
+        // value r of tile tt is position t0 + 32 tt + 16 (r / 8) + 8 hf + r % 8
+        if (masked) {
+            const int see = min(pos, p.hi - 1) - t0 - 8 * hf;
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int at = 32 * tt + 16 * (r >> 3) + (r & 7);
+                    sc[tt][r] = at > see || (bad >> (2 * tt + (r >> 3)) & 1) ? -INFINITY : sc[tt][r] * unscale;
+                }
+        } else {
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    sc[tt][r] *= unscale;
+        }
+        float mx = sc[0][0];
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                mx = fmaxf(mx, sc[tt][r]);
+        if (__any(mx > m + 9.0f)) {
+            const float mn = fmaxf(m, max_x32(mx));
+            const float f = m == mn ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+            m = mn;
+            l *= f;
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    o[d][r] *= f;
+        }
+        const float ref = m == -INFINITY ? 0.f : 6.0f - m;
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                sc[tt][r] = __builtin_amdgcn_exp2f(sc[tt][r] + ref);
+                l += sc[tt][r];
+            }
+        bool odd = false;
+        if (masked) {
+            // a position hidden from some rows may hold an infinity or NaN, and 0 x NaN is NaN
+            uint32_t nf = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int d = 0; d < DT; ++d) {
+                    const au4 v = *reinterpret_cast<const au4 *>(vb_ + voff[k] + d * 4096);
+#pragma unroll
+                    for (int w = 0; w < 4; ++w)
+                        nf |= nonfinite2<T>(v[w]);
+                }
+            odd = __any(nf != 0);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float pr[8];
+            au4 pf[NP];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                pr[e] = sc[k >> 1][8 * (k & 1) + e];
+            split8<T>(pr, pf);
+            if (!odd) {
+#pragma unroll
+                for (int d = 0; d < DT; ++d) {
+                    const au4 v = *reinterpret_cast<const au4 *>(vb_ + voff[k] + d * 4096);
+#pragma unroll
+                    for (int y = NP - 1; y >= 0; --y)
+                        o[d] = mm32<T>(v, pf[y], o[d]);
+                }
+            } else {
+                // such values leave the product and come back as the count of a row's visible ones:
+                // any +inf (or NaN) adds +inf, any -inf (or NaN) adds -inf
+#pragma unroll 1
+                for (int d = 0; d < DT; ++d) {
+                    au4 v = *reinterpret_cast<const au4 *>(vb_ + voff[k] + d * 4096), up, dn;
+                    const uint32_t one = T == KV_F16 ? 0x3C00u : 0x3F80u, inf = T == KV_F16 ? 0x7C00u : 0x7F80u;
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        uint32_t u = 0, n = 0, keep = 0;
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t x = (v[w] >> (16 * e)) & 0xFFFFu, ab = x & 0x7FFFu;
+                            const bool nan = ab > inf;
+                            u |= (nan || x == inf ? one : 0u) << (16 * e);
+                            n |= (nan || x == (inf | 0x8000u) ? one : 0u) << (16 * e);
+                            keep |= (ab < inf ? 0xFFFFu : 0u) << (16 * e);
+                        }
+                        up[w] = u;
+                        dn[w] = n;
+                        v[w] &= keep;
+                    }
+                    af16 cu, cd, acc;
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        cu[r] = cd[r] = acc[r] = 0.f;
+                    cu = mm32<T>(up, pf[0], cu);
+                    cd = mm32<T>(dn, pf[0], cd);
+#pragma unroll
+                    for (int y = NP - 1; y >= 0; --y)
+                        acc = mm32<T>(v, pf[y], acc);
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        acc[r] += (cu[r] > 0.f ? INFINITY : 0.f) + (cd[r] > 0.f ? -INFINITY : 0.f);
+#pragma unroll
+                    for (int dd = 0; dd < DT; ++dd)
+                        if (dd == d)
+                            o[dd] += acc;
+                }
+            }
+        }
+    };
+
+    const int s0 = p.chunk0, s1 = p.chunk1;
+    if (s1 > s0) {
+        uint32_t bad_next = issue(s0, 0, ids_of(s0)), seen_bad = 0;
+        int ids = ids_of(s0 + 1);
+        for (int s = s0; s < s1; ++s) {
+            const int buf = (s - s0) & 1;
+            const uint32_t bad = bad_next;
+            seen_bad |= bad;
+            // this thread's copies of step s have landed; after the barrier everyone's have, and
+            // everyone is done with step s - 1, whose buffer the next copies overwrite
+            pt_wait_all();
+            pt_barrier();
+            if (s + 1 < s1) {
+                bad_next = issue(s + 1, buf ^ 1, ids);
+                ids = ids_of(s + 2);
+            }
+            compute(s, buf, bad);
+        }
+        if (seen_bad && tid == 0)
+            atomicOr(c.err, 1u);
+    }
+
+    // O^T: lane's row, channels 32 d + 8 (r / 4) + 4 hf + r % 4
+    l = sum_x32(l);
+    if (splits > 1) {
+        float *part = a.part + ((int64_t)(id * c.nkv + hkv) * n_split + blockIdx.y) * prompt_part_floats(D);
+        float *row = part + (32 * wave + col) * D + 4 * hf;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                *reinterpret_cast<af4 *>(row + 32 * d + 8 * r) =
+                    af4{o[d][4 * r], o[d][4 * r + 1], o[d][4 * r + 2], o[d][4 * r + 3]};
+        if (hf == 0) {
+            float *ml = part + PT_ROWS * D + 2 * (32 * wave + col);
+            ml[0] = m;
+            ml[1] = l;
+        }
+    } else if (live) {
+        const float inv = m == -INFINITY ? 0.f : 1.0f / l;
+        float *row = a.o + ((int64_t)(p.row0 + tok) * a.nq + head) * D + 4 * hf;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                *reinterpret_cast<af4 *>(row + 32 * d + 8 * r) =
+                    af4{o[d][4 * r] * inv, o[d][4 * r + 1] * inv, o[d][4 * r + 2] * inv, o[d][4 * r + 3] * inv};
+    }
+}
+
+// Rows of a split tile from its partial results, in order.  A workgroup takes one tile's rows
+// blockIdx.y * 8 .. + 7 of one KV head, a thread four channels.
+__global__ __launch_bounds__(256) void k_attn_prompt_join(AttnArgs a, int n_split)
 {
     const KvArgs &c = a.c;
-    __shared__ float sq[256], sp[256], red[4];
-    __shared__ int64_t soff[256];
-    const int64_t r = blockIdx.x;
-    const int h = blockIdx.y, tid = threadIdx.x, hkv = h / a.group;
-    int64_t start, end;
-    const int b = seq_of_row(c, r, start, end);
-    if (b < 0)
+    const int D = c.hd, lanes = D / 4, tid = threadIdx.x;
+    const int hkv = blockIdx.x % c.nkv, id = blockIdx.x / c.nkv;
+    TilePlace p;
+    int splits;
+    if (!tile_place(c, a.group, id, 0, n_split, p, splits) || splits <= 1)
         return;
-    const int64_t last = c.kv_len[b] - (end - r);       // the row's position
-    for (int d = tid; d < c.hd; d += 256)
-        sq[d] = a.q[r * a.q_stride + (int64_t)h * c.hd + d] * a.scale;
-    float m = -INFINITY, l = 0.f, o = 0.f;
-    __syncthreads();
-    for (int64_t t0 = 0; t0 <= last && (t0 >> c.ps_log2) < c.max_pages; t0 += 256) {
-        const int64_t t = t0 + tid;
-        float s = -INFINITY;
-        int64_t off = -1;
-        if (t <= last)
-            off = page_at(c, b, t);
-        if (off >= 0) {
-            off += ((int64_t)hkv * c.hd << c.ps_log2);
-            const int slot = (int)(t & ((1 << c.ps_log2) - 1));
-            s = 0.f;
-            for (int d = 0; d < c.hd; ++d)
-                s = fmaf(sq[d], kv_float<T>(c.k[off + (int64_t)slot * c.hd + d]), s);
-            off += slot;
+    const float *part = a.part + (int64_t)(id * c.nkv + hkv) * n_split * prompt_part_floats(D);
+    for (int x = tid; x < 8 * lanes; x += 256) {
+        const int r = 8 * blockIdx.y + x / lanes, d4 = x % lanes;
+        const int rho = p.rho0 + r, tok = rho / a.group;
+        if (tok >= p.rows)
+            continue;
+        const float *ml = part + PT_ROWS * D + 2 * r;
+        float m = -INFINITY;
+        for (int k = 0; k < splits; ++k)
+            m = fmaxf(m, ml[k * prompt_part_floats(D)]);
+        float l = 0.f;
+        af4 sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (int k = 0; k < splits; ++k) {
+            const float mk = ml[k * prompt_part_floats(D)], lk = ml[k * prompt_part_floats(D) + 1];
+            const float f = mk == m ? 1.0f : __builtin_amdgcn_exp2f(mk - m);
+            const af4 v = *reinterpret_cast<const af4 *>(part + k * prompt_part_floats(D) + r * D + 4 * d4);
+            if (mk != -INFINITY) {
+                sum += v * f;
+                l += lk * f;
+            }
         }
-        float mx = s;
-        for (int x = 32; x; x >>= 1)
-            mx = fmaxf(mx, __shfl_xor(mx, x));
-        if ((tid & 63) == 0)
-            red[tid >> 6] = mx;
-        __syncthreads();
-        mx = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-        const float mn = fmaxf(m, mx);
-        const float p = off >= 0 ? expf(s - mn) : 0.f;
-        const float f = m == -INFINITY ? 0.f : expf(m - mn);
-        sp[tid] = p;
-        soff[tid] = off;
-        __syncthreads();
-        o *= f;
-        l *= f;
-        m = mn;
-        for (int j = 0; j < 256; ++j) {
-            l += sp[j];
-            if (soff[j] >= 0 && tid < c.hd)
-                o = fmaf(sp[j], kv_float<T>(c.v[soff[j] + ((int64_t)tid << c.ps_log2)]), o);
-        }
-        __syncthreads();
+        *reinterpret_cast<af4 *>(a.o + ((int64_t)(p.row0 + tok) * a.nq + hkv * a.group + rho % a.group) * D +
+                                 4 * d4) = sum * (m == -INFINITY ? 0.f : 1.0f / l);
     }
-    if (tid < c.hd)
-        a.o[r * a.nq * c.hd + (int64_t)h * c.hd + tid] = m == -INFINITY ? 0.f : o / l;
 }
 
-static int launch_plain(int kv_type, const AttnArgs &a, void *stream)
+// Tile ids of a call (at least its tiles), and splits over the cache's length: with fewer than one
+// workgroup per compute unit the tiles are split until two are.
+PromptPlan plan_prompt(int64_t n_rows, int n_seq, int nkv, int group)
+{
+    PromptPlan p;
+    p.tiles = n_rows * group / PT_ROWS + n_seq;
+    p.n_split = p.tiles * nkv >= PROMPT_SLOTS / 2 ? 1 : (int)(PROMPT_SLOTS / (p.tiles * nkv));
+    return p;
+}
+
+int launch_attn_prompt(int kv_type, const AttnArgs &a, void *stream)
 {
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const dim3 grid((unsigned)a.c.n_rows, (unsigned)a.nq);
-    if (kv_type == KV_F16)
-        hipLaunchKernelGGL(k_attn_plain<KV_F16>, grid, dim3(256), 0, s, a);
-    else
-        hipLaunchKernelGGL(k_attn_plain<KV_BF16>, grid, dim3(256), 0, s, a);
+    const PromptPlan p = plan_prompt(a.c.n_rows, a.c.n_seq, a.c.nkv, a.group);
+    void (*k)(AttnArgs, int) = nullptr;
+#define QG_PROMPT_D(DD) k = kv_type == KV_F16 ? k_attn_prompt<KV_F16, DD> : k_attn_prompt<KV_BF16, DD>
+    switch (a.c.hd) {
+    case 64: QG_PROMPT_D(64); break;
+    case 96: QG_PROMPT_D(96); break;
+    case 128: QG_PROMPT_D(128); break;
+    case 192: QG_PROMPT_D(192); break;
+    default: QG_PROMPT_D(256); break;
+    }
+#undef QG_PROMPT_D
+    const unsigned grid = (unsigned)(p.tiles * a.c.nkv);
+    hipLaunchKernelGGL(k, dim3(grid, p.n_split), dim3(256), 0, s, a, p.n_split);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || p.n_split == 1)
+        return (int)e;
+    hipLaunchKernelGGL(k_attn_prompt_join, dim3(grid, PT_ROWS / 8), dim3(256), 0, s, a, p.n_split);
     return (int)hipGetLastError();
 }
-
-int launch_attn_prompt(int kv_type, const AttnArgs &a, void *stream) { return launch_plain(kv_type, a, stream); }
 
 }  // namespace qg
