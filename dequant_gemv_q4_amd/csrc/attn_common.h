@@ -64,8 +64,8 @@ __device__ __forceinline__ void split8(const float (&v)[8], au4 (&out)[PIECES<T>
             const uint32_t p = pack2<T>(r[2 * e], r[2 * e + 1]);
             out[i][e] = p;
             if (i + 1 < PIECES<T>) {
-                r[2 * e] -= low_of<T>(p);
-                r[2 * e + 1] -= high_of<T>(p);
+                r[2 * e] = fmaf(low_of<T>(p), -1.0f, r[2 * e]);     // f16: one instruction
+                r[2 * e + 1] = fmaf(high_of<T>(p), -1.0f, r[2 * e + 1]);
             }
         }
 }

@@ -11,8 +11,10 @@
 // 4 (i / 8 % 2) + i % 4, which makes a lane's eight values consecutive positions).
 //
 // K and V go from the pages to LDS without registers (global_load_lds, 16 bytes a lane), one step
-// ahead, two buffers, one barrier a step.  The copies land in lane order, so the 16-byte pieces of a
-// row are permuted at the source instead (piece ^ key of the row): eight lanes that read eight rows
+// ahead, two buffers, one barrier a step.  Wave w copies the step's 16-position block w, which lies
+// in one page, so page numbers and bases are scalars.  K: [position][channel], V: [block][channel]
+// [16 positions].  The copies land in lane order, so the 16-byte pieces of a K row (of a V channel's
+// two) are permuted at the source instead, piece ^ key of the row: eight lanes that read eight rows
 // then use different banks.
 #include <hip/hip_runtime.h>
 
@@ -23,11 +25,12 @@ namespace qg {
 constexpr int PT_ROWS = 128;      // rows of a tile
 constexpr int PT_STEP = 64;       // positions of a step
 
-// Global -> LDS copy of 16 bytes per lane to lds_dst + 16 lane.  Written as asm so that the compiler
-// does not wait for it at the next LDS read: the kernel waits with vmcnt itself, once a step.
-__device__ __forceinline__ void pt_copy16(const void *src, uint32_t lds_dst)
+// Global -> LDS copy of 16 bytes per lane, from base + off, to lds_dst + 16 lane.  Written as asm so
+// that the compiler does not wait for it at the next LDS read: the kernel waits with vmcnt itself,
+// once a step.
+__device__ __forceinline__ void pt_copy16(const uint16_t *base, uint32_t off, uint32_t lds_dst)
 {
-    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(src), "{m0}"(lds_dst) : "memory");
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(off), "s"(base), "{m0}"(lds_dst) : "memory");
 }
 __device__ __forceinline__ void pt_wait_all()
 {
@@ -113,8 +116,9 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
     constexpr int PR = D / 8;                          // 16-byte pieces of a K row
     constexpr int KEYM = D % 64 == 0 ? 7 : 3;          // bits of the piece number that the key takes
     constexpr int HALF = PT_STEP * D * 2;              // bytes of a K (or V) buffer
-    constexpr int PASS = HALF / 4096;                  // copies of a thread for either
+    constexpr int PASS = HALF / 4096;                  // copies of a wave for either
     __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * HALF];   // K0 V0 K1 V1
+    __shared__ int s_odd[4];
     const KvArgs &c = a.c;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 31, hf = lane >> 5;
@@ -153,8 +157,8 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
                 amax = fmaxf(amax, fabsf(v[k][e]));
             }
         }
-        const float sc = q_scale<T>(max_x32(amax));
-        unscale = a.scale * LOG2E / sc;
+        const float sc0 = q_scale<T>(max_x32(amax)), sc = a.scale < 0.f ? -sc0 : sc0;
+        unscale = a.scale * LOG2E / sc;                // not negative: the largest score stays it
 #pragma unroll
         for (int k = 0; k < KB; ++k) {
             float w[8];
@@ -169,49 +173,47 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
         }
     }
 
-    // copies: LDS piece idx = 256 pass + tid of a buffer.  K: row idx / PR, source piece
-    // (idx % PR) ^ key(row); V: channel idx / 8, source piece (idx % 8) ^ (channel % 8)
+    // copies: wave w's 16-position block w.  K: piece idx = 64 x + lane of the block, row idx / PR,
+    // source piece (idx % PR) ^ key(row); V: channel 32 x + lane / 2, source piece lane % 2 ^ its key
     const int32_t *table = c.table + (int64_t)p.b * c.max_pages;
     const int ps_mask = (1 << c.ps_log2) - 1;
     const int last_entry = p.hi > 0 ? (p.hi - 1) >> c.ps_log2 : 0;
     const int64_t head_off = (int64_t)hkv * D << c.ps_log2;
-    const uint32_t lds0 = (uint32_t)(uintptr_t)lds + (uint32_t)wave * 1024u;
-    const int vpiece = (tid & 7) ^ ((tid >> 3) & 7);
+    const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
+    auto key = [](int row) { return ((row & 3) | ((row >> 1) & 4)) & KEYM; };
+    uint32_t ksrc[PASS];
+#pragma unroll
+    for (int x = 0; x < PASS; ++x) {
+        const int idx = 64 * x + lane, row = idx / PR;
+        ksrc[x] = (uint32_t)(row * D + 8 * ((idx % PR) ^ key(row))) * 2;
+    }
+    const uint32_t vsrc = (uint32_t)(((lane >> 1) << c.ps_log2) + 8 * ((lane & 1) ^ ((lane >> 3) & 1))) * 2;
     // page number of 16-position block lane % 4 of a step
     auto ids_of = [&](int s) { return table[min((s * PT_STEP + 16 * (lane & 3)) >> c.ps_log2, last_entry)]; };
-    auto key = [](int row) { return ((row & 3) | ((row >> 1) & 4)) & KEYM; };
     auto issue = [&](int s, int buf, int ids) -> uint32_t {
         const bool ok = ids >= 0 && ids < c.n_pages;
         const uint32_t bad = (uint32_t)__ballot(!ok) & 15u;
-        const int page = ok ? ids : 0;
-        const int t0 = s * PT_STEP;
-        const uint32_t dst = lds0 + (uint32_t)buf * 2 * HALF;
+        const int page = __builtin_amdgcn_readlane(ok ? ids : 0, wave);
+        const int slot = (s * PT_STEP + 16 * wave) & ps_mask;
+        const int64_t at = (int64_t)page * c.page_stride + head_off;
+        const uint16_t *kp = c.k + at + slot * D, *vp = c.v + at + slot;
+        const uint32_t dst = lds0 + (uint32_t)(buf * 2 * HALF + wave * (HALF / 4));
 #pragma unroll
-        for (int x = 0; x < PASS; ++x) {
-            const int idx = 256 * x + tid, row = idx / PR, piece = (idx % PR) ^ key(row);
-            const int pg = __shfl(page, row >> 4);
-            const uint16_t *src = c.k + ((int64_t)pg * c.page_stride + head_off) +
-                                  (((t0 + row) & ps_mask) * D + 8 * piece);
-            pt_copy16(src, __builtin_amdgcn_readfirstlane(dst + 4096 * x));
-        }
-        const int pg = __shfl(page, vpiece >> 1);
-        const uint16_t *vsrc = c.v + ((int64_t)pg * c.page_stride + head_off) + ((t0 + 8 * vpiece) & ps_mask);
+        for (int x = 0; x < PASS; ++x)
+            pt_copy16(kp, ksrc[x], __builtin_amdgcn_readfirstlane(dst + 1024 * x));
 #pragma unroll
-        for (int x = 0; x < PASS; ++x) {
-            const int chan = 32 * x + (tid >> 3);
-            pt_copy16(vsrc + (chan << c.ps_log2), __builtin_amdgcn_readfirstlane(dst + HALF + 4096 * x));
-        }
+        for (int x = 0; x < PASS; ++x)
+            pt_copy16(vp + ((32 * x) << c.ps_log2), vsrc, __builtin_amdgcn_readfirstlane(dst + HALF + 1024 * x));
         return bad;
     };
 
-    // operand reads: K row of score row col, pieces 2 k + hf; V channel col of 32, pieces 2 k + hf
+    // operand reads: K row of score row col, pieces 2 k + hf; V channel col of 32, piece hf of block k
     const int krow = 16 * (col >> 4) + 8 * ((col >> 2) & 1) + 4 * ((col >> 3) & 1) + (col & 3);
-    uint32_t koff[4], voff[4];
+    uint32_t koff[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 4; ++j)
         koff[j] = (uint32_t)(krow * D * 2) + (uint32_t)(((2 * j + hf) ^ key(krow)) << 4);
-        voff[j] = (uint32_t)(col * 128) + (uint32_t)(((2 * j + hf) ^ (col & 7)) << 4);
-    }
+    const uint32_t voff = (uint32_t)(col * 32 + ((hf ^ ((col >> 2) & 1)) << 4));
 
     af16 o[DT];
 #pragma unroll
@@ -221,50 +223,43 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
             o[d][r] = 0.f;
     float m = -INFINITY, l = 0.f;
 
-    auto compute = [&](int s, int buf, uint32_t bad) {
-        const int t0 = s * PT_STEP;
-        if (t0 > wave_max)
-            return;                                    // nothing of this step is seen by the wave
-        const uint8_t *kb_ = lds + buf * 2 * HALF, *vb_ = kb_ + HALF;
-        af16 sc[2];
+    // raw (unscaled) scores of step s
+    auto scores = [&](int buf, af16 (&sc)[2]) {
+        const uint8_t *kb = lds + buf * 2 * HALF;
 #pragma unroll
         for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
             for (int r = 0; r < 16; ++r)
                 sc[tt][r] = 0.f;
-#pragma unroll
-        for (int k = 0; k < KB; ++k)
-#pragma unroll
-            for (int tt = 0; tt < 2; ++tt) {
-                const au4 kf = *reinterpret_cast<const au4 *>(kb_ + koff[k & 3] + (k >> 2) * 128 + tt * 64 * D);
-#pragma unroll
-                for (int y = NP - 1; y >= 0; --y)
-                    sc[tt] = mm32<T>(kf, qf[y][k], sc[tt]);
-            }
-        const bool masked = bad != 0 || t0 + PT_STEP - 1 > wave_min;
-        // value r of tile tt is position t0 + 32 tt + 16 (r / 8) + 8 hf + r % 8
-        if (masked) {
-            const int see = min(pos, p.hi - 1) - t0 - 8 * hf;
+        // operands are read two channel blocks ahead of their products (the fences keep the compiler
+        // from reading all of them first, for which there are no registers)
+        au4 kf[3][2];
+        auto read = [&](int k) {
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt)
+                kf[k % 3][tt] = *reinterpret_cast<const au4 *>(kb + koff[k & 3] + (k >> 2) * 128 + tt * 64 * D);
+        };
+        read(0);
+        read(1);
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int at = 32 * tt + 16 * (r >> 3) + (r & 7);
-                    sc[tt][r] = at > see || (bad >> (2 * tt + (r >> 3)) & 1) ? -INFINITY : sc[tt][r] * unscale;
-                }
-        } else {
+        for (int k = 0; k < KB; ++k) {
+            if (k + 2 < KB)
+                read(k + 2);
 #pragma unroll
-            for (int tt = 0; tt < 2; ++tt)
+            for (int y = NP - 1; y >= 0; --y)
 #pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    sc[tt][r] *= unscale;
+                for (int tt = 0; tt < 2; ++tt)
+                    sc[tt] = mm32<T>(kf[k % 3][tt], qf[y][k], sc[tt]);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        float mx = sc[0][0];
+    };
+    // scores -> probabilities (times 2^6 over the reference), maximum and sum kept up
+    auto softmax = [&](af16 (&sc)[2]) {
+        float mx = fmaxf(sc[0][0], sc[1][0]);
 #pragma unroll
-        for (int tt = 0; tt < 2; ++tt)
-#pragma unroll
-            for (int r = 0; r < 16; ++r)
-                mx = fmaxf(mx, sc[tt][r]);
+        for (int r = 1; r < 16; ++r)
+            mx = fmaxf(fmaxf(mx, sc[0][r]), sc[1][r]);
+        mx *= unscale;
         if (__any(mx > m + 9.0f)) {
             const float mn = fmaxf(m, max_x32(mx));
             const float f = m == mn ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
@@ -277,85 +272,122 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
                     o[d][r] *= f;
         }
         const float ref = m == -INFINITY ? 0.f : 6.0f - m;
+        float la = 0.f, lb = 0.f;
 #pragma unroll
-        for (int tt = 0; tt < 2; ++tt)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                sc[tt][r] = __builtin_amdgcn_exp2f(sc[tt][r] + ref);
-                l += sc[tt][r];
-            }
-        bool odd = false;
-        if (masked) {
-            // a position hidden from some rows may hold an infinity or NaN, and 0 x NaN is NaN
-            uint32_t nf = 0;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-                for (int d = 0; d < DT; ++d) {
-                    const au4 v = *reinterpret_cast<const au4 *>(vb_ + voff[k] + d * 4096);
-#pragma unroll
-                    for (int w = 0; w < 4; ++w)
-                        nf |= nonfinite2<T>(v[w]);
-                }
-            odd = __any(nf != 0);
+        for (int r = 0; r < 16; ++r) {
+            sc[0][r] = __builtin_amdgcn_exp2f(fmaf(sc[0][r], unscale, ref));
+            sc[1][r] = __builtin_amdgcn_exp2f(fmaf(sc[1][r], unscale, ref));
+            la += sc[0][r];
+            lb += sc[1][r];
         }
+        l += la + lb;
+    };
+    // probability operand of 16-position block k
+    auto weights = [&](const af16 (&sc)[2], int k, au4 (&pf)[NP]) {
+        float pr[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            float pr[8];
-            au4 pf[NP];
+        for (int e = 0; e < 8; ++e)
+            pr[e] = sc[k >> 1][8 * (k & 1) + e];
+        split8<T>(pr, pf);
+    };
+    // O += V^T P
+    auto values = [&](const af16 (&sc)[2], int buf) {
+        const uint8_t *vb = lds + buf * 2 * HALF + HALF;
+        auto read = [&](int x) {                        // operand x = DT k + d
+            return *reinterpret_cast<const au4 *>(vb + voff + (x / DT) * (D * 32) + (x % DT) * 1024);
+        };
+        constexpr int AHEAD = 3;
+        au4 v[AHEAD + 1], pf[NP];
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                pr[e] = sc[k >> 1][8 * (k & 1) + e];
-            split8<T>(pr, pf);
-            if (!odd) {
+        for (int x = 0; x < AHEAD; ++x)
+            v[x] = read(x);
 #pragma unroll
-                for (int d = 0; d < DT; ++d) {
-                    const au4 v = *reinterpret_cast<const au4 *>(vb_ + voff[k] + d * 4096);
+        for (int x = 0; x < 4 * DT; ++x) {
+            if (x + AHEAD < 4 * DT)
+                v[(x + AHEAD) % (AHEAD + 1)] = read(x + AHEAD);
+            if (x % DT == 0)
+                weights(sc, x / DT, pf);
 #pragma unroll
-                    for (int y = NP - 1; y >= 0; --y)
-                        o[d] = mm32<T>(v, pf[y], o[d]);
-                }
-            } else {
-                // such values leave the product and come back as the count of a row's visible ones:
-                // any +inf (or NaN) adds +inf, any -inf (or NaN) adds -inf
+            for (int y = NP - 1; y >= 0; --y)
+                o[x % DT] = mm32<T>(v[x % (AHEAD + 1)], pf[y], o[x % DT]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    // Edge steps hold positions that some rows of the tile do not see.  An infinity or NaN in V there
+    // must reach the rows that see it and no other, but 0 x NaN is NaN: such values are added to
+    // their rows one by one and then cleared in LDS.
+    auto scan = [&](int buf) {
+        uint32_t nf = 0;
 #pragma unroll 1
-                for (int d = 0; d < DT; ++d) {
-                    au4 v = *reinterpret_cast<const au4 *>(vb_ + voff[k] + d * 4096), up, dn;
-                    const uint32_t one = T == KV_F16 ? 0x3C00u : 0x3F80u, inf = T == KV_F16 ? 0x7C00u : 0x7F80u;
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        uint32_t u = 0, n = 0, keep = 0;
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const uint32_t x = (v[w] >> (16 * e)) & 0xFFFFu, ab = x & 0x7FFFu;
-                            const bool nan = ab > inf;
-                            u |= (nan || x == inf ? one : 0u) << (16 * e);
-                            n |= (nan || x == (inf | 0x8000u) ? one : 0u) << (16 * e);
-                            keep |= (ab < inf ? 0xFFFFu : 0u) << (16 * e);
-                        }
-                        up[w] = u;
-                        dn[w] = n;
-                        v[w] &= keep;
-                    }
-                    af16 cu, cd, acc;
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        cu[r] = cd[r] = acc[r] = 0.f;
-                    cu = mm32<T>(up, pf[0], cu);
-                    cd = mm32<T>(dn, pf[0], cd);
-#pragma unroll
-                    for (int y = NP - 1; y >= 0; --y)
-                        acc = mm32<T>(v, pf[y], acc);
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        acc[r] += (cu[r] > 0.f ? INFINITY : 0.f) + (cd[r] > 0.f ? -INFINITY : 0.f);
-#pragma unroll
-                    for (int dd = 0; dd < DT; ++dd)
-                        if (dd == d)
-                            o[dd] += acc;
-                }
-            }
+        for (int x = tid; x < HALF / 16; x += 256) {
+            const au4 v = *reinterpret_cast<const au4 *>(lds + buf * 2 * HALF + HALF + 16 * x);
+            nf |= nonfinite2<T>(v[0]) | nonfinite2<T>(v[1]) | nonfinite2<T>(v[2]) | nonfinite2<T>(v[3]);
         }
+        s_odd[wave] = __any(nf != 0);
+        __syncthreads();
+        return (s_odd[0] | s_odd[1] | s_odd[2] | s_odd[3]) != 0;
+    };
+    auto clear = [&](int buf) {
+#pragma unroll 1
+        for (int x = tid; x < HALF / 16; x += 256) {
+            au4 *v = reinterpret_cast<au4 *>(lds + buf * 2 * HALF + HALF + 16 * x);
+            au4 y = *v;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const uint32_t nf = nonfinite2<T>(y[w]);
+                y[w] &= ~((nf - (nf >> 15)) | nf);
+            }
+            *v = y;
+        }
+    };
+    auto add_nonfinite = [&](int see, uint32_t bad, int buf) {
+        const uint8_t *vb = lds + buf * 2 * HALF + HALF;
+#pragma unroll 1
+        for (int t = 0; t < PT_STEP; ++t) {
+            if (bad >> (t >> 4) & 1)
+                continue;
+            const uint32_t at = (t >> 4) * (D * 32) + 2 * (t & 7);
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int ch = 8 * (r >> 2) + 4 * hf + (r & 3);      // channel 32 d + ch
+                    const uint16_t x = *reinterpret_cast<const uint16_t *>(
+                        vb + at + d * 1024 + ch * 32 + ((((t >> 3) & 1) ^ ((ch >> 2) & 1)) << 4));
+                    if (t <= see && nonfinite2<T>(x))
+                        o[d][r] += low_of<T>(x);
+                }
+        }
+    };
+    const int tile_min = p.pos0 + p.rho0 / a.group;     // the tile's least position
+    auto compute = [&](int s, int buf, uint32_t bad) {
+        const int t0 = s * PT_STEP;
+        const bool edge = bad != 0 || t0 + PT_STEP - 1 > tile_min;
+        const bool odd = edge ? scan(buf) : false;
+        const bool active = t0 <= wave_max;            // else nothing of this step is seen by the wave
+        const int see = min(pos, p.hi - 1) - t0;
+        af16 sc[2];
+        if (active) {
+            scores(buf, sc);
+            // value r of tile tt is position t0 + 32 tt + 16 (r / 8) + 8 hf + r % 8
+            if (edge)
+#pragma unroll
+                for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (32 * tt + 16 * (r >> 3) + (r & 7) > see - 8 * hf || (bad >> (2 * tt + (r >> 3)) & 1))
+                            sc[tt][r] = -INFINITY;
+            softmax(sc);
+        }
+        if (odd) {
+            if (active)
+                add_nonfinite(see, bad, buf);
+            __syncthreads();
+            clear(buf);
+            __syncthreads();
+        }
+        if (active)
+            values(sc, buf);
     };
 
     const int s0 = p.chunk0, s1 = p.chunk1;
