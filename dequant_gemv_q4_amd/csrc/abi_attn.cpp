@@ -28,27 +28,20 @@ static bool heads_ok(int nq, int nkv, int hd)
     return nkv >= 1 && nq >= nkv && nq % nkv == 0 && head_dim_ok(hd) && nq <= 4096;
 }
 
-// Workspace: the sticky flag (256 bytes), then of the split over a cache's length the (first slot,
-// chunks) records and the partial results.
-struct WsLayout {
-    int64_t rec, part, total;
-};
+// Workspace: the sticky flag (256 bytes) and the arrival counters of qgemv_attn's split, at the same
+// place for every operation (the counters are 0 between calls and must stay so when operations share
+// a workspace), then the partial results of a split.
+static constexpr int64_t WS_COUNT = 256, WS_PART = WS_COUNT + ATTN_MAX_SLOTS * 4;
 
-static WsLayout ws_layout(int op, int nq, int nkv, int hd)
+static int64_t ws_bytes_of(int op, int nq, int nkv, int hd)
 {
-    WsLayout w = {256, 256, 256};
-    if (op == QG_OP_ATTN) {
-        const int group = nq / nkv;
-        w.part = w.rec + ATTN_SLOTS * 8;     // fewer (sequence, pair)s than slots, or no split
-        w.total = w.part + (int64_t)ATTN_SLOTS * (group < 16 ? group : 16) * (hd + 2) * 4;
-    } else if (op == QG_OP_ATTN_PROMPT) {
-        w.total = w.part + (int64_t)PROMPT_SLOTS * 128 * (hd + 2) * 4;   // 128 rows a tile
-    }
-    w.total = (w.total + 255) / 256 * 256;
-    return w;
+    const int group = nq / nkv;
+    if (op == QG_OP_ATTN)
+        return WS_PART + (attn_slots(hd) * attn_part_floats(group < 16 ? group : 16, hd) * 4 + 255) / 256 * 256;
+    if (op == QG_OP_ATTN_PROMPT)
+        return WS_PART + (int64_t)PROMPT_SLOTS * 128 * (hd + 2) * 4;   // 128 rows a tile
+    return WS_PART;
 }
-
-static int64_t ws_bytes_of(int op, int nq, int nkv, int hd) { return ws_layout(op, nq, nkv, hd).total; }
 
 struct Span {
     const void *p;
@@ -124,7 +117,7 @@ static int run_attn(bool prompt, int kv_type, const void *k_pages, const void *v
     if (q_stride < width || q_stride > ((int64_t)1 << 31) || n_rows * nq > (1 << 30) ||
         !isfinite(scale))
         return QG_ERR_SHAPE;
-    if (prompt && plan_prompt(n_rows, n_seq, nkv, nq / nkv).tiles * nkv > 0x7fffffffLL)
+    if (prompt && plan_prompt(n_rows, n_seq, nkv, nq / nkv, 0).tiles * nkv > 0x7fffffffLL)
         return QG_ERR_SHAPE;
     if (!al(q, 16) || !al(o, 16) || q_stride % 4)
         return QG_ERR_ALIGN;
@@ -144,9 +137,8 @@ static int run_attn(bool prompt, int kv_type, const void *k_pages, const void *v
         overlap(o, n_rows * width * 4, ws, (int64_t)ws_bytes))
         return QG_ERR_ALIAS;
     a.c.err = static_cast<unsigned int *>(ws);
-    const WsLayout w = ws_layout(prompt ? QG_OP_ATTN_PROMPT : QG_OP_ATTN, nq, nkv, hd);
-    a.rec = static_cast<uint8_t *>(ws) + w.rec;
-    a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + w.part);
+    a.count = reinterpret_cast<unsigned int *>(static_cast<uint8_t *>(ws) + WS_COUNT);
+    a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + WS_PART);
     a.q = q;
     a.q_stride = q_stride;
     a.o = o;

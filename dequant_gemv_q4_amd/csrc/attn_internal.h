@@ -8,8 +8,15 @@
 
 namespace qg {
 
-// Workgroup slots of the split over a cache's length (qgemv_attn): two per compute unit.
-#define ATTN_SLOTS 512
+// Workgroup slots of the split over a cache's length (qgemv_attn): as many workgroups as are resident
+// at once, two per compute unit up to head_dim 128 (8-wave registers), one above.  More, smaller
+// chunks cost more than they balance: 64 x 7500 positions x 2 heads of 128 98.0 us with 512 slots and
+// 102.9 with 768, 16 x 4000 x 4 heads of 256 53.6 with 256 and 62.2 with 512, 16 x 16000 x 8 heads of
+// 64 90.2 with 512 and 99.5 with 1024.
+#define ATTN_MAX_SLOTS 512
+__host__ __device__ constexpr int attn_slots(int hd) { return hd <= 128 ? 512 : 256; }
+// Floats of one slot's partial result: O of `cols` query heads, their maxima and sums.
+__host__ __device__ constexpr int64_t attn_part_floats(int cols, int hd) { return (int64_t)cols * (hd + 2); }
 // The same of qgemv_attn_prompt: tile splits, and with them partial results, of a call.
 #define PROMPT_SLOTS 512
 
@@ -42,7 +49,7 @@ struct AttnArgs {
     int64_t q_stride;
     float *o;                   // [n_rows][nq * hd]
     float *part;                // workspace: partial results of a split
-    void *rec;                  // workspace: (first slot, chunks) of each (sequence, pair)
+    unsigned int *count;        // workspace: arrival counters of a split, one per slot, 0 between calls
     int nq, group;              // query heads; query heads per KV head
     float scale;
 };
@@ -60,7 +67,7 @@ struct PromptPlan {
     int64_t tiles;              // tile ids per KV head
     int n_split;                // splits of a tile over the cache's length
 };
-PromptPlan plan_prompt(int64_t n_rows, int n_seq, int nkv, int group);
+PromptPlan plan_prompt(int64_t n_rows, int n_seq, int nkv, int group, int64_t positions);
 
 // Launchers: a hipError_t value (0 = success).
 int launch_kv_append(int kv_type, const AppendArgs &a, void *stream);

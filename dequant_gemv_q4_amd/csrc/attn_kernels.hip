@@ -100,65 +100,78 @@ __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a)
 //
 // Split over the length: the lengths are on the device, so every workgroup derives the same plan
 // from them: the smallest chunk (whole 128-position units) for which the chunks of all sequences
-// fit the ATTN_SLOTS workgroups of the grid; a sequence's chunks are equal to one unit.  One chunk:
-// the workgroup writes o; several: partial O, maximum and sum go to the workspace and k_attn_join
-// adds them in chunk order (no atomics: results do not depend on the order of execution).
+// fit the grid's workgroup slots; a sequence's chunks are equal to one unit.  One chunk: the
+// workgroup writes o.  Several: partial O, maximum and sum go to the workspace, and of every
+// JOIN_RADIX chunks the last to finish adds them up (then of as many such groups, until one is
+// left), always in chunk order, so that results do not depend on the order of execution.  A second
+// launch for the joining took 4.5 us on the device and 3 us on the host of calls of 7 to 100 us.
 
 constexpr int ATTN_UNIT_LOG2 = 7;
+constexpr int ATTN_SOLO = 4;         // units of a sequence that is not split
+constexpr int ATTN_LEAST = 2;        // units of a chunk, at least
+constexpr int JOIN_RADIX = 8;
 
 struct AttnPlan {
     int b, pair, chunk, n_chunk;   // this workgroup's sequence, (KV head, 16-head tile), chunk
-    int64_t len;                   // the sequence's positions
+    int slot0;                     // workgroup id of the pair's first chunk
+    int len;                       // the sequence's positions
 };
 
 // Positions of sequence b that have a place in its table.
-__device__ __forceinline__ int64_t seq_len(const KvArgs &c, int b)
+__device__ __forceinline__ int seq_len(const KvArgs &c, int b)
 {
-    const int64_t n = c.kv_len[b], cap = (int64_t)c.max_pages << c.ps_log2;
+    const int n = c.kv_len[b], cap = c.max_pages << c.ps_log2;          // cap <= 2^24
     if (n > cap)
         atomicOr(c.err, 1u);
     return n < 0 ? 0 : n < cap ? n : cap;
 }
 
-__device__ __forceinline__ int wave_sum(int v)
+// Inclusive sum over the lanes up to this one; lane 63 has the total.
+__device__ __forceinline__ int wave_scan(int v)
 {
-#pragma unroll
-    for (int x = 32; x; x >>= 1)
-        v += __shfl_xor(v, x);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);      // row_shr 1, 2, 4, 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);     // row 0 -> 1, 2 -> 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);     // rows 0, 1 -> 2, 3
     return v;
 }
+__device__ __forceinline__ int wave_sum(int v) { return __builtin_amdgcn_readlane(wave_scan(v), 63); }
+
+__device__ __forceinline__ int units_of(int n) { return (n + (1 << ATTN_UNIT_LOG2) - 1) >> ATTN_UNIT_LOG2; }
 
 // Chunks of a sequence of n positions when a chunk has u units (at least one, so that an empty
 // sequence's rows are written).
-__device__ __forceinline__ int chunks_of(int64_t n, int u)
+__device__ __forceinline__ int chunks_of(int n, int u)
 {
-    const int units = (int)((n + (1 << ATTN_UNIT_LOG2) - 1) >> ATTN_UNIT_LOG2);
-    return units <= u ? 1 : (units + u - 1) / u;
+    const int units = units_of(n);
+    return units <= u || units <= ATTN_SOLO ? 1 : (units + u - 1) / u;
 }
 
 // Workgroup id -> its place in the plan; false if the plan has fewer workgroups.  Runs in every
-// wave (no barrier); lane l looks at sequences l, l + 64, ...
-__device__ bool attn_plan(const KvArgs &c, int pairs, int id, AttnPlan &p)
+// wave (no barrier); lane l looks at sequences l, l + 64, ... (the first 64 held in a register).
+__device__ __forceinline__ bool attn_plan(const KvArgs &c, int pairs, int slots, int id, AttnPlan &p)
 {
     const int lane = threadIdx.x & 63;
+    const int n0 = lane < c.n_seq ? seq_len(c, lane) : 0;
+    auto sum = [&](auto of) {
+        int v = lane < c.n_seq ? of(n0) : 0;
+        for (int b = lane + 64; b < c.n_seq; b += 64)
+            v += of(seq_len(c, b));
+        return wave_sum(v);
+    };
     int u = 0x3fffffff;
-    if (c.n_seq * pairs < ATTN_SLOTS) {
-        // total chunks <= units / u + n_seq: u_hi is enough, u_lo is the least that could be
-        int units = 0;
-        for (int b = lane; b < c.n_seq; b += 64)
-            units += (int)((seq_len(c, b) + (1 << ATTN_UNIT_LOG2) - 1) >> ATTN_UNIT_LOG2);
-        units = wave_sum(units);
-        const int room = ATTN_SLOTS / pairs;              // workgroups per pair
-        int lo = (units + room - 1) / room;
-        lo = lo > 1 ? lo : 1;
-        int hi = (units + room - c.n_seq - 1) / (room - c.n_seq > 0 ? room - c.n_seq : 1);
-        hi = room > c.n_seq ? (hi > lo ? hi : lo) : 0x3fffffff;
+    if (c.n_seq * pairs < slots) {
+        // chunks <= units / u + n_seq, so u = units / (room - n_seq) is enough; units / room is the
+        // least that could be
+        const int units = sum([](int n) { return units_of(n); }), room = slots / pairs;
+        int lo = max((units + room - 1) / room, ATTN_LEAST), hi = 0x3fffffff;
+        if (room > c.n_seq)
+            hi = max((units + room - c.n_seq - 1) / (room - c.n_seq), lo);
         while (lo < hi) {
             const int mid = lo + (hi - lo) / 2;
-            int n = 0;
-            for (int b = lane; b < c.n_seq; b += 64)
-                n += chunks_of(seq_len(c, b), mid);
-            if (wave_sum(n) * pairs <= ATTN_SLOTS)
+            if (sum([=](int n) { return chunks_of(n, mid); }) <= room)
                 hi = mid;
             else
                 lo = mid + 1;
@@ -168,47 +181,88 @@ __device__ bool attn_plan(const KvArgs &c, int pairs, int id, AttnPlan &p)
     int base = 0;
     for (int b0 = 0; b0 < c.n_seq; b0 += 64) {
         const int b = b0 + lane;
-        const int64_t n = b < c.n_seq ? seq_len(c, b) : 0;
+        const int n = b0 == 0 ? n0 : b < c.n_seq ? seq_len(c, b) : 0;
         const int nc = b < c.n_seq ? chunks_of(n, u) : 0;
-        int end = nc * pairs;                             // inclusive scan over the lanes
-#pragma unroll
-        for (int x = 1; x < 64; x <<= 1) {
-            const int y = __shfl_up(end, x);
-            end += lane >= x ? y : 0;
-        }
-        end += base;
+        const int end = base + wave_scan(nc * pairs);
         const uint64_t in = __ballot(id < end && b < c.n_seq);
         if (in) {
             const int l = __ffsll((unsigned long long)in) - 1;
             p.b = b0 + l;
-            p.n_chunk = __shfl(nc, l);
-            p.len = __shfl((int)n, l);
-            const int rel = id - (__shfl(end, l) - p.n_chunk * pairs);
-            p.pair = rel / p.n_chunk;
-            p.chunk = rel % p.n_chunk;
+            p.n_chunk = __builtin_amdgcn_readlane(nc, l);
+            p.len = __builtin_amdgcn_readlane(n, l);
+            p.slot0 = __builtin_amdgcn_readlane(end, l) - p.n_chunk * pairs;
+            p.pair = (id - p.slot0) / p.n_chunk;
+            p.slot0 += p.pair * p.n_chunk;
+            p.chunk = id - p.slot0;
             return true;
         }
-        base = __shfl(end, 63);
+        base = __builtin_amdgcn_readlane(end, 63);
     }
     return false;
 }
 
-// Workspace of a split: per slot, the tile's O (unnormalised) [cols][hd], then (maximum, sum)
-// [cols]; then per (sequence, pair) its first slot and chunk count.
-__host__ __device__ constexpr int64_t attn_part_floats(int cols, int hd) { return (int64_t)cols * (hd + 2); }
+// Partial results of a slot: the tile's O (unnormalised) [cols][hd], then (maximum, sum) [cols].
+// They pass between workgroups of one launch, which may run on different XCDs: every access carries
+// the agent-scope bit (sc1), so that it neither stays in nor is answered by the L2 of one XCD.
+constexpr int AGENT_SCOPE = 16;                           // the buffer instructions' sc1
+typedef uint32_t au2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ void put4(__amdgpu_buffer_rsrc_t r, uint32_t at, af4 v)
+{
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(au4, v), r, 4 * at, 0, AGENT_SCOPE);
+}
+__device__ __forceinline__ af4 get4(__amdgpu_buffer_rsrc_t r, uint32_t at)
+{
+    return __builtin_bit_cast(af4, __builtin_amdgcn_raw_buffer_load_b128(r, 4 * at, 0, AGENT_SCOPE));
+}
+__device__ __forceinline__ void put2(__amdgpu_buffer_rsrc_t r, uint32_t at, float a, float b)
+{
+    const au2 v = {__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b)};
+    __builtin_amdgcn_raw_buffer_store_b64(v, r, 4 * at, 0, AGENT_SCOPE);
+}
+__device__ __forceinline__ void get2(__amdgpu_buffer_rsrc_t r, uint32_t at, float &a, float &b)
+{
+    const au2 v = __builtin_amdgcn_raw_buffer_load_b64(r, 4 * at, 0, AGENT_SCOPE);
+    const uint32_t v0 = v[0], v1 = v[1];
+    a = __builtin_bit_cast(float, v0);
+    b = __builtin_bit_cast(float, v1);
+}
+
+// Whether this workgroup is the last of `members` to arrive at a counter (left at 0 by the last).
+// Its partial results are complete in memory before it arrives: each wave waits for its own stores
+// (vmcnt counts an agent-scope store until it is done), then the workgroup meets.
+__device__ __forceinline__ bool last_to_arrive(unsigned int *cnt, int members, int *s_last)
+{
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        const unsigned int before =
+            __hip_atomic_fetch_add(cnt, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        *s_last = before + 1 == (unsigned int)members;
+        if (*s_last)
+            __hip_atomic_store(cnt, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __syncthreads();
+    asm volatile("" ::: "memory");
+    return *s_last != 0;
+}
 
 template <int T, int D>
 __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn(AttnArgs a)
 {
     constexpr int KB = D / 32, DT = D / 16, NP = PIECES<T>;
     __shared__ __attribute__((aligned(16))) float s_o[4][16][D];
-    __shared__ float s_m[4][16], s_l[4][16];
+    __shared__ float s_m[4][16], s_l[4][16], s_mo[16], s_lo[16];
+    __shared__ int s_last;
+    // queries of the wide heads: every wave multiplies by the same ones, and in registers they would
+    // leave none for the loads ahead
+    constexpr bool Q_LDS = D > 128;
+    __shared__ __attribute__((aligned(16))) au4 s_q[Q_LDS ? PIECES<T> * (D / 32) * 64 : 1];
     const KvArgs &c = a.c;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int i = lane & 15, g = lane >> 4;
     const int tiles = (a.group + 15) / 16, pairs = c.nkv * tiles;
     AttnPlan p;
-    if (!attn_plan(c, pairs, blockIdx.x, p))
+    if (!attn_plan(c, pairs, attn_slots(D), blockIdx.x, p))
         return;
     const int b = __builtin_amdgcn_readfirstlane(p.b), pair = __builtin_amdgcn_readfirstlane(p.pair);
     const int chunk = __builtin_amdgcn_readfirstlane(p.chunk);
@@ -226,7 +280,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn(AttnArgs a)
     const int n_steps = t_end > t_begin + 32 * wave ? (t_end - t_begin - 32 * wave + 127) / 128 : 0;
 
     // queries of column i: scaled, split
-    au4 qf[NP][KB];
+    au4 qf[Q_LDS ? 1 : NP][Q_LDS ? 1 : KB];
     float unscale;
     {
         const float *qr = a.q + (int64_t)b * a.q_stride + (int64_t)(h0 + (i < cols ? i : 0)) * D;
@@ -255,9 +309,14 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn(AttnArgs a)
             split8<T>(w, out);
 #pragma unroll
             for (int x = 0; x < NP; ++x)
-                qf[x][k] = out[x];
+                if constexpr (!Q_LDS)
+                    qf[x][k] = out[x];
+                else if (k % 4 == wave)
+                    s_q[(x * KB + k) * 64 + lane] = out[x];
         }
     }
+    if constexpr (Q_LDS)
+        __syncthreads();
 
     af4 o[DT];
 #pragma unroll
@@ -302,8 +361,16 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn(AttnArgs a)
             for (int d = 0; d < DT; ++d)
                 x.v[d] = *reinterpret_cast<const au4 *>(vp + ((16 * d) << c.ps_log2));
         };
+        auto q_at = [&](int y, int k) {
+            if constexpr (Q_LDS)
+                return s_q[(y * KB + k) * 64 + lane];
+            else
+                return qf[y][k];
+        };
         auto compute = [&](Buf &x, int s) {
             const int t = step_t(s);
+            if constexpr (Q_LDS)
+                asm volatile("" ::: "memory");            // the queries are read anew each step
             float sc[8];
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt) {
@@ -312,7 +379,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn(AttnArgs a)
                 for (int y = NP - 1; y >= 0; --y)
 #pragma unroll
                     for (int k = 0; k < KB; ++k)
-                        acc = mm16<T>(x.k[tt][k], qf[y][k], acc);
+                        acc = mm16<T>(x.k[tt][k], q_at(y, k), acc);
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
                     sc[4 * tt + r] = acc[r] * unscale;
@@ -386,18 +453,32 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn(AttnArgs a)
     for (int d = 0; d < DT; ++d)
         *reinterpret_cast<af4 *>(&s_o[wave][i][16 * d + 4 * g]) = o[d];
     __syncthreads();
-    float *part = nullptr;
-    if (n_chunk > 1) {
-        part = a.part + (int64_t)blockIdx.x * attn_part_floats(min(16, a.group), D);
-        if (chunk == 0 && threadIdx.x == 0) {             // k_attn_join's record of this pair
-            int *rec = reinterpret_cast<int *>(a.rec) + 2 * (b * pairs + pair);
-            rec[0] = blockIdx.x;
-            rec[1] = n_chunk;
+    const int width = min(16, a.group), items = cols * (D / 4);
+    const uint32_t stride = (uint32_t)attn_part_floats(width, D);
+    const __amdgpu_buffer_rsrc_t part = __builtin_amdgcn_make_buffer_rsrc(
+        a.part + (int64_t)p.slot0 * stride, 0, n_chunk * stride * 4, 0x00020000);
+    // four channels of a column: to o, or as the partial result of chunk `at`
+    auto finish = [&](int e, af4 sum, float mm, float ls, int at) {
+        const int col = e / (D / 4), d4 = e % (D / 4);
+        if (at < 0) {
+            const float inv = mm == -INFINITY ? 0.f : 1.0f / ls;
+            *reinterpret_cast<af4 *>(a.o + ((int64_t)b * a.nq + h0 + col) * D + 4 * d4) = sum * inv;
+            return;
         }
-    } else if (threadIdx.x == 0 && c.n_seq * pairs < ATTN_SLOTS) {
-        reinterpret_cast<int *>(a.rec)[2 * (b * pairs + pair) + 1] = 1;
-    }
-    for (int e = threadIdx.x; e < cols * (D / 4); e += 256) {
+        put4(part, at * stride + col * D + 4 * d4, sum);
+        if (d4 == 0) {
+            s_mo[col] = mm;
+            s_lo[col] = ls;
+        }
+    };
+    // the maxima and sums of a partial result, once nobody reads what they replace
+    auto finish_sums = [&](int at) {
+        __syncthreads();
+        if ((int)threadIdx.x < cols)
+            put2(part, at * stride + width * D + 2 * threadIdx.x, s_mo[threadIdx.x], s_lo[threadIdx.x]);
+    };
+
+    for (int e = threadIdx.x; e < items; e += 256) {
         const int col = e / (D / 4), d4 = e % (D / 4);
         const float mm = fmaxf(fmaxf(s_m[0][col], s_m[1][col]), fmaxf(s_m[2][col], s_m[3][col]));
         af4 sum = {0.f, 0.f, 0.f, 0.f};
@@ -411,84 +492,50 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn(AttnArgs a)
                 ls += s_l[w][col] * f;
             }
         }
-        if (n_chunk > 1) {
-            *reinterpret_cast<af4 *>(part + col * D + 4 * d4) = sum;
-            if (d4 == 0) {
-                float *ml = part + (int64_t)min(16, a.group) * D + 2 * col;
-                ml[0] = mm;
-                ml[1] = ls;
+        finish(e, sum, mm, ls, n_chunk > 1 ? chunk : -1);
+    }
+    if (n_chunk > 1)
+        finish_sums(chunk);
+    // nodes of 1, 8, 64, ... chunks; a node's result lies in the slot of its first chunk.  The group
+    // that starts at chunk g0 of level L arrives at the pair's counter g0 + L: all of a level's g0
+    // are multiples of JOIN_RADIX, so no two share one
+    for (int node = 1, level = 0; node < n_chunk; node *= JOIN_RADIX, ++level) {
+        const int g0 = chunk / (node * JOIN_RADIX) * (node * JOIN_RADIX);
+        const int members = min(JOIN_RADIX, (n_chunk - g0 + node - 1) / node);
+        if (members == 1)
+            continue;                                     // already in its place
+        if (!last_to_arrive(a.count + p.slot0 + g0 + level, members, &s_last))
+            return;
+        const bool top = node * JOIN_RADIX >= n_chunk;
+        for (int e = threadIdx.x; e < items; e += 256) {
+            const int col = e / (D / 4), d4 = e % (D / 4);
+            float mk[JOIN_RADIX], lk[JOIN_RADIX];
+            af4 x[JOIN_RADIX];
+#pragma unroll
+            for (int k = 0; k < JOIN_RADIX; ++k) {              // all loads in flight at once
+                mk[k] = -INFINITY;
+                if (k < members) {
+                    const uint32_t from = (uint32_t)(g0 + k * node) * stride;
+                    get2(part, from + width * D + 2 * col, mk[k], lk[k]);
+                    x[k] = get4(part, from + col * D + 4 * d4);
+                }
             }
-        } else {
-            const float inv = mm == -INFINITY ? 0.f : 1.0f / ls;
-            *reinterpret_cast<af4 *>(a.o + ((int64_t)b * a.nq + h0 + col) * D + 4 * d4) = sum * inv;
+            float mm = -INFINITY, ls = 0.f;
+#pragma unroll
+            for (int k = 0; k < JOIN_RADIX; ++k)
+                mm = fmaxf(mm, mk[k]);
+            af4 sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < JOIN_RADIX; ++k)
+                if (k < members && mk[k] != -INFINITY) {
+                    const float f = mk[k] == mm ? 1.0f : __builtin_amdgcn_exp2f(mk[k] - mm);
+                    sum += x[k] * f;
+                    ls += lk[k] * f;
+                }
+            finish(e, sum, mm, ls, top ? -1 : g0);
         }
-    }
-}
-
-// o of one (sequence, pair, column) from its chunks' partial results, in chunk order.
-__global__ __launch_bounds__(512) void k_attn_join(AttnArgs a)
-{
-    __shared__ float s_f[ATTN_SLOTS], s_red[8][2];
-    __shared__ __attribute__((aligned(16))) float s_sum[512 * 4];
-    const KvArgs &c = a.c;
-    const int tiles = (a.group + 15) / 16, pairs = c.nkv * tiles, width = min(16, a.group);
-    const int col = blockIdx.x % width, bp = blockIdx.x / width;
-    const int pair = bp % pairs, b = bp / pairs;
-    const int first = reinterpret_cast<const int *>(a.rec)[2 * bp], n = reinterpret_cast<const int *>(a.rec)[2 * bp + 1];
-    const int h = (pair / tiles) * a.group + (pair % tiles) * 16 + col;
-    if (n <= 1 || (pair % tiles) * 16 + col >= a.group)
-        return;
-    const int D = c.hd, tid = threadIdx.x;
-    const int64_t stride = attn_part_floats(width, D);
-    const float *part = a.part + first * stride;
-    float m = -INFINITY;
-    for (int k = tid; k < n; k += 512) {
-        const float v = part[k * stride + (int64_t)width * D + 2 * col];
-        s_f[k] = v;
-        m = fmaxf(m, v);
-    }
-#pragma unroll
-    for (int x = 32; x; x >>= 1)
-        m = fmaxf(m, __shfl_xor(m, x));
-    if ((tid & 63) == 0)
-        s_red[tid >> 6][0] = m;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < 8; ++w)
-        m = fmaxf(m, s_red[w][0]);
-    float l = 0.f;
-    for (int k = tid; k < n; k += 512) {
-        const float v = s_f[k];
-        const float f = v == -INFINITY ? 0.f : v == m ? 1.0f : __builtin_amdgcn_exp2f(v - m);
-        s_f[k] = f;
-        l += f == 0.f ? 0.f : f * part[k * stride + (int64_t)width * D + 2 * col + 1];
-    }
-#pragma unroll
-    for (int x = 32; x; x >>= 1)
-        l += __shfl_xor(l, x);
-    if ((tid & 63) == 0)
-        s_red[tid >> 6][1] = l;
-    __syncthreads();
-    l = 0.f;
-#pragma unroll
-    for (int w = 0; w < 8; ++w)
-        l += s_red[w][1];
-    const int lanes = D / 4, groups = 512 / lanes, d4 = tid % lanes, grp = tid / lanes;
-    af4 sum = {0.f, 0.f, 0.f, 0.f};
-    if (grp < groups)
-#pragma unroll 8
-        for (int k = grp; k < n; k += groups) {
-            const float f = s_f[k];
-            const af4 v = *reinterpret_cast<const af4 *>(part + k * stride + (int64_t)col * D + 4 * d4);
-            sum += f == 0.f ? af4{0.f, 0.f, 0.f, 0.f} : v * f;
-        }
-    *reinterpret_cast<af4 *>(s_sum + 4 * tid) = sum;
-    __syncthreads();
-    if (tid < lanes) {
-        for (int k = 1; k < groups; ++k)
-            sum += *reinterpret_cast<const af4 *>(s_sum + 4 * (tid + k * lanes));
-        *reinterpret_cast<af4 *>(a.o + ((int64_t)b * a.nq + h) * D + 4 * tid) =
-            sum * (m == -INFINITY ? 0.f : 1.0f / l);
+        if (!top)
+            finish_sums(g0);
     }
 }
 
@@ -506,7 +553,7 @@ int launch_attn(int kv_type, const AttnArgs &a, void *stream)
 {
     hipStream_t s = static_cast<hipStream_t>(stream);
     const int pairs = a.c.nkv * ((a.group + 15) / 16), all = a.c.n_seq * pairs;
-    const int grid = all > ATTN_SLOTS ? all : ATTN_SLOTS;
+    const int slots = attn_slots(a.c.hd), grid = all > slots ? all : slots;
     void (*k)(AttnArgs) = nullptr;
 #define QG_ATTN_D(DD) k = kv_type == KV_F16 ? k_attn<KV_F16, DD> : k_attn<KV_BF16, DD>
     switch (a.c.hd) {
@@ -518,12 +565,6 @@ int launch_attn(int kv_type, const AttnArgs &a, void *stream)
     }
 #undef QG_ATTN_D
     hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(256), 0, s, a);
-    const hipError_t e = hipGetLastError();
-    // no sequence is split when there are as many (sequence, pair)s as workgroup slots
-    if (e != hipSuccess || all >= ATTN_SLOTS)
-        return (int)e;
-    const int cols = a.group < 16 ? a.group : 16;
-    hipLaunchKernelGGL(k_attn_join, dim3((unsigned)(all * cols)), dim3(512), 0, s, a);
     return (int)hipGetLastError();
 }
 

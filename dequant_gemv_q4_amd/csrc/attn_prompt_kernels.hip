@@ -71,11 +71,16 @@ __device__ bool tile_place(const KvArgs &c, int group, int id, int split, int n_
         return (int)(s < 0 ? 0 : s < c.n_rows ? s : c.n_rows);
     };
     int b = -1;
-#pragma unroll 4
-    for (int b0 = 0; b0 < c.n_seq; b0 += 64) {
-        const int i = b0 + lane;
-        const bool in = i < c.n_seq && (int64_t)start(i) * group / PT_ROWS + i <= id;
-        b += __popcll(__ballot(in));
+    for (int b0 = 0; b0 < c.n_seq; b0 += 256) {          // four loads in flight
+        int first[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            first[x] = start(min(b0 + 64 * x + lane, c.n_seq));
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const int i = b0 + 64 * x + lane;
+            b += __popcll(__ballot(i < c.n_seq && (int64_t)first[x] * group / PT_ROWS + i <= id));
+        }
     }
     if (b < 0)
         return false;
@@ -114,6 +119,8 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
 {
     constexpr int NP = PIECES<T>, KB = D / 16, DT = D / 32;
     constexpr int PR = D / 8;                          // 16-byte pieces of a K row
+    // 32-position tiles of scores held at a time: three query pieces leave registers for one
+    constexpr int NT = NP * D > 384 ? 1 : 2;
     constexpr int KEYM = D % 64 == 0 ? 7 : 3;          // bits of the piece number that the key takes
     constexpr int HALF = PT_STEP * D * 2;              // bytes of a K (or V) buffer
     constexpr int PASS = HALF / 4096;                  // copies of a wave for either
@@ -133,11 +140,10 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
     const int rho = p.rho0 + 32 * wave + col;
     const int tok = rho / a.group, head = hkv * a.group + rho % a.group;
     const bool live = tok < p.rows;
-    // the wave's least and largest position (rows rise with the column); rows past the sequence
-    // compute along with the last one and are not stored
+    // the wave's largest position (rows rise with the column); rows past the sequence compute along
+    // with the last one and are not stored
     const int wave_tok0 = (p.rho0 + 32 * wave) / a.group;
     const int wave_tok1 = min((p.rho0 + 32 * wave + 31) / a.group, p.rows - 1);
-    const int wave_min = p.pos0 + wave_tok0;
     const int wave_max = wave_tok0 < p.rows ? p.pos0 + wave_tok1 : -1;
     const int pos = live ? p.pos0 + tok : wave_max;    // the row sees positions 0..pos
 
@@ -223,42 +229,46 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
             o[d][r] = 0.f;
     float m = -INFINITY, l = 0.f;
 
-    // raw (unscaled) scores of step s
-    auto scores = [&](int buf, af16 (&sc)[2]) {
-        const uint8_t *kb = lds + buf * 2 * HALF;
+    // raw (unscaled) scores of positions 32 NT sub .. of a step
+    auto scores = [&](int buf, int sub, af16 (&sc)[NT]) {
+        const uint8_t *kb = lds + buf * 2 * HALF + sub * (NT * 64 * D);
 #pragma unroll
-        for (int tt = 0; tt < 2; ++tt)
+        for (int tt = 0; tt < NT; ++tt)
 #pragma unroll
             for (int r = 0; r < 16; ++r)
                 sc[tt][r] = 0.f;
-        // operands are read two channel blocks ahead of their products (the fences keep the compiler
+        // operands are read one or two channel blocks ahead of their products (the fences keep the compiler
         // from reading all of them first, for which there are no registers)
-        au4 kf[3][2];
+        constexpr int AHEAD = D > 192 ? 1 : 2;
+        au4 kf[AHEAD + 1][NT];
         auto read = [&](int k) {
 #pragma unroll
-            for (int tt = 0; tt < 2; ++tt)
-                kf[k % 3][tt] = *reinterpret_cast<const au4 *>(kb + koff[k & 3] + (k >> 2) * 128 + tt * 64 * D);
+            for (int tt = 0; tt < NT; ++tt)
+                kf[k % (AHEAD + 1)][tt] = *reinterpret_cast<const au4 *>(kb + koff[k & 3] + (k >> 2) * 128 + tt * 64 * D);
         };
-        read(0);
-        read(1);
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+            read(k);
 #pragma unroll
         for (int k = 0; k < KB; ++k) {
-            if (k + 2 < KB)
-                read(k + 2);
+            if (k + AHEAD < KB)
+                read(k + AHEAD);
 #pragma unroll
             for (int y = NP - 1; y >= 0; --y)
 #pragma unroll
-                for (int tt = 0; tt < 2; ++tt)
-                    sc[tt] = mm32<T>(kf[k % 3][tt], qf[y][k], sc[tt]);
+                for (int tt = 0; tt < NT; ++tt)
+                    sc[tt] = mm32<T>(kf[k % (AHEAD + 1)][tt], qf[y][k], sc[tt]);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
     // scores -> probabilities (times 2^6 over the reference), maximum and sum kept up
-    auto softmax = [&](af16 (&sc)[2]) {
-        float mx = fmaxf(sc[0][0], sc[1][0]);
+    auto softmax = [&](af16 (&sc)[NT]) {
+        float mx = sc[0][0];
 #pragma unroll
-        for (int r = 1; r < 16; ++r)
-            mx = fmaxf(fmaxf(mx, sc[0][r]), sc[1][r]);
+        for (int r = 0; r < 16; ++r)
+#pragma unroll
+            for (int tt = 0; tt < NT; ++tt)
+                mx = fmaxf(mx, sc[tt][r]);
         mx *= unscale;
         if (__any(mx > m + 9.0f)) {
             const float mn = fmaxf(m, max_x32(mx));
@@ -272,18 +282,18 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
                     o[d][r] *= f;
         }
         const float ref = m == -INFINITY ? 0.f : 6.0f - m;
-        float la = 0.f, lb = 0.f;
+        float sum[NT];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            sc[0][r] = __builtin_amdgcn_exp2f(fmaf(sc[0][r], unscale, ref));
-            sc[1][r] = __builtin_amdgcn_exp2f(fmaf(sc[1][r], unscale, ref));
-            la += sc[0][r];
-            lb += sc[1][r];
-        }
-        l += la + lb;
+        for (int r = 0; r < 16; ++r)
+#pragma unroll
+            for (int tt = 0; tt < NT; ++tt) {
+                sc[tt][r] = __builtin_amdgcn_exp2f(fmaf(sc[tt][r], unscale, ref));
+                sum[tt] = r == 0 ? sc[tt][0] : sum[tt] + sc[tt][r];
+            }
+        l += NT == 2 ? sum[0] + sum[NT - 1] : sum[0];
     };
     // probability operand of 16-position block k
-    auto weights = [&](const af16 (&sc)[2], int k, au4 (&pf)[NP]) {
+    auto weights = [&](const af16 (&sc)[NT], int k, au4 (&pf)[NP]) {
         float pr[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -291,19 +301,19 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
         split8<T>(pr, pf);
     };
     // O += V^T P
-    auto values = [&](const af16 (&sc)[2], int buf) {
-        const uint8_t *vb = lds + buf * 2 * HALF + HALF;
+    auto values = [&](const af16 (&sc)[NT], int buf, int sub) {
+        const uint8_t *vb = lds + buf * 2 * HALF + HALF + sub * (NT * 64 * D);
         auto read = [&](int x) {                        // operand x = DT k + d
             return *reinterpret_cast<const au4 *>(vb + voff + (x / DT) * (D * 32) + (x % DT) * 1024);
         };
-        constexpr int AHEAD = 3;
+        constexpr int AHEAD = D > 192 ? 2 : 3;
         au4 v[AHEAD + 1], pf[NP];
 #pragma unroll
         for (int x = 0; x < AHEAD; ++x)
             v[x] = read(x);
 #pragma unroll
-        for (int x = 0; x < 4 * DT; ++x) {
-            if (x + AHEAD < 4 * DT)
+        for (int x = 0; x < 2 * NT * DT; ++x) {
+            if (x + AHEAD < 2 * NT * DT)
                 v[(x + AHEAD) % (AHEAD + 1)] = read(x + AHEAD);
             if (x % DT == 0)
                 weights(sc, x / DT, pf);
@@ -316,6 +326,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
     // Edge steps hold positions that some rows of the tile do not see.  An infinity or NaN in V there
     // must reach the rows that see it and no other, but 0 x NaN is NaN: such values are added to
     // their rows one by one and then cleared in LDS.
+    constexpr int SUB = NT * 64 * D;                    // bytes of V that belong to NT tiles
     auto scan = [&](int buf) {
         uint32_t nf = 0;
 #pragma unroll 1
@@ -327,10 +338,10 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
         __syncthreads();
         return (s_odd[0] | s_odd[1] | s_odd[2] | s_odd[3]) != 0;
     };
-    auto clear = [&](int buf) {
+    auto clear = [&](int buf, int sub) {
 #pragma unroll 1
-        for (int x = tid; x < HALF / 16; x += 256) {
-            au4 *v = reinterpret_cast<au4 *>(lds + buf * 2 * HALF + HALF + 16 * x);
+        for (int x = tid; x < SUB / 16; x += 256) {
+            au4 *v = reinterpret_cast<au4 *>(lds + buf * 2 * HALF + HALF + sub * SUB + 16 * x);
             au4 y = *v;
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
@@ -340,10 +351,10 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
             *v = y;
         }
     };
-    auto add_nonfinite = [&](int see, uint32_t bad, int buf) {
+    auto add_nonfinite = [&](int see, uint32_t bad, int buf, int sub) {
         const uint8_t *vb = lds + buf * 2 * HALF + HALF;
 #pragma unroll 1
-        for (int t = 0; t < PT_STEP; ++t) {
+        for (int t = 32 * NT * sub; t < 32 * NT * (sub + 1); ++t) {
             if (bad >> (t >> 4) & 1)
                 continue;
             const uint32_t at = (t >> 4) * (D * 32) + 2 * (t & 7);
@@ -356,6 +367,8 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
                         vb + at + d * 1024 + ch * 32 + ((((t >> 3) & 1) ^ ((ch >> 2) & 1)) << 4));
                     if (t <= see && nonfinite2<T>(x))
                         o[d][r] += low_of<T>(x);
+                    if (r % 8 == 7)
+                        __builtin_amdgcn_sched_barrier(0);
                 }
         }
     };
@@ -366,28 +379,33 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
         const bool odd = edge ? scan(buf) : false;
         const bool active = t0 <= wave_max;            // else nothing of this step is seen by the wave
         const int see = min(pos, p.hi - 1) - t0;
-        af16 sc[2];
-        if (active) {
-            scores(buf, sc);
-            // value r of tile tt is position t0 + 32 tt + 16 (r / 8) + 8 hf + r % 8
-            if (edge)
 #pragma unroll
-                for (int tt = 0; tt < 2; ++tt)
+        for (int sub = 0; sub < 2 / NT; ++sub) {
+            af16 sc[NT];
+            if (active) {
+                scores(buf, sub, sc);
+                // value r of tile tt is position t0 + 32 (NT sub + tt) + 16 (r / 8) + 8 hf + r % 8
+                if (edge)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        if (32 * tt + 16 * (r >> 3) + (r & 7) > see - 8 * hf || (bad >> (2 * tt + (r >> 3)) & 1))
-                            sc[tt][r] = -INFINITY;
-            softmax(sc);
-        }
-        if (odd) {
+                    for (int tt = 0; tt < NT; ++tt)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) {
+                            const int blk = 2 * (NT * sub + tt) + (r >> 3);
+                            if (16 * blk + (r & 7) > see - 8 * hf || (bad >> blk & 1))
+                                sc[tt][r] = -INFINITY;
+                        }
+                softmax(sc);
+            }
+            if (odd) {
+                if (active)
+                    add_nonfinite(see, bad, buf, sub);
+                __syncthreads();
+                clear(buf, sub);
+                __syncthreads();
+            }
             if (active)
-                add_nonfinite(see, bad, buf);
-            __syncthreads();
-            clear(buf);
-            __syncthreads();
+                values(sc, buf, sub);
         }
-        if (active)
-            values(sc, buf);
     };
 
     const int s0 = p.chunk0, s1 = p.chunk1;
@@ -479,19 +497,22 @@ __global__ __launch_bounds__(256) void k_attn_prompt_join(AttnArgs a, int n_spli
 }
 
 // Tile ids of a call (at least its tiles), and splits over the cache's length: with fewer than one
-// workgroup per compute unit the tiles are split until two are.
-PromptPlan plan_prompt(int64_t n_rows, int n_seq, int nkv, int group)
+// workgroup per compute unit the tiles are split until two are, as far as a table of `positions` can
+// give every split its eight steps.
+PromptPlan plan_prompt(int64_t n_rows, int n_seq, int nkv, int group, int64_t positions)
 {
     PromptPlan p;
     p.tiles = n_rows * group / PT_ROWS + n_seq;
-    p.n_split = p.tiles * nkv >= PROMPT_SLOTS / 2 ? 1 : (int)(PROMPT_SLOTS / (p.tiles * nkv));
+    const int64_t most = positions / (8 * PT_STEP), want = PROMPT_SLOTS / (p.tiles * nkv);
+    p.n_split = p.tiles * nkv >= PROMPT_SLOTS / 2 || most <= 1 ? 1 : (int)(want < most ? want : most);
     return p;
 }
 
 int launch_attn_prompt(int kv_type, const AttnArgs &a, void *stream)
 {
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const PromptPlan p = plan_prompt(a.c.n_rows, a.c.n_seq, a.c.nkv, a.group);
+    const PromptPlan p = plan_prompt(a.c.n_rows, a.c.n_seq, a.c.nkv, a.group,
+                                     (int64_t)a.c.max_pages << a.c.ps_log2);
     void (*k)(AttnArgs, int) = nullptr;
 #define QG_PROMPT_D(DD) k = kv_type == KV_F16 ? k_attn_prompt<KV_F16, DD> : k_attn_prompt<KV_BF16, DD>
     switch (a.c.hd) {

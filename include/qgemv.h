@@ -306,8 +306,8 @@ int qgemv_kv_append(int kv_type, void *k_pages, void *v_pages, int64_t n_pages, 
 /* Attention of one new token per sequence: o[b][h] = sum_t p_t V_t over the positions
  * t < kv_len[b], p = softmax_t(scale q[b][h] . K_t).  q is f32, row b at q + b * q_stride, heads
  * back to back (the fused QKV output itself); o is f32 [n_seq][n_q_heads * head_dim], the x of
- * the output projection's qgemv_res.  Long caches are split over workgroups by the lengths found
- * on the device and joined by a second, small launch on `stream`. */
+ * the output projection's qgemv_res.  One launch: long caches are split over workgroups by the
+ * lengths found on the device, and the last workgroups to finish join the parts. */
 int qgemv_attn(int kv_type, const void *k_pages, const void *v_pages, int64_t n_pages,
                int page_size, int64_t page_stride, int n_kv_heads, int head_dim,
                const int32_t *table, int max_pages, const int32_t *kv_len, int n_seq,
