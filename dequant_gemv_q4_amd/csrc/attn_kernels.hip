@@ -6,74 +6,96 @@
 
 namespace qg {
 
-// Round to nearest-even, as the conversion instructions do.
-template <int T>
-__device__ __forceinline__ uint16_t kv_round(float v)
-{
-    if constexpr (T == KV_F16)
-        return __builtin_bit_cast(uint16_t, (_Float16)v);
-    else
-        return __builtin_bit_cast(uint16_t, (__bf16)v);
-}
-template <int T>
-__device__ __forceinline__ float kv_float(uint16_t b)
-{
-    if constexpr (T == KV_F16)
-        return (float)__builtin_bit_cast(_Float16, b);
-    else
-        return __builtin_bit_cast(float, (uint32_t)b << 16);
-}
-
-// Sequence of row r: the last b whose q_start is <= r and whose end is behind r, or -1.
-__device__ __forceinline__ int seq_of_row(const KvArgs &c, int64_t r, int64_t &start, int64_t &end)
-{
-    if (!c.q_start) {
-        start = r;
-        end = r + 1;
-        return (int)r;
-    }
-    for (int b = 0; b < c.n_seq; ++b) {
-        start = c.q_start[b];
-        end = c.q_start[b + 1];
-        if (r >= start && r < end)
-            return b;
-    }
-    return -1;
-}
-
-// Element offset of position t's page, or -1 (sticky flag set) if it has no valid one.
-__device__ __forceinline__ int64_t page_at(const KvArgs &c, int b, int64_t t)
-{
-    const int64_t i = t >> c.ps_log2;
-    const int page = i < c.max_pages ? c.table[(int64_t)b * c.max_pages + i] : -1;
-    if (page < 0 || page >= c.n_pages) {
-        atomicOr(c.err, 1u);
-        return -1;
-    }
-    return page * c.page_stride;
-}
-
-template <int T>
+// ------------------------------------------------------------------------------------ new rows
+//
+// A workgroup stores one KV head of one block of 16 or 32 positions (at most a page) of a sequence.
+// K: a thread takes eight channels of a position (32 bytes read, 16 written).  V is transposed on
+// the way: a thread takes eight positions of a channel, one 4-byte load each, and writes them as 16
+// bytes; neighbouring lanes take the pieces of a channel, then the next channel, so that a wave
+// writes 1 KB in one run (pages of 16 and 32) or in runs of 64 bytes, and reads runs of 64 or 128
+// bytes.  A piece with positions that are not new is written element by element.
+//
+// Blocks start at multiples of their size; sequence b's begin at block id q_start[b] / size + 2 b,
+// which leaves every sequence enough ids wherever its first position lies.
+template <int T, int BL>
 __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a)
 {
+    constexpr int BLOCK = 1 << BL, PIECES_V = BLOCK / 8;
     const KvArgs &c = a.c;
-    const int64_t r = blockIdx.x;
-    int64_t start, end;
-    const int b = seq_of_row(c, r, start, end);
-    if (b < 0)
+    const int tid = threadIdx.x, lane = tid & 63, h = blockIdx.y, id = blockIdx.x;
+    int b = id, r0 = id, rows = 1, block = 0;
+    if (c.q_start) {
+        auto start = [&](int i) {
+            const int64_t v = c.q_start[i];
+            return (int)(v < 0 ? 0 : v < c.n_rows ? v : c.n_rows);
+        };
+        b = -1;
+        for (int b0 = 0; b0 < c.n_seq; b0 += 256) {       // four loads in flight
+            int first[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                first[x] = start(min(b0 + 64 * x + lane, c.n_seq));
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const int i = b0 + 64 * x + lane;
+                b += __popcll(__ballot(i < c.n_seq && (first[x] >> BL) + 2 * i <= id));
+            }
+        }
+        if (b < 0)
+            return;
+        b = __builtin_amdgcn_readfirstlane(b);
+        r0 = start(b);
+        rows = start(b + 1) - r0;
+        block = id - ((r0 >> BL) + 2 * b);
+        if (rows <= 0 || block < 0)
+            return;
+    }
+    // positions [lo, hi) of the sequence are new; this block is positions [t0, t0 + BLOCK)
+    const int64_t hi = c.kv_len[b], first = hi - rows, lo = first > 0 ? first : 0;
+    const int64_t t0 = ((lo >> BL) + block) << BL;
+    if (t0 >= hi)
         return;
-    const int64_t t = c.kv_len[b] - (end - r);
-    if (t < 0)
+    const int64_t entry = t0 >> c.ps_log2;
+    const int page = entry < c.max_pages ? c.table[(int64_t)b * c.max_pages + entry] : -1;
+    if (page < 0 || page >= c.n_pages) {
+        if (tid == 0 && h == 0)
+            atomicOr(c.err, 1u);
         return;
-    const int64_t off = page_at(c, b, t);
-    if (off < 0)
-        return;
-    const int slot = (int)(t & ((1 << c.ps_log2) - 1));
-    for (int e = threadIdx.x; e < c.nkv * c.hd; e += 256) {
-        const int h = e / c.hd, d = e % c.hd;
-        const int64_t blk = off + ((int64_t)h * c.hd << c.ps_log2);
-        c.k[blk + (int64_t)slot * c.hd + d] = kv_round<T>(a.ksrc[r * a.stride + e]);
-        c.v[blk + ((int64_t)d << c.ps_log2) + slot] = kv_round<T>(a.vsrc[r * a.stride + e]);
+    }
+    // new positions of the block: [from, to); row of position t0 + t at src + t * stride
+    const int from = (int)(lo > t0 ? lo - t0 : 0), to = (int)(hi - t0 < BLOCK ? hi - t0 : BLOCK);
+    const int64_t at = (r0 + (t0 - first)) * a.stride + (int64_t)h * c.hd;
+    const float *ks = a.ksrc + at, *vs = a.vsrc + at;
+    const int64_t out = (int64_t)page * c.page_stride + ((int64_t)h * c.hd << c.ps_log2);
+    const int slot = (int)(t0 & ((1 << c.ps_log2) - 1));
+    uint16_t *kd = c.k + out + (int64_t)slot * c.hd, *vd = c.v + out + slot;
+
+    const int kp = c.hd / 8;                               // pieces of a K row
+    for (int x = from * kp + tid; x < to * kp; x += 256) {
+        const int t = x / kp, p = x % kp;
+        const float4 u = *reinterpret_cast<const float4 *>(ks + t * a.stride + 8 * p);
+        const float4 w = *reinterpret_cast<const float4 *>(ks + t * a.stride + 8 * p + 4);
+        const au4 v = {pack2<T>(u.x, u.y), pack2<T>(u.z, u.w), pack2<T>(w.x, w.y), pack2<T>(w.z, w.w)};
+        *reinterpret_cast<au4 *>(kd + (int64_t)t * c.hd + 8 * p) = v;
+    }
+    for (int x = tid; x < c.hd * PIECES_V; x += 256) {
+        const int d = x / PIECES_V, t = 8 * (x % PIECES_V);
+        if (t >= to || t + 8 <= from)
+            continue;
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            f[e] = vs[min(max(t + e, from), to - 1) * a.stride + d];
+        const au4 v = {pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7])};
+        uint16_t *dst = vd + ((int64_t)d << c.ps_log2) + t;
+        if (t >= from && t + 8 <= to) {
+            *reinterpret_cast<au4 *>(dst) = v;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (t + e >= from && t + e < to)
+                    dst[e] = (uint16_t)(v[e / 2] >> (16 * (e % 2)));
+        }
     }
 }
 
@@ -542,10 +564,11 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn(AttnArgs a)
 int launch_kv_append(int kv_type, const AppendArgs &a, void *stream)
 {
     hipStream_t s = static_cast<hipStream_t>(stream);
-    if (kv_type == KV_F16)
-        hipLaunchKernelGGL(k_kv_append<KV_F16>, dim3((unsigned)a.c.n_rows), dim3(256), 0, s, a);
-    else
-        hipLaunchKernelGGL(k_kv_append<KV_BF16>, dim3((unsigned)a.c.n_rows), dim3(256), 0, s, a);
+    const int bl = a.c.ps_log2 < 5 ? 4 : 5;
+    const int64_t blocks = a.c.q_start ? (a.c.n_rows >> bl) + 2 * (int64_t)a.c.n_seq : a.c.n_seq;
+    auto k = kv_type == KV_F16 ? (bl == 4 ? k_kv_append<KV_F16, 4> : k_kv_append<KV_F16, 5>)
+                               : (bl == 4 ? k_kv_append<KV_BF16, 4> : k_kv_append<KV_BF16, 5>);
+    hipLaunchKernelGGL(k, dim3((unsigned)blocks, (unsigned)a.c.nkv), dim3(256), 0, s, a);
     return (int)hipGetLastError();
 }
 
