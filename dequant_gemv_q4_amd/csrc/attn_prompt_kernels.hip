@@ -458,41 +458,71 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
     }
 }
 
-// Rows of a split tile from its partial results, in order.  A workgroup takes one tile's rows
-// blockIdx.y * 8 .. + 7 of one KV head, a thread four channels.
+// Rows of a split tile from its partial results.  A workgroup takes four rows of one KV head; a thread
+// four channels of a row and every `parts`-th split, in order, then the parts are added in order.
 __global__ __launch_bounds__(256) void k_attn_prompt_join(AttnArgs a, int n_split)
 {
+    __shared__ float s_f[4][PROMPT_SLOTS], s_l[4];
+    __shared__ __attribute__((aligned(16))) af4 s_sum[256];
     const KvArgs &c = a.c;
     const int D = c.hd, lanes = D / 4, tid = threadIdx.x;
-    const int hkv = blockIdx.x % c.nkv, id = blockIdx.x / c.nkv;
+    const int hkv = blockIdx.x % c.nkv, id = blockIdx.x / c.nkv, r0 = 4 * blockIdx.y;
     TilePlace p;
     int splits;
-    if (!tile_place(c, a.group, id, 0, n_split, p, splits) || splits <= 1)
+    if (!tile_place(c, a.group, id, 0, n_split, p, splits) || splits <= 1 ||
+        (p.rho0 + r0) / a.group >= p.rows)
         return;
-    const float *part = a.part + (int64_t)(id * c.nkv + hkv) * n_split * prompt_part_floats(D);
-    for (int x = tid; x < 8 * lanes; x += 256) {
-        const int r = 8 * blockIdx.y + x / lanes, d4 = x % lanes;
-        const int rho = p.rho0 + r, tok = rho / a.group;
-        if (tok >= p.rows)
-            continue;
-        const float *ml = part + PT_ROWS * D + 2 * r;
-        float m = -INFINITY;
-        for (int k = 0; k < splits; ++k)
-            m = fmaxf(m, ml[k * prompt_part_floats(D)]);
-        float l = 0.f;
-        af4 sum = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-        for (int k = 0; k < splits; ++k) {
-            const float mk = ml[k * prompt_part_floats(D)], lk = ml[k * prompt_part_floats(D) + 1];
-            const float f = mk == m ? 1.0f : __builtin_amdgcn_exp2f(mk - m);
-            const af4 v = *reinterpret_cast<const af4 *>(part + k * prompt_part_floats(D) + r * D + 4 * d4);
-            if (mk != -INFINITY) {
-                sum += v * f;
-                l += lk * f;
+    const int64_t stride = prompt_part_floats(D);
+    const float *part = a.part + (int64_t)(id * c.nkv + hkv) * n_split * stride;
+    // wave w: the factors 2^(m_k - m) of row r0 + w, and its sum
+    {
+        const int w = tid >> 6, lane = tid & 63;
+        const float *ml = part + PT_ROWS * D + 2 * (r0 + w);
+        float m = -INFINITY, l = 0.f;
+        for (int k = lane; k < splits; k += 64)
+            m = fmaxf(m, ml[k * stride]);
+#pragma unroll
+        for (int x = 32; x; x >>= 1)
+            m = fmaxf(m, __shfl_xor(m, x));
+        for (int k = lane; k < splits; k += 64) {
+            const float mk = ml[k * stride];
+            const float f = mk == -INFINITY ? 0.f : mk == m ? 1.0f : __builtin_amdgcn_exp2f(mk - m);
+            s_f[w][k] = f;
+            l += f == 0.f ? 0.f : f * ml[k * stride + 1];
+        }
+#pragma unroll
+        for (int x = 32; x; x >>= 1)
+            l += __shfl_xor(l, x);
+        if (lane == 0)
+            s_l[w] = m == -INFINITY ? 0.f : 1.0f / l;
+    }
+    __syncthreads();
+    const int items = 4 * lanes, parts = 256 / items, e = tid % items, k0 = tid / items;
+    const int row = e / lanes, d4 = e % lanes;
+    af4 sum = {0.f, 0.f, 0.f, 0.f};
+    if (k0 < parts) {
+        const float *from = part + (r0 + row) * D + 4 * d4;
+        for (int kb = k0; kb < splits; kb += 8 * parts) {
+            af4 v[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x)                        // all loads in flight at once
+                v[x] = *reinterpret_cast<const af4 *>(from + min(kb + x * parts, splits - 1) * stride);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const float f = kb + x * parts < splits ? s_f[row][kb + x * parts] : 0.f;
+                if (f != 0.f)
+                    sum += v[x] * f;
             }
         }
+    }
+    s_sum[tid] = sum;
+    __syncthreads();
+    const int rho = p.rho0 + r0 + row, tok = rho / a.group;
+    if (k0 == 0 && tok < p.rows) {
+        for (int x = 1; x < parts; ++x)
+            sum += s_sum[e + x * items];
         *reinterpret_cast<af4 *>(a.o + ((int64_t)(p.row0 + tok) * a.nq + hkv * a.group + rho % a.group) * D +
-                                 4 * d4) = sum * (m == -INFINITY ? 0.f : 1.0f / l);
+                                 4 * d4) = sum * s_l[row];
     }
 }
 
@@ -528,7 +558,7 @@ int launch_attn_prompt(int kv_type, const AttnArgs &a, void *stream)
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.n_split == 1)
         return (int)e;
-    hipLaunchKernelGGL(k_attn_prompt_join, dim3(grid, PT_ROWS / 8), dim3(256), 0, s, a, p.n_split);
+    hipLaunchKernelGGL(k_attn_prompt_join, dim3(grid, PT_ROWS / 4), dim3(256), 0, s, a, p.n_split);
     return (int)hipGetLastError();
 }
 
