@@ -138,6 +138,14 @@ __device__ __forceinline__ float q_scale(float amax)
     return ldexpf(1.0f, k < 126 ? k : 126);
 }
 
+// Bits 15 and 31 set where a half of the pair is an infinity or NaN.
+template <int T>
+__device__ __forceinline__ uint32_t nonfinite2(uint32_t v)
+{
+    return T == KV_F16 ? ((v & 0x7C007C00u) + 0x04000400u) & 0x80008000u
+                       : ((v & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+}
+
 constexpr float LOG2E = 1.44269504088896340736f;
 
 }  // namespace qg

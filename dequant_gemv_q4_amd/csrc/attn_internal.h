@@ -72,6 +72,7 @@ PromptPlan plan_prompt(int64_t n_rows, int n_seq, int nkv, int group, int64_t po
 // Launchers: a hipError_t value (0 = success).
 int launch_kv_append(int kv_type, const AppendArgs &a, void *stream);
 int launch_attn(int kv_type, const AttnArgs &a, void *stream);
+int launch_attn_rows(int kv_type, const AttnArgs &a, void *stream);     // few rows per sequence
 int launch_attn_prompt(int kv_type, const AttnArgs &a, void *stream);
 int launch_route(const RouteArgs &a, void *stream);
 

@@ -99,11 +99,12 @@ __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a)
     }
 }
 
-// ---------------------------------------------------------------------- one new token per sequence
+// --------------------------------------------------------------- one or a few new rows per sequence
 //
 // o = sum_t softmax(scale q . K_t) V_t for the query heads of one KV head: a workgroup takes up to
-// 16 of them against one run (chunk) of positions.  Both products run on the matrix cores with the
-// positions in the rows and the query heads in the columns, S^T = K Q^T and O^T = V^T P^T
+// 16 columns rho = token * group + head of them (one token: its heads) against one run (chunk) of
+// positions.  Both products run on the matrix cores with the positions in the rows and the query
+// heads in the columns, S^T = K Q^T and O^T = V^T P^T
 // (v_mfma_f32_16x16x32), so that
 //  - K, and V as the cache holds it (transposed inside the page), are the A operands: eight
 //    consecutive halves each, loaded from the cache straight into registers by 16-byte loads;
@@ -134,9 +135,10 @@ constexpr int ATTN_LEAST = 2;        // units of a chunk, at least
 constexpr int JOIN_RADIX = 8;
 
 struct AttnPlan {
-    int b, pair, chunk, n_chunk;   // this workgroup's sequence, (KV head, 16-head tile), chunk
+    int b, pair, chunk, n_chunk;   // this workgroup's sequence, (KV head, 16-column tile), chunk
     int slot0;                     // workgroup id of the pair's first chunk
     int len;                       // the sequence's positions
+    int row0, rows;                // its new rows
 };
 
 // Positions of sequence b that have a place in its table.
@@ -172,28 +174,49 @@ __device__ __forceinline__ int chunks_of(int n, int u)
 }
 
 // Workgroup id -> its place in the plan; false if the plan has fewer workgroups.  Runs in every
-// wave (no barrier); lane l looks at sequences l, l + 64, ... (the first 64 held in a register).
-__device__ __forceinline__ bool attn_plan(const KvArgs &c, int pairs, int slots, int id, AttnPlan &p)
+// wave (no barrier); lane l looks at sequences l, l + 64, ... (the first 64 held in registers).
+// ROWS: sequence b has the rows between its q_start and the next; else one row, row b.
+template <bool ROWS>
+__device__ __forceinline__ bool attn_plan(const KvArgs &c, int group, int slots, int id, AttnPlan &p)
 {
     const int lane = threadIdx.x & 63;
-    const int n0 = lane < c.n_seq ? seq_len(c, lane) : 0;
+    struct Seq {
+        int n, pairs, row0, rows;
+    };
+    auto start = [&](int i) {
+        const int64_t v = c.q_start[i];
+        return (int)(v < 0 ? 0 : v < c.n_rows ? v : c.n_rows);
+    };
+    auto seq = [&](int b) {
+        Seq s = {0, 0, b, 1};
+        if (b < c.n_seq) {
+            s.n = seq_len(c, b);
+            if constexpr (ROWS) {
+                s.row0 = start(b);
+                s.rows = max(start(b + 1) - s.row0, 0);
+            }
+            s.pairs = c.nkv * ((s.rows * group + 15) / 16);
+        }
+        return s;
+    };
+    const Seq s0 = seq(lane);
     auto sum = [&](auto of) {
-        int v = lane < c.n_seq ? of(n0) : 0;
-        for (int b = lane + 64; b < c.n_seq; b += 64)
-            v += of(seq_len(c, b));
+        int v = of(s0);
+        for (int b0 = 64; b0 < c.n_seq; b0 += 64)
+            v += of(seq(b0 + lane));
         return wave_sum(v);
     };
     int u = 0x3fffffff;
-    if (c.n_seq * pairs < slots) {
-        // chunks <= units / u + n_seq, so u = units / (room - n_seq) is enough; units / room is the
-        // least that could be
-        const int units = sum([](int n) { return units_of(n); }), room = slots / pairs;
-        int lo = max((units + room - 1) / room, ATTN_LEAST), hi = 0x3fffffff;
-        if (room > c.n_seq)
-            hi = max((units + room - c.n_seq - 1) / (room - c.n_seq), lo);
+    const int pairs = sum([](const Seq &s) { return s.pairs; });
+    if (pairs < slots) {
+        // chunks <= units / u + 1 each, so u = units / (slots - pairs), over all pairs, is enough;
+        // units / slots is the least that could be
+        const int units = sum([](const Seq &s) { return s.pairs * units_of(s.n); });
+        int lo = max((units + slots - 1) / slots, ATTN_LEAST);
+        int hi = max((units + slots - pairs - 1) / (slots - pairs), lo);
         while (lo < hi) {
             const int mid = lo + (hi - lo) / 2;
-            if (sum([=](int n) { return chunks_of(n, mid); }) <= room)
+            if (sum([=](const Seq &s) { return s.pairs * chunks_of(s.n, mid); }) <= slots)
                 hi = mid;
             else
                 lo = mid + 1;
@@ -202,17 +225,17 @@ __device__ __forceinline__ bool attn_plan(const KvArgs &c, int pairs, int slots,
     }
     int base = 0;
     for (int b0 = 0; b0 < c.n_seq; b0 += 64) {
-        const int b = b0 + lane;
-        const int n = b0 == 0 ? n0 : b < c.n_seq ? seq_len(c, b) : 0;
-        const int nc = b < c.n_seq ? chunks_of(n, u) : 0;
-        const int end = base + wave_scan(nc * pairs);
-        const uint64_t in = __ballot(id < end && b < c.n_seq);
+        const Seq s = b0 == 0 ? s0 : seq(b0 + lane);
+        const int nc = chunks_of(s.n, u), end = base + wave_scan(nc * s.pairs);
+        const uint64_t in = __ballot(id < end);
         if (in) {
             const int l = __ffsll((unsigned long long)in) - 1;
             p.b = b0 + l;
             p.n_chunk = __builtin_amdgcn_readlane(nc, l);
-            p.len = __builtin_amdgcn_readlane(n, l);
-            p.slot0 = __builtin_amdgcn_readlane(end, l) - p.n_chunk * pairs;
+            p.len = __builtin_amdgcn_readlane(s.n, l);
+            p.slot0 = __builtin_amdgcn_readlane(end - nc * s.pairs, l);
+            p.row0 = ROWS ? __builtin_amdgcn_readlane(s.row0, l) : p.b;
+            p.rows = ROWS ? __builtin_amdgcn_readlane(s.rows, l) : 1;
             p.pair = (id - p.slot0) / p.n_chunk;
             p.slot0 += p.pair * p.n_chunk;
             p.chunk = id - p.slot0;
@@ -268,7 +291,7 @@ __device__ __forceinline__ bool last_to_arrive(unsigned int *cnt, int members, i
     return *s_last != 0;
 }
 
-template <int T, int D>
+template <int T, int D, bool ROWS>
 __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn(AttnArgs a)
 {
     constexpr int KB = D / 32, DT = D / 16, NP = PIECES<T>;
@@ -282,30 +305,38 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn(AttnArgs a)
     const KvArgs &c = a.c;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int i = lane & 15, g = lane >> 4;
-    const int tiles = (a.group + 15) / 16, pairs = c.nkv * tiles;
     AttnPlan p;
-    if (!attn_plan(c, pairs, attn_slots(D), blockIdx.x, p))
+    if (!attn_plan<ROWS>(c, a.group, attn_slots(D), blockIdx.x, p))
         return;
-    const int b = __builtin_amdgcn_readfirstlane(p.b), pair = __builtin_amdgcn_readfirstlane(p.pair);
-    const int chunk = __builtin_amdgcn_readfirstlane(p.chunk);
-    const int n_chunk = __builtin_amdgcn_readfirstlane(p.n_chunk);
-    const int len = __builtin_amdgcn_readfirstlane((int)p.len);
-    const int hkv = pair / tiles, h0 = hkv * a.group + (pair % tiles) * 16;
-    const int cols = min(16, a.group - (pair % tiles) * 16);
+    const int b = p.b, chunk = p.chunk, n_chunk = p.n_chunk, len = p.len;
+    const int tiles = (p.rows * a.group + 15) / 16, hkv = p.pair / tiles, rho0 = p.pair % tiles * 16;
+    const int cols = min(16, p.rows * a.group - rho0);
+    // offset of column col in o, and of its row and head in q
+    auto head_of = [&](int col) { return hkv * a.group + (ROWS ? (rho0 + col) % a.group : rho0 + col); };
+    auto row_of = [&](int col) { return p.row0 + (ROWS ? (rho0 + col) / a.group : 0); };
 
     // this chunk's 32-position steps, dealt to the waves in turn
-    const int units = (len + (1 << ATTN_UNIT_LOG2) - 1) >> ATTN_UNIT_LOG2;
+    const int units = units_of(len);
     const int per = units / n_chunk, more = units % n_chunk;
     const int unit0 = chunk * per + min(chunk, more);
     const int t_begin = unit0 << ATTN_UNIT_LOG2;
     const int t_end = min(len, (unit0 + per + (chunk < more ? 1 : 0)) << ATTN_UNIT_LOG2);
+    // positions this lane's column sees, [0, see), and those that all columns see (columns without a
+    // row see what the last one does and are not stored)
+    int see = t_end, see_all = t_end;
+    if constexpr (ROWS) {
+        const int pos0 = max(c.kv_len[b], -(1 << 30)) - p.rows;
+        see = min(t_end, pos0 + (rho0 + min(i, cols - 1)) / a.group + 1);
+        see_all = min(t_end, pos0 + rho0 / a.group + 1);
+    }
     const int n_steps = t_end > t_begin + 32 * wave ? (t_end - t_begin - 32 * wave + 127) / 128 : 0;
 
     // queries of column i: scaled, split
     au4 qf[Q_LDS ? 1 : NP][Q_LDS ? 1 : KB];
     float unscale;
     {
-        const float *qr = a.q + (int64_t)b * a.q_stride + (int64_t)(h0 + (i < cols ? i : 0)) * D;
+        const int col = i < cols ? i : 0;
+        const float *qr = a.q + (int64_t)row_of(col) * a.q_stride + (int64_t)head_of(col) * D;
         float v[KB][8], amax = 0.f;
         const float f = i < cols ? a.scale * LOG2E : 0.f;
 #pragma unroll
@@ -407,13 +438,14 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn(AttnArgs a)
                     sc[4 * tt + r] = acc[r] * unscale;
             }
             const uint64_t any_bad = __ballot(x.bad);
-            const bool masked = any_bad != 0 || t + 32 > t_end;
-            if (masked) {
+            bool odd = false;
+            uint16_t *sv = reinterpret_cast<uint16_t *>(&s_o[wave][0][0]);      // [D][32]
+            if (any_bad != 0 || t + 32 > see_all) {
                 if (any_bad && lane == 0)
                     atomicOr(c.err, 1u);
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    sc[e] = x.bad || t + 8 * g + e >= t_end ? -INFINITY : sc[e];
+                    sc[e] = x.bad || t + 8 * g + e >= see ? -INFINITY : sc[e];
                 // what a masked position holds must not reach the product: 0 x NaN is NaN
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
@@ -422,6 +454,31 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn(AttnArgs a)
 #pragma unroll
                     for (int d = 0; d < DT; ++d)
                         x.v[d][w] &= keep;
+                }
+                // positions that some columns see: infinities and NaN leave the product and are
+                // added one by one to the columns that see them
+                if constexpr (ROWS) {
+                    uint32_t nf = 0;
+#pragma unroll
+                    for (int d = 0; d < DT; ++d)
+#pragma unroll
+                        for (int w = 0; w < 4; ++w)
+                            nf |= nonfinite2<T>(x.v[d][w]);
+                    odd = __any(nf != 0);
+                    if (odd) {
+#pragma unroll
+                        for (int d = 0; d < DT; ++d) {
+                            *reinterpret_cast<au4 *>(sv + (16 * d + i) * 32 + 8 * g) = x.v[d];
+#pragma unroll
+                            for (int w = 0; w < 4; ++w) {
+                                const uint32_t f = nonfinite2<T>(x.v[d][w]);
+                                x.v[d][w] &= ~((f - (f >> 15)) | f);
+                            }
+                        }
+                        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+                        __builtin_amdgcn_wave_barrier();
+                        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+                    }
                 }
             }
             float mx = fmaxf(fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3])),
@@ -450,6 +507,20 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn(AttnArgs a)
 #pragma unroll
                 for (int d = 0; d < DT; ++d)
                     o[d] = mm16<T>(x.v[d], pf[y], o[d]);
+            if (ROWS && odd) {
+#pragma unroll 1
+                for (int y = 0; y < 32 && t + y < t_end; ++y)
+#pragma unroll
+                    for (int d = 0; d < DT; ++d)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const uint32_t v = sv[(16 * d + 4 * g + r) * 32 + y];
+                            if (t + y < see && nonfinite2<T>(v))
+                                o[d][r] += low_of<T>(v);
+                            if (r == 3)
+                                __builtin_amdgcn_sched_barrier(0);
+                        }
+            }
         };
         Buf A, B;
         Ids i0 = ids_of(0), i1 = ids_of(1);
@@ -475,7 +546,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn(AttnArgs a)
     for (int d = 0; d < DT; ++d)
         *reinterpret_cast<af4 *>(&s_o[wave][i][16 * d + 4 * g]) = o[d];
     __syncthreads();
-    const int width = min(16, a.group), items = cols * (D / 4);
+    const int width = ROWS ? 16 : min(16, a.group), items = cols * (D / 4);
     const uint32_t stride = (uint32_t)attn_part_floats(width, D);
     const __amdgpu_buffer_rsrc_t part = __builtin_amdgcn_make_buffer_rsrc(
         a.part + (int64_t)p.slot0 * stride, 0, n_chunk * stride * 4, 0x00020000);
@@ -484,7 +555,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn(AttnArgs a)
         const int col = e / (D / 4), d4 = e % (D / 4);
         if (at < 0) {
             const float inv = mm == -INFINITY ? 0.f : 1.0f / ls;
-            *reinterpret_cast<af4 *>(a.o + ((int64_t)b * a.nq + h0 + col) * D + 4 * d4) = sum * inv;
+            *reinterpret_cast<af4 *>(a.o + ((int64_t)row_of(col) * a.nq + head_of(col)) * D + 4 * d4) = sum * inv;
             return;
         }
         put4(part, at * stride + col * D + 4 * d4, sum);
@@ -572,13 +643,12 @@ int launch_kv_append(int kv_type, const AppendArgs &a, void *stream)
     return (int)hipGetLastError();
 }
 
-int launch_attn(int kv_type, const AttnArgs &a, void *stream)
+template <bool ROWS>
+static int launch_k_attn(int kv_type, const AttnArgs &a, int64_t pairs, void *stream)
 {
-    hipStream_t s = static_cast<hipStream_t>(stream);
-    const int pairs = a.c.nkv * ((a.group + 15) / 16), all = a.c.n_seq * pairs;
-    const int slots = attn_slots(a.c.hd), grid = all > slots ? all : slots;
+    const int slots = attn_slots(a.c.hd);
     void (*k)(AttnArgs) = nullptr;
-#define QG_ATTN_D(DD) k = kv_type == KV_F16 ? k_attn<KV_F16, DD> : k_attn<KV_BF16, DD>
+#define QG_ATTN_D(DD) k = kv_type == KV_F16 ? k_attn<KV_F16, DD, ROWS> : k_attn<KV_BF16, DD, ROWS>
     switch (a.c.hd) {
     case 64: QG_ATTN_D(64); break;
     case 96: QG_ATTN_D(96); break;
@@ -587,8 +657,19 @@ int launch_attn(int kv_type, const AttnArgs &a, void *stream)
     default: QG_ATTN_D(256); break;
     }
 #undef QG_ATTN_D
-    hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(k, dim3((unsigned)(pairs > slots ? pairs : slots)), dim3(256), 0,
+                       static_cast<hipStream_t>(stream), a);
     return (int)hipGetLastError();
+}
+
+int launch_attn(int kv_type, const AttnArgs &a, void *stream)
+{
+    return launch_k_attn<false>(kv_type, a, (int64_t)a.c.n_seq * a.c.nkv * ((a.group + 15) / 16), stream);
+}
+
+int launch_attn_rows(int kv_type, const AttnArgs &a, void *stream)
+{
+    return launch_k_attn<true>(kv_type, a, a.c.nkv * (a.c.n_rows * a.group / 16 + a.c.n_seq), stream);
 }
 
 }  // namespace qg

@@ -43,14 +43,6 @@ __device__ __forceinline__ void pt_barrier()
     asm volatile("" ::: "memory");
 }
 
-// Bits 15 and 31 set where a half of the pair is an infinity or NaN.
-template <int T>
-__device__ __forceinline__ uint32_t nonfinite2(uint32_t v)
-{
-    return T == KV_F16 ? ((v & 0x7C007C00u) + 0x04000400u) & 0x80008000u
-                       : ((v & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
-}
-
 struct TilePlace {
     int b;                 // sequence
     int row0, rows;        // first packed row of the sequence, its new rows
@@ -540,6 +532,19 @@ PromptPlan plan_prompt(int64_t n_rows, int n_seq, int nkv, int group, int64_t po
 
 int launch_attn_prompt(int kv_type, const AttnArgs &a, void *stream)
 {
+    // Few columns (rows times query heads of a KV head): the one-token kernel takes 16 at a time,
+    // with the positions spread over all waves, where this one's 128-row tiles would mostly be empty
+    // or too few.  It reads the cache once per 16 columns, so it takes the call when all its
+    // workgroups are resident at once and the columns of a sequence are at most 384 on average or
+    // the table is short (128-row tiles -> 16 columns, us: 16 sequences x 4 rows x 4000 positions, 32 /
+    // 8 heads of 128, 64.7 -> 39.3; one of 32 rows x 20000, 12 / 2 heads, 36.3 -> 34.1; of 128 rows
+    // 57.9 -> 84.1; three of 31 rows alone 9.6 -> 6.8; one of 128 rows alone, 32 / 8 heads, 11.4 -> 8.4;
+    // 16 of 32 rows alone, twice the resident workgroups, 11.0 -> 19.9).
+    const int64_t pairs = a.c.nkv * (a.c.n_rows * a.group / 16 + a.c.n_seq);
+    const int64_t table = (int64_t)a.c.max_pages << a.c.ps_log2;
+    if (pairs <= attn_slots(a.c.hd) &&
+        (a.c.n_rows * a.group <= 384 * (int64_t)a.c.n_seq || table <= 1024))
+        return launch_attn_rows(kv_type, a, stream);
     hipStream_t s = static_cast<hipStream_t>(stream);
     const PromptPlan p = plan_prompt(a.c.n_rows, a.c.n_seq, a.c.nkv, a.group,
                                      (int64_t)a.c.max_pages << a.c.ps_log2);

@@ -317,11 +317,13 @@ int qgemv_attn(int kv_type, const void *k_pages, const void *v_pages, int64_t n_
 /* Causal attention of packed sequences of new rows (a prompt, a prefill chunk behind cached
  * positions, or several tokens to verify): row r at position t attends to the positions <= t of
  * its sequence.  q as in qgemv_attn, one row per new row; o is f32 [n_rows][n_q_heads *
- * head_dim], rows outside every sequence left as they were.  Few rows over a long cache are split
- * over its length and joined by a second launch.
+ * head_dim], rows outside every sequence left as they were.  n_rows * n_q_heads <= 2^30.  Few rows
+ * over a long cache are split over its length and joined, within the launch or by a second one.
  * Accuracy of both: scores, softmax statistics and sums in f32; q and the probabilities enter the
- * f16 / bf16 products as the sum of two halves of that type (2^-17 relative for bf16, 2^-21 for
- * f16), K and V exactly as stored. */
+ * products with f16 K and V as the sum of two f16 values (22 bits), with bf16 as that of three bf16
+ * values (24 bits); K and V exactly as stored.  An infinity or NaN in K or V makes the outputs of
+ * the rows that see its position non-finite (NaN also where the definition gives an infinity) and
+ * touches no other row. */
 int qgemv_attn_prompt(int kv_type, const void *k_pages, const void *v_pages, int64_t n_pages,
                       int page_size, int64_t page_stride, int n_kv_heads, int head_dim,
                       const int32_t *table, int max_pages, const int32_t *q_start,
