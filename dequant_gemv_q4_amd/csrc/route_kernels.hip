@@ -4,10 +4,16 @@
 // with the largest sum of their best group_top c stay; the topk largest c among them, ties to the
 // lower index; weights s (renormalised) * scale.
 //
-// One wave per row, expert e = lane + 64 i in register i.  Scores and choices are f64: two choices
-// that differ by less than an f32 rounding (a bias near the scores' own spacing) must come out in
-// their true order, and gfx950 runs f64 at the f32 rate.  A choice is compared as the unsigned
-// image of its bits (order-preserving), 0 meaning "not selectable".
+// One wave per row, lane l holding experts NI l .. NI l + NI - 1, so that the first of several lanes
+// with equal choices has the lowest expert and a group is a run of lanes.  Scores and choices are
+// f64: two choices that differ by less than an f32 rounding (a bias near the scores' own spacing)
+// must come out in their true order, and gfx950 runs f64 at the f32 rate.  A choice is compared as
+// the unsigned image of its bits (order-preserving), 0 meaning "not selectable".  A round of the
+// selection is a maximum over the wave of the images' upper halves (lane shifts in the VALU) and a
+// vote; the lower halves only decide when several lanes share the upper one.
+//
+// Bound by VALU issue (the exponentials, then the rounds): 8000 x 256 sigmoid, 8 groups, top 8 of 4
+// groups: 31.1 us with shuffled 64-bit maxima and a serial scan of the groups, MEASURED now.
 #include <hip/hip_runtime.h>
 
 #include "attn_internal.h"
@@ -23,7 +29,67 @@ __device__ __forceinline__ uint64_t route_key(double c)
     return b >> 63 ? ~b : b | 0x8000000000000000ull;
 }
 
-// The wave's largest key and the lowest index holding it.
+// Lane shifts of the wave-wide reductions: after the six steps lane 63 has the result; a lane that
+// nothing is shifted into takes `none`.
+template <int CTRL, int ROWS, class V>
+__device__ __forceinline__ V dpp_or(V none, V v)
+{
+    return __builtin_bit_cast(V, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, none),
+                                                             __builtin_bit_cast(int, v), CTRL, ROWS, 0xF, false));
+}
+template <class V, class F>
+__device__ __forceinline__ V wave_reduce(V v, V none, F f)
+{
+    v = f(v, dpp_or<0x111, 0xF>(none, v));              // row_shr 1, 2, 4, 8
+    v = f(v, dpp_or<0x112, 0xF>(none, v));
+    v = f(v, dpp_or<0x114, 0xF>(none, v));
+    v = f(v, dpp_or<0x118, 0xF>(none, v));
+    v = f(v, dpp_or<0x142, 0xA>(none, v));              // row 0 -> 1, 2 -> 3
+    v = f(v, dpp_or<0x143, 0xC>(none, v));              // rows 0, 1 -> 2, 3
+    return __builtin_bit_cast(V, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v)
+{
+    return wave_reduce(v, 0u, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_add(double v)
+{
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = dpp_or<CTRL, ROWS>(0u, (uint32_t)b), hi = dpp_or<CTRL, ROWS>(0u, (uint32_t)(b >> 32));
+    return v + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double lane_double(double v, int lane)
+{
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)b, lane);
+    const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(b >> 32), lane);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double wave_sum(double v)
+{
+    v = dpp_add<0x111, 0xF>(v);
+    v = dpp_add<0x112, 0xF>(v);
+    v = dpp_add<0x114, 0xF>(v);
+    v = dpp_add<0x118, 0xF>(v);
+    v = dpp_add<0x142, 0xA>(v);
+    v = dpp_add<0x143, 0xC>(v);
+    return lane_double(v, 63);
+}
+
+// First lane that holds the wave's largest key.
+__device__ __forceinline__ int best_lane(uint64_t key)
+{
+    const uint32_t hi = (uint32_t)(key >> 32), lo = (uint32_t)key, top = wave_max(hi);
+    uint64_t who = __ballot(hi == top);
+    if (__popcll(who) > 1) {
+        const uint32_t low = wave_max(hi == top ? lo : 0u);
+        who = __ballot(hi == top && lo == low);
+    }
+    return __ffsll((unsigned long long)who) - 1;
+}
+
+// The wave's largest key and the lowest index holding it (any layout of the indices).
 __device__ __forceinline__ void wave_best(uint64_t &key, int &idx)
 {
 #pragma unroll
@@ -37,128 +103,159 @@ __device__ __forceinline__ void wave_best(uint64_t &key, int &idx)
     }
 }
 
+// Best two of a run of values.
+struct Top2 {
+    double a, b;
+    __device__ __forceinline__ void add(double c)
+    {
+        c = c == c ? c : -INFINITY;
+        b = fmax(b, fmin(a, c));
+        a = fmax(a, c);
+    }
+    __device__ __forceinline__ void merge(double a2, double b2)
+    {
+        b = fmax(fmin(a, a2), fmax(b, b2));
+        a = fmax(a, a2);
+    }
+};
+
 template <int NI>
 __global__ __launch_bounds__(256) void k_route(RouteArgs a)
 {
-    __shared__ double sc[4][64 * NI];
-    __shared__ uint8_t keep[4][64 * NI];
+    __shared__ double s_c[4][64 * NI];
+    __shared__ uint8_t s_keep[4][64 * NI];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const int64_t r = (int64_t)blockIdx.x * 4 + wave;
     if (r >= a.n_rows)
         return;                                   // no workgroup barrier below
     const float *zr = a.z + r * a.n_exp;
+    const int e0 = NI * lane;
     float z[NI];
-    double s[NI];
-    float m = -INFINITY;
+    double s[NI], c[NI];
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-        const int e = lane + 64 * i;
-        z[i] = e < a.n_exp ? zr[e] : -INFINITY;
-        m = fmaxf(m, z[i]);
-    }
+    for (int i = 0; i < NI; ++i)
+        z[i] = e0 + i < a.n_exp ? zr[e0 + i] : -INFINITY;
     if (a.sigmoid) {
 #pragma unroll
         for (int i = 0; i < NI; ++i)
             s[i] = 1.0 / (1.0 + exp(-(double)z[i]));
     } else {
+        float m = -INFINITY;
 #pragma unroll
-        for (int x = 32; x; x >>= 1)
-            m = fmaxf(m, __shfl_xor(m, x));
+        for (int i = 0; i < NI; ++i)
+            m = fmaxf(m, z[i]);
+        m = wave_reduce(m, -INFINITY, [](float x, float y) { return fmaxf(x, y); });
         double sum = 0.0;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            s[i] = lane + 64 * i < a.n_exp ? exp((double)z[i] - (double)m) : 0.0;
+            s[i] = e0 + i < a.n_exp ? exp((double)z[i] - (double)m) : 0.0;
             sum += s[i];
         }
-#pragma unroll
-        for (int x = 32; x; x >>= 1)
-            sum += __shfl_xor(sum, x);
+        const double inv = 1.0 / wave_sum(sum);
 #pragma unroll
         for (int i = 0; i < NI; ++i)
-            s[i] /= sum;
+            s[i] *= inv;
+    }
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+        c[i] = a.bias && e0 + i < a.n_exp ? s[i] + (double)a.bias[e0 + i] : s[i];
+
+    uint32_t keep = ~0u;                          // bit i: expert e0 + i is in a group that stays
+    if (a.n_group > 1) {
+        const int size = a.n_exp / a.n_group, run = size / NI;
+        if (size % NI == 0 && (run & (run - 1)) == 0) {
+            // a group is a run of 2^k lanes
+            Top2 t = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+                t.add(c[i]);
+            for (int x = 1; x < run; x <<= 1)
+                t.merge(__shfl_xor(t.a, x), __shfl_xor(t.b, x));
+            const int g = lane / run;
+            uint64_t gk = g < a.n_group ? route_key(a.group_top == 2 ? t.a + t.b : t.a) : 0;
+            keep = 0;
+            for (int x = 0; x < a.topk_group; ++x)
+                if (best_lane(gk) / run == g) {
+                    gk = 0;
+                    keep = ~0u;
+                }
+        } else {
+            // any other size: the choices in LDS, a lane per group (groups lane, lane + 64, ...)
+            auto wave_sync = []() {
+                __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+                __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+            };
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+                s_c[wave][e0 + i] = c[i];
+            wave_sync();
+            uint64_t gk[NI];
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const int g = lane + 64 * i;
+                gk[i] = 0;
+                s_keep[wave][g] = 0;
+                if (g < a.n_group) {
+                    Top2 t = {-INFINITY, -INFINITY};
+                    for (int j = 0; j < size; ++j)
+                        t.add(s_c[wave][g * size + j]);
+                    gk[i] = route_key(a.group_top == 2 ? t.a + t.b : t.a);
+                }
+            }
+            for (int x = 0; x < a.topk_group; ++x) {
+                uint64_t k = 0;
+                int idx = 0x7fffffff;
+#pragma unroll
+                for (int i = 0; i < NI; ++i)
+                    if (gk[i] > k) {
+                        k = gk[i];
+                        idx = lane + 64 * i;
+                    }
+                wave_best(k, idx);
+#pragma unroll
+                for (int i = 0; i < NI; ++i)
+                    if (idx == lane + 64 * i) {
+                        gk[i] = 0;
+                        s_keep[wave][idx] = 1;
+                    }
+            }
+            wave_sync();
+            keep = 0;
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+                if (e0 + i < a.n_exp && s_keep[wave][(e0 + i) / size])
+                    keep |= 1u << i;
+        }
     }
     uint64_t key[NI];
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-        const int e = lane + 64 * i;
-        const double c = a.bias && e < a.n_exp ? s[i] + (double)a.bias[e] : s[i];
-        key[i] = e < a.n_exp ? route_key(c) : 0;
-        sc[wave][e] = c;
-    }
-    auto wave_sync = []() {
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-    };
-    if (a.n_group > 1) {
-        wave_sync();
-        const int size = a.n_exp / a.n_group;
-        uint64_t gk[NI];
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const int g = lane + 64 * i;
-            gk[i] = 0;
-            keep[wave][g] = 0;
-            if (g < a.n_group) {
-                double b1 = -INFINITY, b2 = -INFINITY;
-                for (int j = 0; j < size; ++j) {
-                    double c = sc[wave][g * size + j];
-                    c = c == c ? c : -INFINITY;
-                    b2 = fmax(b2, fmin(b1, c));
-                    b1 = fmax(b1, c);
-                }
-                gk[i] = route_key(a.group_top == 2 ? b1 + b2 : b1);
-            }
-        }
-        for (int t = 0; t < a.topk_group; ++t) {
-            uint64_t k = 0;
-            int idx = 0x7fffffff;
-#pragma unroll
-            for (int i = 0; i < NI; ++i)
-                if (gk[i] > k) {
-                    k = gk[i];
-                    idx = lane + 64 * i;
-                }
-            wave_best(k, idx);
-#pragma unroll
-            for (int i = 0; i < NI; ++i)
-                if (idx == lane + 64 * i) {
-                    gk[i] = 0;
-                    keep[wave][idx] = 1;
-                }
-        }
-        wave_sync();
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const int e = lane + 64 * i;
-            if (e < a.n_exp && !keep[wave][e / size])
-                key[i] = 0;
-        }
-    }
+    for (int i = 0; i < NI; ++i)
+        key[i] = e0 + i < a.n_exp && (keep >> i & 1) ? route_key(c[i]) : 0;
+
     double total = 0.0, mine = 0.0;
     int my_id = 0;
     for (int t = 0; t < a.topk; ++t) {
-        uint64_t k = 0;
-        int idx = 0x7fffffff;
-        double sv = 0.0;
+        uint64_t k = key[0];
+        double sk = s[0];
+        int at = 0;
 #pragma unroll
-        for (int i = 0; i < NI; ++i)
+        for (int i = 1; i < NI; ++i)
             if (key[i] > k) {
                 k = key[i];
-                idx = lane + 64 * i;
+                sk = s[i];
+                at = i;
             }
-        wave_best(k, idx);
+        const int w = best_lane(k);
+        const int wi = __builtin_amdgcn_readlane(at, w);
+        const double sv = lane_double(sk, w);
 #pragma unroll
         for (int i = 0; i < NI; ++i)
-            if (idx == lane + 64 * i) {
-                key[i] = 0;
-                sv = s[i];
-            }
-        sv = __shfl(sv, idx & 63);
+            key[i] = lane == w && i == wi ? 0 : key[i];
         total += sv;
         if (lane == t) {
             mine = sv;
-            my_id = idx;
+            my_id = NI * w + wi;
         }
     }
     if (lane < a.topk) {
