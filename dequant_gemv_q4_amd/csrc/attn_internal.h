@@ -60,6 +60,7 @@ struct RouteArgs {
     float *wts;
     int64_t n_rows;
     int n_exp, sigmoid, n_group, group_top, topk_group, topk, renorm;
+    int run_log2;               // set by the launcher
     float scale;
 };
 

@@ -8,12 +8,17 @@
 // with equal choices has the lowest expert and a group is a run of lanes.  Scores and choices are
 // f64: two choices that differ by less than an f32 rounding (a bias near the scores' own spacing)
 // must come out in their true order, and gfx950 runs f64 at the f32 rate.  A choice is compared as
-// the unsigned image of its bits (order-preserving), 0 meaning "not selectable".  A round of the
-// selection is a maximum over the wave of the images' upper halves (lane shifts in the VALU) and a
-// vote; the lower halves only decide when several lanes share the upper one.
+// the unsigned image of its bits (order-preserving), 0 meaning "not selectable".
 //
-// Bound by VALU issue (the exponentials, then the rounds): 8000 x 256 sigmoid, 8 groups, top 8 of 4
-// groups: 31.1 us with shuffled 64-bit maxima and a serial scan of the groups, MEASURED now.
+// The rounds of the selection first compare only the upper 32 bits of the images, with the lane's
+// slot in the lowest of them: a round is a maximum over the wave (lane shifts in the VALU) and a
+// vote.  Two choices next to each other in the result that share the compared bits (2^-16 of their
+// value or nearer) may be in the wrong order; then, for the whole wave, the selection is done anew
+// on all 64 bits.
+//
+// Bound by VALU issue, not by the 8.7 MB it moves: 8000 x 256, sigmoid, 8 groups, top 8 of 4 groups,
+// takes 31.1 us with shuffled 64-bit maxima and a serial scan of the groups, 15.2 us with lane shifts
+// and 64-bit rounds, MEASURED us as it is.
 #include <hip/hip_runtime.h>
 
 #include "attn_internal.h"
@@ -103,19 +108,32 @@ __device__ __forceinline__ void wave_best(uint64_t &key, int &idx)
     }
 }
 
+// Maximum and minimum of values that are no NaN, in one instruction each (fmax would first quieten
+// its operands).
+__device__ __forceinline__ double max64(double a, double b)
+{
+    double r;
+    asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+}
+__device__ __forceinline__ double min64(double a, double b)
+{
+    double r;
+    asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+}
 // Best two of a run of values.
 struct Top2 {
     double a, b;
     __device__ __forceinline__ void add(double c)
     {
-        c = c == c ? c : -INFINITY;
-        b = fmax(b, fmin(a, c));
-        a = fmax(a, c);
+        b = max64(b, min64(a, c));
+        a = max64(a, c);
     }
     __device__ __forceinline__ void merge(double a2, double b2)
     {
-        b = fmax(fmin(a, a2), fmax(b, b2));
-        a = fmax(a, a2);
+        b = max64(min64(a, a2), max64(b, b2));
+        a = max64(a, a2);
     }
 };
 
@@ -157,30 +175,32 @@ __global__ __launch_bounds__(256) void k_route(RouteArgs a)
             s[i] *= inv;
     }
 #pragma unroll
-    for (int i = 0; i < NI; ++i)
+    for (int i = 0; i < NI; ++i) {
         c[i] = a.bias && e0 + i < a.n_exp ? s[i] + (double)a.bias[e0 + i] : s[i];
+        c[i] = c[i] == c[i] ? c[i] : -INFINITY;
+    }
 
     uint32_t keep = ~0u;                          // bit i: expert e0 + i is in a group that stays
     if (a.n_group > 1) {
-        const int size = a.n_exp / a.n_group, run = size / NI;
-        if (size % NI == 0 && (run & (run - 1)) == 0) {
+        if (a.run_log2 >= 0) {
             // a group is a run of 2^k lanes
             Top2 t = {-INFINITY, -INFINITY};
 #pragma unroll
             for (int i = 0; i < NI; ++i)
                 t.add(c[i]);
-            for (int x = 1; x < run; x <<= 1)
-                t.merge(__shfl_xor(t.a, x), __shfl_xor(t.b, x));
-            const int g = lane / run;
+            for (int x = 0; x < a.run_log2; ++x)
+                t.merge(__shfl_xor(t.a, 1 << x), __shfl_xor(t.b, 1 << x));
+            const int g = lane >> a.run_log2;
             uint64_t gk = g < a.n_group ? route_key(a.group_top == 2 ? t.a + t.b : t.a) : 0;
             keep = 0;
             for (int x = 0; x < a.topk_group; ++x)
-                if (best_lane(gk) / run == g) {
+                if (best_lane(gk) >> a.run_log2 == g) {
                     gk = 0;
                     keep = ~0u;
                 }
         } else {
             // any other size: the choices in LDS, a lane per group (groups lane, lane + 64, ...)
+            const int size = a.n_exp / a.n_group;
             auto wave_sync = []() {
                 __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
                 __builtin_amdgcn_wave_barrier();
@@ -233,47 +253,83 @@ __global__ __launch_bounds__(256) void k_route(RouteArgs a)
     for (int i = 0; i < NI; ++i)
         key[i] = e0 + i < a.n_exp && (keep >> i & 1) ? route_key(c[i]) : 0;
 
-    double total = 0.0, mine = 0.0;
-    int my_id = 0;
-    for (int t = 0; t < a.topk; ++t) {
-        uint64_t k = key[0];
-        double sk = s[0];
-        int at = 0;
-#pragma unroll
-        for (int i = 1; i < NI; ++i)
-            if (key[i] > k) {
-                k = key[i];
-                sk = s[i];
-                at = i;
-            }
-        const int w = best_lane(k);
-        const int wi = __builtin_amdgcn_readlane(at, w);
-        const double sv = lane_double(sk, w);
+    // lane t's result: slot my_slot of lane my_lane
+    int my_lane = 0, my_slot = 0;
+    bool near = false;
+    {
+        uint32_t k[NI], last = 0;
 #pragma unroll
         for (int i = 0; i < NI; ++i)
-            key[i] = lane == w && i == wi ? 0 : key[i];
-        total += sv;
-        if (lane == t) {
-            mine = sv;
-            my_id = NI * w + wi;
+            k[i] = key[i] ? ((uint32_t)(key[i] >> 32) & ~(uint32_t)(NI - 1)) | (NI - 1 - i) : 0u;
+        for (int t = 0; t <= a.topk; ++t) {       // one more than needed: the best that is left
+            uint32_t best = k[0];
+#pragma unroll
+            for (int i = 1; i < NI; ++i)
+                best = best > k[i] ? best : k[i];
+            const uint32_t top = wave_max(best);
+            near |= t > 0 && top != 0 && (top ^ last) < (uint32_t)NI;
+            last = top;
+            const int w = __ffsll((unsigned long long)__ballot(best == top)) - 1;
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+                k[i] = lane == w && k[i] == top ? 0u : k[i];
+            if (lane == t) {
+                my_lane = w;
+                my_slot = NI - 1 - (int)(top & (NI - 1));
+            }
         }
     }
+    if (near) {
+        for (int t = 0; t < a.topk; ++t) {
+            uint64_t k = key[0];
+            int at = 0;
+#pragma unroll
+            for (int i = 1; i < NI; ++i)
+                if (key[i] > k) {
+                    k = key[i];
+                    at = i;
+                }
+            const int w = best_lane(k);
+            const int wi = __builtin_amdgcn_readlane(at, w);
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+                key[i] = lane == w && i == wi ? 0 : key[i];
+            if (lane == t) {
+                my_lane = w;
+                my_slot = wi;
+            }
+        }
+    }
+    double mine = 0.0;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        const double v = __shfl(s[i], my_lane);
+        mine = i == my_slot ? v : mine;
+    }
+    mine = lane < a.topk ? mine : 0.0;
+    if (a.renorm) {
+        const double total = wave_sum(mine);
+        mine = total == 0.0 ? 0.0 : mine / total;
+    }
     if (lane < a.topk) {
-        if (a.renorm)
-            mine = total == 0.0 ? 0.0 : mine / total;
-        a.ids[r * a.topk + lane] = my_id;
+        a.ids[r * a.topk + lane] = NI * my_lane + my_slot;
         a.wts[r * a.topk + lane] = (float)(mine * (double)a.scale);
     }
 }
 
-int launch_route(const RouteArgs &a, void *stream)
+int launch_route(const RouteArgs &args, void *stream)
 {
-    hipStream_t s = static_cast<hipStream_t>(stream);
-    const dim3 grid((unsigned)((a.n_rows + 3) / 4));
-    const int ni = (a.n_exp + 63) / 64;
-    auto k = ni <= 1 ? k_route<1> : ni <= 2 ? k_route<2> : ni <= 4 ? k_route<4> : ni <= 8 ? k_route<8>
-                                                                                      : k_route<16>;
-    hipLaunchKernelGGL(k, grid, dim3(256), 0, s, a);
+    RouteArgs a = args;
+    const int lanes = (a.n_exp + 63) / 64;
+    const int ni = lanes <= 1 ? 1 : lanes <= 2 ? 2 : lanes <= 4 ? 4 : lanes <= 8 ? 8 : 16;
+    const int size = a.n_exp / a.n_group, run = size / ni;
+    a.run_log2 = -1;                              // log2 of the lanes of a group, if it is a run of 2^k
+    if (size % ni == 0 && (run & (run - 1)) == 0)
+        for (a.run_log2 = 0; 1 << a.run_log2 < run;)
+            ++a.run_log2;
+    void (*k)(RouteArgs) = ni == 1 ? k_route<1> : ni == 2 ? k_route<2> : ni == 4 ? k_route<4> : ni == 8 ? k_route<8>
+                                                                                                : k_route<16>;
+    hipLaunchKernelGGL(k, dim3((unsigned)((a.n_rows + 3) / 4)), dim3(256), 0, static_cast<hipStream_t>(stream), a);
     return (int)hipGetLastError();
 }
 
