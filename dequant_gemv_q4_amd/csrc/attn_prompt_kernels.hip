@@ -14,8 +14,10 @@
 // ahead, two buffers, one barrier a step.  Wave w copies the step's 16-position block w, which lies
 // in one page, so page numbers and bases are scalars.  K: [position][channel], V: [block][channel]
 // [16 positions].  The copies land in lane order, so the 16-byte pieces of a K row (of a V channel's
-// two) are permuted at the source instead, piece ^ key of the row: eight lanes that read eight rows
-// then use different banks.
+// two) are permuted at the source instead, piece ^ key of the row: a 16-byte LDS read serves 16 lanes
+// (0-3, 12-15, 20-23, 24-27 and so on) from 64 banks at a time, and with these keys their 16 rows lie in
+// different banks: SQ_LDS_BANK_CONFLICT 0, against four cycles a read with keys made for eight lanes
+// in a row.
 #include <hip/hip_runtime.h>
 
 #include "attn_common.h"
@@ -113,7 +115,8 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
     constexpr int PR = D / 8;                          // 16-byte pieces of a K row
     // 32-position tiles of scores held at a time: three query pieces leave registers for one
     constexpr int NT = NP * D > 384 ? 1 : 2;
-    constexpr int KEYM = D % 64 == 0 ? 7 : 3;          // bits of the piece number that the key takes
+    // pieces that the key permutes, in pairs (heads of 256 have no registers for eight offsets)
+    constexpr int KO = D == 96 ? 2 : D == 128 ? 8 : 4;
     constexpr int HALF = PT_STEP * D * 2;              // bytes of a K (or V) buffer
     constexpr int PASS = HALF / 4096;                  // copies of a wave for either
     __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * HALF];   // K0 V0 K1 V1
@@ -178,14 +181,14 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
     const int last_entry = p.hi > 0 ? (p.hi - 1) >> c.ps_log2 : 0;
     const int64_t head_off = (int64_t)hkv * D << c.ps_log2;
     const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
-    auto key = [](int row) { return ((row & 3) | ((row >> 1) & 4)) & KEYM; };
+    auto key = [](int row) { return KO == 8 ? row & 15 : KO == 4 ? (row >> 1) & 7 : (row >> 2) & 3; };
     uint32_t ksrc[PASS];
 #pragma unroll
     for (int x = 0; x < PASS; ++x) {
         const int idx = 64 * x + lane, row = idx / PR;
         ksrc[x] = (uint32_t)(row * D + 8 * ((idx % PR) ^ key(row))) * 2;
     }
-    const uint32_t vsrc = (uint32_t)(((lane >> 1) << c.ps_log2) + 8 * ((lane & 1) ^ ((lane >> 3) & 1))) * 2;
+    const uint32_t vsrc = (uint32_t)(((lane >> 1) << c.ps_log2) + 8 * ((lane & 1) ^ (lane >> 5))) * 2;
     // page number of 16-position block lane % 4 of a step
     auto ids_of = [&](int s) { return table[min((s * PT_STEP + 16 * (lane & 3)) >> c.ps_log2, last_entry)]; };
     auto issue = [&](int s, int buf, int ids) -> uint32_t {
@@ -207,11 +210,11 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
 
     // operand reads: K row of score row col, pieces 2 k + hf; V channel col of 32, piece hf of block k
     const int krow = 16 * (col >> 4) + 8 * ((col >> 2) & 1) + 4 * ((col >> 3) & 1) + (col & 3);
-    uint32_t koff[4];
+    uint32_t koff[KO];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < KO; ++j)
         koff[j] = (uint32_t)(krow * D * 2) + (uint32_t)(((2 * j + hf) ^ key(krow)) << 4);
-    const uint32_t voff = (uint32_t)(col * 32 + ((hf ^ ((col >> 2) & 1)) << 4));
+    const uint32_t voff = (uint32_t)(col * 32 + ((hf ^ (col >> 4)) << 4));
 
     af16 o[DT];
 #pragma unroll
@@ -236,7 +239,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
         auto read = [&](int k) {
 #pragma unroll
             for (int tt = 0; tt < NT; ++tt)
-                kf[k % (AHEAD + 1)][tt] = *reinterpret_cast<const au4 *>(kb + koff[k & 3] + (k >> 2) * 128 + tt * 64 * D);
+                kf[k % (AHEAD + 1)][tt] = *reinterpret_cast<const au4 *>(kb + koff[k % KO] + (k / KO) * (KO * 32) + tt * 64 * D);
         };
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k)
@@ -356,7 +359,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
                 for (int r = 0; r < 16; ++r) {
                     const int ch = 8 * (r >> 2) + 4 * hf + (r & 3);      // channel 32 d + ch
                     const uint16_t x = *reinterpret_cast<const uint16_t *>(
-                        vb + at + d * 1024 + ch * 32 + ((((t >> 3) & 1) ^ ((ch >> 2) & 1)) << 4));
+                        vb + at + d * 1024 + ch * 32 + ((((t >> 3) & 1) ^ (ch >> 4)) << 4));
                     if (t <= see && nonfinite2<T>(x))
                         o[d][r] += low_of<T>(x);
                     if (r % 8 == 7)
