@@ -3,7 +3,8 @@
 Every function has the name and argument order of its C entry point.  Array arguments may be
 torch tensors (their data pointer is passed; device tensors for the compute calls) or plain
 integer addresses.  ``stream`` defaults to torch's current HIP stream.  A non-zero status
-raises :class:`QgemvError`; nothing is ever computed on the host.
+raises :class:`QgemvError`; nothing is ever computed on the host.  The attention-side calls, which
+take several kinds of arrays, check the type, device and layout of the tensors they get (TypeError).
 """
 from __future__ import annotations
 
@@ -105,7 +106,7 @@ def _stream(s):
     if s is None:
         import torch
         # the raw handle: building a Stream object takes 2.7 us, this 0.2
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -116,7 +117,7 @@ def _nbytes(ws):
         return 0
     if isinstance(ws, int):
         raise TypeError("pass ws_bytes together with an integer workspace address")
-    return ws.numel() * ws.element_size()
+    return ws.nbytes
 
 
 def _check(fn, st):
@@ -246,35 +247,72 @@ def qgemv_attn_workspace_bytes(op: int, n_seq: int, n_q_heads: int, n_kv_heads: 
     return lib().qgemv_attn_workspace_bytes(op, n_seq, n_q_heads, n_kv_heads, head_dim)
 
 
+_types = None      # torch's int32, float32, and the cache types by kv_type; the current device's index
+
+
+def _torch_types():
+    global _types
+    if _types is None:
+        import torch
+        _types = (torch.int32, torch.float32, {F16: torch.float16, BF16: torch.bfloat16},
+                  torch._C._cuda_getDevice)
+    return _types
+
+
+def _t(a, dtype, dev, whole=True):
+    """Address of an array of the attention side.  A tensor has to be of the type that the entry
+    point reads, on the current device and, unless its rows have a stride argument, contiguous."""
+    if a is None or a.__class__ is int:
+        return a
+    if (dtype is not None and a.dtype is not dtype) or a.get_device() != dev or \
+            (whole and not a.is_contiguous()):
+        raise TypeError(f"expected a {'contiguous ' if whole else ''}{dtype or 'workspace'} tensor on cuda:{dev}, "
+                        f"got {a.dtype}, {a.device}, strides {a.stride()}")
+    return a.data_ptr()
+
+
 def qgemv_kv_append(kv_type, k_pages, v_pages, n_pages, page_size, page_stride, n_kv_heads,
                     head_dim, table, max_pages, q_start, kv_len, n_seq, k, v, kv_stride, n_rows, ws,
                     ws_bytes=None, stream=None):
-    _check("qgemv_kv_append",
-           lib().qgemv_kv_append(kv_type, _p(k_pages), _p(v_pages), n_pages, page_size, page_stride,
-                                 n_kv_heads, head_dim, _p(table), max_pages, _p(q_start),
-                                 _p(kv_len), n_seq, _p(k), _p(v), kv_stride, n_rows, _p(ws),
-                                 _nbytes(ws) if ws_bytes is None else ws_bytes, _stream(stream)))
+    i32, f32, kv, device = _torch_types()
+    d, c = device(), kv.get(kv_type)
+    st = lib().qgemv_kv_append(kv_type, _t(k_pages, c, d, False), _t(v_pages, c, d, False), n_pages,
+                               page_size, page_stride, n_kv_heads, head_dim, _t(table, i32, d),
+                               max_pages, _t(q_start, i32, d), _t(kv_len, i32, d), n_seq,
+                               _t(k, f32, d, False), _t(v, f32, d, False), kv_stride, n_rows,
+                               _t(ws, None, d), _nbytes(ws) if ws_bytes is None else ws_bytes,
+                               _stream(stream))
+    if st:
+        _check("qgemv_kv_append", st)
 
 
 def qgemv_attn(kv_type, k_pages, v_pages, n_pages, page_size, page_stride, n_kv_heads, head_dim,
                table, max_pages, kv_len, n_seq, q, q_stride, n_q_heads, scale, o, ws,
                ws_bytes=None, stream=None):
-    _check("qgemv_attn",
-           lib().qgemv_attn(kv_type, _p(k_pages), _p(v_pages), n_pages, page_size, page_stride,
-                            n_kv_heads, head_dim, _p(table), max_pages, _p(kv_len), n_seq, _p(q),
-                            q_stride, n_q_heads, scale, _p(o), _p(ws),
-                            _nbytes(ws) if ws_bytes is None else ws_bytes, _stream(stream)))
+    i32, f32, kv, device = _torch_types()
+    d, c = device(), kv.get(kv_type)
+    st = lib().qgemv_attn(kv_type, _t(k_pages, c, d, False), _t(v_pages, c, d, False), n_pages,
+                          page_size, page_stride, n_kv_heads, head_dim, _t(table, i32, d), max_pages,
+                          _t(kv_len, i32, d), n_seq, _t(q, f32, d, False), q_stride, n_q_heads, scale,
+                          _t(o, f32, d), _t(ws, None, d),
+                          _nbytes(ws) if ws_bytes is None else ws_bytes, _stream(stream))
+    if st:
+        _check("qgemv_attn", st)
 
 
 def qgemv_attn_prompt(kv_type, k_pages, v_pages, n_pages, page_size, page_stride, n_kv_heads,
                       head_dim, table, max_pages, q_start, kv_len, n_seq, q, q_stride, n_rows,
                       n_q_heads, scale, o, ws, ws_bytes=None, stream=None):
-    _check("qgemv_attn_prompt",
-           lib().qgemv_attn_prompt(kv_type, _p(k_pages), _p(v_pages), n_pages, page_size,
-                                   page_stride, n_kv_heads, head_dim, _p(table), max_pages,
-                                   _p(q_start), _p(kv_len), n_seq, _p(q), q_stride, n_rows,
-                                   n_q_heads, scale, _p(o), _p(ws),
-                                   _nbytes(ws) if ws_bytes is None else ws_bytes, _stream(stream)))
+    i32, f32, kv, device = _torch_types()
+    d, c = device(), kv.get(kv_type)
+    st = lib().qgemv_attn_prompt(kv_type, _t(k_pages, c, d, False), _t(v_pages, c, d, False), n_pages,
+                                 page_size, page_stride, n_kv_heads, head_dim, _t(table, i32, d),
+                                 max_pages, _t(q_start, i32, d), _t(kv_len, i32, d), n_seq,
+                                 _t(q, f32, d, False), q_stride, n_rows, n_q_heads, scale,
+                                 _t(o, f32, d), _t(ws, None, d),
+                                 _nbytes(ws) if ws_bytes is None else ws_bytes, _stream(stream))
+    if st:
+        _check("qgemv_attn_prompt", st)
 
 
 def qgemv_attn_error(ws, stream=None) -> int:
@@ -285,7 +323,10 @@ def qgemv_attn_error(ws, stream=None) -> int:
 
 def qgemv_route(logits, n_rows, n_exp, score, bias, n_group, group_top, topk_group, topk, renorm,
                 scale, ids, wts, stream=None):
-    _check("qgemv_route",
-           lib().qgemv_route(_p(logits), n_rows, n_exp, score, _p(bias), n_group, group_top,
-                             topk_group, topk, 1 if renorm else 0, scale, _p(ids), _p(wts),
-                             _stream(stream)))
+    i32, f32, _, device = _torch_types()
+    d = device()
+    st = lib().qgemv_route(_t(logits, f32, d), n_rows, n_exp, score, _t(bias, f32, d), n_group,
+                           group_top, topk_group, topk, 1 if renorm else 0, scale, _t(ids, i32, d),
+                           _t(wts, f32, d), _stream(stream))
+    if st:
+        _check("qgemv_route", st)

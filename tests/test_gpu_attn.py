@@ -604,3 +604,34 @@ def test_two_graphs_share_a_workspace():
         for g, o, ref, run in jobs:
             assert np.array_equal(host(o), ref), rep
         jobs[rep % 2][3]()
+
+
+def test_tensors_of_the_wrong_type_device_or_layout_are_refused():
+    rng = np.random.default_rng(26)
+    c, start, qkv, width, rows = _step(rng, q.F16, 4, 2, 64, 16, [(1, 30), (1, 7)])
+    ws = D.attn_workspace(q.OP_ATTN, 2, 4, 2, 64)
+    o = torch.empty((rows, 256), device="cuda")
+
+    def call(**kw):
+        a = dict(zip(("kv_type", "k", "v", "n_pages", "page", "stride", "nkv", "hd", "table", "max_pages"), c.args()))
+        a.update(kv_len=c.kv_len, n_seq=2, q=qkv, q_stride=width, nq=4, scale=0.1, o=o, ws=ws)
+        a.update(kw)
+        q.qgemv_attn(*a.values())
+
+    call()
+    wide = torch.zeros((2, c.max_pages + 3), dtype=torch.int32, device="cuda")
+    for kw in (dict(kv_len=c.kv_len.long()), dict(table=c.table.long()), dict(table=wide[:, :c.max_pages]),
+               dict(kv_len=c.kv_len.cpu()), dict(q=qkv.half()), dict(o=o.cpu()), dict(k=c.k.bfloat16()),
+               dict(kv_type=q.BF16), dict(ws=ws.cpu()), dict(o=torch.empty((rows, 512), device="cuda")[:, ::2])):
+        with pytest.raises(TypeError):
+            call(**kw)
+    z = torch.zeros((4, 8), device="cuda")
+    ids, w = torch.zeros((4, 2), dtype=torch.int32, device="cuda"), torch.zeros((4, 2), device="cuda")
+    q.qgemv_route(z, 4, 8, 0, None, 1, 1, 1, 2, True, 1.0, ids, w)
+    for args in ((z.double(), ids, w), (z, ids.long(), w), (z, ids, w.half()), (z.cpu(), ids, w)):
+        with pytest.raises(TypeError):
+            q.qgemv_route(args[0], 4, 8, 0, None, 1, 1, 1, 2, True, 1.0, args[1], args[2])
+    with pytest.raises(q.QgemvError):
+        q.qgemv_route(z, 4, 8, 0, None, 1, 1, 1, 9, True, 1.0, ids, w)
+    with pytest.raises(q.QgemvError):
+        call(ws=None)
