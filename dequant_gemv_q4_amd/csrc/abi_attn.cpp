@@ -32,6 +32,8 @@ static bool heads_ok(int nq, int nkv, int hd)
 // place for every operation (the counters are 0 between calls and must stay so when operations share
 // a workspace), then the partial results of a split.
 static constexpr int64_t WS_COUNT = 256, WS_PART = WS_COUNT + ATTN_MAX_SLOTS * 4;
+// qgemv_attn_prompt's part of it begins with its pair count and its split tiles (32 bytes each).
+static constexpr int64_t WS_SPLITS = 256 + PROMPT_SPLITS * 32;
 
 static int64_t ws_bytes_of(int op, int nq, int nkv, int hd)
 {
@@ -39,7 +41,7 @@ static int64_t ws_bytes_of(int op, int nq, int nkv, int hd)
     if (op == QG_OP_ATTN)
         return WS_PART + (attn_slots(hd) * attn_part_floats(group < 16 ? group : 16, hd) * 4 + 255) / 256 * 256;
     if (op == QG_OP_ATTN_PROMPT)
-        return WS_PART + (int64_t)PROMPT_SLOTS * 128 * (hd + 2) * 4;   // 128 rows a tile
+        return WS_PART + WS_SPLITS + (int64_t)prompt_slots(hd) * 128 * (hd + 2) * 4;   // 128 columns a tile
     return WS_PART;
 }
 
@@ -117,7 +119,7 @@ static int run_attn(bool prompt, int kv_type, const void *k_pages, const void *v
     if (q_stride < width || q_stride > ((int64_t)1 << 31) || n_rows * nq > (1 << 30) ||
         !isfinite(scale))
         return QG_ERR_SHAPE;
-    if (prompt && plan_prompt(n_rows, n_seq, nkv, nq / nkv, 0).tiles * nkv > 0x7fffffffLL)
+    if (prompt && plan_prompt(n_rows, n_seq, nkv, nq / nkv, hd, 0).pairs > 0x7fffffffLL)
         return QG_ERR_SHAPE;
     if (!al(q, 16) || !al(o, 16) || q_stride % 4)
         return QG_ERR_ALIGN;
@@ -138,7 +140,10 @@ static int run_attn(bool prompt, int kv_type, const void *k_pages, const void *v
         return QG_ERR_ALIAS;
     a.c.err = static_cast<unsigned int *>(ws);
     a.count = reinterpret_cast<unsigned int *>(static_cast<uint8_t *>(ws) + WS_COUNT);
-    a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + WS_PART);
+    uint8_t *part = static_cast<uint8_t *>(ws) + WS_PART;
+    a.pairs = reinterpret_cast<int *>(part);
+    a.splits = reinterpret_cast<PromptSplit *>(part + 256);
+    a.part = reinterpret_cast<float *>(prompt ? part + WS_SPLITS : part);
     a.q = q;
     a.q_stride = q_stride;
     a.o = o;

@@ -148,4 +148,161 @@ __device__ __forceinline__ uint32_t nonfinite2(uint32_t v)
 
 constexpr float LOG2E = 1.44269504088896340736f;
 
+// ------------------------------------------------------------- work of a call, from lengths on the device
+//
+// The new rows of a sequence times the query heads of a KV head are columns rho = token * group +
+// head; a workgroup takes COLS of them (a pair: sequence and KV head, tile of columns) against a
+// chunk of the sequence's positions.  The lengths are on the device, so every workgroup derives the
+// same plan from them: where there are fewer pairs than workgroup slots, the smallest chunk (whole
+// units of 2^UNIT_LOG2 positions, at least LEAST) for which the chunks of all pairs fit the slots; a
+// pair's chunks are equal to one unit.  Sequences of up to SOLO units are not split.  INDEX: the plan
+// also numbers the pairs.
+template <int COLS_, int UNIT_LOG2_, int LEAST_, int SOLO_, bool INDEX_>
+struct PlanOf {
+    static constexpr int COLS = COLS_, UNIT_LOG2 = UNIT_LOG2_, LEAST = LEAST_, SOLO = SOLO_;
+    static constexpr bool INDEX = INDEX_;
+    static __device__ __forceinline__ int units(int n) { return (n + (1 << UNIT_LOG2) - 1) >> UNIT_LOG2; }
+    // at least one, so that an empty sequence's rows are written
+    static __device__ __forceinline__ int chunks(int n, int u)
+    {
+        const int x = units(n);
+        return x <= u || x <= SOLO ? 1 : (x + u - 1) / u;
+    }
+};
+
+struct AttnPlan {
+    int b, pair, chunk, n_chunk;   // this workgroup's sequence, pair within it, chunk of its chunks
+    int slot0;                     // workgroup id of the pair's first chunk
+    int first_pair, pairs;         // pairs of earlier sequences (where INDEX), of all
+    int len;                       // the sequence's positions
+    int row0, rows;                // its new rows
+};
+
+// What the plan has to know of a sequence.
+struct AttnSeq {
+    int n, pairs, row0, rows;
+};
+
+// Positions of sequence b that have a place in its table.
+__device__ __forceinline__ int seq_len(const KvArgs &c, int b)
+{
+    const int n = c.kv_len[b], cap = c.max_pages << c.ps_log2;          // cap <= 2^24
+    if (n > cap)
+        atomicOr(c.err, 1u);
+    return n < 0 ? 0 : n < cap ? n : cap;
+}
+
+// First new row of sequence i, cut to the rows there are.
+__device__ __forceinline__ int row_start(const KvArgs &c, int i)
+{
+    const int64_t v = c.q_start[i];
+    return (int)(v < 0 ? 0 : v < c.n_rows ? v : c.n_rows);
+}
+
+// Inclusive sum over the lanes up to this one; lane 63 has the total.
+__device__ __forceinline__ int wave_scan(int v)
+{
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);      // row_shr 1, 2, 4, 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);     // row 0 -> 1, 2 -> 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);     // rows 0, 1 -> 2, 3
+    return v;
+}
+__device__ __forceinline__ int wave_sum(int v) { return __builtin_amdgcn_readlane(wave_scan(v), 63); }
+
+// The plan from the sequences `seq(b0)` of lanes b0 .. b0 + 63 of each round.
+template <class P, bool ROWS, class Seq>
+__device__ __forceinline__ bool attn_plan_of(const KvArgs &c, int n_seq, int group, int slots, int id, AttnPlan &p,
+                                             bool last_first, Seq seq)
+{
+    auto sum = [&](auto of) {
+        int v = 0;
+        for (int b0 = 0; b0 < n_seq; b0 += 64)
+            v += of(seq(b0));
+        return wave_sum(v);
+    };
+    int u = 0x3fffffff;
+    p.pairs = ROWS ? sum([](const AttnSeq &s) { return s.pairs; })
+                   : c.n_seq * c.nkv * ((group + P::COLS - 1) / P::COLS);
+    if (p.pairs < slots) {
+        // chunks <= units / u + 1 each, so u = units / (slots - pairs), over all pairs, is enough;
+        // units / slots is the least that could be
+        const int units = sum([](const AttnSeq &s) { return s.pairs * P::units(s.n); });
+        int lo = max((units + slots - 1) / slots, P::LEAST);
+        int hi = max((units + slots - p.pairs - 1) / (slots - p.pairs), lo);
+        while (lo < hi) {
+            const int mid = lo + (hi - lo) / 2;
+            if (sum([=](const AttnSeq &s) { return s.pairs * P::chunks(s.n, mid); }) <= slots)
+                hi = mid;
+            else
+                lo = mid + 1;
+        }
+        u = lo;
+    } else if (last_first)
+        id = p.pairs - 1 - id;
+    if (id < 0)
+        return false;
+    int base = 0, before = 0;
+    for (int b0 = 0; b0 < n_seq; b0 += 64) {
+        const AttnSeq s = seq(b0);
+        const int nc = P::chunks(s.n, u), end = base + wave_scan(nc * s.pairs);
+        const int pe = P::INDEX ? before + wave_scan(s.pairs) : 0;
+        const uint64_t in = __ballot(id < end);
+        if (in) {
+            const int l = __ffsll((unsigned long long)in) - 1;
+            p.b = b0 + l;
+            p.n_chunk = __builtin_amdgcn_readlane(nc, l);
+            p.len = __builtin_amdgcn_readlane(s.n, l);
+            p.slot0 = __builtin_amdgcn_readlane(end - nc * s.pairs, l);
+            p.first_pair = P::INDEX ? __builtin_amdgcn_readlane(pe - s.pairs, l) : 0;
+            p.row0 = ROWS ? __builtin_amdgcn_readlane(s.row0, l) : p.b;
+            p.rows = ROWS ? __builtin_amdgcn_readlane(s.rows, l) : 1;
+            p.pair = (id - p.slot0) / p.n_chunk;
+            p.slot0 += p.pair * p.n_chunk;
+            p.chunk = id - p.slot0;
+            return true;
+        }
+        base = __builtin_amdgcn_readlane(end, 63);
+        before = P::INDEX ? __builtin_amdgcn_readlane(pe, 63) : 0;
+    }
+    return false;
+}
+
+// Workgroup id -> its place in the plan; false if the plan has fewer workgroups.  All threads of the
+// workgroup call it; every wave finds the same.  Up to 64 sequences are held a lane each, more in LDS
+// scratch (QG_ATTN_MAX_SEQ entries, free again afterwards).  ROWS: sequence b has the rows between its
+// q_start and the next; else one row, row b.  slots 0: nothing is split.  last_first: without a split,
+// id 0 is the last pair (the longest rows first).
+template <class P, bool ROWS>
+__device__ __forceinline__ bool attn_plan(const KvArgs &c, int group, int slots, int id, AttnPlan &p,
+                                          AttnSeq *scratch, bool last_first = false)
+{
+    const int lane = threadIdx.x & 63;
+    auto load = [&](int b) {
+        AttnSeq s = {0, 0, b, 1};
+        if (b < c.n_seq) {
+            s.n = seq_len(c, b);
+            if constexpr (ROWS) {
+                s.row0 = row_start(c, b);
+                s.rows = max(row_start(c, b + 1) - s.row0, 0);
+            }
+            s.pairs = c.nkv * (int)(((int64_t)s.rows * group + P::COLS - 1) / P::COLS);
+        }
+        return s;
+    };
+    if (c.n_seq <= 64) {
+        const AttnSeq s = load(lane);
+        return attn_plan_of<P, ROWS>(c, 1, group, slots, id, p, last_first, [&](int) { return s; });
+    }
+    for (int b = threadIdx.x; b < (c.n_seq + 63) / 64 * 64; b += 256)
+        scratch[b] = load(b);
+    __syncthreads();
+    const bool found = attn_plan_of<P, ROWS>(c, c.n_seq, group, slots, id, p, last_first,
+                                             [&](int b0) { return scratch[b0 + lane]; });
+    __syncthreads();
+    return found;
+}
+
 }  // namespace qg

@@ -17,8 +17,10 @@ namespace qg {
 __host__ __device__ constexpr int attn_slots(int hd) { return hd <= 128 ? 512 : 256; }
 // Floats of one slot's partial result: O of `cols` query heads, their maxima and sums.
 __host__ __device__ constexpr int64_t attn_part_floats(int cols, int hd) { return (int64_t)cols * (hd + 2); }
-// The same of qgemv_attn_prompt: tile splits, and with them partial results, of a call.
+// The same of qgemv_attn_prompt's 128-column tiles, and the most pairs of a call that may be split.
 #define PROMPT_SLOTS 512
+#define PROMPT_SPLITS 1024
+__host__ __device__ constexpr int prompt_slots(int hd) { return hd <= 128 ? PROMPT_SLOTS : 256; }
 
 enum KvType { KV_F16 = 1, KV_BF16 = 30 };
 
@@ -43,12 +45,16 @@ struct AppendArgs {
     int64_t stride;             // floats from row to row
 };
 
+struct PromptSplit;             // a split tile (attn_prompt_kernels.hip)
+
 struct AttnArgs {
     KvArgs c;
     const float *q;
     int64_t q_stride;
     float *o;                   // [n_rows][nq * hd]
     float *part;                // workspace: partial results of a split
+    int *pairs;                 // workspace: pairs of a prompt call
+    PromptSplit *splits;        // workspace: its split tiles, by pair
     unsigned int *count;        // workspace: arrival counters of a split, one per slot, 0 between calls
     int nq, group;              // query heads; query heads per KV head
     float scale;
@@ -65,10 +71,10 @@ struct RouteArgs {
 };
 
 struct PromptPlan {
-    int64_t tiles;              // tile ids per KV head
-    int n_split;                // splits of a tile over the cache's length
+    int64_t pairs;              // pairs of a tile and a KV head, at most
+    int slots;                  // workgroup slots of a split over the cache's length, 0: none
 };
-PromptPlan plan_prompt(int64_t n_rows, int n_seq, int nkv, int group, int64_t positions);
+PromptPlan plan_prompt(int64_t n_rows, int n_seq, int nkv, int group, int hd, int64_t positions);
 
 // Launchers: a hipError_t value (0 = success).
 int launch_kv_append(int kv_type, const AppendArgs &a, void *stream);

@@ -129,122 +129,9 @@ __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a)
 // left), always in chunk order, so that results do not depend on the order of execution.  A second
 // launch for the joining took 4.5 us on the device and 3 us on the host of calls of 7 to 100 us.
 
-constexpr int ATTN_UNIT_LOG2 = 7;
-constexpr int ATTN_SOLO = 4;         // units of a sequence that is not split
-constexpr int ATTN_LEAST = 2;        // units of a chunk, at least
+// 16 columns; chunks of whole 128-position units, at least two, sequences of up to four unsplit.
+typedef PlanOf<16, 7, 2, 4, false> AttnCols;
 constexpr int JOIN_RADIX = 8;
-
-struct AttnPlan {
-    int b, pair, chunk, n_chunk;   // this workgroup's sequence, (KV head, 16-column tile), chunk
-    int slot0;                     // workgroup id of the pair's first chunk
-    int len;                       // the sequence's positions
-    int row0, rows;                // its new rows
-};
-
-// Positions of sequence b that have a place in its table.
-__device__ __forceinline__ int seq_len(const KvArgs &c, int b)
-{
-    const int n = c.kv_len[b], cap = c.max_pages << c.ps_log2;          // cap <= 2^24
-    if (n > cap)
-        atomicOr(c.err, 1u);
-    return n < 0 ? 0 : n < cap ? n : cap;
-}
-
-// Inclusive sum over the lanes up to this one; lane 63 has the total.
-__device__ __forceinline__ int wave_scan(int v)
-{
-    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);      // row_shr 1, 2, 4, 8
-    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);     // row 0 -> 1, 2 -> 3
-    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);     // rows 0, 1 -> 2, 3
-    return v;
-}
-__device__ __forceinline__ int wave_sum(int v) { return __builtin_amdgcn_readlane(wave_scan(v), 63); }
-
-__device__ __forceinline__ int units_of(int n) { return (n + (1 << ATTN_UNIT_LOG2) - 1) >> ATTN_UNIT_LOG2; }
-
-// Chunks of a sequence of n positions when a chunk has u units (at least one, so that an empty
-// sequence's rows are written).
-__device__ __forceinline__ int chunks_of(int n, int u)
-{
-    const int units = units_of(n);
-    return units <= u || units <= ATTN_SOLO ? 1 : (units + u - 1) / u;
-}
-
-// Workgroup id -> its place in the plan; false if the plan has fewer workgroups.  Runs in every
-// wave (no barrier); lane l looks at sequences l, l + 64, ... (the first 64 held in registers).
-// ROWS: sequence b has the rows between its q_start and the next; else one row, row b.
-template <bool ROWS>
-__device__ __forceinline__ bool attn_plan(const KvArgs &c, int group, int slots, int id, AttnPlan &p)
-{
-    const int lane = threadIdx.x & 63;
-    struct Seq {
-        int n, pairs, row0, rows;
-    };
-    auto start = [&](int i) {
-        const int64_t v = c.q_start[i];
-        return (int)(v < 0 ? 0 : v < c.n_rows ? v : c.n_rows);
-    };
-    auto seq = [&](int b) {
-        Seq s = {0, 0, b, 1};
-        if (b < c.n_seq) {
-            s.n = seq_len(c, b);
-            if constexpr (ROWS) {
-                s.row0 = start(b);
-                s.rows = max(start(b + 1) - s.row0, 0);
-            }
-            s.pairs = c.nkv * ((s.rows * group + 15) / 16);
-        }
-        return s;
-    };
-    const Seq s0 = seq(lane);
-    auto sum = [&](auto of) {
-        int v = of(s0);
-        for (int b0 = 64; b0 < c.n_seq; b0 += 64)
-            v += of(seq(b0 + lane));
-        return wave_sum(v);
-    };
-    int u = 0x3fffffff;
-    const int pairs = sum([](const Seq &s) { return s.pairs; });
-    if (pairs < slots) {
-        // chunks <= units / u + 1 each, so u = units / (slots - pairs), over all pairs, is enough;
-        // units / slots is the least that could be
-        const int units = sum([](const Seq &s) { return s.pairs * units_of(s.n); });
-        int lo = max((units + slots - 1) / slots, ATTN_LEAST);
-        int hi = max((units + slots - pairs - 1) / (slots - pairs), lo);
-        while (lo < hi) {
-            const int mid = lo + (hi - lo) / 2;
-            if (sum([=](const Seq &s) { return s.pairs * chunks_of(s.n, mid); }) <= slots)
-                hi = mid;
-            else
-                lo = mid + 1;
-        }
-        u = lo;
-    }
-    int base = 0;
-    for (int b0 = 0; b0 < c.n_seq; b0 += 64) {
-        const Seq s = b0 == 0 ? s0 : seq(b0 + lane);
-        const int nc = chunks_of(s.n, u), end = base + wave_scan(nc * s.pairs);
-        const uint64_t in = __ballot(id < end);
-        if (in) {
-            const int l = __ffsll((unsigned long long)in) - 1;
-            p.b = b0 + l;
-            p.n_chunk = __builtin_amdgcn_readlane(nc, l);
-            p.len = __builtin_amdgcn_readlane(s.n, l);
-            p.slot0 = __builtin_amdgcn_readlane(end - nc * s.pairs, l);
-            p.row0 = ROWS ? __builtin_amdgcn_readlane(s.row0, l) : p.b;
-            p.rows = ROWS ? __builtin_amdgcn_readlane(s.rows, l) : 1;
-            p.pair = (id - p.slot0) / p.n_chunk;
-            p.slot0 += p.pair * p.n_chunk;
-            p.chunk = id - p.slot0;
-            return true;
-        }
-        base = __builtin_amdgcn_readlane(end, 63);
-    }
-    return false;
-}
 
 // Partial results of a slot: the tile's O (unnormalised) [cols][hd], then (maximum, sum) [cols].
 // They pass between workgroups of one launch, which may run on different XCDs: every access carries
@@ -306,7 +193,8 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn(AttnArgs a)
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int i = lane & 15, g = lane >> 4;
     AttnPlan p;
-    if (!attn_plan<ROWS>(c, a.group, attn_slots(D), blockIdx.x, p))
+    if (!attn_plan<AttnCols, ROWS>(c, a.group, attn_slots(D), blockIdx.x, p,
+                                   reinterpret_cast<AttnSeq *>(&s_o[0][0][0])))
         return;
     const int b = p.b, chunk = p.chunk, n_chunk = p.n_chunk, len = p.len;
     const int tiles = (p.rows * a.group + 15) / 16, hkv = p.pair / tiles, rho0 = p.pair % tiles * 16;
@@ -316,11 +204,11 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn(AttnArgs a)
     auto row_of = [&](int col) { return p.row0 + (ROWS ? (rho0 + col) / a.group : 0); };
 
     // this chunk's 32-position steps, dealt to the waves in turn
-    const int units = units_of(len);
+    const int units = AttnCols::units(len);
     const int per = units / n_chunk, more = units % n_chunk;
     const int unit0 = chunk * per + min(chunk, more);
-    const int t_begin = unit0 << ATTN_UNIT_LOG2;
-    const int t_end = min(len, (unit0 + per + (chunk < more ? 1 : 0)) << ATTN_UNIT_LOG2);
+    const int t_begin = unit0 << AttnCols::UNIT_LOG2;
+    const int t_end = min(len, (unit0 + per + (chunk < more ? 1 : 0)) << AttnCols::UNIT_LOG2);
     // positions this lane's column sees, [0, see), and those that all columns see (columns without a
     // row see what the last one does and are not stored)
     int see = t_end, see_all = t_end;
