@@ -226,7 +226,7 @@ __device__ __forceinline__ bool attn_plan_of(const KvArgs &c, int n_seq, int gro
     int u = 0x3fffffff;
     p.pairs = ROWS ? sum([](const AttnSeq &s) { return s.pairs; })
                    : c.n_seq * c.nkv * ((group + P::COLS - 1) / P::COLS);
-    if (p.pairs < slots) {
+    if (p.pairs >= 0 && p.pairs < slots) {
         // chunks <= units / u + 1 each, so u = units / (slots - pairs), over all pairs, is enough;
         // units / slots is the least that could be
         const int units = sum([](const AttnSeq &s) { return s.pairs * P::units(s.n); });
@@ -262,7 +262,8 @@ __device__ __forceinline__ bool attn_plan_of(const KvArgs &c, int n_seq, int gro
             p.pair = (id - p.slot0) / p.n_chunk;
             p.slot0 += p.pair * p.n_chunk;
             p.chunk = id - p.slot0;
-            return true;
+            // (row starts that are not in order could give sums beyond an int)
+            return !ROWS || (p.pair >= 0 && p.pair < __builtin_amdgcn_readlane(s.pairs, l));
         }
         base = __builtin_amdgcn_readlane(end, 63);
         before = P::INDEX ? __builtin_amdgcn_readlane(pe, 63) : 0;

@@ -78,6 +78,13 @@ def test_attn_many_sequences():
     _decode(q.BF16, 4, 2, 64, 16, [int(v) for v in rng.integers(0, 40, 1024)], 5)
 
 
+def test_attn_split_among_more_sequences_than_lanes():
+    rng = np.random.default_rng(31)
+    lens = [int(v) for v in rng.integers(0, 60, 150)]
+    lens[3], lens[90], lens[149] = 9000, 1300, 700
+    _decode(q.F16, 4, 1, 64, 16, lens, 6)
+
+
 def test_attn_sharp_scores_and_negative_scale():
     """Scores of a hundred units (one position takes all), a negative and a zero scale."""
     _decode(q.F16, 4, 2, 128, 16, [300, 77], 1, scale=1.0, qmul=4.0)
@@ -264,6 +271,17 @@ def test_prompt_wide(kv_type, nq, nkv, hd, page):
 ])
 def test_prompt_wide_long(kv_type, nq, nkv, hd, page, seqs):
     _prompt(kv_type, nq, nkv, hd, page, seqs, len(seqs), tail=1, wide=True)
+
+
+def test_prompt_split_among_more_sequences_than_lanes():
+    """16-column tiles of 100 sequences, 128-column tiles of 66, a few of them with long contexts."""
+    rng = np.random.default_rng(32)
+    seqs = [(int(a), int(a + c)) for a, c in zip(rng.integers(0, 3, 100), rng.integers(0, 30, 100))]
+    seqs[70], seqs[99] = (2, 4000), (1, 2500)
+    _prompt(q.BF16, 4, 1, 64, 16, seqs, 8, tail=1)
+    seqs = [(25, 25 + int(c)) for c in rng.integers(0, 30, 66)]
+    seqs[64], seqs[5] = (26, 3000), (0, 7)
+    _prompt(q.F16, 16, 1, 64, 16, seqs, 9, wide=True)
 
 
 def test_prompt_wide_many_heads_one_query_each():
