@@ -438,26 +438,14 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn(AttnArgs a)
     const uint32_t stride = (uint32_t)attn_part_floats(width, D);
     const __amdgpu_buffer_rsrc_t part = __builtin_amdgcn_make_buffer_rsrc(
         a.part + (int64_t)p.slot0 * stride, 0, n_chunk * stride * 4, 0x00020000);
-    // four channels of a column: to o, or as the partial result of chunk `at`
-    auto finish = [&](int e, af4 sum, float mm, float ls, int at) {
+    // four channels of a column to o
+    auto store = [&](int e, af4 sum, float mm, float ls) {
         const int col = e / (D / 4), d4 = e % (D / 4);
-        if (at < 0) {
-            const float inv = mm == -INFINITY ? 0.f : 1.0f / ls;
-            *reinterpret_cast<af4 *>(a.o + ((int64_t)row_of(col) * a.nq + head_of(col)) * D + 4 * d4) = sum * inv;
-            return;
-        }
-        put4(part, at * stride + col * D + 4 * d4, sum);
-        if (d4 == 0) {
-            s_mo[col] = mm;
-            s_lo[col] = ls;
-        }
+        const float inv = mm == -INFINITY ? 0.f : 1.0f / ls;
+        *reinterpret_cast<af4 *>(a.o + ((int64_t)row_of(col) * a.nq + head_of(col)) * D + 4 * d4) = sum * inv;
     };
-    // the maxima and sums of a partial result, once nobody reads what they replace
-    auto finish_sums = [&](int at) {
-        __syncthreads();
-        if ((int)threadIdx.x < cols)
-            put2(part, at * stride + width * D + 2 * threadIdx.x, s_mo[threadIdx.x], s_lo[threadIdx.x]);
-    };
+    auto sums_at = [&](int at, int col) { return at * stride + width * D + 2 * col; };
+    auto part_at = [&](int at, int e) { return at * stride + 4 * e; };
 
     for (int e = threadIdx.x; e < items; e += 256) {
         const int col = e / (D / 4), d4 = e % (D / 4);
@@ -473,10 +461,14 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn(AttnArgs a)
                 ls += s_l[w][col] * f;
             }
         }
-        finish(e, sum, mm, ls, n_chunk > 1 ? chunk : -1);
+        if (n_chunk == 1) {
+            store(e, sum, mm, ls);
+        } else {
+            put4(part, part_at(chunk, e), sum);
+            if (d4 == 0)
+                put2(part, sums_at(chunk, col), mm, ls);
+        }
     }
-    if (n_chunk > 1)
-        finish_sums(chunk);
     // nodes of 1, 8, 64, ... chunks; a node's result lies in the slot of its first chunk.  The group
     // that starts at chunk g0 of level L arrives at the pair's counter g0 + L: all of a level's g0
     // are multiples of JOIN_RADIX, so no two share one
@@ -496,9 +488,8 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn(AttnArgs a)
             for (int k = 0; k < JOIN_RADIX; ++k) {              // all loads in flight at once
                 mk[k] = -INFINITY;
                 if (k < members) {
-                    const uint32_t from = (uint32_t)(g0 + k * node) * stride;
-                    get2(part, from + width * D + 2 * col, mk[k], lk[k]);
-                    x[k] = get4(part, from + col * D + 4 * d4);
+                    get2(part, sums_at(g0 + k * node, col), mk[k], lk[k]);
+                    x[k] = get4(part, part_at(g0 + k * node, e));
                 }
             }
             float mm = -INFINITY, ls = 0.f;
@@ -513,10 +504,22 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn(AttnArgs a)
                     sum += x[k] * f;
                     ls += lk[k] * f;
                 }
-            finish(e, sum, mm, ls, top ? -1 : g0);
+            if (top) {
+                store(e, sum, mm, ls);
+            } else {
+                // the maximum and sum replace what other threads of the column may still have to read
+                put4(part, part_at(g0, e), sum);
+                if (d4 == 0) {
+                    s_mo[col] = mm;
+                    s_lo[col] = ls;
+                }
+            }
         }
-        if (!top)
-            finish_sums(g0);
+        if (!top) {
+            __syncthreads();
+            if ((int)threadIdx.x < cols)
+                put2(part, sums_at(g0, threadIdx.x), s_mo[threadIdx.x], s_lo[threadIdx.x]);
+        }
     }
 }
 
