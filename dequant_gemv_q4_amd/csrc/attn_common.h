@@ -155,18 +155,20 @@ constexpr float LOG2E = 1.44269504088896340736f;
 // chunk of the sequence's positions.  The lengths are on the device, so every workgroup derives the
 // same plan from them: where there are fewer pairs than workgroup slots, the smallest chunk (whole
 // units of 2^UNIT_LOG2 positions, at least LEAST) for which the chunks of all pairs fit the slots; a
-// pair's chunks are equal to one unit.  Sequences of up to SOLO units are not split.  INDEX: the plan
-// also numbers the pairs.
-template <int COLS_, int UNIT_LOG2_, int LEAST_, int SOLO_, bool INDEX_>
+// pair's chunks are equal to one unit.  Sequences of up to SOLO units are not split, those of up to
+// FLAT units into at most RADIX chunks.  INDEX: the plan also numbers the pairs.
+template <int COLS_, int UNIT_LOG2_, int LEAST_, int SOLO_, int FLAT_, int RADIX_, bool INDEX_>
 struct PlanOf {
     static constexpr int COLS = COLS_, UNIT_LOG2 = UNIT_LOG2_, LEAST = LEAST_, SOLO = SOLO_;
+    static constexpr int FLAT = FLAT_, RADIX = RADIX_;
     static constexpr bool INDEX = INDEX_;
     static __device__ __forceinline__ int units(int n) { return (n + (1 << UNIT_LOG2) - 1) >> UNIT_LOG2; }
     // at least one, so that an empty sequence's rows are written
     static __device__ __forceinline__ int chunks(int n, int u)
     {
         const int x = units(n);
-        return x <= u || x <= SOLO ? 1 : (x + u - 1) / u;
+        const int n_chunk = x <= u || x <= SOLO ? 1 : (x + u - 1) / u;
+        return x <= FLAT && n_chunk > RADIX ? RADIX : n_chunk;
     }
 };
 

@@ -17,6 +17,9 @@ namespace qg {
 //
 // Blocks start at multiples of their size; sequence b's begin at block id q_start[b] / size + 2 b,
 // which leaves every sequence enough ids wherever its first position lies.
+//
+// Bound by HBM: 8000 rows of 8 heads of 128 (98.3 MB read and written) take 22.4 us, 4.4 TB/s, where a
+// copy reaches 4.94; one position at a time took 75 us.  One row of 2 heads: 2.8 us, a launch.
 template <int T, int BL>
 __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a)
 {
@@ -128,10 +131,16 @@ __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a)
 // JOIN_RADIX chunks the last to finish adds them up (then of as many such groups, until one is
 // left), always in chunk order, so that results do not depend on the order of execution.  A second
 // launch for the joining took 4.5 us on the device and 3 us on the host of calls of 7 to 100 us.
-
-// 16 columns; chunks of whole 128-position units, at least two, sequences of up to four unsplit.
-typedef PlanOf<16, 7, 2, 4, false> AttnCols;
+//
+// Bound by HBM where the cache is long: 64 sequences of 7500 positions (12 / 2 heads of 128, bf16) take
+// 98 us, 5.01 TB/s; seven of up to 60000 (32 / 8, f16) 72 us, 5.13 TB/s.  By latency where it is short:
+// 165 positions 6.9 us, one after the other the lengths, the page numbers, K and V.
 constexpr int JOIN_RADIX = 8;
+// 16 columns; chunks of whole 128-position units, at least two; sequences of up to four are not split,
+// and those of up to 32 not into more chunks than one join takes: four sequences of 4090 positions (32 / 8
+// heads of 128) took 18.2 us with sixteen chunks and a second join, 15.9 with eight; one of 4090 (12 / 2)
+// 10.9 and 11.2, and one of 5100 already 11.0 and 13.0.
+typedef PlanOf<16, 7, 2, 4, 32, JOIN_RADIX, false> AttnCols;
 
 // Partial results of a slot: the tile's O (unnormalised) [cols][hd], then (maximum, sum) [cols].
 // They pass between workgroups of one launch, which may run on different XCDs: every access carries

@@ -18,6 +18,10 @@
 // (0-3, 12-15, 20-23, 24-27 and so on) from 64 banks at a time, and with these keys their 16 rows lie in
 // different banks: SQ_LDS_BANK_CONFLICT 0, against four cycles a read with keys made for eight lanes
 // in a row.
+//
+// Bound by the matrix cores: 8192 rows (32 / 8 heads of 128, f16) take 937 us, 1.17 PFLOP/s with each
+// product's two pieces counted, what a large f16 product reaches on the card; 4500 rows of nine prompts
+// (24 / 8 of 64, bf16, three pieces) 40 us.
 #include <hip/hip_runtime.h>
 
 #include "attn_common.h"
@@ -48,7 +52,7 @@ __device__ __forceinline__ void pt_barrier()
 // 128 columns; chunks of whole steps, at least eight.  A partial result is 66 KB (heads of 128), written
 // once and read once, so that up to sixteen steps are not split (one sequence of 1024 rows, 32 / 8
 // heads: 39 us, in halves 59; sixteen of 32 rows behind 4000 positions: 122 us unsplit, 56).
-typedef PlanOf<PT_ROWS, 6, 8, 16, true> PromptCols;
+typedef PlanOf<PT_ROWS, 6, 8, 16, 0, 0, true> PromptCols;
 
 // A split tile, for its join.
 struct PromptSplit {

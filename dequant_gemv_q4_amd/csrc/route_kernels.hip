@@ -18,7 +18,8 @@
 //
 // Bound by VALU issue, not by the 8.7 MB it moves: 8000 x 256, sigmoid, 8 groups, top 8 of 4 groups,
 // takes 31.1 us with shuffled 64-bit maxima and a serial scan of the groups, 15.2 us with lane shifts
-// and 64-bit rounds, MEASURED us as it is.
+// and 64-bit rounds, 12.6 us as it is (700 VALU instructions a row); 16 x 64, top 8, 5.4 us, of which the
+// kernel is 3.0.
 #include <hip/hip_runtime.h>
 
 #include "attn_internal.h"
