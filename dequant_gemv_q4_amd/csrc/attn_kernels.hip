@@ -120,9 +120,11 @@ __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a)
 //
 // Each of the four waves takes every fourth 32-position step, loads one step ahead (K, V) and two
 // ahead (page numbers), and keeps its own maximum, sum and O^T; they are joined in LDS at the end.
-// The reference of the exponentials moves only when a score exceeds it by 2^9 (a wave vote), so the
-// accumulators are hardly ever rescaled; probabilities are held times 2^6 (f16: 2^-30 of the
-// reference still has its first piece's bits, 2^15 does not overflow).
+// The reference of the exponentials moves only when a score exceeds it by more than 7 powers of two (a
+// wave vote), so the accumulators are hardly ever rescaled; probabilities are held times 2^6 (f16: 2^-30
+// of the reference still has its first piece's bits).  They stay below the f16 range's end of 2^16 for
+// scores of any size: the excess over the reference is exact, a multiple of the scores' spacing, and
+// 6 - m rounds to 8 - m at most (spacing 4, excess at most 4; spacing 8, excess 0; wider, -m and 0).
 //
 // Split over the length: the lengths are on the device, so every workgroup derives the same plan
 // from them: the smallest chunk (whole 128-position units) for which the chunks of all sequences
@@ -380,7 +382,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn(AttnArgs a)
             }
             float mx = fmaxf(fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3])),
                              fmaxf(fmaxf(sc[4], sc[5]), fmaxf(sc[6], sc[7])));
-            if (__any(mx > m + 9.0f)) {
+            if (__any(mx - m > 7.0f)) {
                 mx = max_x32(max_x16(mx));
                 const float mn = fmaxf(m, mx);
                 const float f = m == mn ? 1.0f : __builtin_amdgcn_exp2f(m - mn);

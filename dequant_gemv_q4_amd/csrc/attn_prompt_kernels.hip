@@ -130,15 +130,19 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
                 amax = fmaxf(amax, fabsf(v[k][e]));
             }
         }
-        const float sc0 = q_scale<T>(max_x32(amax)), sc = a.scale < 0.f ? -sc0 : sc0;
-        unscale = a.scale * LOG2E / sc;                // not negative: the largest score stays it
+        // the mantissa of the scale goes into the queries and the rest is a power of two: scores come out
+        // of their product with it exact (as their maximum is), none of either sign or zero is turned,
+        // and a masked -inf stays one
+        int e2 = 0;
+        const float f = frexpf(a.scale, &e2) * LOG2E, sc = q_scale<T>(max_x32(amax));
+        unscale = fmaxf(ldexpf(1.0f / sc, e2), 0x1p-126f);
 #pragma unroll
         for (int k = 0; k < KB; ++k) {
             float w[8];
             au4 out[NP];
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                w[e] = v[k][e] * sc;
+                w[e] = v[k][e] * sc * f;
             split8<T>(w, out);
 #pragma unroll
             for (int x = 0; x < NP; ++x)
@@ -237,7 +241,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
             for (int tt = 0; tt < NT; ++tt)
                 mx = fmaxf(mx, sc[tt][r]);
         mx *= unscale;
-        if (__any(mx > m + 9.0f)) {
+        if (__any(mx - m > 7.0f)) {
             const float mn = fmaxf(m, max_x32(mx));
             const float f = m == mn ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
             m = mn;
@@ -339,7 +343,8 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
                 }
         }
     };
-    const int tile_min = p.pos0 + p.rho0 / a.group;     // the tile's least position
+    // the tile's least position; a table that ends before it may end inside a step
+    const int tile_min = min(p.pos0 + p.rho0 / a.group, p.hi - 1);
     auto compute = [&](int s, int buf, uint32_t bad) {
         const int t0 = s * PT_STEP;
         const bool edge = bad != 0 || t0 + PT_STEP - 1 > tile_min;

@@ -187,14 +187,14 @@ def test_attn_all_pages_bad_gives_zero():
 # --------------------------------------------------------------------------------------- prompts
 
 def _prompt(kv_type, nq, nkv, hd, page, seqs, seed, tail=0, qmul=1.0, K=None, V=None, check=None,
-            wide=False):
+            wide=False, scale=None):
     """seqs: (new rows, cached positions with them); tail rows behind the last sequence.  wide: sizes
     that the 128-row tiles take (many columns per sequence and a table of over 1024 positions)."""
     say(f"prompt type={kv_type} nq={nq} nkv={nkv} hd={hd} page={page} seqs={seqs[:6]} wide={wide}")
     if wide:
         assert sum(a for a, _ in seqs) * (nq // nkv) > 384 * len(seqs)
     rng = np.random.default_rng([78, seed])
-    scale = hd ** -0.5
+    scale = hd ** -0.5 if scale is None else scale
     lens = [b for _, b in seqs]
     if K is None:
         K, V = _draw(rng, [max(0, b) for b in lens], nkv, hd, kv_type)
@@ -288,6 +288,55 @@ def test_prompt_wide_many_heads_one_query_each():
     _prompt(q.F16, 3, 3, 128, 16, [(390, 400)], 2, wide=True)
 
 
+@pytest.mark.parametrize("wide", [False, True])
+def test_prompt_sharp_scores_and_other_scales(wide):
+    """As for single tokens: scores of a hundred units, negative, zero, tiny and huge scales."""
+    seqs = [(110, 300), (100, 131)] if wide else [(31, 300), (5, 77)]
+    _prompt(q.F16, 4, 1, 128, 16, seqs, 1, wide=wide, scale=1.0, qmul=2.0)
+    _prompt(q.BF16, 4, 1, 128, 16, seqs, 2, wide=wide, scale=-0.09)
+    _prompt(q.F16, 4, 1, 64, 16, seqs, 3, wide=wide, scale=0.0)
+    _prompt(q.BF16, 4, 1, 64, 16, seqs, 4, wide=wide, scale=-0.0)
+    _prompt(q.F16, 4, 1, 64, 16, seqs, 5, wide=wide, scale=-1e-6, qmul=1e6)
+    _prompt(q.F16, 4, 1, 64, 16, seqs, 6, wide=wide, scale=1e6, qmul=1e-6)
+    _prompt(q.BF16, 4, 1, 64, 16, seqs, 7, wide=wide, scale=1e-40, qmul=1e-3)
+
+
+@pytest.mark.parametrize("kv_type", [q.F16, q.BF16])
+@pytest.mark.parametrize("top", [1e7, 2e7, 4e7, 8e7, 1.6e8, 3.2e8, 1e9, 1e12])
+def test_scores_wider_apart_than_their_spread_stay_finite(kv_type, top):
+    """Scores of 1e7 to 1e12 that grow slowly with the position: f32 spaces them by 1 to 2^17, and no
+    rounding against the running maximum may leave the range of a weight.  The outputs have to be means of
+    the values seen (sums of 400 terms and weights: 2^-14 covers 802 roundings); nearer than the scores'
+    own rounding allows, the definition does not say which."""
+    hd, nq, page, n, rows = 64, 4, 16, 400, 130
+    rng = np.random.default_rng(36)
+    for every in (24, 40):
+        K = np.zeros((n, 1, hd), np.float32)
+        K[:, 0, 0], K[:, 0, 1] = 1.0, np.arange(n) // every
+        V = rounded(rng.standard_normal((n, 1, hd)), kv_type)
+        x = np.zeros((rows, nq * hd), np.float32)
+        x[:, 0::hd], x[:, 1::hd] = np.float32(top) * rng.uniform(0.9, 1.1, (rows, nq)), 1.0
+        c = Paged(kv_type, [K], [V], page, 1, hd, rng, extra_entries=70)
+        for count in (0, 12, rows):                  # single token, 16-column tiles, 128-row tiles
+            say(f"large scores top={top} every={every} rows={count}")
+            m = max(count, 1)
+            xd, o = dev(x[:m]), torch.full((m, nq * hd), float("nan"), device="cuda")
+            if count:
+                ws = D.attn_workspace(q.OP_ATTN_PROMPT, 1, nq, 1, hd)
+                q.qgemv_attn_prompt(*c.args(), torch.tensor([0, m], dtype=torch.int32, device="cuda"), c.kv_len, 1,
+                                    xd, nq * hd, m, nq, 1.0, o, ws)
+            else:
+                ws = D.attn_workspace(q.OP_ATTN, 1, nq, 1, hd)
+                q.qgemv_attn(*c.args(), c.kv_len, 1, xd, nq * hd, nq, 1.0, o, ws)
+            last = [n - m + r for r in range(m)]
+            got = host(o).reshape(m, nq, hd)
+            assert np.isfinite(got).all()
+            for r in range(m):
+                seen = V[:last[r] + 1, 0]
+                slack = 2.0 ** -14 * np.abs(seen).max(axis=0)
+                assert (got[r] <= seen.max(axis=0) + slack).all() and (got[r] >= seen.min(axis=0) - slack).all()
+
+
 def test_prompt_padded_rows_attend_to_nothing():
     """kv_len below the new rows (a padded batch): the first rows are at negative positions."""
     _prompt(q.F16, 4, 2, 64, 16, [(5, 2), (3, 0), (40, 39), (2, -3)], 1, tail=2)
@@ -344,6 +393,27 @@ def test_prompt_wide_bad_pages_are_left_out():
                          int((keep <= r).sum()) - 1) for r in range(n)]
     ref, A, S = _cat(parts)
     check_attention(host(o), ref, A, S, np.arange(1, n + 1), hd, q.BF16, "bad pages, wide")
+    assert q.qgemv_attn_error(ws) == 1 and q.qgemv_attn_error(ws) == 0
+
+
+@pytest.mark.parametrize("kv_type,beyond", [(q.F16, 8), (q.F16, 300), (q.BF16, 300), (q.BF16, 2 ** 31 - 1 - 1040)])
+def test_prompt_wide_table_ends_inside_a_step(kv_type, beyond):
+    """Lengths beyond a table of 1040 positions (a step is 64): rows up to and behind its end see what
+    the table has, and the flag is set."""
+    hd, nq, page, n, cap = 64, 4, 16, 130, 1040
+    rng = np.random.default_rng(35)
+    K, V = _draw(rng, [cap], 1, hd, kv_type)
+    c = Paged(kv_type, K, V, page, 1, hd, rng, extra_entries=0)
+    assert c.max_pages * page == cap and n * nq > 384
+    x = rng.standard_normal((n, nq * hd)).astype(np.float32)
+    o = torch.full((n, nq * hd), float("nan"), device="cuda")
+    ws = D.attn_workspace(q.OP_ATTN_PROMPT, 1, nq, 1, hd)
+    q.qgemv_attn_prompt(*c.args(), torch.tensor([0, n], dtype=torch.int32, device="cuda"),
+                        torch.tensor([cap + beyond], dtype=torch.int32, device="cuda"), 1, dev(x), nq * hd, n, nq,
+                        0.125, o, ws)
+    last = [min(cap + beyond - n + r, cap - 1) for r in range(n)]
+    ref, A, S = _cat([attention64(x[r].reshape(nq, hd), K[0], V[0], 1, 0.125, last[r]) for r in range(n)])
+    check_attention(host(o), ref, A, S, np.array(last) + 1, hd, kv_type, "table ends inside a step")
     assert q.qgemv_attn_error(ws) == 1 and q.qgemv_attn_error(ws) == 0
 
 
