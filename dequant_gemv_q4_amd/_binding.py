@@ -104,9 +104,9 @@ def _p(a):
 
 def _stream(s):
     if s is None:
-        import torch
         # the raw handle: building a Stream object takes 2.7 us, this 0.2
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        t = _torch_types()
+        return t[4](t[3]())
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -247,7 +247,8 @@ def qgemv_attn_workspace_bytes(op: int, n_seq: int, n_q_heads: int, n_kv_heads: 
     return lib().qgemv_attn_workspace_bytes(op, n_seq, n_q_heads, n_kv_heads, head_dim)
 
 
-_types = None      # torch's int32, float32, and the cache types by kv_type; the current device's index
+# torch's int32, float32, and the cache types by kv_type; the current device's index, its stream
+_types = None
 
 
 def _torch_types():
@@ -255,7 +256,7 @@ def _torch_types():
     if _types is None:
         import torch
         _types = (torch.int32, torch.float32, {F16: torch.float16, BF16: torch.bfloat16},
-                  torch._C._cuda_getDevice)
+                  torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
     return _types
 
 
@@ -274,14 +275,14 @@ def _t(a, dtype, dev, whole=True):
 def qgemv_kv_append(kv_type, k_pages, v_pages, n_pages, page_size, page_stride, n_kv_heads,
                     head_dim, table, max_pages, q_start, kv_len, n_seq, k, v, kv_stride, n_rows, ws,
                     ws_bytes=None, stream=None):
-    i32, f32, kv, device = _torch_types()
+    i32, f32, kv, device, raw = _torch_types()
     d, c = device(), kv.get(kv_type)
     st = lib().qgemv_kv_append(kv_type, _t(k_pages, c, d, False), _t(v_pages, c, d, False), n_pages,
                                page_size, page_stride, n_kv_heads, head_dim, _t(table, i32, d),
                                max_pages, _t(q_start, i32, d), _t(kv_len, i32, d), n_seq,
                                _t(k, f32, d, False), _t(v, f32, d, False), kv_stride, n_rows,
                                _t(ws, None, d), _nbytes(ws) if ws_bytes is None else ws_bytes,
-                               _stream(stream))
+                               raw(d) if stream is None else _stream(stream))
     if st:
         _check("qgemv_kv_append", st)
 
@@ -289,13 +290,14 @@ def qgemv_kv_append(kv_type, k_pages, v_pages, n_pages, page_size, page_stride, 
 def qgemv_attn(kv_type, k_pages, v_pages, n_pages, page_size, page_stride, n_kv_heads, head_dim,
                table, max_pages, kv_len, n_seq, q, q_stride, n_q_heads, scale, o, ws,
                ws_bytes=None, stream=None):
-    i32, f32, kv, device = _torch_types()
+    i32, f32, kv, device, raw = _torch_types()
     d, c = device(), kv.get(kv_type)
     st = lib().qgemv_attn(kv_type, _t(k_pages, c, d, False), _t(v_pages, c, d, False), n_pages,
                           page_size, page_stride, n_kv_heads, head_dim, _t(table, i32, d), max_pages,
                           _t(kv_len, i32, d), n_seq, _t(q, f32, d, False), q_stride, n_q_heads, scale,
                           _t(o, f32, d), _t(ws, None, d),
-                          _nbytes(ws) if ws_bytes is None else ws_bytes, _stream(stream))
+                          _nbytes(ws) if ws_bytes is None else ws_bytes,
+                          raw(d) if stream is None else _stream(stream))
     if st:
         _check("qgemv_attn", st)
 
@@ -303,14 +305,15 @@ def qgemv_attn(kv_type, k_pages, v_pages, n_pages, page_size, page_stride, n_kv_
 def qgemv_attn_prompt(kv_type, k_pages, v_pages, n_pages, page_size, page_stride, n_kv_heads,
                       head_dim, table, max_pages, q_start, kv_len, n_seq, q, q_stride, n_rows,
                       n_q_heads, scale, o, ws, ws_bytes=None, stream=None):
-    i32, f32, kv, device = _torch_types()
+    i32, f32, kv, device, raw = _torch_types()
     d, c = device(), kv.get(kv_type)
     st = lib().qgemv_attn_prompt(kv_type, _t(k_pages, c, d, False), _t(v_pages, c, d, False), n_pages,
                                  page_size, page_stride, n_kv_heads, head_dim, _t(table, i32, d),
                                  max_pages, _t(q_start, i32, d), _t(kv_len, i32, d), n_seq,
                                  _t(q, f32, d, False), q_stride, n_rows, n_q_heads, scale,
                                  _t(o, f32, d), _t(ws, None, d),
-                                 _nbytes(ws) if ws_bytes is None else ws_bytes, _stream(stream))
+                                 _nbytes(ws) if ws_bytes is None else ws_bytes,
+                                 raw(d) if stream is None else _stream(stream))
     if st:
         _check("qgemv_attn_prompt", st)
 
@@ -323,10 +326,10 @@ def qgemv_attn_error(ws, stream=None) -> int:
 
 def qgemv_route(logits, n_rows, n_exp, score, bias, n_group, group_top, topk_group, topk, renorm,
                 scale, ids, wts, stream=None):
-    i32, f32, _, device = _torch_types()
+    i32, f32, _, device, raw = _torch_types()
     d = device()
     st = lib().qgemv_route(_t(logits, f32, d), n_rows, n_exp, score, _t(bias, f32, d), n_group,
                            group_top, topk_group, topk, 1 if renorm else 0, scale, _t(ids, i32, d),
-                           _t(wts, f32, d), _stream(stream))
+                           _t(wts, f32, d), raw(d) if stream is None else _stream(stream))
     if st:
         _check("qgemv_route", st)
