@@ -156,7 +156,8 @@ constexpr float LOG2E = 1.44269504088896340736f;
 // same plan from them: where there are fewer pairs than workgroup slots, the smallest chunk (whole
 // units of 2^UNIT_LOG2 positions, at least LEAST) for which the chunks of all pairs fit the slots; a
 // pair's chunks are equal to one unit.  Sequences of up to SOLO units are not split, those of up to
-// FLAT units into at most RADIX chunks.  INDEX: the plan also numbers the pairs.
+// FLAT units into at most RADIX chunks.  INDEX: the plan also numbers the pairs
+// and, where nothing is split, puts the longest first.
 template <int COLS_, int UNIT_LOG2_, int LEAST_, int SOLO_, int FLAT_, int RADIX_, bool INDEX_>
 struct PlanOf {
     static constexpr int COLS = COLS_, UNIT_LOG2 = UNIT_LOG2_, LEAST = LEAST_, SOLO = SOLO_;
@@ -175,7 +176,7 @@ struct PlanOf {
 struct AttnPlan {
     int b, pair, chunk, n_chunk;   // this workgroup's sequence, pair within it, chunk of its chunks
     int slot0;                     // workgroup id of the pair's first chunk
-    int first_pair, pairs;         // pairs of earlier sequences (where INDEX), of all
+    int first_pair, pairs;         // where INDEX, first_pair + pair numbers the pairs; pairs of all
     int len;                       // the sequence's positions
     int row0, rows;                // its new rows
 };
@@ -201,23 +202,96 @@ __device__ __forceinline__ int row_start(const KvArgs &c, int i)
     return (int)(v < 0 ? 0 : v < c.n_rows ? v : c.n_rows);
 }
 
-// Inclusive sum over the lanes up to this one; lane 63 has the total.
-__device__ __forceinline__ int wave_scan(int v)
+// Inclusive sum (or f, with f(v, 0) = v) over the lanes up to this one; lane 63 has the total.
+template <class F>
+__device__ __forceinline__ int wave_scan(int v, F f)
 {
-    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);      // row_shr 1, 2, 4, 8
-    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);     // row 0 -> 1, 2 -> 3
-    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);     // rows 0, 1 -> 2, 3
+    v = f(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true));      // row_shr 1, 2, 4, 8
+    v = f(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true));
+    v = f(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true));
+    v = f(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true));
+    v = f(v, __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false));     // row 0 -> 1, 2 -> 3
+    v = f(v, __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false));     // rows 0, 1 -> 2, 3
     return v;
 }
+__device__ __forceinline__ int wave_scan(int v)
+{
+    return wave_scan(v, [](int a, int b) { return a + b; });
+}
 __device__ __forceinline__ int wave_sum(int v) { return __builtin_amdgcn_readlane(wave_scan(v), 63); }
+__device__ __forceinline__ int wave_top(int v)          // v >= 0
+{
+    return __builtin_amdgcn_readlane(wave_scan(v, [](int a, int b) { return a > b ? a : b; }), 63);
+}
+
+// The id-th pair of an unsplit plan in falling order of work, so that the workgroups that start last are
+// short and all end together.  Tile x of a sequence counts x + 1 and the tiles that its earlier positions
+// would fill; the counts are cut into up to LEVELS levels (a binary search of six steps), within a level
+// the pairs go by sequence.  Against sequence after sequence: nine prompts, 4500 rows (24 / 8 heads of 64,
+// bf16) 40.0 -> 36.5 us; five, 2000 rows (32 / 8 of 128, bf16) 47.0 -> 39.1; a hundred, 8000 rows behind up
+// to 500 positions (12 / 2 of 128) 59.3 -> 51.5; two of 2000 (8 / 8 of 256) 68.0 -> 67.8; three, 4000 rows
+// behind up to 8000 (32 / 8 of 128) 621 -> 635.
+template <class P, class Seq>
+__device__ __forceinline__ bool longest_first(const KvArgs &c, int n_seq, int group, int id, AttnPlan &p, Seq seq)
+{
+    constexpr int LEVELS = 64;
+    auto behind = [&](const AttnSeq &s) { return (int)((int64_t)max(s.n - s.rows, 0) * group / P::COLS); };
+    auto tiles = [&](const AttnSeq &s) { return (int)(((int64_t)s.rows * group + P::COLS - 1) / P::COLS); };
+    int top = 0;
+    for (int b0 = 0; b0 < n_seq; b0 += 64) {
+        const AttnSeq s = seq(b0);
+        top = max(top, tiles(s) + behind(s));
+    }
+    top = wave_top(top);
+    const int step = top / LEVELS + 1;
+    // tiles of a sequence at a level or above
+    auto from = [&](const AttnSeq &s, int level) {
+        const int t = tiles(s);
+        return min(max(t + behind(s) + 1 - level * step, 0), t);
+    };
+    auto pairs_from = [&](int level) {
+        int v = 0;
+        for (int b0 = 0; b0 < n_seq; b0 += 64)
+            v += from(seq(b0), level);
+        return c.nkv * wave_sum(v);
+    };
+    int lo = 0, hi = top / step;
+    while (lo < hi) {
+        const int mid = lo + (hi - lo + 1) / 2;
+        if (pairs_from(mid) > id)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    int base = pairs_from(lo + 1);
+    for (int b0 = 0; b0 < n_seq; b0 += 64) {
+        const AttnSeq s = seq(b0);
+        const int above = from(s, lo + 1), here = c.nkv * (from(s, lo) - above), end = base + wave_scan(here);
+        const uint64_t in = __ballot(id < end);
+        if (in) {
+            const int l = __ffsll((unsigned long long)in) - 1;
+            const int r = id - __builtin_amdgcn_readlane(end - here, l);
+            const int x = __builtin_amdgcn_readlane(tiles(s) - 1 - above, l) - r / c.nkv;
+            p.b = b0 + l;
+            p.pair = x * c.nkv + r % c.nkv;
+            p.chunk = p.slot0 = 0;
+            p.n_chunk = 1;
+            p.first_pair = id - p.pair;
+            p.len = __builtin_amdgcn_readlane(s.n, l);
+            p.row0 = __builtin_amdgcn_readlane(s.row0, l);
+            p.rows = __builtin_amdgcn_readlane(s.rows, l);
+            // (row starts that are not in order could give sums beyond an int)
+            return r >= 0 && x >= 0;
+        }
+        base = __builtin_amdgcn_readlane(end, 63);
+    }
+    return false;
+}
 
 // The plan from the sequences `seq(b0)` of lanes b0 .. b0 + 63 of each round.
 template <class P, bool ROWS, class Seq>
 __device__ __forceinline__ bool attn_plan_of(const KvArgs &c, int n_seq, int group, int slots, int id, AttnPlan &p,
-                                             bool last_first, Seq seq)
+                                             Seq seq)
 {
     auto sum = [&](auto of) {
         int v = 0;
@@ -242,10 +316,13 @@ __device__ __forceinline__ bool attn_plan_of(const KvArgs &c, int n_seq, int gro
                 lo = mid + 1;
         }
         u = lo;
-    } else if (last_first)
+    } else if (P::INDEX) {
+        if (id >= p.pairs)
+            return false;
+        if (c.n_seq > 1)
+            return longest_first<P>(c, n_seq, group, id, p, seq);
         id = p.pairs - 1 - id;
-    if (id < 0)
-        return false;
+    }
     int base = 0, before = 0;
     for (int b0 = 0; b0 < n_seq; b0 += 64) {
         const AttnSeq s = seq(b0);
@@ -276,11 +353,10 @@ __device__ __forceinline__ bool attn_plan_of(const KvArgs &c, int n_seq, int gro
 // Workgroup id -> its place in the plan; false if the plan has fewer workgroups.  All threads of the
 // workgroup call it; every wave finds the same.  Up to 64 sequences are held a lane each, more in LDS
 // scratch (QG_ATTN_MAX_SEQ entries, free again afterwards).  ROWS: sequence b has the rows between its
-// q_start and the next; else one row, row b.  slots 0: nothing is split.  last_first: without a split,
-// id 0 is the last pair (the longest rows first).
+// q_start and the next; else one row, row b.  slots 0: nothing is split.
 template <class P, bool ROWS>
 __device__ __forceinline__ bool attn_plan(const KvArgs &c, int group, int slots, int id, AttnPlan &p,
-                                          AttnSeq *scratch, bool last_first = false)
+                                          AttnSeq *scratch)
 {
     const int lane = threadIdx.x & 63;
     auto load = [&](int b) {
@@ -297,12 +373,12 @@ __device__ __forceinline__ bool attn_plan(const KvArgs &c, int group, int slots,
     };
     if (c.n_seq <= 64) {
         const AttnSeq s = load(lane);
-        return attn_plan_of<P, ROWS>(c, 1, group, slots, id, p, last_first, [&](int) { return s; });
+        return attn_plan_of<P, ROWS>(c, 1, group, slots, id, p, [&](int) { return s; });
     }
     for (int b = threadIdx.x; b < (c.n_seq + 63) / 64 * 64; b += 256)
         scratch[b] = load(b);
     __syncthreads();
-    const bool found = attn_plan_of<P, ROWS>(c, c.n_seq, group, slots, id, p, last_first,
+    const bool found = attn_plan_of<P, ROWS>(c, c.n_seq, group, slots, id, p,
                                              [&](int b0) { return scratch[b0 + lane]; });
     __syncthreads();
     return found;

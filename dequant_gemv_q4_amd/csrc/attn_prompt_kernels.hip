@@ -21,7 +21,7 @@
 //
 // Bound by the matrix cores: 8192 rows (32 / 8 heads of 128, f16) take 937 us, 1.17 PFLOP/s with each
 // product's two pieces counted, what a large f16 product reaches on the card; 4500 rows of nine prompts
-// (24 / 8 of 64, bf16, three pieces) 40 us.
+// (24 / 8 of 64, bf16, three pieces) 36.5 us.
 #include <hip/hip_runtime.h>
 
 #include "attn_common.h"
@@ -79,7 +79,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
     const int col = lane & 31, hf = lane >> 5;
     AttnPlan w;
     const bool work = attn_plan<PromptCols, true>(c, a.group, slots, blockIdx.x, w,
-                                                  reinterpret_cast<AttnSeq *>(lds), true);
+                                                  reinterpret_cast<AttnSeq *>(lds));
     if (blockIdx.x == 0 && tid == 0 && slots)
         *a.pairs = w.pairs;
     if (!work)

@@ -284,6 +284,19 @@ def test_prompt_split_among_more_sequences_than_lanes():
     _prompt(q.F16, 16, 1, 64, 16, seqs, 9, wide=True)
 
 
+def test_prompt_wide_more_tiles_than_are_resident():
+    """128-column tiles in falling order of work: four sequences (tiles of 1 to 112 tiles' work), 70 of them
+    (more than lanes), a padded and an empty one."""
+    seqs = [(300, 300), (0, 40), (100, 900), (250, 250), (9, 4), (400, 420)]
+    assert 4 * sum((a * 16 + 127) // 128 for a, _ in seqs) > 512
+    _prompt(q.F16, 64, 4, 64, 32, seqs, 10, tail=2, wide=True)
+    rng = np.random.default_rng(37)
+    seqs = [(25 + int(c % 2), 25 + int(c)) for c in rng.integers(1, 60, 70)]
+    seqs[66], seqs[3] = (60, 700), (0, 9)
+    assert 2 * sum((a * 16 + 127) // 128 for a, _ in seqs) > 512
+    _prompt(q.BF16, 32, 2, 64, 16, seqs, 11, tail=1, wide=True)
+
+
 def test_prompt_wide_many_heads_one_query_each():
     _prompt(q.F16, 3, 3, 128, 16, [(390, 400)], 2, wide=True)
 
