@@ -155,9 +155,9 @@ constexpr float LOG2E = 1.44269504088896340736f;
 // chunk of the sequence's positions.  The lengths are on the device, so every workgroup derives the
 // same plan from them: where there are fewer pairs than workgroup slots, the smallest chunk (whole
 // units of 2^UNIT_LOG2 positions, at least LEAST) for which the chunks of all pairs fit the slots; a
-// pair's chunks are equal to one unit.  Sequences of up to SOLO units are not split, those of up to
-// FLAT units into at most RADIX chunks.  INDEX: the plan also numbers the pairs
-// and, where nothing is split, puts the longest first.
+// pair's chunks are equal to one unit.  With as many pairs as slots only the longest are split.  Sequences
+// of up to SOLO units are not split, those of up to FLAT units into at most RADIX chunks.  INDEX: the plan
+// also numbers the pairs and, with as many as slots, splits none and puts the longest first.
 template <int COLS_, int UNIT_LOG2_, int LEAST_, int SOLO_, int FLAT_, int RADIX_, bool INDEX_>
 struct PlanOf {
     static constexpr int COLS = COLS_, UNIT_LOG2 = UNIT_LOG2_, LEAST = LEAST_, SOLO = SOLO_;
@@ -300,6 +300,7 @@ __device__ __forceinline__ bool attn_plan_of(const KvArgs &c, int n_seq, int gro
         return wave_sum(v);
     };
     int u = 0x3fffffff;
+    bool some = false, whole = false;                  // some pairs are split; this is one of those that are not
     p.pairs = ROWS ? sum([](const AttnSeq &s) { return s.pairs; })
                    : c.n_seq * c.nkv * ((group + P::COLS - 1) / P::COLS);
     if (p.pairs >= 0 && p.pairs < slots) {
@@ -322,11 +323,47 @@ __device__ __forceinline__ bool attn_plan_of(const KvArgs &c, int n_seq, int gro
         if (c.n_seq > 1)
             return longest_first<P>(c, n_seq, group, id, p, seq);
         id = p.pairs - 1 - id;
+    } else if (slots && p.pairs > 0) {
+        // As many pairs as slots: only those of more units than a slot's share are split (their chunks
+        // come first), as far as their parts fit the slots; at twice the share they do.  64 sequences, the
+        // longest of 20000 positions, 13 MB in all a head (32 / 8 heads of 128): unsplit 286 us, 184; of
+        // 10000 (8 / 8 of 64) 107 and 61; 256 of about 1100 (12 / 2), where none is split, 58.1 and 58.8.
+        int longest = 0;
+        for (int b0 = 0; b0 < n_seq; b0 += 64) {
+            const AttnSeq s = seq(b0);
+            longest = max(longest, s.pairs ? P::units(s.n) : 0);
+        }
+        longest = wave_top(longest);
+        // (up to 2^29 units a sequence: summed in two halves)
+        const int units0 = sum([](const AttnSeq &s) { return s.pairs * P::units(s.n) & 0xFFF; });
+        const int units1 = sum([](const AttnSeq &s) { return s.pairs * P::units(s.n) >> 12; });
+        const int share = (int)((((int64_t)units1 << 12) + units0 + slots - 1) / slots);
+        int lo = max(share, max(P::LEAST, P::SOLO)), hi = max(2 * share, lo);
+        if (longest > lo) {
+            auto split_at = [&](int v) {
+                return sum([=](const AttnSeq &s) { return P::chunks(s.n, v) > 1 ? s.pairs * P::chunks(s.n, v) : 0; });
+            };
+            while (lo < hi) {
+                const int mid = lo + (hi - lo) / 2;
+                if (split_at(mid) <= slots)
+                    hi = mid;
+                else
+                    lo = mid + 1;
+            }
+            u = lo;
+            const int split = split_at(u);
+            some = true;
+            whole = id >= split;
+            id -= whole ? split : 0;
+        }
     }
     int base = 0, before = 0;
     for (int b0 = 0; b0 < n_seq; b0 += 64) {
         const AttnSeq s = seq(b0);
-        const int nc = P::chunks(s.n, u), end = base + wave_scan(nc * s.pairs);
+        int nc = P::chunks(s.n, u);
+        if (some)
+            nc = whole == (nc == 1) ? nc : 0;
+        const int end = base + wave_scan(nc * s.pairs);
         const int pe = P::INDEX ? before + wave_scan(s.pairs) : 0;
         const uint64_t in = __ballot(id < end);
         if (in) {

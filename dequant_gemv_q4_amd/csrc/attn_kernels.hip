@@ -128,7 +128,8 @@ __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a)
 //
 // Split over the length: the lengths are on the device, so every workgroup derives the same plan
 // from them: the smallest chunk (whole 128-position units) for which the chunks of all sequences
-// fit the grid's workgroup slots; a sequence's chunks are equal to one unit.  One chunk: the
+// fit the grid's workgroup slots (where the sequences alone fill them, only the longest are split); a
+// sequence's chunks are equal to one unit.  One chunk: the
 // workgroup writes o.  Several: partial O, maximum and sum go to the workspace, and of every
 // JOIN_RADIX chunks the last to finish adds them up (then of as many such groups, until one is
 // left), always in chunk order, so that results do not depend on the order of execution.  A second
@@ -559,7 +560,10 @@ static int launch_k_attn(int kv_type, const AttnArgs &a, int64_t pairs, void *st
     default: QG_ATTN_D(256); break;
     }
 #undef QG_ATTN_D
-    hipLaunchKernelGGL(k, dim3((unsigned)(pairs > slots ? pairs : slots)), dim3(256), 0,
+    // as many pairs as slots: those that are much longer than the rest are split all the same
+    const int64_t table = (int64_t)a.c.max_pages << a.c.ps_log2;
+    const int64_t grid = pairs < slots ? slots : table > AttnCols::SOLO << AttnCols::UNIT_LOG2 ? pairs + slots : pairs;
+    hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(256), 0,
                        static_cast<hipStream_t>(stream), a);
     return (int)hipGetLastError();
 }

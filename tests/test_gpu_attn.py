@@ -85,6 +85,22 @@ def test_attn_split_among_more_sequences_than_lanes():
     _decode(q.F16, 4, 1, 64, 16, lens, 6)
 
 
+@pytest.mark.parametrize("kv_type,nq,nkv,hd,n_seq,long", [
+    (q.F16, 8, 8, 64, 66, {0: 6000, 65: 1500}),       # over 64 sequences, 528 pairs for 512 slots
+    (q.BF16, 8, 8, 64, 64, {40: 9000}),               # exactly as many pairs as slots
+    (q.F16, 4, 4, 256, 64, {10: 3000, 11: 2999}),     # 256 slots
+    (q.F16, 34, 2, 128, 129, {128: 5000, 3: 700}),    # two tiles of columns a KV head
+])
+def test_attn_more_pairs_than_slots_and_a_few_long(kv_type, nq, nkv, hd, n_seq, long):
+    """Long sequences among so many others that nothing would be split for want of workgroups."""
+    lens = [int(n) for n in np.random.default_rng(38).integers(1, 200, n_seq)]
+    lens[7] = 0
+    for b, n in long.items():
+        lens[b] = n
+    _decode(kv_type, nq, nkv, hd, 16, lens, n_seq)
+    _decode(kv_type, nq, nkv, hd, 16, [300] * n_seq, n_seq + 1)
+
+
 def test_attn_sharp_scores_and_negative_scale():
     """Scores of a hundred units (one position takes all), a negative and a zero scale."""
     _decode(q.F16, 4, 2, 128, 16, [300, 77], 1, scale=1.0, qmul=4.0)
@@ -295,6 +311,11 @@ def test_prompt_wide_more_tiles_than_are_resident():
     seqs[66], seqs[3] = (60, 700), (0, 9)
     assert 2 * sum((a * 16 + 127) // 128 for a, _ in seqs) > 512
     _prompt(q.BF16, 32, 2, 64, 16, seqs, 11, tail=1, wide=True)
+
+
+def test_prompt_narrow_tiles_that_fill_the_slots():
+    """16-column tiles, 512 for 512 slots, of which the longer sequence's are split."""
+    _prompt(q.F16, 8, 8, 64, 16, [(500, 990), (497, 497)], 12)
 
 
 def test_prompt_wide_many_heads_one_query_each():
