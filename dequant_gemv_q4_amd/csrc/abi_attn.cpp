@@ -28,7 +28,7 @@ static bool heads_ok(int nq, int nkv, int hd)
     return nkv >= 1 && nq >= nkv && nq % nkv == 0 && head_dim_ok(hd) && nq <= 4096;
 }
 
-// Workspace: the sticky flag (256 bytes) and the arrival counters of qgemv_attn's split, at the same
+// Workspace: the sticky flag (256 bytes) and the arrival counters of a split joined in its launch, at the same
 // place for every operation (the counters are 0 between calls and must stay so when operations share
 // a workspace), then the partial results of a split.
 static constexpr int64_t WS_COUNT = 256, WS_PART = WS_COUNT + ATTN_MAX_SLOTS * 4;

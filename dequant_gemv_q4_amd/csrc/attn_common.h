@@ -148,6 +148,51 @@ __device__ __forceinline__ uint32_t nonfinite2(uint32_t v)
 
 constexpr float LOG2E = 1.44269504088896340736f;
 
+// Partial results that pass between workgroups of one launch, which may run on different XCDs: every
+// access carries the agent-scope bit (sc1), so that it neither stays in nor is answered by the L2 of one
+// XCD.  Offsets in floats.
+constexpr int AGENT_SCOPE = 16;                           // the buffer instructions' sc1
+typedef uint32_t au2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ void put4(__amdgpu_buffer_rsrc_t r, uint32_t at, af4 v)
+{
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(au4, v), r, 4 * at, 0, AGENT_SCOPE);
+}
+__device__ __forceinline__ af4 get4(__amdgpu_buffer_rsrc_t r, uint32_t at)
+{
+    return __builtin_bit_cast(af4, __builtin_amdgcn_raw_buffer_load_b128(r, 4 * at, 0, AGENT_SCOPE));
+}
+__device__ __forceinline__ void put2(__amdgpu_buffer_rsrc_t r, uint32_t at, float a, float b)
+{
+    const au2 v = {__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b)};
+    __builtin_amdgcn_raw_buffer_store_b64(v, r, 4 * at, 0, AGENT_SCOPE);
+}
+__device__ __forceinline__ void get2(__amdgpu_buffer_rsrc_t r, uint32_t at, float &a, float &b)
+{
+    const au2 v = __builtin_amdgcn_raw_buffer_load_b64(r, 4 * at, 0, AGENT_SCOPE);
+    const uint32_t v0 = v[0], v1 = v[1];
+    a = __builtin_bit_cast(float, v0);
+    b = __builtin_bit_cast(float, v1);
+}
+
+// Whether this workgroup is the last of `members` to arrive at a counter (left at 0 by the last).
+// Its partial results are complete in memory before it arrives: each wave waits for its own stores
+// (vmcnt counts an agent-scope store until it is done), then the workgroup meets.
+__device__ __forceinline__ bool last_to_arrive(unsigned int *cnt, int members, int *s_last)
+{
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        const unsigned int before =
+            __hip_atomic_fetch_add(cnt, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        *s_last = before + 1 == (unsigned int)members;
+        if (*s_last)
+            __hip_atomic_store(cnt, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __syncthreads();
+    asm volatile("" ::: "memory");
+    return *s_last != 0;
+}
+
 // ------------------------------------------------------------- work of a call, from lengths on the device
 //
 // The new rows of a sequence times the query heads of a KV head are columns rho = token * group +
@@ -157,7 +202,7 @@ constexpr float LOG2E = 1.44269504088896340736f;
 // units of 2^UNIT_LOG2 positions, at least LEAST) for which the chunks of all pairs fit the slots; a
 // pair's chunks are equal to one unit.  With as many pairs as slots only the longest are split.  Sequences
 // of up to SOLO units are not split, those of up to FLAT units into at most RADIX chunks.  INDEX: the plan
-// also numbers the pairs and, with as many as slots, splits none and puts the longest first.
+// also numbers the pairs and, with as many as slots, puts the longest of those that are not split first.
 template <int COLS_, int UNIT_LOG2_, int LEAST_, int SOLO_, int FLAT_, int RADIX_, bool INDEX_>
 struct PlanOf {
     static constexpr int COLS = COLS_, UNIT_LOG2 = UNIT_LOG2_, LEAST = LEAST_, SOLO = SOLO_;
@@ -176,7 +221,8 @@ struct PlanOf {
 struct AttnPlan {
     int b, pair, chunk, n_chunk;   // this workgroup's sequence, pair within it, chunk of its chunks
     int slot0;                     // workgroup id of the pair's first chunk
-    int first_pair, pairs;         // where INDEX, first_pair + pair numbers the pairs; pairs of all
+    int first_pair, pairs;         // pairs of earlier sequences (where INDEX and all), of all
+    bool all;                      // fewer pairs than slots: all of them share the slots
     int len;                       // the sequence's positions
     int row0, rows;                // its new rows
 };
@@ -276,7 +322,6 @@ __device__ __forceinline__ bool longest_first(const KvArgs &c, int n_seq, int gr
             p.pair = x * c.nkv + r % c.nkv;
             p.chunk = p.slot0 = 0;
             p.n_chunk = 1;
-            p.first_pair = id - p.pair;
             p.len = __builtin_amdgcn_readlane(s.n, l);
             p.row0 = __builtin_amdgcn_readlane(s.row0, l);
             p.rows = __builtin_amdgcn_readlane(s.rows, l);
@@ -290,8 +335,8 @@ __device__ __forceinline__ bool longest_first(const KvArgs &c, int n_seq, int gr
 
 // The plan from the sequences `seq(b0)` of lanes b0 .. b0 + 63 of each round.
 template <class P, bool ROWS, class Seq>
-__device__ __forceinline__ bool attn_plan_of(const KvArgs &c, int n_seq, int group, int slots, int id, AttnPlan &p,
-                                             Seq seq)
+__device__ __forceinline__ bool attn_plan_of(const KvArgs &c, int n_seq, int group, int slots, bool all, int id,
+                                             AttnPlan &p, Seq seq)
 {
     auto sum = [&](auto of) {
         int v = 0;
@@ -303,7 +348,8 @@ __device__ __forceinline__ bool attn_plan_of(const KvArgs &c, int n_seq, int gro
     bool some = false, whole = false;                  // some pairs are split; this is one of those that are not
     p.pairs = ROWS ? sum([](const AttnSeq &s) { return s.pairs; })
                    : c.n_seq * c.nkv * ((group + P::COLS - 1) / P::COLS);
-    if (p.pairs >= 0 && p.pairs < slots) {
+    p.all = all && p.pairs >= 0 && p.pairs < slots;
+    if (p.all) {
         // chunks <= units / u + 1 each, so u = units / (slots - pairs), over all pairs, is enough;
         // units / slots is the least that could be
         const int units = sum([](const AttnSeq &s) { return s.pairs * P::units(s.n); });
@@ -317,26 +363,20 @@ __device__ __forceinline__ bool attn_plan_of(const KvArgs &c, int n_seq, int gro
                 lo = mid + 1;
         }
         u = lo;
-    } else if (P::INDEX) {
-        if (id >= p.pairs)
-            return false;
-        if (c.n_seq > 1)
-            return longest_first<P>(c, n_seq, group, id, p, seq);
-        id = p.pairs - 1 - id;
-    } else if (slots && p.pairs > 0) {
+    } else if (slots && p.pairs > 0 && !(P::INDEX && all)) {
         // As many pairs as slots: only those of more units than a slot's share are split (their chunks
-        // come first), as far as their parts fit the slots; at twice the share they do.  64 sequences, the
-        // longest of 20000 positions, 13 MB in all a head (32 / 8 heads of 128): unsplit 286 us, 184; of
-        // 10000 (8 / 8 of 64) 107 and 61; 256 of about 1100 (12 / 2), where none is split, 58.1 and 58.8.
+        // come first), as far as their parts fit the slots; at twice the share they do.  64 sequences of
+        // one token, the longest of 20000 positions (32 / 8 heads of 128): unsplit 286 us, 184; of 10000
+        // (8 / 8 of 64) 107 and 61; 256 of about 1100 (12 / 2), where none is split, 58.1 and 58.8.
         int longest = 0;
         for (int b0 = 0; b0 < n_seq; b0 += 64) {
             const AttnSeq s = seq(b0);
             longest = max(longest, s.pairs ? P::units(s.n) : 0);
         }
         longest = wave_top(longest);
-        // (up to 2^29 units a sequence: summed in two halves)
-        const int units0 = sum([](const AttnSeq &s) { return s.pairs * P::units(s.n) & 0xFFF; });
-        const int units1 = sum([](const AttnSeq &s) { return s.pairs * P::units(s.n) >> 12; });
+        // (up to 2^41 units: summed in two halves)
+        const int units0 = sum([](const AttnSeq &s) { return (int)((int64_t)s.pairs * P::units(s.n) & 0xFFF); });
+        const int units1 = sum([](const AttnSeq &s) { return (int)((int64_t)s.pairs * P::units(s.n) >> 12); });
         const int share = (int)((((int64_t)units1 << 12) + units0 + slots - 1) / slots);
         int lo = max(share, max(P::LEAST, P::SOLO)), hi = max(2 * share, lo);
         if (longest > lo) {
@@ -356,6 +396,19 @@ __device__ __forceinline__ bool attn_plan_of(const KvArgs &c, int n_seq, int gro
             whole = id >= split;
             id -= whole ? split : 0;
         }
+    }
+    if (P::INDEX && !p.all && (whole || !some)) {
+        if (id >= p.pairs)
+            return false;
+        if (c.n_seq > 1)
+            return longest_first<P>(c, n_seq, group, id, p, [&](int b0) {
+                AttnSeq s = seq(b0);
+                const bool mine = !some || P::chunks(s.n, u) == 1;
+                s.n = mine ? s.n : 0;
+                s.rows = mine ? s.rows : 0;
+                return s;
+            });
+        id = p.pairs - 1 - id;
     }
     int base = 0, before = 0;
     for (int b0 = 0; b0 < n_seq; b0 += 64) {
@@ -379,7 +432,8 @@ __device__ __forceinline__ bool attn_plan_of(const KvArgs &c, int n_seq, int gro
             p.slot0 += p.pair * p.n_chunk;
             p.chunk = id - p.slot0;
             // (row starts that are not in order could give sums beyond an int)
-            return !ROWS || (p.pair >= 0 && p.pair < __builtin_amdgcn_readlane(s.pairs, l));
+            return !ROWS || (p.pair >= 0 && p.pair < __builtin_amdgcn_readlane(s.pairs, l) &&
+                             (p.n_chunk == 1 || (p.slot0 >= 0 && p.slot0 + p.n_chunk <= slots)));
         }
         base = __builtin_amdgcn_readlane(end, 63);
         before = P::INDEX ? __builtin_amdgcn_readlane(pe, 63) : 0;
@@ -390,16 +444,18 @@ __device__ __forceinline__ bool attn_plan_of(const KvArgs &c, int n_seq, int gro
 // Workgroup id -> its place in the plan; false if the plan has fewer workgroups.  All threads of the
 // workgroup call it; every wave finds the same.  Up to 64 sequences are held a lane each, more in LDS
 // scratch (QG_ATTN_MAX_SEQ entries, free again afterwards).  ROWS: sequence b has the rows between its
-// q_start and the next; else one row, row b.  slots 0: nothing is split.
+// q_start and the next; else one row, row b.  slots 0: nothing is split.  INDEX: all pairs
+// or only the longest are split, as `all` says.
 template <class P, bool ROWS>
 __device__ __forceinline__ bool attn_plan(const KvArgs &c, int group, int slots, int id, AttnPlan &p,
-                                          AttnSeq *scratch)
+                                          AttnSeq *scratch, bool all = true)
 {
     const int lane = threadIdx.x & 63;
     auto load = [&](int b) {
-        AttnSeq s = {0, 0, b, 1};
+        AttnSeq s = {0, 0, b, 0};
         if (b < c.n_seq) {
             s.n = seq_len(c, b);
+            s.rows = 1;
             if constexpr (ROWS) {
                 s.row0 = row_start(c, b);
                 s.rows = max(row_start(c, b + 1) - s.row0, 0);
@@ -410,12 +466,12 @@ __device__ __forceinline__ bool attn_plan(const KvArgs &c, int group, int slots,
     };
     if (c.n_seq <= 64) {
         const AttnSeq s = load(lane);
-        return attn_plan_of<P, ROWS>(c, 1, group, slots, id, p, [&](int) { return s; });
+        return attn_plan_of<P, ROWS>(c, 1, group, slots, all, id, p, [&](int) { return s; });
     }
     for (int b = threadIdx.x; b < (c.n_seq + 63) / 64 * 64; b += 256)
         scratch[b] = load(b);
     __syncthreads();
-    const bool found = attn_plan_of<P, ROWS>(c, c.n_seq, group, slots, id, p,
+    const bool found = attn_plan_of<P, ROWS>(c, c.n_seq, group, slots, all, id, p,
                                              [&](int b0) { return scratch[b0 + lane]; });
     __syncthreads();
     return found;

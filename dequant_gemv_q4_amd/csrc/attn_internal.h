@@ -73,6 +73,8 @@ struct RouteArgs {
 struct PromptPlan {
     int64_t pairs;              // pairs of a tile and a KV head, at most
     int slots;                  // workgroup slots of a split over the cache's length, 0: none
+    bool second;                // a second launch joins the parts
+    int64_t grid;               // workgroups
 };
 PromptPlan plan_prompt(int64_t n_rows, int n_seq, int nkv, int group, int hd, int64_t positions);
 

@@ -146,50 +146,6 @@ constexpr int JOIN_RADIX = 8;
 typedef PlanOf<16, 7, 2, 4, 32, JOIN_RADIX, false> AttnCols;
 
 // Partial results of a slot: the tile's O (unnormalised) [cols][hd], then (maximum, sum) [cols].
-// They pass between workgroups of one launch, which may run on different XCDs: every access carries
-// the agent-scope bit (sc1), so that it neither stays in nor is answered by the L2 of one XCD.
-constexpr int AGENT_SCOPE = 16;                           // the buffer instructions' sc1
-typedef uint32_t au2 __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ void put4(__amdgpu_buffer_rsrc_t r, uint32_t at, af4 v)
-{
-    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(au4, v), r, 4 * at, 0, AGENT_SCOPE);
-}
-__device__ __forceinline__ af4 get4(__amdgpu_buffer_rsrc_t r, uint32_t at)
-{
-    return __builtin_bit_cast(af4, __builtin_amdgcn_raw_buffer_load_b128(r, 4 * at, 0, AGENT_SCOPE));
-}
-__device__ __forceinline__ void put2(__amdgpu_buffer_rsrc_t r, uint32_t at, float a, float b)
-{
-    const au2 v = {__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b)};
-    __builtin_amdgcn_raw_buffer_store_b64(v, r, 4 * at, 0, AGENT_SCOPE);
-}
-__device__ __forceinline__ void get2(__amdgpu_buffer_rsrc_t r, uint32_t at, float &a, float &b)
-{
-    const au2 v = __builtin_amdgcn_raw_buffer_load_b64(r, 4 * at, 0, AGENT_SCOPE);
-    const uint32_t v0 = v[0], v1 = v[1];
-    a = __builtin_bit_cast(float, v0);
-    b = __builtin_bit_cast(float, v1);
-}
-
-// Whether this workgroup is the last of `members` to arrive at a counter (left at 0 by the last).
-// Its partial results are complete in memory before it arrives: each wave waits for its own stores
-// (vmcnt counts an agent-scope store until it is done), then the workgroup meets.
-__device__ __forceinline__ bool last_to_arrive(unsigned int *cnt, int members, int *s_last)
-{
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        const unsigned int before =
-            __hip_atomic_fetch_add(cnt, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        *s_last = before + 1 == (unsigned int)members;
-        if (*s_last)
-            __hip_atomic_store(cnt, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-    __syncthreads();
-    asm volatile("" ::: "memory");
-    return *s_last != 0;
-}
-
 template <int T, int D, bool ROWS>
 __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn(AttnArgs a)
 {

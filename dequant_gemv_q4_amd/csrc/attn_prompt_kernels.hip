@@ -51,7 +51,9 @@ __device__ __forceinline__ void pt_barrier()
 
 // 128 columns; chunks of whole steps, at least eight.  A partial result is 66 KB (heads of 128), written
 // once and read once, so that up to sixteen steps are not split (one sequence of 1024 rows, 32 / 8
-// heads: 39 us, in halves 59; sixteen of 32 rows behind 4000 positions: 122 us unsplit, 56).
+// heads: 39 us, in halves 59; sixteen of 32 rows behind 4000 positions: 122 us unsplit, 56).  With as many
+// tiles as slots, those behind contexts longer than a slot's share are split (512 rows behind 29500
+// positions beside five prompts of 307, 32 / 8 heads of 128: 842 us unsplit, 469).
 typedef PlanOf<PT_ROWS, 6, 8, 16, 0, 0, true> PromptCols;
 
 // A split tile, for its join.
@@ -61,7 +63,10 @@ struct PromptSplit {
 
 __host__ __device__ constexpr int64_t prompt_part_floats(int hd) { return (int64_t)PT_ROWS * (hd + 2); }
 
-template <int T, int D>
+// FEW: there are at least as many tiles as slots, and only those behind much longer contexts than the rest
+// are split and joined in this launch (in a kernel of its own: the code of that join costs nine prompts
+// without a split 36.3 -> 38.2 us).  Else, with slots, all are split and a second launch joins.
+template <int T, int D, bool FEW>
 __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs a, int slots)
 {
     constexpr int NP = PIECES<T>, KB = D / 16, DT = D / 32;
@@ -73,15 +78,15 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
     constexpr int HALF = PT_STEP * D * 2;              // bytes of a K (or V) buffer
     constexpr int PASS = HALF / 4096;                  // copies of a wave for either
     __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * HALF];   // K0 V0 K1 V1
-    __shared__ int s_odd[4];
+    __shared__ int s_odd[4], s_last;
     const KvArgs &c = a.c;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 31, hf = lane >> 5;
     AttnPlan w;
     const bool work = attn_plan<PromptCols, true>(c, a.group, slots, blockIdx.x, w,
-                                                  reinterpret_cast<AttnSeq *>(lds));
-    if (blockIdx.x == 0 && tid == 0 && slots)
-        *a.pairs = w.pairs;
+                                                  reinterpret_cast<AttnSeq *>(lds), !FEW);
+    if (!FEW && blockIdx.x == 0 && tid == 0 && slots)
+        *a.pairs = w.all ? w.pairs : 0;
     if (!work)
         return;
     // pairs of a sequence: tile by tile, heads side by side (the workgroups of one XCD share heads)
@@ -98,9 +103,9 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
     const int units = PromptCols::units(w.len), per = units / w.n_chunk, more = units % w.n_chunk;
     const int s0 = w.chunk * per + min(w.chunk, more);
     const int s1 = min(s0 + per + (w.chunk < more ? 1 : 0), PromptCols::units(p.hi));
-    if (w.n_chunk > 1 && w.chunk == 0 && tid == 0)
+    if (w.all && w.n_chunk > 1 && w.chunk == 0 && tid == 0)
         a.splits[w.first_pair + w.pair] = PromptSplit{w.slot0, w.n_chunk, p.row0, p.rows, p.rho0, hkv, {0, 0}};
-    if (w.n_chunk == 1 && slots && tid == 0 && w.first_pair + w.pair < PROMPT_SPLITS)
+    if (w.all && w.n_chunk == 1 && tid == 0)
         a.splits[w.first_pair + w.pair].n_chunk = 1;
 
     // this lane's row
@@ -403,7 +408,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
 
     // O^T: lane's row, channels 32 d + 8 (r / 4) + 4 hf + r % 4
     l = sum_x32(l);
-    if (w.n_chunk > 1) {
+    if (!FEW && w.n_chunk > 1) {
         float *part = a.part + (int64_t)(w.slot0 + w.chunk) * prompt_part_floats(D);
         float *row = part + (32 * wave + col) * D + 4 * hf;
 #pragma unroll
@@ -417,7 +422,59 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
             ml[0] = m;
             ml[1] = l;
         }
-    } else if (live) {
+        return;
+    }
+    if (FEW && w.n_chunk > 1) {
+        // one of a few split tiles among many whole ones: the last of its workgroups to finish adds the
+        // parts, in the order of the chunks
+        const uint32_t stride = (uint32_t)prompt_part_floats(D);
+        const __amdgpu_buffer_rsrc_t part = __builtin_amdgcn_make_buffer_rsrc(
+            a.part + (int64_t)w.slot0 * stride, 0, w.n_chunk * stride * 4, 0x00020000);
+        const uint32_t row = (32 * wave + col) * D + 4 * hf, ml = PT_ROWS * D + 2 * (32 * wave + col);
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                put4(part, w.chunk * stride + row + 32 * d + 8 * r,
+                     af4{o[d][4 * r], o[d][4 * r + 1], o[d][4 * r + 2], o[d][4 * r + 3]});
+        if (hf == 0)
+            put2(part, w.chunk * stride + ml, m, l);
+        if (!last_to_arrive(a.count + w.slot0, w.n_chunk, &s_last))
+            return;
+        m = -INFINITY;
+        for (int k = 0; k < w.n_chunk; ++k) {
+            float mk, lk;
+            get2(part, k * stride + ml, mk, lk);
+            m = fmaxf(m, mk);
+        }
+        l = 0.f;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                o[d][r] = 0.f;
+#pragma unroll 1
+        for (int k = 0; k < w.n_chunk; ++k) {
+            float mk, lk;
+            get2(part, k * stride + ml, mk, lk);
+            const float f = mk == -INFINITY ? 0.f : mk == m ? 1.0f : __builtin_amdgcn_exp2f(mk - m);
+            af4 x[DT][4];
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    x[d][r] = get4(part, k * stride + row + 32 * d + 8 * r);
+            if (f != 0.f) {
+                l += lk * f;
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        o[d][r] += x[d][r / 4][r % 4] * f;
+            }
+        }
+    }
+    if (live) {
         const float inv = m == -INFINITY ? 0.f : 1.0f / l;
         float *row = a.o + ((int64_t)(p.row0 + tok) * a.nq + head) * D + 4 * hf;
 #pragma unroll
@@ -509,15 +566,18 @@ __global__ __launch_bounds__(256) void k_attn_prompt_join(AttnArgs a)
     }
 }
 
-// Pairs (tiles times KV heads) of a call at most, and whether any may be split: there could be fewer
-// than slots, and the table holds more positions than a chunk alone takes.
+// Pairs (tiles times KV heads) of a call at most; whether any may be split (the table holds more positions
+// than a chunk alone takes); and whether that is for having fewer than slots, so that a second launch joins
+// them, or for being longer than others (the tiles of one sequence are alike).
 PromptPlan plan_prompt(int64_t n_rows, int n_seq, int nkv, int group, int hd, int64_t positions)
 {
     PromptPlan p;
     p.pairs = nkv * (n_rows * group / PT_ROWS + n_seq);
-    p.slots = nkv * (n_rows * group / PT_ROWS) < prompt_slots(hd) && p.pairs <= PROMPT_SPLITS &&
-                      positions > (PromptCols::SOLO << PromptCols::UNIT_LOG2)
-                  ? prompt_slots(hd) : 0;
+    const bool may = positions > (PromptCols::SOLO << PromptCols::UNIT_LOG2);
+    // (a sequence's last tile is half full on average)
+    p.second = may && nkv * (n_rows * group / PT_ROWS + n_seq / 2) < prompt_slots(hd) && p.pairs <= PROMPT_SPLITS;
+    p.slots = p.second || (may && n_seq > 1) ? prompt_slots(hd) : 0;
+    p.grid = !p.second ? p.pairs + p.slots : p.pairs > p.slots ? p.pairs : p.slots;
     return p;
 }
 
@@ -538,8 +598,11 @@ int launch_attn_prompt(int kv_type, const AttnArgs &a, void *stream)
         return launch_attn_rows(kv_type, a, stream);
     hipStream_t s = static_cast<hipStream_t>(stream);
     const PromptPlan p = plan_prompt(a.c.n_rows, a.c.n_seq, a.c.nkv, a.group, a.c.hd, table);
+    const bool few = p.slots && !p.second;
     void (*k)(AttnArgs, int) = nullptr;
-#define QG_PROMPT_D(DD) k = kv_type == KV_F16 ? k_attn_prompt<KV_F16, DD> : k_attn_prompt<KV_BF16, DD>
+#define QG_PROMPT_D(DD)                                                                                  \
+    k = kv_type == KV_F16 ? few ? k_attn_prompt<KV_F16, DD, true> : k_attn_prompt<KV_F16, DD, false>     \
+                          : few ? k_attn_prompt<KV_BF16, DD, true> : k_attn_prompt<KV_BF16, DD, false>
     switch (a.c.hd) {
     case 64: QG_PROMPT_D(64); break;
     case 96: QG_PROMPT_D(96); break;
@@ -548,9 +611,9 @@ int launch_attn_prompt(int kv_type, const AttnArgs &a, void *stream)
     default: QG_PROMPT_D(256); break;
     }
 #undef QG_PROMPT_D
-    hipLaunchKernelGGL(k, dim3((unsigned)(p.pairs > p.slots ? p.pairs : p.slots)), dim3(256), 0, s, a, p.slots);
+    hipLaunchKernelGGL(k, dim3((unsigned)p.grid), dim3(256), 0, s, a, p.slots);
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !p.slots)
+    if (e != hipSuccess || !p.second)
         return (int)e;
     // the fewer tiles, the more workgroups share one, about 4096 in all (sixteen sequences of 32 rows
     // behind 4000 positions: 56.3 us, with 2048 61.4; 8192 that find nothing to join cost 1 us more)

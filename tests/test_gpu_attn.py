@@ -313,6 +313,32 @@ def test_prompt_wide_more_tiles_than_are_resident():
     _prompt(q.BF16, 32, 2, 64, 16, seqs, 11, tail=1, wide=True)
 
 
+@pytest.mark.parametrize("kv_type,hd,seqs", [
+    (q.F16, 64, [(40, 6000), (300, 300), (250, 250), (0, 5000), (400, 420), (9, 3000), (330, 330), (100, 100)]),
+    (q.BF16, 128, [(10, 2600), (300, 300), (250, 250), (400, 420), (330, 330), (100, 100)]),
+    (q.F16, 256, [(10, 2600), (300, 300), (250, 250), (12, 5)]),                    # 256 slots
+    (q.BF16, 64, [(7, 3000)] + [(20, 25)] * 70 + [(9, 2500)]),                      # more than lanes
+])
+def test_prompt_wide_a_few_long_tiles_among_many(kv_type, hd, seqs):
+    """More tiles than slots, of which those behind long contexts are split; their parts are joined within
+    the launch."""
+    nq, nkv = (96, 4) if len(seqs) > 64 else (64, 4)
+    slots = 512 if hd <= 128 else 256
+    assert nkv * (sum(a for a, _ in seqs) * (nq // nkv) // 128) >= slots
+    _prompt(kv_type, nq, nkv, hd, 32, seqs, 14, tail=2, wide=True)
+
+
+@pytest.mark.parametrize("n_seq", [70, 80])
+def test_prompt_wide_tiles_that_fill_the_slots_only_when_counted(n_seq):
+    """Sequences of four tiles, the last hardly begun: fewer pairs than slots by rows, more in fact, two behind
+    long contexts."""
+    rng = np.random.default_rng(39)
+    seqs = [(25, 25 + int(c)) for c in rng.integers(0, 60, n_seq)]
+    seqs[n_seq - 5], seqs[2] = (25, 5000), (25, 2500)
+    assert 2 * (sum(a for a, _ in seqs) * 16 // 128) < 512 <= 2 * sum((a * 16 + 127) // 128 for a, _ in seqs)
+    _prompt(q.BF16, 32, 2, 64, 16, seqs, 15, tail=1, wide=True)
+
+
 def test_prompt_narrow_tiles_that_fill_the_slots():
     """16-column tiles, 512 for 512 slots, of which the longer sequence's are split."""
     _prompt(q.F16, 8, 8, 64, 16, [(500, 990), (497, 497)], 12)
@@ -614,7 +640,9 @@ def test_one_workspace_serves_every_operation_in_turn():
 
 
 @pytest.mark.parametrize("seqs,wide", [([(1, 9000), (1, 17), (1, 2500)], False), ([(3, 6000), (2, 900)], False),
-                                       ([(70, 6000)], True), ([(420, 420)], True)])
+                                       ([(70, 6000)], True), ([(420, 420)], True),
+                                       ([(200, 6000)] + [(600, 600)] * 9, True),
+                                       ([(1, 20000)] + [(1, 30)] * 300, False)])
 def test_repeated_calls_are_bitwise_identical(seqs, wide):
     rng = np.random.default_rng(22)
     nq, nkv, hd = 12, 2, 128
