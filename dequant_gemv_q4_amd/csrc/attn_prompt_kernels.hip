@@ -590,7 +590,9 @@ int launch_attn_prompt(int kv_type, const AttnArgs &a, void *stream)
     // the table is short (128-row tiles -> 16 columns, us: 16 sequences x 4 rows x 4000 positions, 32 /
     // 8 heads of 128, 64.7 -> 39.3; one of 32 rows x 20000, 12 / 2 heads, 36.3 -> 34.1; of 128 rows
     // 57.9 -> 84.1; three of 31 rows alone 9.6 -> 6.8; one of 128 rows alone, 32 / 8 heads, 11.4 -> 8.4;
-    // 16 of 32 rows alone, twice the resident workgroups, 11.0 -> 19.9).
+    // 16 of 32 rows alone, twice the resident workgroups, 11.0 -> 19.9).  64 sequences of 4 rows x 4000
+    // positions would gain as well (189.7 -> 181.9, at 8 rows 192 -> 285), but as many rows may be one
+    // prompt among single tokens, whose cache it would read a hundred times.
     const int64_t pairs = a.c.nkv * (a.c.n_rows * a.group / 16 + a.c.n_seq);
     const int64_t table = (int64_t)a.c.max_pages << a.c.ps_log2;
     if (pairs <= attn_slots(a.c.hd) &&
