@@ -333,10 +333,27 @@ __device__ __forceinline__ bool longest_first(const KvArgs &c, int n_seq, int gr
     return false;
 }
 
+// Units of the longest sequence and of all pairs (up to 2^41, in two halves).
+struct AttnTotals {
+    int longest, low, high;
+    template <class P> __device__ __forceinline__ void add(const AttnSeq &s)
+    {
+        const int n = P::units(s.n);
+        const int64_t v = (int64_t)s.pairs * n;
+        longest = max(longest, s.pairs ? n : 0);
+        low += (int)(v & 0xFFF);
+        high += (int)(v >> 12);
+    }
+    __device__ __forceinline__ AttnTotals of_wave() const
+    {
+        return {wave_top(longest), wave_sum(low), wave_sum(high)};
+    }
+};
+
 // The plan from the sequences `seq(b0)` of lanes b0 .. b0 + 63 of each round.
-template <class P, bool ROWS, class Seq>
+template <class P, bool ROWS, class Seq, class Totals>
 __device__ __forceinline__ bool attn_plan_of(const KvArgs &c, int n_seq, int group, int slots, bool all, int id,
-                                             AttnPlan &p, Seq seq)
+                                             AttnPlan &p, Seq seq, Totals totals)
 {
     auto sum = [&](auto of) {
         int v = 0;
@@ -367,19 +384,11 @@ __device__ __forceinline__ bool attn_plan_of(const KvArgs &c, int n_seq, int gro
         // As many pairs as slots: only those of more units than a slot's share are split (their chunks
         // come first), as far as their parts fit the slots; at twice the share they do.  64 sequences of
         // one token, the longest of 20000 positions (32 / 8 heads of 128): unsplit 286 us, 184; of 10000
-        // (8 / 8 of 64) 107 and 61; 256 of about 1100 (12 / 2), where none is split, 58.1 and 58.8.
-        int longest = 0;
-        for (int b0 = 0; b0 < n_seq; b0 += 64) {
-            const AttnSeq s = seq(b0);
-            longest = max(longest, s.pairs ? P::units(s.n) : 0);
-        }
-        longest = wave_top(longest);
-        // (up to 2^41 units: summed in two halves)
-        const int units0 = sum([](const AttnSeq &s) { return (int)((int64_t)s.pairs * P::units(s.n) & 0xFFF); });
-        const int units1 = sum([](const AttnSeq &s) { return (int)((int64_t)s.pairs * P::units(s.n) >> 12); });
-        const int share = (int)((((int64_t)units1 << 12) + units0 + slots - 1) / slots);
+        // (8 / 8 of 64) 107 and 61; 256 of about 1100 (12 / 2), where none is split, 58.1 and 58.2.
+        const AttnTotals t = totals();
+        const int share = (int)((((int64_t)t.high << 12) + t.low + slots - 1) / slots);
         int lo = max(share, max(P::LEAST, P::SOLO)), hi = max(2 * share, lo);
-        if (longest > lo) {
+        if (t.longest > lo) {
             auto split_at = [&](int v) {
                 return sum([=](const AttnSeq &s) { return P::chunks(s.n, v) > 1 ? s.pairs * P::chunks(s.n, v) : 0; });
             };
@@ -409,6 +418,20 @@ __device__ __forceinline__ bool attn_plan_of(const KvArgs &c, int n_seq, int gro
                 return s;
             });
         id = p.pairs - 1 - id;
+    }
+    if (!P::INDEX && !ROWS && !p.all && !some) {           // every sequence has the same pairs
+        const int per = c.nkv * ((group + P::COLS - 1) / P::COLS);
+        p.b = id / per;
+        if (p.b >= c.n_seq)
+            return false;
+        const AttnSeq s = seq(p.b & ~63);
+        p.pair = id % per;
+        p.chunk = p.slot0 = 0;
+        p.n_chunk = 1;
+        p.len = __builtin_amdgcn_readlane(s.n, p.b & 63);
+        p.row0 = p.b;
+        p.rows = 1;
+        return true;
     }
     int base = 0, before = 0;
     for (int b0 = 0; b0 < n_seq; b0 += 64) {
@@ -466,13 +489,34 @@ __device__ __forceinline__ bool attn_plan(const KvArgs &c, int group, int slots,
     };
     if (c.n_seq <= 64) {
         const AttnSeq s = load(lane);
-        return attn_plan_of<P, ROWS>(c, 1, group, slots, all, id, p, [&](int) { return s; });
+        return attn_plan_of<P, ROWS>(c, 1, group, slots, all, id, p, [&](int) { return s; }, [&]() {
+            AttnTotals t = {0, 0, 0};
+            t.add<P>(s);
+            return t.of_wave();
+        });
     }
-    for (int b = threadIdx.x; b < (c.n_seq + 63) / 64 * 64; b += 256)
-        scratch[b] = load(b);
+    __shared__ AttnTotals s_tot[4];
+    AttnTotals t = {0, 0, 0};
+    for (int b = threadIdx.x; b < (c.n_seq + 63) / 64 * 64; b += 256) {
+        const AttnSeq s = load(b);
+        scratch[b] = s;
+        t.add<P>(s);
+    }
+    t = t.of_wave();
+    if (lane == 0)
+        s_tot[threadIdx.x >> 6] = t;
     __syncthreads();
-    const bool found = attn_plan_of<P, ROWS>(c, c.n_seq, group, slots, all, id, p,
-                                             [&](int b0) { return scratch[b0 + lane]; });
+    const bool found = attn_plan_of<P, ROWS>(
+        c, c.n_seq, group, slots, all, id, p, [&](int b0) { return scratch[b0 + lane]; }, [&]() {
+            AttnTotals v = {0, 0, 0};
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                v.longest = max(v.longest, s_tot[w].longest);
+                v.low += s_tot[w].low;
+                v.high += s_tot[w].high;
+            }
+            return v;
+        });
     __syncthreads();
     return found;
 }
