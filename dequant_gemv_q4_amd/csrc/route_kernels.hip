@@ -18,8 +18,9 @@
 //
 // Bound by VALU issue, not by the 8.7 MB it moves: 8000 x 256, sigmoid, 8 groups, top 8 of 4 groups,
 // takes 31.1 us with shuffled 64-bit maxima and a serial scan of the groups, 15.2 us with lane shifts
-// and 64-bit rounds, 12.6 us as it is (700 VALU instructions a row); 16 x 64, top 8, 5.4 us, of which the
-// kernel is 3.0.
+// and 64-bit rounds, 12.6 us as it is (700 VALU instructions a row); 16 x 64, top 8, 5.3 us, of which the
+// kernel is 3.0.  8000 x 1000, softmax, 8 groups of 125 (no run of lanes), a lane scanning a group: 192 us,
+// eight lanes 69.
 #include <hip/hip_runtime.h>
 
 #include "attn_internal.h"
@@ -138,8 +139,10 @@ struct Top2 {
     }
 };
 
+// Eight and sixteen experts a lane are held to 128 registers: left alone, all their exponentials run side by
+// side in 478 (8000 x 1024: 84.6 us, 40.2; x 512: 23.7, 21.8).
 template <int NI>
-__global__ __launch_bounds__(256) void k_route(RouteArgs a)
+__global__ __launch_bounds__(256, NI >= 8 ? 4 : 1) void k_route(RouteArgs a)
 {
     __shared__ double s_c[4][64 * NI];
     __shared__ uint8_t s_keep[4][64 * NI];
@@ -200,8 +203,10 @@ __global__ __launch_bounds__(256) void k_route(RouteArgs a)
                     keep = ~0u;
                 }
         } else {
-            // any other size: the choices in LDS, a lane per group (groups lane, lane + 64, ...)
+            // any other size: the choices in LDS, 2^k lanes per group, or one for groups lane, lane + 64, ...
             const int size = a.n_exp / a.n_group;
+            const int lanes = a.n_group > 32 ? 1 : 1 << (31 - __builtin_clz(64 / a.n_group));
+            const int step = 64 / lanes, first = lane / lanes, sub = lane % lanes;
             auto wave_sync = []() {
                 __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
                 __builtin_amdgcn_wave_barrier();
@@ -214,14 +219,18 @@ __global__ __launch_bounds__(256) void k_route(RouteArgs a)
             uint64_t gk[NI];
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
-                const int g = lane + 64 * i;
+                const int g = first + step * i;
                 gk[i] = 0;
-                s_keep[wave][g] = 0;
-                if (g < a.n_group) {
+                s_keep[wave][lane + 64 * i] = 0;
+                if (step * i < a.n_group) {
                     Top2 t = {-INFINITY, -INFINITY};
-                    for (int j = 0; j < size; ++j)
-                        t.add(s_c[wave][g * size + j]);
-                    gk[i] = route_key(a.group_top == 2 ? t.a + t.b : t.a);
+                    if (g < a.n_group)
+                        for (int j = sub; j < size; j += lanes)
+                            t.add(s_c[wave][g * size + j]);
+                    for (int x = 1; x < lanes; x *= 2)
+                        t.merge(__shfl_xor(t.a, x), __shfl_xor(t.b, x));
+                    if (g < a.n_group && sub == 0)
+                        gk[i] = route_key(a.group_top == 2 ? t.a + t.b : t.a);
                 }
             }
             for (int x = 0; x < a.topk_group; ++x) {
@@ -231,12 +240,12 @@ __global__ __launch_bounds__(256) void k_route(RouteArgs a)
                 for (int i = 0; i < NI; ++i)
                     if (gk[i] > k) {
                         k = gk[i];
-                        idx = lane + 64 * i;
+                        idx = first + step * i;
                     }
                 wave_best(k, idx);
 #pragma unroll
                 for (int i = 0; i < NI; ++i)
-                    if (idx == lane + 64 * i) {
+                    if (sub == 0 && idx == first + step * i) {
                         gk[i] = 0;
                         s_keep[wave][idx] = 1;
                     }

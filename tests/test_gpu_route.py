@@ -48,6 +48,22 @@ def test_route(score, n, groups, gtop, keep, topk, bias, renorm):
     _check(z, score, b, groups, gtop, keep, topk, renorm, 2.5 if renorm else 1.0)
 
 
+@pytest.mark.parametrize("n,groups,gtop,keep,topk", [
+    (1000, 8, 2, 4, 8), (1000, 125, 1, 7, 8), (1000, 20, 2, 3, 8), (999, 27, 2, 5, 6), (660, 33, 2, 8, 8), (1020, 340, 2, 9, 8),
+    (96, 32, 1, 4, 4), (10, 2, 2, 1, 3), (189, 63, 1, 8, 8)])
+def test_route_groups_that_are_no_run_of_lanes(n, groups, gtop, keep, topk):
+    """A group's lanes are 32 down to one; equal choices within and across them go to the lower index."""
+    rng = np.random.default_rng([92, n, groups])
+    z = (rng.standard_normal((9, n)) * 2).astype(np.float32)
+    z[3] = np.round(z[3])
+    z[4] = 0.25
+    z[5, ::2] = -np.inf
+    b = np.round(rng.standard_normal(n) * 8).astype(np.float32) / 64
+    for bias in (None, b):
+        _check(z, q.SCORE_SIGMOID, bias, groups, gtop, keep, topk, True, 1.0)
+        _check(z, q.SCORE_SOFTMAX, bias, groups, gtop, keep, topk, False, 2.0)
+
+
 def test_route_many_rows():
     rng = np.random.default_rng(5)
     z = rng.standard_normal((4099, 64)).astype(np.float32)
