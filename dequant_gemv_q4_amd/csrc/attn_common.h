@@ -203,11 +203,12 @@ __device__ __forceinline__ bool last_to_arrive(unsigned int *cnt, int members, i
 // pair's chunks are equal to one unit.  With as many pairs as slots only the longest are split.  Sequences
 // of up to SOLO units are not split, those of up to FLAT units into at most RADIX chunks.  INDEX: the plan
 // also numbers the pairs and, with as many as slots, puts the longest of those that are not split first.
-template <int COLS_, int UNIT_LOG2_, int LEAST_, int SOLO_, int FLAT_, int RADIX_, bool INDEX_>
+// SIDE: a KV head's tiles that read the same chunk come side by side, not each tile's chunks.
+template <int COLS_, int UNIT_LOG2_, int LEAST_, int SOLO_, int FLAT_, int RADIX_, bool INDEX_, bool SIDE_>
 struct PlanOf {
     static constexpr int COLS = COLS_, UNIT_LOG2 = UNIT_LOG2_, LEAST = LEAST_, SOLO = SOLO_;
     static constexpr int FLAT = FLAT_, RADIX = RADIX_;
-    static constexpr bool INDEX = INDEX_;
+    static constexpr bool INDEX = INDEX_, SIDE = SIDE_;
     static __device__ __forceinline__ int units(int n) { return (n + (1 << UNIT_LOG2) - 1) >> UNIT_LOG2; }
     // at least one, so that an empty sequence's rows are written
     static __device__ __forceinline__ int chunks(int n, int u)
@@ -220,7 +221,7 @@ struct PlanOf {
 
 struct AttnPlan {
     int b, pair, chunk, n_chunk;   // this workgroup's sequence, pair within it, chunk of its chunks
-    int slot0;                     // workgroup id of the pair's first chunk
+    int slot0;                     // slot of the pair's first chunk
     int first_pair, pairs;         // pairs of earlier sequences (where INDEX and all), of all
     bool all;                      // fewer pairs than slots: all of them share the slots
     int len;                       // the sequence's positions
@@ -451,11 +452,18 @@ __device__ __forceinline__ bool attn_plan_of(const KvArgs &c, int n_seq, int gro
             p.first_pair = P::INDEX ? __builtin_amdgcn_readlane(pe - s.pairs, l) : 0;
             p.row0 = ROWS ? __builtin_amdgcn_readlane(s.row0, l) : p.b;
             p.rows = ROWS ? __builtin_amdgcn_readlane(s.rows, l) : 1;
-            p.pair = (id - p.slot0) / p.n_chunk;
+            const int pairs = __builtin_amdgcn_readlane(s.pairs, l), r = id - p.slot0;
+            if (!P::SIDE) {
+                p.pair = r / p.n_chunk;
+                p.chunk = r - p.pair * p.n_chunk;
+            } else {
+                const int tiles = pairs / c.nkv, head = r / (tiles * p.n_chunk), x = r - head * tiles * p.n_chunk;
+                p.chunk = x / tiles;
+                p.pair = head * tiles + x - p.chunk * tiles;
+            }
             p.slot0 += p.pair * p.n_chunk;
-            p.chunk = id - p.slot0;
             // (row starts that are not in order could give sums beyond an int)
-            return !ROWS || (p.pair >= 0 && p.pair < __builtin_amdgcn_readlane(s.pairs, l) &&
+            return !ROWS || (p.pair >= 0 && p.pair < pairs && p.chunk >= 0 &&
                              (p.n_chunk == 1 || (p.slot0 >= 0 && p.slot0 + p.n_chunk <= slots)));
         }
         base = __builtin_amdgcn_readlane(end, 63);

@@ -57,6 +57,7 @@ struct AttnArgs {
     PromptSplit *splits;        // workspace: its split tiles, by pair
     unsigned int *count;        // workspace: arrival counters of a split, one per slot, 0 between calls
     int nq, group;              // query heads; query heads per KV head
+    int side;                   // set by the launcher: tiles that read the same positions
     float scale;
 };
 

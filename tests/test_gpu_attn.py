@@ -101,6 +101,14 @@ def test_attn_more_pairs_than_slots_and_a_few_long(kv_type, nq, nkv, hd, n_seq, 
     _decode(kv_type, nq, nkv, hd, 16, [300] * n_seq, n_seq + 1)
 
 
+@pytest.mark.parametrize("kv_type,nq,nkv,hd,lens", [
+    (q.F16, 40, 2, 128, [9000, 100, 3000]), (q.BF16, 66, 2, 64, [5000]), (q.F16, 17, 1, 256, [2500, 700, 0, 1]),
+    (q.BF16, 40, 2, 96, [600 + i for i in range(130)] + [4000])])
+def test_attn_tiles_side_by_side(kv_type, nq, nkv, hd, lens):
+    """More than 16 query heads a KV head, with and without a split."""
+    _decode(kv_type, nq, nkv, hd, 16, lens, 40)
+
+
 def test_attn_sharp_scores_and_negative_scale():
     """Scores of a hundred units (one position takes all), a negative and a zero scale."""
     _decode(q.F16, 4, 2, 128, 16, [300, 77], 1, scale=1.0, qmul=4.0)
