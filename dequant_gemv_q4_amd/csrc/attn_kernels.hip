@@ -25,7 +25,15 @@ __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a)
 {
     constexpr int BLOCK = 1 << BL, PIECES_V = BLOCK / 8;
     const KvArgs &c = a.c;
-    const int tid = threadIdx.x, lane = tid & 63, h = blockIdx.y, id = blockIdx.x;
+    const int tid = threadIdx.x, lane = tid & 63, h = blockIdx.y;
+    int id = blockIdx.x;
+    if (c.q_start && c.ps_log2 > BL) {
+        // two blocks to an XCD, eight workgroups apart: halves of the same lines of V may meet in its L2
+        // (8000 rows, pages of 64: 24.4 -> 23.4 us)
+        const int r = id % 16;
+        if (id - r + 16 <= (int)gridDim.x)
+            id += r % 8 * 2 + r / 8 - r;
+    }
     int b = id, r0 = id, rows = 1, block = 0;
     if (c.q_start) {
         auto start = [&](int i) {
