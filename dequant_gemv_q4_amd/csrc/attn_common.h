@@ -208,6 +208,7 @@ template <int COLS_, int UNIT_LOG2_, int LEAST_, int SOLO_, int FLAT_, int RADIX
 struct PlanOf {
     static constexpr int COLS = COLS_, UNIT_LOG2 = UNIT_LOG2_, LEAST = LEAST_, SOLO = SOLO_;
     static constexpr int FLAT = FLAT_, RADIX = RADIX_;
+    static_assert(RADIX >= 1, "a sequence without positions has a chunk");
     static constexpr bool INDEX = INDEX_, SIDE = SIDE_;
     static __device__ __forceinline__ int units(int n) { return (n + (1 << UNIT_LOG2) - 1) >> UNIT_LOG2; }
     // at least one, so that an empty sequence's rows are written

@@ -54,7 +54,7 @@ __device__ __forceinline__ void pt_barrier()
 // heads: 39 us, in halves 59; sixteen of 32 rows behind 4000 positions: 122 us unsplit, 56).  With as many
 // tiles as slots, those behind contexts longer than a slot's share are split (512 rows behind 29500
 // positions beside five prompts of 307, 32 / 8 heads of 128: 842 us unsplit, 469).
-typedef PlanOf<PT_ROWS, 6, 8, 16, 0, 0, true, false> PromptCols;
+typedef PlanOf<PT_ROWS, 6, 8, 16, 0, 1, true, false> PromptCols;
 
 // A split tile, for its join.
 struct PromptSplit {

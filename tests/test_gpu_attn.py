@@ -410,6 +410,15 @@ def test_prompt_padded_rows_attend_to_nothing():
     _prompt(q.F16, 4, 2, 64, 16, [(5, 2), (3, 0), (40, 39), (2, -3)], 1, tail=2)
 
 
+@pytest.mark.parametrize("seqs", [
+    [(200, 3000), (150, 0), (130, -3), (140, 139)],                         # split, joined by a second launch
+    [(20, 4000), (400, 0), (300, 1200), (380, -1), (10, 0)],                # a few split among many
+    [(400, 0), (300, 0), (400, 20)]])                                       # none
+def test_prompt_wide_padded_rows_are_zero(seqs):
+    """128-row tiles of sequences without positions: their rows are written, with zeros."""
+    _prompt(q.F16, 64 if len(seqs) > 4 else 32, 8, 64, 16, seqs, 16, tail=2, wide=True)
+
+
 def test_prompt_many_sequences():
     rng = np.random.default_rng(6)
     _prompt(q.BF16, 2, 1, 64, 16, [(int(a), int(a + c)) for a, c in zip(rng.integers(0, 4, 1024),
@@ -735,6 +744,47 @@ def test_graph_replays_follow_the_lengths_on_the_device():
         torch.cuda.synchronize()
         for a, b in zip(got, (o, po, c.k.view(torch.int16), c.v.view(torch.int16))):
             assert np.array_equal(a, host(b)), rep
+
+
+def test_graph_replays_where_the_batch_fills_the_slots():
+    """70 sequences of one token and a prompt batch of more tiles than slots, captured once on one workspace:
+    none split, a few split and only one left by turns, each with the eager call's bits."""
+    rng = np.random.default_rng(41)
+    nq, nkv, hd, n = 64, 8, 64, 70
+    c, _, qkv, width, _ = _step(rng, q.BF16, nq, nkv, hd, 16, [(1, 3000)] + [(1, 300)] * (n - 2) + [(1, 1500)])
+    pseqs = [(20, 4000), (400, 400), (300, 1200), (380, 380)]
+    cp, pstart, pqkv, pwidth, prows = _step(rng, q.F16, nq, nkv, hd, 16, pseqs, True)
+    assert nkv * (prows * (nq // nkv) // 128) >= 512
+    ws = D.attn_workspace(q.OP_ATTN_PROMPT, n, nq, nkv, hd)
+    o, po = torch.empty((n, nq * hd), device="cuda"), torch.empty((prows, nq * hd), device="cuda")
+
+    def run():
+        q.qgemv_attn(*c.args(), c.kv_len, n, qkv, width, nq, 0.09, o, ws)
+        q.qgemv_attn_prompt(*cp.args(), pstart, cp.kv_len, len(pseqs), pqkv, pwidth, prows, nq, 0.09, po, ws)
+
+    run()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run()
+    full = [3000] + [300] * (n - 2) + [1500]
+    for rep, (lens, plens) in enumerate(((full, [4000, 400, 1200, 380]), ([200] * n, [20, 400, 300, 380]),
+                                         ([3000] + [0] * (n - 1), [4000, 0, 0, 0]), (full, [3999, 400, 1200, 300]))):
+        c.kv_len.copy_(torch.tensor(lens, dtype=torch.int32))
+        cp.kv_len.copy_(torch.tensor(plens, dtype=torch.int32))
+        qkv.normal_()
+        o.fill_(-1)
+        po.fill_(-1)
+        g.replay()
+        torch.cuda.synchronize()
+        got = [host(t).copy() for t in (o, po)]
+        o.fill_(-2)
+        po.fill_(-2)
+        run()
+        torch.cuda.synchronize()
+        for a, b in zip(got, (o, po)):
+            assert np.isfinite(a).all() and np.array_equal(a, host(b)), rep
+    assert q.qgemv_attn_error(ws) == 0
 
 
 def test_two_graphs_share_a_workspace():
