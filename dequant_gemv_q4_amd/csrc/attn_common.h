@@ -148,6 +148,18 @@ __device__ __forceinline__ uint32_t nonfinite2(uint32_t v)
 
 constexpr float LOG2E = 1.44269504088896340736f;
 
+// Joining partial results (O, maximum, sum) of parts of the positions: each O and sum is weighted by
+// join_weight, whatever it is, and the whole divided by the sum.  A part in which a row sees nothing has
+// zeros and no maximum (-inf).  So does, as to the maximum, one in which it sees only NaN scores (fmaxf
+// passes NaN over), and a part with some may weigh 0; their sums are NaN and stay so, as 0 x NaN is NaN:
+// no part may be left out for its maximum or its weight.
+__device__ __forceinline__ float join_weight(float part_max, float max_all)
+{
+    return part_max == max_all ? 1.0f : __builtin_amdgcn_exp2f(part_max - max_all);
+}
+// 1 / sum, or 0 for a row that sees nothing.
+__device__ __forceinline__ float inverse_sum(float l) { return l == 0.f ? 0.f : 1.0f / l; }
+
 // Partial results that pass between workgroups of one launch, which may run on different XCDs: every
 // access carries the agent-scope bit (sc1), so that it neither stays in nor is answered by the L2 of one
 // XCD.  Offsets in floats.

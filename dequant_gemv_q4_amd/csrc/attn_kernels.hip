@@ -426,10 +426,10 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn(AttnArgs a)
     const __amdgpu_buffer_rsrc_t part = __builtin_amdgcn_make_buffer_rsrc(
         a.part + (int64_t)p.slot0 * stride, 0, n_chunk * stride * 4, 0x00020000);
     // four channels of a column to o
-    auto store = [&](int e, af4 sum, float mm, float ls) {
+    auto store = [&](int e, af4 sum, float ls) {
         const int col = e / (D / 4), d4 = e % (D / 4);
-        const float inv = mm == -INFINITY ? 0.f : 1.0f / ls;
-        *reinterpret_cast<af4 *>(a.o + ((int64_t)row_of(col) * a.nq + head_of(col)) * D + 4 * d4) = sum * inv;
+        *reinterpret_cast<af4 *>(a.o + ((int64_t)row_of(col) * a.nq + head_of(col)) * D + 4 * d4) =
+            sum * inverse_sum(ls);
     };
     auto sums_at = [&](int at, int col) { return at * stride + width * D + 2 * col; };
     auto part_at = [&](int at, int e) { return at * stride + 4 * e; };
@@ -441,15 +441,12 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn(AttnArgs a)
         float ls = 0.f;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-            const float mw = s_m[w][col];
-            if (mw != -INFINITY) {
-                const float f = mw == mm ? 1.0f : __builtin_amdgcn_exp2f(mw - mm);
-                sum += *reinterpret_cast<const af4 *>(&s_o[w][col][4 * d4]) * f;
-                ls += s_l[w][col] * f;
-            }
+            const float f = join_weight(s_m[w][col], mm);
+            sum += *reinterpret_cast<const af4 *>(&s_o[w][col][4 * d4]) * f;
+            ls += s_l[w][col] * f;
         }
         if (n_chunk == 1) {
-            store(e, sum, mm, ls);
+            store(e, sum, ls);
         } else {
             put4(part, part_at(chunk, e), sum);
             if (d4 == 0)
@@ -486,13 +483,13 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn(AttnArgs a)
             af4 sum = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int k = 0; k < JOIN_RADIX; ++k)
-                if (k < members && mk[k] != -INFINITY) {
-                    const float f = mk[k] == mm ? 1.0f : __builtin_amdgcn_exp2f(mk[k] - mm);
+                if (k < members) {
+                    const float f = join_weight(mk[k], mm);
                     sum += x[k] * f;
                     ls += lk[k] * f;
                 }
             if (top) {
-                store(e, sum, mm, ls);
+                store(e, sum, ls);
             } else {
                 // the maximum and sum replace what other threads of the column may still have to read
                 put4(part, part_at(g0, e), sum);

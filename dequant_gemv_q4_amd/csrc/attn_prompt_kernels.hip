@@ -457,25 +457,23 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
         for (int k = 0; k < w.n_chunk; ++k) {
             float mk, lk;
             get2(part, k * stride + ml, mk, lk);
-            const float f = mk == -INFINITY ? 0.f : mk == m ? 1.0f : __builtin_amdgcn_exp2f(mk - m);
+            const float f = join_weight(mk, m);
             af4 x[DT][4];
 #pragma unroll
             for (int d = 0; d < DT; ++d)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
                     x[d][r] = get4(part, k * stride + row + 32 * d + 8 * r);
-            if (f != 0.f) {
-                l += lk * f;
+            l += lk * f;
 #pragma unroll
-                for (int d = 0; d < DT; ++d)
+            for (int d = 0; d < DT; ++d)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        o[d][r] += x[d][r / 4][r % 4] * f;
-            }
+                for (int r = 0; r < 16; ++r)
+                    o[d][r] += x[d][r / 4][r % 4] * f;
         }
     }
     if (live) {
-        const float inv = m == -INFINITY ? 0.f : 1.0f / l;
+        const float inv = inverse_sum(l);
         float *row = a.o + ((int64_t)(p.row0 + tok) * a.nq + head) * D + 4 * hf;
 #pragma unroll
         for (int d = 0; d < DT; ++d)
@@ -502,9 +500,6 @@ __global__ __launch_bounds__(256) void k_attn_prompt_join(AttnArgs a)
     const int D = a.c.hd, lanes = D / 4, items = 4 * lanes, parts = 256 / items;
     const int tid = threadIdx.x, e = tid % items, k0 = tid / items, row = e / lanes, d4 = e % lanes;
     const int64_t stride = prompt_part_floats(D);
-    auto weight = [](float mk, float m) {
-        return mk == -INFINITY ? 0.f : mk == m ? 1.0f : __builtin_amdgcn_exp2f(mk - m);
-    };
     for (int r0 = 4 * blockIdx.y; r0 < PT_ROWS && (p.rho0 + r0) / a.group < p.rows; r0 += 4 * gridDim.y) {
         const float *part = a.part + p.slot0 * stride, *from = part + (r0 + row) * D + 4 * d4;
         const float *ml = part + PT_ROWS * D + 2 * (r0 + row);
@@ -523,18 +518,17 @@ __global__ __launch_bounds__(256) void k_attn_prompt_join(AttnArgs a)
 #pragma unroll
             for (int x = 0; x < 8; ++x)
                 mb = fmaxf(mb, w[x].x);
-            const float f0 = weight(m, mb);
+            const float f0 = join_weight(m, mb);
             sum *= f0;
             l *= f0;
             m = mb;
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                const float f = kb + x * parts < splits ? weight(w[x].x, m) : 0.f;
-                if (f != 0.f) {
+            for (int x = 0; x < 8; ++x)
+                if (kb + x * parts < splits) {
+                    const float f = join_weight(w[x].x, m);
                     sum += v[x] * f;
                     l += w[x].y * f;
                 }
-            }
         }
         if (parts > 1) {
             s_sum[tid] = sum;
@@ -545,24 +539,21 @@ __global__ __launch_bounds__(256) void k_attn_prompt_join(AttnArgs a)
                 float all = m;
                 for (int x = 1; x < parts; ++x)
                     all = fmaxf(all, s_m[e + x * items]);
-                const float f0 = weight(m, all);
+                const float f0 = join_weight(m, all);
                 sum *= f0;
                 l *= f0;
                 for (int x = 1; x < parts; ++x) {
-                    const float f = weight(s_m[e + x * items], all);
-                    if (f != 0.f) {
-                        sum += s_sum[e + x * items] * f;
-                        l += s_l[e + x * items] * f;
-                    }
+                    const float f = join_weight(s_m[e + x * items], all);
+                    sum += s_sum[e + x * items] * f;
+                    l += s_l[e + x * items] * f;
                 }
-                m = all;
             }
             __syncthreads();
         }
         const int rho = p.rho0 + r0 + row, tok = rho / a.group;
         if (k0 == 0 && tok < p.rows)
             *reinterpret_cast<af4 *>(a.o + ((int64_t)(p.row0 + tok) * a.nq + p.hkv * a.group + rho % a.group) * D +
-                                     4 * d4) = sum * (m == -INFINITY ? 0.f : 1.0f / l);
+                                     4 * d4) = sum * inverse_sum(l);
     }
 }
 

@@ -321,9 +321,11 @@ int qgemv_attn(int kv_type, const void *k_pages, const void *v_pages, int64_t n_
  * over a long cache are split over its length and joined, within the launch or by a second one.
  * Accuracy of both: scores, softmax statistics and sums in f32; q and the probabilities enter the
  * products with f16 K and V as the sum of two f16 values (22 bits), with bf16 as that of three bf16
- * values (24 bits); K and V exactly as stored.  An infinity or NaN in K or V makes the outputs of
- * the rows that see its position non-finite (NaN also where the definition gives an infinity) and
- * touches no other row. */
+ * values (24 bits); K and V exactly as stored.  A NaN or an infinity in a query makes the
+ * outputs of its row and head non-finite, one in K or V those of the rows that see its position (of V
+ * its channel's; NaN also where the definition gives an infinity), and touches no other row.  Only an
+ * infinity in K whose score comes out as -inf has weight 0; a row all of whose scores are -inf gets 0,
+ * as one that sees no position. */
 int qgemv_attn_prompt(int kv_type, const void *k_pages, const void *v_pages, int64_t n_pages,
                       int page_size, int64_t page_stride, int n_kv_heads, int head_dim,
                       const int32_t *table, int max_pages, const int32_t *q_start,
