@@ -14,8 +14,9 @@ typedef float af16 __attribute__((ext_vector_type(16)));
 typedef uint32_t au4 __attribute__((ext_vector_type(4)));
 
 // Pieces an f32 value (a scaled query, a probability) is split into for the products with f16 / bf16
-// operands: two f16 hold 22 of its 24 bits, three bf16 all of them.  (Two bf16, 2^-18, left
-// attention outputs 2.4e-6 off in the root mean square where f32 sums leave 0.7e-6.)
+// operands: two f16 hold 22 of its 24 bits down to 2^-3 (below that, 2^-25 is lost), three bf16 all of
+// them.  (Two bf16, 2^-18, left attention outputs 2.4e-6 off in the root mean square where f32 sums leave
+// 0.7e-6.)
 template <int T> constexpr int PIECES = T == KV_F16 ? 2 : 3;
 
 // Two floats rounded to nearest-even to the cache's type, packed (a in the low half): one
@@ -148,14 +149,35 @@ __device__ __forceinline__ uint32_t nonfinite2(uint32_t v)
 
 constexpr float LOG2E = 1.44269504088896340736f;
 
-// Joining partial results (O, maximum, sum) of parts of the positions: each O and sum is weighted by
-// join_weight, whatever it is, and the whole divided by the sum.  A part in which a row sees nothing has
-// zeros and no maximum (-inf).  So does, as to the maximum, one in which it sees only NaN scores (fmaxf
-// passes NaN over), and a part with some may weigh 0; their sums are NaN and stay so, as 0 x NaN is NaN:
-// no part may be left out for its maximum or its weight.
-__device__ __forceinline__ float join_weight(float part_max, float max_all)
+// The weight of a score s (in powers of two) is held as 2^(s + shift).  A row's shift is LIFT less the
+// largest score it has seen, until a later one would bring the exponent above TOP: then it moves (a wave
+// vote, so that the accumulators are rescaled a few times in a row's life).  f16 ends at 2^16 and loses
+// what is below 2^-25, so of weights far below the largest one 2^-25 / 2^12 = 2^-37 of it is lost at most.
+// (With LIFT 6, 2^-31 of it: one position with 90 % of the weight and a hundredth of the others' values
+// before 8191 others, outputs 2.3e-6 off in the root mean square, 0.3e-6 with 12.)  A LIFT nearer to TOP
+// rescales more often: 4096 rows (16 / 8 heads of 256) 303 us with 6 and 13, 316 with 13 and 15, 309 with
+// these.
+template <int T> constexpr float LIFT = T == KV_F16 ? 12.0f : 6.0f;
+template <int T> constexpr float TOP = T == KV_F16 ? 15.9f : 13.0f;
+// No score yet: any score moves it, and a masked one (-inf) weighs 0.
+constexpr float NO_SHIFT = 3.402823466e38f;
+// Scores beyond 2^24 are more than 2 apart, and LIFT less one of them is rounded to such steps: where that
+// would end above TOP, 0 is as good for weights that are steps of 2^-8 apart.
+template <int T>
+__device__ __forceinline__ float shift_of(float top_score)
 {
-    return part_max == max_all ? 1.0f : __builtin_amdgcn_exp2f(part_max - max_all);
+    const float r = LIFT<T> - top_score;
+    return r + top_score > TOP<T> ? -top_score : r;
+}
+
+// Joining partial results (O, exponent m = -shift, sum) of parts of the positions: each O and sum is
+// weighted by join_weight with the largest m, whatever it is, and the whole divided by the sum.  A part in
+// which a row sees nothing has zeros and the lowest m.  So does, as to m, one in which it sees only NaN
+// scores (fmaxf passes NaN over), and a part with some may weigh 0; their sums are NaN and stay so, as 0 x
+// NaN is NaN: no part may be left out for its m or its weight.
+__device__ __forceinline__ float join_weight(float part_m, float largest_m)
+{
+    return part_m == largest_m ? 1.0f : __builtin_amdgcn_exp2f(part_m - largest_m);
 }
 // 1 / sum, or 0 for a row that sees nothing.
 __device__ __forceinline__ float inverse_sum(float l) { return l == 0.f ? 0.f : 1.0f / l; }

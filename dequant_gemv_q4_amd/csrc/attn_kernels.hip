@@ -128,11 +128,7 @@ __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a)
 //
 // Each of the four waves takes every fourth 32-position step, loads one step ahead (K, V) and two
 // ahead (page numbers), and keeps its own maximum, sum and O^T; they are joined in LDS at the end.
-// The reference of the exponentials moves only when a score exceeds it by more than 7 powers of two (a
-// wave vote), so the accumulators are hardly ever rescaled; probabilities are held times 2^6 (f16: 2^-30
-// of the reference still has its first piece's bits).  They stay below the f16 range's end of 2^16 for
-// scores of any size: the excess over the reference is exact, a multiple of the scores' spacing, and
-// 6 - m rounds to 8 - m at most (spacing 4, excess at most 4; spacing 8, excess 0; wider, -m and 0).
+// The exponentials' reference (shift_of) moves by a wave vote, so the accumulators are hardly ever rescaled.
 //
 // Split over the length: the lengths are on the device, so every workgroup derives the same plan
 // from them: the smallest chunk (whole 128-position units) for which the chunks of all sequences
@@ -250,7 +246,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn(AttnArgs a)
 #pragma unroll
     for (int d = 0; d < DT; ++d)
         o[d] = af4{0.f, 0.f, 0.f, 0.f};
-    float m = -INFINITY, l = 0.f;
+    float shift = NO_SHIFT, l = 0.f;
 
     if (n_steps > 0) {
         const int last_entry = (len - 1) >> c.ps_log2, ps_mask = (1 << c.ps_log2) - 1;
@@ -358,21 +354,19 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn(AttnArgs a)
             }
             float mx = fmaxf(fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3])),
                              fmaxf(fmaxf(sc[4], sc[5]), fmaxf(sc[6], sc[7])));
-            if (__any(mx - m > 7.0f)) {
-                mx = max_x32(max_x16(mx));
-                const float mn = fmaxf(m, mx);
-                const float f = m == mn ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
-                m = mn;
+            if (__any(mx + shift > TOP<T>)) {
+                const float to = fminf(shift, shift_of<T>(max_x32(max_x16(mx))));
+                const float f = __builtin_amdgcn_exp2f(to - shift);
+                shift = to;
                 l *= f;
 #pragma unroll
                 for (int d = 0; d < DT; ++d)
                     o[d] *= f;
             }
             float pr[8];
-            const float ref = m == -INFINITY ? 0.f : 6.0f - m;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                pr[e] = __builtin_amdgcn_exp2f(sc[e] + ref);
+                pr[e] = __builtin_amdgcn_exp2f(sc[e] + shift);
                 l += pr[e];
             }
             au4 pf[NP];
@@ -414,7 +408,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn(AttnArgs a)
     // join the waves: column i of O^T, rows 16 d + 4 g + r
     l = sum_x32(sum_x16(l));
     if (g == 0) {
-        s_m[wave][i] = m;
+        s_m[wave][i] = -shift;
         s_l[wave][i] = l;
     }
 #pragma unroll

@@ -203,7 +203,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
 #pragma unroll
         for (int r = 0; r < 16; ++r)
             o[d][r] = 0.f;
-    float m = -INFINITY, l = 0.f;
+    float shift = NO_SHIFT, l = 0.f;
 
     // raw (unscaled) scores of positions 32 NT sub .. of a step
     auto scores = [&](int buf, int sub, af16 (&sc)[NT]) {
@@ -237,7 +237,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    // scores -> probabilities (times 2^6 over the reference), maximum and sum kept up
+    // scores -> probabilities (2^(score + shift)), shift and sum kept up
     auto softmax = [&](af16 (&sc)[NT]) {
         float mx = sc[0][0];
 #pragma unroll
@@ -246,10 +246,10 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
             for (int tt = 0; tt < NT; ++tt)
                 mx = fmaxf(mx, sc[tt][r]);
         mx *= unscale;
-        if (__any(mx - m > 7.0f)) {
-            const float mn = fmaxf(m, max_x32(mx));
-            const float f = m == mn ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
-            m = mn;
+        if (__any(mx + shift > TOP<T>)) {
+            const float to = fminf(shift, shift_of<T>(max_x32(mx)));
+            const float f = __builtin_amdgcn_exp2f(to - shift);
+            shift = to;
             l *= f;
 #pragma unroll
             for (int d = 0; d < DT; ++d)
@@ -257,13 +257,12 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
                 for (int r = 0; r < 16; ++r)
                     o[d][r] *= f;
         }
-        const float ref = m == -INFINITY ? 0.f : 6.0f - m;
         float sum[NT];
 #pragma unroll
         for (int r = 0; r < 16; ++r)
 #pragma unroll
             for (int tt = 0; tt < NT; ++tt) {
-                sc[tt][r] = __builtin_amdgcn_exp2f(fmaf(sc[tt][r], unscale, ref));
+                sc[tt][r] = __builtin_amdgcn_exp2f(fmaf(sc[tt][r], unscale, shift));
                 sum[tt] = r == 0 ? sc[tt][0] : sum[tt] + sc[tt][r];
             }
         l += NT == 2 ? sum[0] + sum[NT - 1] : sum[0];
@@ -419,7 +418,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
                     af4{o[d][4 * r], o[d][4 * r + 1], o[d][4 * r + 2], o[d][4 * r + 3]};
         if (hf == 0) {
             float *ml = part + PT_ROWS * D + 2 * (32 * wave + col);
-            ml[0] = m;
+            ml[0] = -shift;
             ml[1] = l;
         }
         return;
@@ -438,10 +437,10 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
                 put4(part, w.chunk * stride + row + 32 * d + 8 * r,
                      af4{o[d][4 * r], o[d][4 * r + 1], o[d][4 * r + 2], o[d][4 * r + 3]});
         if (hf == 0)
-            put2(part, w.chunk * stride + ml, m, l);
+            put2(part, w.chunk * stride + ml, -shift, l);
         if (!last_to_arrive(a.count + w.slot0, w.n_chunk, &s_last))
             return;
-        m = -INFINITY;
+        float m = -INFINITY;
         for (int k = 0; k < w.n_chunk; ++k) {
             float mk, lk;
             get2(part, k * stride + ml, mk, lk);
