@@ -140,7 +140,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
         // and a masked -inf stays one
         int e2 = 0;
         const float f = frexpf(a.scale, &e2) * LOG2E, sc = q_scale<T>(max_x32(amax));
-        unscale = fmaxf(ldexpf(1.0f / sc, e2), 0x1p-126f);
+        unscale = fmaxf(ldexpf(1.0f / sc, e2), 0x1p-149f);
 #pragma unroll
         for (int k = 0; k < KB; ++k) {
             float w[8];

@@ -50,3 +50,16 @@ def test_values_below_the_normal_range(kv_type, rows):
     K = rounded(rng.standard_normal((n, 1, hd)), kv_type)
     V = rounded(rng.standard_normal((n, 1, hd)) * (3e-7 if kv_type == q.F16 else 1e-30), kv_type)
     _check(kv_type, x, K, V, rows, hd ** -0.5, "small V")
+
+
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("scale", [1e-37, 2e-38, 5e-39, 1e-39, -1e-39, 1e-40])
+def test_scales_below_the_normal_range(scale, rows):
+    """Products of q and K near 1e38 times a scale around f32's least normal value, 1.2e-38."""
+    hd, nq, n, m = 64, 4, 300, max(rows, 1)
+    rng = np.random.default_rng(73)
+    x, K = np.zeros((m, nq, hd), np.float32), np.zeros((n, 1, hd), np.float32)
+    x[..., 0] = 1e19 * rng.uniform(0.5, 1.0, (m, nq))
+    K[:, 0, 0] = rng.uniform(-1.0, 1.0, n) * min(1e19, 4.0 / abs(scale) / 1e19)
+    K, V = rounded(K, q.BF16), rounded(rng.standard_normal((n, 1, hd)), q.BF16)
+    _check(q.BF16, x, K, V, rows, scale, f"scale {scale}")
