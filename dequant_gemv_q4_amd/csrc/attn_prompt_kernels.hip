@@ -571,22 +571,32 @@ PromptPlan plan_prompt(int64_t n_rows, int n_seq, int nkv, int group, int hd, in
     return p;
 }
 
+// Few columns (rows times query heads of a KV head): the one-token kernel takes 16 at a time, with the
+// positions spread over all waves, where this one's 128-row tiles would mostly be empty or too few.  It
+// reads the cache once per 16 columns, so it takes the call when all its workgroups are resident at once, the
+// columns of a sequence are at most 384 on average or the table is short, and the whole work is bounded
+// however the rows are dealt to the sequences, which only the device knows: every column times every position
+// of the table stays under 2^31 channels (of longer tables 16384 positions count: a table is sized for the
+// longest cache, and the 16-column tiles are done 20 us earlier where it is not full).
+// 128-row tiles -> 16 columns, us: 16 sequences x 4 rows x 4000 positions, 32 / 8 heads of 128, 64.7 -> 38.9;
+// one of 32 rows x 20000, 12 / 2 heads, 36.3 -> 34.1; of 128 rows 57.9 -> 84.1; three of 31 rows alone
+// 9.6 -> 6.8; one of 128 rows alone, 32 / 8 heads, 11.4 -> 8.4; 16 of 32 rows alone, twice the resident
+// workgroups, 11.0 -> 19.9; four of 32 rows x 2000, 12 / 2, 29.9 -> 21.8; 177 rows behind 30000 positions
+// among 15 single tokens, 24 / 2 heads (156 columns on average), 139 -> 528.  Over 1119 mixes of rows and
+// caches, heads of 64 to 256, the choice costs 2.7 % against the faster one each; without the bound on the
+// work 11.8 %, and 280 % at worst.  64 sequences of 4 rows x 4000 positions would gain as well (189.7 ->
+// 181.9, at 8 rows 192 -> 285), but as many rows may be one prompt among single tokens.
+bool prompt_in_16s(int64_t n_rows, int n_seq, int nq, int nkv, int hd, int64_t positions)
+{
+    const int64_t columns = n_rows * (nq / nkv);
+    return nkv * (columns / 16 + n_seq) <= attn_slots(hd) && (columns <= 384 * (int64_t)n_seq || positions <= 1024) &&
+           columns * nkv * hd * (positions < 16384 ? positions : 16384) <= (int64_t)1 << 31;
+}
+
 int launch_attn_prompt(int kv_type, const AttnArgs &a, void *stream)
 {
-    // Few columns (rows times query heads of a KV head): the one-token kernel takes 16 at a time,
-    // with the positions spread over all waves, where this one's 128-row tiles would mostly be empty
-    // or too few.  It reads the cache once per 16 columns, so it takes the call when all its
-    // workgroups are resident at once and the columns of a sequence are at most 384 on average or
-    // the table is short (128-row tiles -> 16 columns, us: 16 sequences x 4 rows x 4000 positions, 32 /
-    // 8 heads of 128, 64.7 -> 39.3; one of 32 rows x 20000, 12 / 2 heads, 36.3 -> 34.1; of 128 rows
-    // 57.9 -> 84.1; three of 31 rows alone 9.6 -> 6.8; one of 128 rows alone, 32 / 8 heads, 11.4 -> 8.4;
-    // 16 of 32 rows alone, twice the resident workgroups, 11.0 -> 19.9).  64 sequences of 4 rows x 4000
-    // positions would gain as well (189.7 -> 181.9, at 8 rows 192 -> 285), but as many rows may be one
-    // prompt among single tokens, whose cache it would read a hundred times.
-    const int64_t pairs = a.c.nkv * (a.c.n_rows * a.group / 16 + a.c.n_seq);
     const int64_t table = (int64_t)a.c.max_pages << a.c.ps_log2;
-    if (pairs <= attn_slots(a.c.hd) &&
-        (a.c.n_rows * a.group <= 384 * (int64_t)a.c.n_seq || table <= 1024))
+    if (prompt_in_16s(a.c.n_rows, a.c.n_seq, a.nq, a.c.nkv, a.c.hd, table))
         return launch_attn_rows(kv_type, a, stream);
     hipStream_t s = static_cast<hipStream_t>(stream);
     const PromptPlan p = plan_prompt(a.c.n_rows, a.c.n_seq, a.c.nkv, a.group, a.c.hd, table);
