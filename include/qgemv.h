@@ -321,7 +321,7 @@ int qgemv_attn(int kv_type, const void *k_pages, const void *v_pages, int64_t n_
  * over a long cache are split over its length and joined, within the launch or by a second one.
  * Accuracy of both: scores, softmax statistics and sums in f32; q and the probabilities enter the
  * products with f16 K and V as the sum of two f16 values (22 bits; of q below 2^-16 of the row's
- * largest 2^-38 of that, of probabilities 2^-37 of the row's largest, is lost at most), with bf16 as
+ * largest 2^-38 of that, of probabilities 2^-35 of the row's largest, is lost at most), with bf16 as
  * that of three bf16 values (24 bits); K and V exactly as stored.  A NaN or an infinity in a query makes the
  * outputs of its row and head non-finite, one in K or V those of the rows that see its position (of V
  * its channel's; NaN also where the definition gives an infinity), and touches no other row.  Only an

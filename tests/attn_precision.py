@@ -19,8 +19,8 @@ the division by some u |o|; so the root of the mean square of (error) over that 
 N = sqrt(sum p^2 (v - o)^2 + o^2) is held to 2^-21 (1 + Q').
 
 Far below the largest weight the two f16 pieces end at the type's least step 2^-24: weights are held times
-2^12 of the reference, which is no larger than the largest, so that what is lost there is at most half a step,
-2^-25 / 2^12 = 2^-37 of the largest weight, for every position.
+2^10 of the reference, which is no larger than the largest, so that what is lost there is at most half a step,
+2^-25 / 2^10 = 2^-35 of the largest weight, for every position.
 """
 from __future__ import annotations
 
@@ -29,7 +29,7 @@ import numpy as np
 from gpu_common import q
 
 U = 2.0 ** -24
-F16_LOST = 2.0 ** -37               # of the largest weight, a position
+F16_LOST = 2.0 ** -35               # of the largest weight, a position
 
 
 def parts64(qr, K, V, nkv, scale, last):

@@ -7,7 +7,7 @@ import dequant_gemv_q4_amd as q
 from attn_common import rounded
 from attn_precision import dominant_case, emulate, parts64, rms_bound, rms_ratio, tail_case, tail_tolerance
 
-LIFT = {q.F16: 12, q.BF16: -7}
+LIFT = {q.F16: 10, q.BF16: -7}
 PIECES = {q.F16: 2, q.BF16: 3}
 
 
