@@ -282,9 +282,12 @@ int qgemv_moe_error(const void *ws, int64_t n_exp, int64_t N, int64_t K, int fmt
  * Order: append the step's K and V first, then attend, on one stream.  Two sequences may share
  * pages that neither appends to; appending to one page position from two rows is a race.
  * page_size is 16, 32, 64, 128 or 256; head_dim 64, 96, 128, 192 or 256; n_kv_heads divides
- * n_q_heads (query head h reads KV head h / (n_q_heads / n_kv_heads)); n_seq in
- * [1, QG_ATTN_MAX_SEQ]; max_pages * page_size <= 2^24; n_rows in [1, QG_GEMM_MAX_M].  All float
- * pointers and both page arrays are 16-byte aligned, row strides are multiples of 4 floats. */
+ * n_q_heads (query head h reads KV head h / (n_q_heads / n_kv_heads)), which is at most 4096 (for
+ * qgemv_kv_append n_kv_heads is); n_seq in [1, QG_ATTN_MAX_SEQ]; max_pages * page_size <= 2^24; n_rows in
+ * [1, QG_GEMM_MAX_M]; n_pages in [1, 2^28]; page_stride < 2^32; q_stride (kv_stride) from n_q_heads *
+ * head_dim (n_kv_heads * head_dim) to 2^31 floats; scale finite.  All float pointers and both page arrays are
+ * 16-byte aligned, row strides are multiples of 4 floats.  Calls that share a workspace are ordered on
+ * one stream, as above; calls with workspaces of their own may run side by side. */
 
 /* Workspace bytes of an attention-side operation (QG_OP_KV_APPEND, QG_OP_ATTN,
  * QG_OP_ATTN_PROMPT), or -1 on invalid sizes.  It holds the sticky flag and the partial results of
