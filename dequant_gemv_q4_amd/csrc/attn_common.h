@@ -154,10 +154,10 @@ constexpr float LOG2E = 1.44269504088896340736f;
 // vote, so that the accumulators are rescaled a few times in a row's life).  f16 ends at 2^16 and loses
 // what is below 2^-25, so of weights far below the largest one 2^-25 / 2^10 = 2^-35 of it is lost at most.
 // (With LIFT 6, 2^-31 of it: one position with 90 % of the weight and a hundredth of the others' values
-// before 8191 others, outputs 2.3e-6 off in the root mean square; 1.07e-6 with 10, and 1.06e-6 with bf16's 24 bits.)
-// A LIFT nearer to TOP rescales more often: three prompts of 1310 rows (14 / 2 heads of 256) 42.9 us with 6
-// and 13, 42.9 with these, 45.0 with 12.  bf16 has f32's range, so its weights are at most 1: with V up to the type's end their products
-// stay within f32.
+// before 8191 others, outputs 2.3e-6 off in the root mean square; 1.07e-6 with 10, and 1.06e-6 with bf16's
+// 24 bits.)  A LIFT nearer to TOP rescales more often: three prompts of 1310 rows in all (14 / 2 heads of
+// 256) 42.9 us with 6 and 13, 42.4 with these, 45.0 with 12.  bf16 has f32's range, so its weights are at
+// most 1: with V up to the type's end their products stay within f32.
 template <int T> constexpr float LIFT = T == KV_F16 ? 10.0f : -7.0f;
 template <int T> constexpr float TOP = T == KV_F16 ? 15.9f : 0.0f;
 // No score yet: any score moves it, and a masked one (-inf) weighs 0.

@@ -15,7 +15,7 @@ namespace qg {
 // 64 90.2 with 512 and 99.5 with 1024.
 #define ATTN_MAX_SLOTS 512
 __host__ __device__ constexpr int attn_slots(int hd) { return hd <= 128 ? 512 : 256; }
-// Floats of one slot's partial result: O of `cols` query heads, their maxima and sums.
+// Floats of one slot's partial result: O of `cols` query heads, their exponents and sums.
 __host__ __device__ constexpr int64_t attn_part_floats(int cols, int hd) { return (int64_t)cols * (hd + 2); }
 // The same of qgemv_attn_prompt's 128-column tiles, and the most pairs of a call that may be split.
 #define PROMPT_SLOTS 512

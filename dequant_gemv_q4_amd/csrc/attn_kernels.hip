@@ -119,7 +119,7 @@ __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a)
 // (v_mfma_f32_16x16x32), so that
 //  - K, and V as the cache holds it (transposed inside the page), are the A operands: eight
 //    consecutive halves each, loaded from the cache straight into registers by 16-byte loads;
-//  - a lane's scores all belong to one query head (column l % 16), its running maximum, sum and
+//  - a lane's scores all belong to one query head (column l % 16), its running exponent, sum and
 //    factors are per-lane scalars, and the scores it holds are exactly the probabilities it must
 //    supply to the second product: row i of score tile tt is position 8 (i / 4) + 4 tt + i % 4 of a
 //    32-position step, so lane group g = l / 16 holds positions 8 g .. 8 g + 7.
@@ -127,21 +127,21 @@ __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a)
 // pieces whose products add up in f32 (PIECES); the matrix cores are idle otherwise.
 //
 // Each of the four waves takes every fourth 32-position step, loads one step ahead (K, V) and two
-// ahead (page numbers), and keeps its own maximum, sum and O^T; they are joined in LDS at the end.
+// ahead (page numbers), and keeps its own exponent, sum and O^T; they are joined in LDS at the end.
 // The exponentials' reference (shift_of) moves by a wave vote, so the accumulators are hardly ever rescaled.
 //
 // Split over the length: the lengths are on the device, so every workgroup derives the same plan
 // from them: the smallest chunk (whole 128-position units) for which the chunks of all sequences
 // fit the grid's workgroup slots (where the sequences alone fill them, only the longest are split); a
 // sequence's chunks are equal to one unit.  One chunk: the
-// workgroup writes o.  Several: partial O, maximum and sum go to the workspace, and of every
+// workgroup writes o.  Several: partial O, exponent and sum go to the workspace, and of every
 // JOIN_RADIX chunks the last to finish adds them up (then of as many such groups, until one is
 // left), always in chunk order, so that results do not depend on the order of execution.  A second
 // launch for the joining took 4.5 us on the device and 3 us on the host of calls of 7 to 100 us.
 //
 // Bound by HBM where the cache is long: 64 sequences of 7500 positions (12 / 2 heads of 128, bf16) take
-// 98 us, 5.01 TB/s; seven of up to 60000 (32 / 8, f16) 72 us, 5.13 TB/s.  By latency where it is short:
-// 165 positions 6.9 us, one after the other the lengths, the page numbers, K and V.
+// 98 us, 5.04 TB/s; seven of up to 60000 (32 / 8, f16) 72 us, 5.16 TB/s.  By latency where it is short:
+// 165 positions 6.8 us, one after the other the lengths, the page numbers, K and V.
 constexpr int JOIN_RADIX = 8;
 // 16 columns; chunks of whole 128-position units, at least two; sequences of up to four are not split,
 // and those of up to 32 not into more chunks than one join takes: four sequences of 4090 positions (32 / 8
@@ -150,7 +150,7 @@ constexpr int JOIN_RADIX = 8;
 template <bool SIDE> using AttnPlanOf = PlanOf<16, 7, 2, 4, 32, JOIN_RADIX, false, SIDE>;
 typedef AttnPlanOf<false> AttnCols;
 
-// Partial results of a slot: the tile's O (unnormalised) [cols][hd], then (maximum, sum) [cols].
+// Partial results of a slot: the tile's O (unnormalised) [cols][hd], then (exponent, sum) [cols].
 // SIDE: several tiles of a KV head read the same positions.  They come next to each other and on one XCD
 // (workgroups eight apart), so that one of them finds the other's in the L2: 64 sequences of 7500 positions,
 // 40 / 2 heads of 128: 140.9 us tile by tile, 107 to 111; of 64 75.0 and 58; sixteen of 8 rows x 4000, 24 / 2:
@@ -485,7 +485,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn(AttnArgs a)
             if (top) {
                 store(e, sum, ls);
             } else {
-                // the maximum and sum replace what other threads of the column may still have to read
+                // the exponent and sum replace what other threads of the column may still have to read
                 put4(part, part_at(g0, e), sum);
                 if (d4 == 0) {
                     s_mo[col] = mm;

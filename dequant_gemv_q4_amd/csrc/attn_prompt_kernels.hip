@@ -5,7 +5,7 @@
 // the diagonal is computed in vain) and every K and V element read serves all of them.  Four waves
 // take 32 rows each against steps of 64 positions held in LDS.  As in the one-token kernel the
 // positions are the rows of both products, S^T = K Q^T and O^T = V^T P^T (v_mfma_f32_32x32x16): a
-// lane's 32 scores of a step belong to one row of the tile (column l % 32), so maximum, sum and
+// lane's 32 scores of a step belong to one row of the tile (column l % 32), so exponent, sum and
 // factors are per-lane scalars, and they are the probabilities that the lane supplies to the second
 // product (score row i of a 32-position tile is position 16 (i / 16) + 8 (i / 4 % 2) +
 // 4 (i / 8 % 2) + i % 4, which makes a lane's eight values consecutive positions).
@@ -19,9 +19,9 @@
 // different banks: SQ_LDS_BANK_CONFLICT 0, against four cycles a read with keys made for eight lanes
 // in a row.
 //
-// Bound by the matrix cores: 8192 rows (32 / 8 heads of 128, f16) take 937 us, 1.17 PFLOP/s with each
-// product's two pieces counted, what a large f16 product reaches on the card; 4500 rows of nine prompts
-// (24 / 8 of 64, bf16, three pieces) 36.5 us.
+// Bound by the matrix cores: 8192 rows (32 / 8 heads of 128, f16) take 898 to 985 us from box to box, 1.22
+// to 1.12 PFLOP/s with each product's two pieces counted, what a large f16 product reaches on the card; 4500
+// rows of nine prompts (24 / 8 of 64, bf16, three pieces) 36 us.
 #include <hip/hip_runtime.h>
 
 #include "attn_common.h"

@@ -18,8 +18,8 @@
 //
 // Bound by VALU issue, not by the 8.7 MB it moves: 8000 x 256, sigmoid, 8 groups, top 8 of 4 groups,
 // takes 31.1 us with shuffled 64-bit maxima and a serial scan of the groups, 15.2 us with lane shifts
-// and 64-bit rounds, 12.6 us as it is (700 VALU instructions a row); 16 x 64, top 8, 5.3 us, of which the
-// kernel is 3.0.  8000 x 1000, softmax, 8 groups of 125 (no run of lanes), a lane scanning a group: 192 us,
+// and 64-bit rounds, 13 us as it is (700 VALU instructions a row); 16 x 64, top 8, 5.4 us, of which the
+// kernel is 3.2.  8000 x 1000, softmax, 8 groups of 125 (no run of lanes), a lane scanning a group: 192 us,
 // eight lanes 69.
 #include <hip/hip_runtime.h>
 
@@ -139,8 +139,8 @@ struct Top2 {
     }
 };
 
-// Eight and sixteen experts a lane are held to 128 registers: left alone, all their exponentials run side by
-// side in 478 (8000 x 1024: 84.6 us, 40.2; x 512: 23.7, 21.8).
+// Eight and sixteen experts a lane are held to 128 registers (sixteen spill 17): left alone, all their
+// exponentials run side by side in 478 (8000 x 1024: 84.6 us, 40.2; x 512: 23.7, 21.9).
 template <int NI>
 __global__ __launch_bounds__(256, NI >= 8 ? 4 : 1) void k_route(RouteArgs a)
 {
