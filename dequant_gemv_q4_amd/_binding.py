@@ -18,9 +18,9 @@ HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "qgemv.h")
 
 Q4_0, Q5_0, Q8_0, Q4_K, Q5_K, Q6_K = 2, 6, 8, 12, 13, 14
 IQ4_NL, IQ4_XS, Q1_0, AQ4 = 20, 23, 40, 41
-F16, BF16 = 1, 30
+F16, BF16, I8, F8 = 1, 30, 24, 42
 OP_GEMV, OP_NRM, OP_GUS_NRM, OP_RES, OP_ARGMAX, OP_MOE, OP_NRM_BIAS = range(7)
-OP_KV_APPEND, OP_ATTN, OP_ATTN_PROMPT = 7, 8, 9
+OP_KV_APPEND, OP_ATTN, OP_ATTN_PROMPT, OP_QKV_APPEND, OP_ATTN_SHARED = 7, 8, 9, 10, 11
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 ACT_SILU, ACT_GELU_TANH = 0, 1
 STATUS = {0: "QG_OK", 1: "QG_ERR_NULL", 2: "QG_ERR_FORMAT", 3: "QG_ERR_SHAPE", 4: "QG_ERR_ALIGN",
@@ -63,6 +63,11 @@ _SIGS = {
                           _i64, _i32, _f32, _vp, _vp, _sz, _vp]),
     "qgemv_attn_prompt": (_i32, [_i32, _vp, _vp, _i64, _i32, _i64, _i32, _i32, _vp, _i32, _vp, _vp,
                                  _i32, _vp, _i64, _i64, _i32, _f32, _vp, _vp, _sz, _vp]),
+    "qgemv_qkv_append": (_i32, [_i32, _vp, _vp, _i64, _i32, _i64, _i32, _i32, _vp, _i32, _vp, _vp,
+                                _i32, _vp, _i64, _i64, _i32, _i32, _vp, _vp, _f32, _vp, _vp, _i64,
+                                _vp, _i64, _vp, _sz, _vp]),
+    "qgemv_attn_shared": (_i32, [_i32, _vp, _vp, _i64, _i32, _i64, _i32, _i32, _vp, _i32, _vp, _i32,
+                                 _vp, _vp, _i32, _vp, _i64, _i32, _f32, _vp, _vp, _sz, _vp]),
     "qgemv_attn_error": (_i32, [_vp, ctypes.POINTER(ctypes.c_int), _vp]),
     "qgemv_route": (_i32, [_vp, _i64, _i32, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _f32, _vp,
                            _vp, _vp]),
@@ -255,7 +260,8 @@ def _torch_types():
     global _types
     if _types is None:
         import torch
-        _types = (torch.int32, torch.float32, {F16: torch.float16, BF16: torch.bfloat16},
+        _types = (torch.int32, torch.float32,
+                  {F16: torch.float16, BF16: torch.bfloat16, I8: torch.uint8, F8: torch.uint8},
                   torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
     return _types
 
@@ -287,6 +293,24 @@ def qgemv_kv_append(kv_type, k_pages, v_pages, n_pages, page_size, page_stride, 
         _check("qgemv_kv_append", st)
 
 
+def qgemv_qkv_append(kv_type, k_pages, v_pages, n_pages, page_size, page_stride, n_kv_heads,
+                     head_dim, table, max_pages, q_start, kv_len, n_seq, qkv, qkv_stride, n_rows,
+                     n_q_heads, rope_half, q_gamma, k_gamma, eps, rope_cos, rope_sin, rope_rows, q,
+                     q_stride, ws, ws_bytes=None, stream=None):
+    i32, f32, kv, device, raw = _torch_types()
+    d, c = device(), kv.get(kv_type)
+    st = lib().qgemv_qkv_append(kv_type, _t(k_pages, c, d, False), _t(v_pages, c, d, False), n_pages,
+                                page_size, page_stride, n_kv_heads, head_dim, _t(table, i32, d),
+                                max_pages, _t(q_start, i32, d), _t(kv_len, i32, d), n_seq,
+                                _t(qkv, f32, d, False), qkv_stride, n_rows, n_q_heads, rope_half,
+                                _t(q_gamma, f32, d), _t(k_gamma, f32, d), eps, _t(rope_cos, f32, d),
+                                _t(rope_sin, f32, d), rope_rows, _t(q, f32, d, False), q_stride,
+                                _t(ws, None, d), _nbytes(ws) if ws_bytes is None else ws_bytes,
+                                raw(d) if stream is None else _stream(stream))
+    if st:
+        _check("qgemv_qkv_append", st)
+
+
 def qgemv_attn(kv_type, k_pages, v_pages, n_pages, page_size, page_stride, n_kv_heads, head_dim,
                table, max_pages, kv_len, n_seq, q, q_stride, n_q_heads, scale, o, ws,
                ws_bytes=None, stream=None):
@@ -316,6 +340,22 @@ def qgemv_attn_prompt(kv_type, k_pages, v_pages, n_pages, page_size, page_stride
                                  raw(d) if stream is None else _stream(stream))
     if st:
         _check("qgemv_attn_prompt", st)
+
+
+def qgemv_attn_shared(kv_type, k_pages, v_pages, n_pages, page_size, page_stride, n_kv_heads,
+                      head_dim, table, max_pages, kv_len, n_seq, group_start, shared_len, n_group, q,
+                      q_stride, n_q_heads, scale, o, ws, ws_bytes=None, stream=None):
+    i32, f32, kv, device, raw = _torch_types()
+    d, c = device(), kv.get(kv_type)
+    st = lib().qgemv_attn_shared(kv_type, _t(k_pages, c, d, False), _t(v_pages, c, d, False), n_pages,
+                                 page_size, page_stride, n_kv_heads, head_dim, _t(table, i32, d),
+                                 max_pages, _t(kv_len, i32, d), n_seq, _t(group_start, i32, d),
+                                 _t(shared_len, i32, d), n_group, _t(q, f32, d, False), q_stride,
+                                 n_q_heads, scale, _t(o, f32, d), _t(ws, None, d),
+                                 _nbytes(ws) if ws_bytes is None else ws_bytes,
+                                 raw(d) if stream is None else _stream(stream))
+    if st:
+        _check("qgemv_attn_shared", st)
 
 
 def qgemv_attn_error(ws, stream=None) -> int:

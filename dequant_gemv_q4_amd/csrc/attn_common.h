@@ -285,6 +285,74 @@ __device__ __forceinline__ int row_start(const KvArgs &c, int i)
     return (int)(v < 0 ? 0 : v < c.n_rows ? v : c.n_rows);
 }
 
+// A block of 2^BL positions (at most a page) of a sequence, of which [from, to) are new.
+struct AppendBlock {
+    int b, from, to;
+    int64_t t0;                 // its first position, a multiple of its size
+    int64_t row0;               // row of position t0 (before the sequence's first where from > 0)
+};
+
+// This workgroup's block: those of sequence b begin at block id q_start[b] / size + 2 b, which leaves
+// every sequence enough ids wherever its first position lies.
+template <int BL>
+__device__ __forceinline__ bool append_block(const KvArgs &c, AppendBlock &w)
+{
+    const int lane = threadIdx.x & 63;
+    int id = blockIdx.x;
+    if (c.q_start && c.ps_log2 > BL) {
+        // two blocks to an XCD, eight workgroups apart: halves of the same lines of V may meet in its L2
+        // (8000 rows, pages of 64: 24.4 -> 23.4 us)
+        const int r = id % 16;
+        if (id - r + 16 <= (int)gridDim.x)
+            id += r % 8 * 2 + r / 8 - r;
+    }
+    int b = id, r0 = id, rows = 1, block = 0;
+    if (c.q_start) {
+        auto start = [&](int i) {
+            const int64_t v = c.q_start[i];
+            return (int)(v < 0 ? 0 : v < c.n_rows ? v : c.n_rows);
+        };
+        b = -1;
+        for (int b0 = 0; b0 < c.n_seq; b0 += 256) {       // four loads in flight
+            int first[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                first[x] = start(min(b0 + 64 * x + lane, c.n_seq));
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const int i = b0 + 64 * x + lane;
+                b += __popcll(__ballot(i < c.n_seq && (first[x] >> BL) + 2 * i <= id));
+            }
+        }
+        if (b < 0)
+            return false;
+        b = __builtin_amdgcn_readfirstlane(b);
+        r0 = start(b);
+        rows = start(b + 1) - r0;
+        block = id - ((r0 >> BL) + 2 * b);
+        if (rows <= 0 || block < 0)
+            return false;
+    }
+    // positions [lo, hi) of the sequence are new
+    const int64_t hi = c.kv_len[b], first = hi - rows, lo = first > 0 ? first : 0;
+    w.b = b;
+    w.t0 = ((lo >> BL) + block) << BL;
+    if (w.t0 >= hi)
+        return false;
+    w.from = (int)(lo > w.t0 ? lo - w.t0 : 0);
+    w.to = (int)(hi - w.t0 < 1 << BL ? hi - w.t0 : 1 << BL);
+    w.row0 = r0 + (w.t0 - first);
+    return true;
+}
+
+// The page of a block, or -1 if it has none.
+__device__ __forceinline__ int append_page(const KvArgs &c, const AppendBlock &w)
+{
+    const int64_t entry = w.t0 >> c.ps_log2;
+    const int page = entry < c.max_pages ? c.table[(int64_t)w.b * c.max_pages + entry] : -1;
+    return page < c.n_pages ? page : -1;
+}
+
 // Inclusive sum (or f, with f(v, 0) = v) over the lanes up to this one; lane 63 has the total.
 template <class F>
 __device__ __forceinline__ int wave_scan(int v, F f)

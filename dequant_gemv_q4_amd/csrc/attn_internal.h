@@ -22,12 +22,15 @@ __host__ __device__ constexpr int64_t attn_part_floats(int cols, int hd) { retur
 #define PROMPT_SPLITS 1024
 __host__ __device__ constexpr int prompt_slots(int hd) { return hd <= 128 ? PROMPT_SLOTS : 256; }
 
-enum KvType { KV_F16 = 1, KV_BF16 = 30 };
+enum KvType { KV_F16 = 1, KV_BF16 = 30, KV_I8 = 24, KV_F8 = 42 };
+// Codes of one byte, and behind a block's codes an f32 scale for each of its positions.
+__host__ __device__ constexpr bool kv_bytes(int type) { return type == KV_I8 || type == KV_F8; }
 
 // The paged cache and the step's metadata, as the public header describes them.
 struct KvArgs {
-    uint16_t *k, *v;            // page arrays (2-byte elements)
+    uint16_t *k, *v;            // page arrays (2-byte elements, or bytes: k8, v8)
     int64_t page_stride;        // elements from page to page
+    int64_t block;              // elements of a page's head
     int64_t n_pages;
     const int32_t *table;       // [n_seq][max_pages]
     const int32_t *q_start;     // [n_seq + 1], or NULL: one row per sequence
@@ -37,12 +40,28 @@ struct KvArgs {
     int ps_log2;                // log2 of the page size
     int nkv, hd;
     int64_t n_rows;
+
+    __host__ __device__ uint8_t *k8() const { return reinterpret_cast<uint8_t *>(k); }
+    __host__ __device__ uint8_t *v8() const { return reinterpret_cast<uint8_t *>(v); }
 };
 
 struct AppendArgs {
     KvArgs c;
     const float *ksrc, *vsrc;   // row 0 of the new K and V
     int64_t stride;             // floats from row to row
+};
+
+// Of qgemv_qkv_append, and of qgemv_kv_append into 8-bit pages (no Q heads, nothing turned).
+struct QkvArgs {
+    KvArgs c;
+    const float *q, *k, *v;     // row 0 of the Q, K and V heads
+    int64_t stride;             // floats from row to row
+    float *qo;
+    int64_t qo_stride;
+    const float *q_gamma, *k_gamma, *cos, *sin;
+    int64_t rope_rows;
+    int nq, half;
+    float eps;
 };
 
 struct PromptSplit;             // a split tile (attn_prompt_kernels.hip)
@@ -55,6 +74,9 @@ struct AttnArgs {
     float *part;                // workspace: partial results of a split
     int *pairs;                 // workspace: pairs of a prompt call
     PromptSplit *splits;        // workspace: its split tiles, by pair
+    const int32_t *group_start; // groups of sequences that begin alike [n_group + 1], or NULL
+    const int32_t *shared_len;  // [n_seq]
+    int n_group;
     unsigned int *count;        // workspace: arrival counters of a split, one per slot, 0 between calls
     int nq, group;              // query heads; query heads per KV head
     int side;                   // set by the launcher: tiles that read the same positions
@@ -82,6 +104,8 @@ bool prompt_in_16s(int64_t n_rows, int n_seq, int nq, int nkv, int hd, int64_t p
 
 // Launchers: a hipError_t value (0 = success).
 int launch_kv_append(int kv_type, const AppendArgs &a, void *stream);
+int launch_qkv_append(int kv_type, bool turn, const QkvArgs &a, void *stream);
+int launch_attn_any(int kv_type, const AttnArgs &a, void *stream);
 int launch_attn(int kv_type, const AttnArgs &a, void *stream);
 int launch_attn_rows(int kv_type, const AttnArgs &a, void *stream);     // few rows per sequence
 int launch_attn_prompt(int kv_type, const AttnArgs &a, void *stream);

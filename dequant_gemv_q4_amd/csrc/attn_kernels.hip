@@ -15,9 +15,6 @@ namespace qg {
 // writes 1 KB in one run (pages of 16 and 32) or in runs of 64 bytes, and reads runs of 64 or 128
 // bytes.  A piece with positions that are not new is written element by element.
 //
-// Blocks start at multiples of their size; sequence b's begin at block id q_start[b] / size + 2 b,
-// which leaves every sequence enough ids wherever its first position lies.
-//
 // Bound by HBM: 8000 rows of 8 heads of 128 (98.3 MB read and written) take 22.4 us, 4.4 TB/s, where a
 // copy reaches 4.94; one position at a time took 75 us.  One row of 2 heads: 2.8 us, a launch.
 template <int T, int BL>
@@ -25,57 +22,20 @@ __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a)
 {
     constexpr int BLOCK = 1 << BL, PIECES_V = BLOCK / 8;
     const KvArgs &c = a.c;
-    const int tid = threadIdx.x, lane = tid & 63, h = blockIdx.y;
-    int id = blockIdx.x;
-    if (c.q_start && c.ps_log2 > BL) {
-        // two blocks to an XCD, eight workgroups apart: halves of the same lines of V may meet in its L2
-        // (8000 rows, pages of 64: 24.4 -> 23.4 us)
-        const int r = id % 16;
-        if (id - r + 16 <= (int)gridDim.x)
-            id += r % 8 * 2 + r / 8 - r;
-    }
-    int b = id, r0 = id, rows = 1, block = 0;
-    if (c.q_start) {
-        auto start = [&](int i) {
-            const int64_t v = c.q_start[i];
-            return (int)(v < 0 ? 0 : v < c.n_rows ? v : c.n_rows);
-        };
-        b = -1;
-        for (int b0 = 0; b0 < c.n_seq; b0 += 256) {       // four loads in flight
-            int first[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-                first[x] = start(min(b0 + 64 * x + lane, c.n_seq));
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int i = b0 + 64 * x + lane;
-                b += __popcll(__ballot(i < c.n_seq && (first[x] >> BL) + 2 * i <= id));
-            }
-        }
-        if (b < 0)
-            return;
-        b = __builtin_amdgcn_readfirstlane(b);
-        r0 = start(b);
-        rows = start(b + 1) - r0;
-        block = id - ((r0 >> BL) + 2 * b);
-        if (rows <= 0 || block < 0)
-            return;
-    }
-    // positions [lo, hi) of the sequence are new; this block is positions [t0, t0 + BLOCK)
-    const int64_t hi = c.kv_len[b], first = hi - rows, lo = first > 0 ? first : 0;
-    const int64_t t0 = ((lo >> BL) + block) << BL;
-    if (t0 >= hi)
+    const int tid = threadIdx.x, h = blockIdx.y;
+    AppendBlock w;
+    if (!append_block<BL>(c, w))
         return;
-    const int64_t entry = t0 >> c.ps_log2;
-    const int page = entry < c.max_pages ? c.table[(int64_t)b * c.max_pages + entry] : -1;
-    if (page < 0 || page >= c.n_pages) {
+    const int page = append_page(c, w);
+    if (page < 0) {
         if (tid == 0 && h == 0)
             atomicOr(c.err, 1u);
         return;
     }
-    // new positions of the block: [from, to); row of position t0 + t at src + t * stride
-    const int from = (int)(lo > t0 ? lo - t0 : 0), to = (int)(hi - t0 < BLOCK ? hi - t0 : BLOCK);
-    const int64_t at = (r0 + (t0 - first)) * a.stride + (int64_t)h * c.hd;
+    const int64_t t0 = w.t0;
+    const int from = w.from, to = w.to;
+    // row of position t0 + t at src + t * stride
+    const int64_t at = w.row0 * a.stride + (int64_t)h * c.hd;
     const float *ks = a.ksrc + at, *vs = a.vsrc + at;
     const int64_t out = (int64_t)page * c.page_stride + ((int64_t)h * c.hd << c.ps_log2);
     const int slot = (int)(t0 & ((1 << c.ps_log2) - 1));

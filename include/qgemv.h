@@ -73,10 +73,10 @@
 extern "C" {
 #endif
 
-/* Weight formats, and the two element types of a key-value cache. */
+/* Weight formats, and the element types of a key-value cache. */
 enum { QG_Q4_0 = 2, QG_Q5_0 = 6, QG_Q8_0 = 8, QG_Q4_K = 12, QG_Q5_K = 13, QG_Q6_K = 14,
        QG_IQ4_NL = 20, QG_IQ4_XS = 23, QG_Q1_0 = 40, QG_AQ4 = 41 };
-enum { QG_F16 = 1, QG_BF16 = 30 };
+enum { QG_F16 = 1, QG_BF16 = 30, QG_I8 = 24, QG_F8 = 42 };
 
 enum {
     QG_OK = 0,
@@ -98,7 +98,8 @@ enum { QG_OP_GEMV = 0, QG_OP_NRM = 1, QG_OP_GUS_NRM = 2, QG_OP_RES = 3, QG_OP_AR
        QG_OP_MOE = 5, QG_OP_NRM_BIAS = 6 };
 
 /* Operation ids for qgemv_attn_workspace_bytes. */
-enum { QG_OP_KV_APPEND = 7, QG_OP_ATTN = 8, QG_OP_ATTN_PROMPT = 9 };
+enum { QG_OP_KV_APPEND = 7, QG_OP_ATTN = 8, QG_OP_ATTN_PROMPT = 9, QG_OP_QKV_APPEND = 10,
+       QG_OP_ATTN_SHARED = 11 };
 
 /* Scores of qgemv_route. */
 enum { QG_SCORE_SOFTMAX = 0, QG_SCORE_SIGMOID = 1 };
@@ -253,13 +254,22 @@ int qgemv_moe_error(const void *ws, int64_t n_exp, int64_t N, int64_t K, int fmt
 /* Paged key-value cache and the attention that reads it
  * -----------------------------------------------------
  * The cache is a pool of pages of page_size consecutive positions, in two arrays of one element
- * type (kv_type QG_F16 or QG_BF16).  Page p, head h (64-bit offsets, in elements):
- *   k_pages + p * page_stride + h * page_size * head_dim   holds K as [page_size][head_dim],
- *   v_pages + p * page_stride + h * page_size * head_dim   holds V as [head_dim][page_size]
+ * type (kv_type QG_F16, QG_BF16, or the 8-bit QG_I8 and QG_F8).  Page p, head h (64-bit offsets, in
+ * elements):
+ *   k_pages + p * page_stride + h * block   holds K as [page_size][head_dim],
+ *   v_pages + p * page_stride + h * block   holds V as [head_dim][page_size]
  * (V transposed inside the page: eight consecutive positions of one channel are one 16-byte load,
- * as eight consecutive channels of one position are for K).  page_stride, at least
- * n_kv_heads * page_size * head_dim and a multiple of 8, lets one pool hold several layers or K
- * and V side by side.  table is int32 [n_seq][max_pages]: position t of sequence b lies in slot
+ * as eight consecutive channels of one position are for K).  block is page_size * head_dim for f16
+ * and bf16.  An 8-bit block is page_size * (head_dim + 4) bytes: behind the codes stands one f32
+ * scale d for each of its positions, [page_size], and the value of a code is d * code, for
+ *   QG_I8: code a signed byte, d = max(amax / 127, 2^-126), code = x / d to the nearest, ties to even;
+ *   QG_F8: code an e4m3 (bias 7, largest 448, no infinities), d the least power of two, from 2^-126
+ *          on, with amax <= 448 d, code = x / d to the nearest-even;
+ * amax the largest |x| of the position's head_dim values.  The code is that of the exact quotient.
+ * Where one of the values is not finite, d is NaN and the codes are 0: the whole position of the head
+ * reads as NaN.  The e4m3 NaN codes are never written, and a cache has to hold none at positions in use.
+ * page_stride, at least n_kv_heads * block and a multiple of 8 (8-bit: 16), lets one pool hold several
+ * layers or K and V side by side.  table is int32 [n_seq][max_pages]: position t of sequence b lies in slot
  * t % page_size of page table[b][t / page_size].  Entries behind a sequence's last position are
  * never read.  kv_len, int32 [n_seq], counts a sequence's cached positions WITH the new ones of
  * this step.
@@ -289,14 +299,14 @@ int qgemv_moe_error(const void *ws, int64_t n_exp, int64_t N, int64_t K, int fmt
  * 16-byte aligned, row strides are multiples of 4 floats.  Calls that share a workspace are ordered on
  * one stream, as above; calls with workspaces of their own may run side by side. */
 
-/* Workspace bytes of an attention-side operation (QG_OP_KV_APPEND, QG_OP_ATTN,
- * QG_OP_ATTN_PROMPT), or -1 on invalid sizes.  It holds the sticky flag and the partial results of
+/* Workspace bytes of an attention-side operation (QG_OP_KV_APPEND, QG_OP_QKV_APPEND, QG_OP_ATTN,
+ * QG_OP_ATTN_PROMPT, QG_OP_ATTN_SHARED), or -1 on invalid sizes.  It holds the sticky flag and the partial results of
  * a split over the cache's length, so, like qgemv_moe's, it must be zero-filled once after
  * allocation; a larger one also serves.  Host-only. */
 int64_t qgemv_attn_workspace_bytes(int op, int n_seq, int n_q_heads, int n_kv_heads,
                                    int head_dim);
 
-/* Store the new K and V rows in the cache, rounded to nearest-even.  k and v point at the first K
+/* Store the new K and V rows in the cache, rounded to nearest-even (8-bit: quantised as above).  k and v point at the first K
  * and V value of row 0, f32, kv_stride floats apart from row to row (the fused QKV output: qkv +
  * n_q_heads * head_dim, qkv + (n_q_heads + n_kv_heads) * head_dim, stride (n_q_heads +
  * 2 n_kv_heads) * head_dim), heads back to back. */
@@ -305,6 +315,27 @@ int qgemv_kv_append(int kv_type, void *k_pages, void *v_pages, int64_t n_pages, 
                     int max_pages, const int32_t *q_start, const int32_t *kv_len, int n_seq,
                     const float *k, const float *v, int64_t kv_stride, int64_t n_rows, void *ws,
                     size_t ws_bytes, void *stream);
+
+/* From the fused QKV output to the cache in one pass: what qgemv_qk_norm_rope and qgemv_kv_append do
+ * one after the other, for any number of packed rows.  qkv is f32, row r at qkv + r * qkv_stride: Q
+ * heads, K heads, V heads.  Each Q (K) head is normalised with q_gamma (k_gamma; NULL skips that) and
+ * rotated as in qgemv_qk_norm_rope, but with row t of the tables rope_cos and rope_sin, f32
+ * [rope_rows][rope_half], for a row at position t.  Q goes to q, row r at q + r * q_stride
+ * ([n_rows][n_q_heads * head_dim], what the attentions take), K and V to the cache; K is computed in
+ * 64 bits and rounded once.  q may be qkv itself with q_stride = qkv_stride (in place), else it
+ * overlaps nothing.  K and V of qkv stay as they are.  A row at a negative position, or at or behind
+ * rope_rows where rope_half > 0 (that sets the flag of qgemv_attn_error), is left out: nothing is
+ * stored and its q is not written.  A position without a valid page is not stored; its q is written.
+ * q_start NULL as in qgemv_kv_append.  Limits: 0 <= rope_half <= head_dim / 2, eps >= 0 finite,
+ * rope_rows in [1, 2^24] (rope_half 0: no tables are read and they may be NULL), gammas and tables
+ * 16-byte aligned, n_rows * n_q_heads <= 2^30. */
+int qgemv_qkv_append(int kv_type, void *k_pages, void *v_pages, int64_t n_pages, int page_size,
+                     int64_t page_stride, int n_kv_heads, int head_dim, const int32_t *table,
+                     int max_pages, const int32_t *q_start, const int32_t *kv_len, int n_seq,
+                     const float *qkv, int64_t qkv_stride, int64_t n_rows, int n_q_heads,
+                     int rope_half, const float *q_gamma, const float *k_gamma, float eps,
+                     const float *rope_cos, const float *rope_sin, int64_t rope_rows, float *q,
+                     int64_t q_stride, void *ws, size_t ws_bytes, void *stream);
 
 /* Attention of one new token per sequence: o[b][h] = sum_t p_t V_t over the positions
  * t < kv_len[b], p = softmax_t(scale q[b][h] . K_t).  q is f32, row b at q + b * q_stride, heads
@@ -337,7 +368,23 @@ int qgemv_attn_prompt(int kv_type, const void *k_pages, const void *v_pages, int
                       int64_t n_rows, int n_q_heads, float scale, float *o, void *ws,
                       size_t ws_bytes, void *stream);
 
-/* Reads and clears the flag that the three calls above leave in their workspace (*flag = 1 if any
+/* qgemv_attn for a batch whose sequences begin alike: the shared positions are read once for a group,
+ * by tiles of all its sequences' query heads.  Group g is the sequences group_start[g] ..
+ * group_start[g + 1] - 1 (int32 [n_group + 1], not decreasing, within [0, n_seq]); a sequence before
+ * the first or behind the last group shares nothing.  The first shared_len[b] positions of sequence b
+ * (int32 [n_seq]; below 1: none) are those of its group's first sequence, and are read from that one's
+ * pages: its shared_len has to be its group's largest.  Of another's that is larger the positions
+ * between are left out, and the flag is set.  The positions from shared_len[b] on, a begun page
+ * included, are read from the sequence's own pages.  As everywhere, a sequence sees kv_len[b]
+ * positions in all, also where shared_len[b] is larger.  1 <= n_group <= n_seq. */
+int qgemv_attn_shared(int kv_type, const void *k_pages, const void *v_pages, int64_t n_pages,
+                      int page_size, int64_t page_stride, int n_kv_heads, int head_dim,
+                      const int32_t *table, int max_pages, const int32_t *kv_len, int n_seq,
+                      const int32_t *group_start, const int32_t *shared_len, int n_group,
+                      const float *q, int64_t q_stride, int n_q_heads, float scale, float *o, void *ws,
+                      size_t ws_bytes, void *stream);
+
+/* Reads and clears the flag that the calls above leave in their workspace (*flag = 1 if any
  * position of an earlier call on this workspace had no valid page).  Like qgemv_moe_error it
  * SYNCHRONIZES `stream`. */
 int qgemv_attn_error(const void *ws, int *flag, void *stream);

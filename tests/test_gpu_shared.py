@@ -1,0 +1,157 @@
+"""Attention of a batch whose sequences begin alike, on the GPU, against the definition in 64 bits with each
+sequence's positions spelled out (kv_common)."""
+import numpy as np
+import pytest
+
+from gpu_common import dev, host, require_gpu, say, torch
+
+import dequant_gemv_q4_amd as q
+from dequant_gemv_q4_amd import device as D
+from kv_common import ALL, BYTES, Cache, attention_row, check_rows, held, lost64, scales64
+from test_gpu_kv8 import _draw, ints
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    require_gpu()
+
+
+def shared(kv_type, nq, nkv, hd, page, groups, seed=0, outside=(0, 0), scale=None, extra_entries=2, lens=None,
+           bad_rest=False, gap=0, spread=1.0):
+    """groups: lists of (shared positions, cached positions of its own behind them) of each sequence, the
+    largest share first.  outside: sequences before the first and behind the last group."""
+    say(f"shared type={kv_type} nq={nq} nkv={nkv} hd={hd} page={page} groups={[g[:3] for g in groups[:4]]}")
+    rng = np.random.default_rng([93, seed])
+    scale = hd ** -0.5 if scale is None else scale
+    K, V, tables, starts, share = [], [], {}, [outside[0]], []
+    for i in range(outside[0]):
+        k, v = _draw(rng, [17 + 30 * i], nkv, hd, spread)
+        K += k
+        V += v
+        share.append(9)                                     # not of a group: it shares nothing
+    for g in groups:
+        first = len(K)
+        for i, (s, own) in enumerate(g):
+            k, v = _draw(rng, [s + own], nkv, hd, spread)
+            if i:
+                k[0][:s], v[0][:s] = K[first][:s], V[first][:s]
+                for e in range(s // page):
+                    tables[(first + i, e)] = (first, e)
+            K += k
+            V += v
+            share.append(s)
+        starts.append(len(K))
+    for i in range(outside[1]):
+        k, v = _draw(rng, [40 + i], nkv, hd, spread)
+        K += k
+        V += v
+        share.append(33)
+    c = Cache(kv_type, K, V, page, nkv, hd, rng, extra_entries=extra_entries, tables=tables, gap=gap)
+    if bad_rest:                                            # the others' entries of the prefix are not read
+        for (b, e) in tables:
+            c.table[b, e] = -5
+    n = len(K)
+    kv = c.kv_len if lens is None else ints(lens)
+    length = [len(k) for k in K] if lens is None else lens
+    width = (nq + 2 * nkv) * hd
+    x = rng.standard_normal((n, width)).astype(np.float32)
+    o = torch.full((n, nq * hd), float("nan"), device="cuda")
+    ws = D.attn_workspace(q.OP_ATTN_SHARED, n, nq, nkv, hd)
+    q.qgemv_attn_shared(*c.args(), kv, n, ints(starts), ints(share), len(groups), dev(x), width, nq, scale, o, ws)
+    parts = []
+    for b in range(n):
+        hk, hv = held(K[b], kv_type), held(V[b], kv_type)
+        dv = scales64(V[b], kv_type) if kv_type in BYTES and len(V[b]) else np.ones(V[b].shape[:2])
+        qr = x[b, :nq * hd].reshape(nq, hd)
+        parts.append((*attention_row(qr, hk, hv, nkv, scale, length[b] - 1),
+                      lost64(qr, hk, dv, nkv, scale, length[b] - 1, kv_type)))
+    check_rows(host(o), parts, length, hd, kv_type, "shared")
+    assert q.qgemv_attn_error(ws) == 0
+    return c, x, host(o)
+
+
+@pytest.mark.parametrize("kv_type", ALL)
+@pytest.mark.parametrize("nq,nkv,hd,page", [(12, 2, 128, 16), (8, 8, 64, 32), (5, 1, 96, 16), (20, 1, 64, 64),
+                                            (40, 2, 128, 128), (4, 2, 256, 16), (6, 3, 192, 256)])
+def test_shared_small(kv_type, nq, nkv, hd, page):
+    """Prefixes that end at, before and behind page and tile borders, groups of one, none shared, no tail."""
+    groups = [[(64, 5), (64, 1), (64, 200)], [(33, 7)], [(0, 9), (0, 0), (0, 70)], [(130, 0), (130, 3), (100, 31)],
+              [(16, 1), (15, 1), (1, 1), (0, 2)], [(257, 90), (257, 300), (256, 1), (255, 64)]]
+    shared(kv_type, nq, nkv, hd, page, groups, hd + page, outside=(2, 1))
+
+
+@pytest.mark.parametrize("kv_type,nq,nkv,hd,page,groups", [
+    (q.F16, 12, 2, 128, 16, [[(3000, 40)] * 9]),
+    (q.BF16, 8, 4, 64, 64, [[(1500, 700), (1500, 3)] * 4, [(2000, 20)] * 5]),
+    (q.I8, 16, 1, 128, 32, [[(5000, 100)] * 20]),
+    (q.F8, 24, 8, 64, 16, [[(1800, 100), (1700, 130)] * 16]),
+    (q.F16, 40, 2, 96, 32, [[(900, 9)] * 3, [(4000, 1)] * 2]),
+    (q.F8, 4, 1, 256, 64, [[(2500, 60)] * 40]),
+    (q.BF16, 14, 2, 192, 16, [[(777, 33)] * 11, [(778, 2000), (778, 1)]]),
+    (q.I8, 2, 1, 64, 16, [[(9000, 1)] * 2]),
+])
+def test_shared_long(kv_type, nq, nkv, hd, page, groups):
+    shared(kv_type, nq, nkv, hd, page, groups, len(groups))
+
+
+@pytest.mark.parametrize("kv_type", [q.F16, q.F8])
+def test_shared_many_sequences_and_groups(kv_type):
+    rng = np.random.default_rng(4)
+    groups = [[(int(s), int(a)) for a in rng.integers(0, 40, m)]
+              for s, m in zip(rng.integers(0, 150, 90), rng.integers(1, 5, 90))]
+    shared(kv_type, 4, 2, 64, 16, groups, 5, outside=(3, 4))
+    shared(kv_type, 4, 1, 64, 16, [[(200, int(a)) for a in rng.integers(0, 30, 600)]], 6)
+
+
+@pytest.mark.parametrize("kv_type", ALL)
+def test_shared_pages_of_the_others_are_not_read(kv_type):
+    shared(kv_type, 6, 2, 64, 16, [[(100, 20), (100, 7), (48, 3)], [(300, 2), (300, 40)]], 7, bad_rest=True, gap=32)
+
+
+@pytest.mark.parametrize("kv_type", ALL)
+def test_shared_lengths_below_the_prefix(kv_type):
+    """A padded slot, a length inside the prefix, one that ends with it; kv_len counts everywhere."""
+    shared(kv_type, 4, 2, 128, 16, [[(150, 10), (150, 6), (150, 30), (150, 0), (150, 9)]], 8,
+           lens=[160, 0, 70, 150, -3])
+
+
+@pytest.mark.parametrize("kv_type", ALL)
+def test_shared_promise_broken_and_bad_pages(kv_type):
+    """A share larger than the first sequence's leaves positions out and sets the flag; so does a page of the
+    prefix that is not there, for all its sequences."""
+    nq, nkv, hd, page = 4, 1, 64, 16
+    rng = np.random.default_rng(9)
+    K, V = _draw(rng, [80, 100], nkv, hd)
+    K[1][:64], V[1][:64] = K[0][:64], V[0][:64]
+    c = Cache(kv_type, K, V, page, nkv, hd, rng)
+    x = rng.standard_normal((2, nq * hd)).astype(np.float32)
+
+    def run(share, keep):
+        o = torch.full((2, nq * hd), float("nan"), device="cuda")
+        ws = D.attn_workspace(q.OP_ATTN_SHARED, 2, nq, nkv, hd)
+        q.qgemv_attn_shared(*c.args(), c.kv_len, 2, ints([0, 2]), ints(share), 1, dev(x), nq * hd, nq, 0.125, o, ws)
+        parts = []
+        for b in range(2):
+            k, v = K[b][keep[b]], V[b][keep[b]]
+            dv = scales64(v, kv_type) if kv_type in BYTES else np.ones(v.shape[:2])
+            qr = x[b].reshape(nq, hd)
+            hk = held(k, kv_type)
+            parts.append((*attention_row(qr, hk, held(v, kv_type), nkv, 0.125, len(k) - 1),
+                          lost64(qr, hk, dv, nkv, 0.125, len(k) - 1, kv_type)))
+        check_rows(host(o), parts, [80, 100], hd, kv_type, "left out")
+        assert q.qgemv_attn_error(ws) == 1 and q.qgemv_attn_error(ws) == 0
+
+    run([40, 64], [np.r_[0:80], np.r_[0:40, 64:100]])
+    c.table[0, 1] = -1
+    run([64, 64], [np.r_[0:16, 32:80], np.r_[0:16, 32:100]])
+
+
+def test_shared_is_attention_without_groups():
+    """The same batch by qgemv_attn, pages shared in its table: equal up to the tolerance of either."""
+    c, x, o = shared(q.F16, 8, 2, 64, 16, [[(320, 20), (320, 50), (320, 1)]], 10)
+    one = torch.empty((3, 8 * 64), device="cuda")
+    ws = D.attn_workspace(q.OP_ATTN, 3, 8, 2, 64)
+    q.qgemv_attn(*c.args(), c.kv_len, 3, dev(x), 12 * 64, 8, 64 ** -0.5, one, ws)
+    assert np.abs(host(one) - o).max() <= 2e-5 * np.abs(o).max()
