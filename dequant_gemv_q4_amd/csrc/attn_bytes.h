@@ -1,0 +1,136 @@
+// attn_bytes.h -- device helpers of the attention over 8-bit pages.
+//
+// A cached value is d * code with d one f32 scale for a position of a head, so scores are
+// (q . code) d^K scale and outputs sum p (d^V code): codes enter the products as f16 (an e4m3 and a signed
+// byte are one exactly), the scales the f32 scores and weights.  Queries and weights are two f16 pieces, as
+// over f16 pages.
+//
+// What has to fit f16 is the weight times the scale of V, w = p d^V.  The scales are taken relative to 2^r, r
+// a whole number that follows the largest scale that a wave has met, and a column keeps the exponent `top` of
+// the largest relative scale that it has seen (at least LEAST_TOP): its shift puts the largest p at
+// 2^(LIFT - top), so that w is at most 2^LIFT when the shift moves and under 2^TOP afterwards.  Of w 2^-25 is
+// lost at most: 2^-35 of the largest weight times the largest scale that the column sees.  Sums of p stay in
+// f32.
+#pragma once
+
+#include <utility>
+
+#include "attn_common.h"
+
+namespace qg {
+
+constexpr float LIFT8 = LIFT<KV_F16>, TOP8 = TOP<KV_F16>;
+constexpr float LEAST_TOP = -30.0f;            // so far below 2^r, scales lose bits instead
+constexpr float R_SLACK = 30.0f;               // 2^r moves when a scale is so far above it
+
+// Sixteen codes as f16, in order.
+template <int T>
+__device__ __forceinline__ void halves_of(au4 x, au4 &lo, au4 &hi)
+{
+    typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+    uint32_t out[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (T == KV_F8) {
+            out[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x[i], 1.0f, false));
+            out[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(x[i], 1.0f, true));
+        } else {
+            // 1024 + (128 + code) as an f16 is the byte below 0x64
+            const uint32_t y = x[i] ^ 0x80808080u;
+            const h2 off = {(_Float16)1152.0f, (_Float16)1152.0f};
+            const h2 a = __builtin_bit_cast(h2, __builtin_amdgcn_perm(0x64646464u, y, 0x04010400u)) - off;
+            const h2 b = __builtin_bit_cast(h2, __builtin_amdgcn_perm(0x64646464u, y, 0x04030402u)) - off;
+            out[2 * i] = __builtin_bit_cast(uint32_t, a);
+            out[2 * i + 1] = __builtin_bit_cast(uint32_t, b);
+        }
+    }
+    lo = au4{out[0], out[1], out[2], out[3]};
+    hi = au4{out[4], out[5], out[6], out[7]};
+}
+
+// The value of lane E of each 16 lanes.
+template <int E>
+__device__ __forceinline__ float lane_of_16(float v)
+{
+    return __builtin_bit_cast(float,
+                              __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x150 + E, 0xF, 0xF, true));
+}
+// x[e] *= lane e's v, of 16.
+template <int... E, class X>
+__device__ __forceinline__ void times_lanes(X &&x, float v, std::integer_sequence<int, E...>)
+{
+    ((x(E) *= lane_of_16<E>(v)), ...);
+}
+template <class X>
+__device__ __forceinline__ void times_lanes(X &&x, float v)
+{
+    times_lanes(x, v, std::make_integer_sequence<int, 16>());
+}
+template <int... E, class X>
+__device__ __forceinline__ void each_lane(X &&x, float v, std::integer_sequence<int, E...>)
+{
+    ((x(E, lane_of_16<E>(v))), ...);
+}
+// x(e, lane e's v) for e < 16.
+template <class X>
+__device__ __forceinline__ void each_lane(X &&x, float v)
+{
+    each_lane(x, v, std::make_integer_sequence<int, 16>());
+}
+
+// The largest of a row of 16 lanes, in all of them; NaN is passed over.
+__device__ __forceinline__ float max_of_16(float v)
+{
+    auto turn = [](float x, auto ctrl) {
+        return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x),
+                                                                     decltype(ctrl)::value, 0xF, 0xF, true));
+    };
+    v = fmaxf(v, turn(v, std::integral_constant<int, 0x121>()));      // row_ror 1, 2, 4, 8
+    v = fmaxf(v, turn(v, std::integral_constant<int, 0x122>()));
+    v = fmaxf(v, turn(v, std::integral_constant<int, 0x124>()));
+    return fmaxf(v, turn(v, std::integral_constant<int, 0x128>()));
+}
+
+// The exponent e of the least power of two above v (0: very low).
+__device__ __forceinline__ float exponent_above(float v)
+{
+    return v > 0.f ? (float)__builtin_amdgcn_frexp_expf(v) : -200.0f;
+}
+
+// shift_of for weights that end at 2^(TOP8 - top).  Where scores are so large that LIFT8 - top - score is
+// rounded too far up, one rounding step less than -top - score is as good.
+__device__ __forceinline__ float shift8_of(float top_score, float top)
+{
+    const float r = LIFT8 - top - top_score;
+    return r + top_score > TOP8 - top ? -top_score - top - fabsf(top_score) * 0x1p-23f : r;
+}
+
+// A part of a column's positions is held as its mean (weighted by the weights), the exponent m of its weights
+// and their sum l; parts k join by the factors l_k 2^(m_k - max m) over their sum.  What a part counts for is
+// in l alone, so that a mean near the end of f32 never overflows; 0 x NaN keeps a NaN that was seen.
+struct Factors {
+    float m, l;
+};
+template <int N>
+__device__ __forceinline__ Factors join_factors(const float (&m)[N], const float (&l)[N], int n, float (&f)[N])
+{
+    Factors r = {-INFINITY, 0.f};
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+        if (k < n)
+            r.m = fmaxf(r.m, m[k]);
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+        if (k < n) {
+            f[k] = l[k] * join_weight(m[k], r.m);
+            r.l += f[k];
+        }
+    const float inv = inverse_sum(r.l);
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+        if (k < n)
+            f[k] *= inv;
+    return r;
+}
+
+}  // namespace qg

@@ -105,6 +105,8 @@ bool prompt_in_16s(int64_t n_rows, int n_seq, int nq, int nkv, int hd, int64_t p
 // Launchers: a hipError_t value (0 = success).
 int launch_kv_append(int kv_type, const AppendArgs &a, void *stream);
 int launch_qkv_append(int kv_type, bool turn, const QkvArgs &a, void *stream);
+int launch_attn8(int kv_type, const AttnArgs &a, void *stream);
+int launch_attn8_rows(int kv_type, const AttnArgs &a, void *stream);    // few rows per sequence
 int launch_attn_any(int kv_type, const AttnArgs &a, void *stream);
 int launch_attn(int kv_type, const AttnArgs &a, void *stream);
 int launch_attn_rows(int kv_type, const AttnArgs &a, void *stream);     // few rows per sequence
