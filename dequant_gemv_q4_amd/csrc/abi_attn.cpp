@@ -192,9 +192,7 @@ static int run_attn(int op, int kv_type, const void *k_pages, const void *v_page
     a.n_group = groups.n;
     if (op == QG_OP_ATTN && kv_bytes(kv_type))
         return launch_status(launch_attn8(kv_type, a, stream));
-    if (prompt && kv_bytes(kv_type) && prompt_in_16s(n_rows, n_seq, nq, nkv, hd, (int64_t)max_pages << a.c.ps_log2))
-        return launch_status(launch_attn8_rows(kv_type, a, stream));
-    if (shared || kv_bytes(kv_type))
+    if (shared)
         return launch_status(launch_attn_any(kv_type, a, stream));
     return launch_status(prompt ? launch_attn_prompt(kv_type, a, stream)
                                 : launch_attn(kv_type, a, stream));

@@ -55,7 +55,18 @@ __device__ __forceinline__ float lane_of_16(float v)
     return __builtin_bit_cast(float,
                               __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x150 + E, 0xF, 0xF, true));
 }
-// x[e] *= lane e's v, of 16.
+// An element of a register vector.
+template <class V>
+struct Ref {
+    V &v;
+    int e;
+    __device__ __forceinline__ Ref &operator*=(float f)
+    {
+        v[e] *= f;
+        return *this;
+    }
+};
+// x(e) *= lane e's v, of 16.
 template <int... E, class X>
 __device__ __forceinline__ void times_lanes(X &&x, float v, std::integer_sequence<int, E...>)
 {

@@ -24,7 +24,7 @@
 // rows of nine prompts (24 / 8 of 64, bf16, three pieces) 36 us.
 #include <hip/hip_runtime.h>
 
-#include "attn_common.h"
+#include "attn_bytes.h"
 
 namespace qg {
 
@@ -69,7 +69,9 @@ __host__ __device__ constexpr int64_t prompt_part_floats(int hd) { return (int64
 template <int T, int D, bool FEW>
 __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs a, int slots)
 {
-    constexpr int NP = PIECES<T>, KB = D / 16, DT = D / 32;
+    constexpr bool BYTES = kv_bytes(T);
+    constexpr int F = BYTES ? KV_F16 : T;              // operands of the products
+    constexpr int NP = PIECES<F>, KB = D / 16, DT = D / 32;
     constexpr int PR = D / 8;                          // 16-byte pieces of a K row
     // 32-position tiles of scores held at a time: three query pieces leave registers for one
     constexpr int NT = NP * D > 384 ? 1 : 2;
@@ -78,6 +80,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
     constexpr int HALF = PT_STEP * D * 2;              // bytes of a K (or V) buffer
     constexpr int PASS = HALF / 4096;                  // copies of a wave for either
     __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * HALF];   // K0 V0 K1 V1
+    __shared__ float s_scale[BYTES ? 2 : 1][2][PT_STEP];               // of K and V
     __shared__ int s_odd[4], s_last;
     const KvArgs &c = a.c;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -139,7 +142,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
         // of their product with it exact (as their maximum is), none of either sign or zero is turned,
         // and a masked -inf stays one
         int e2 = 0;
-        const float f = frexpf(a.scale, &e2) * LOG2E, sc = q_scale<T>(max_x32(amax));
+        const float f = frexpf(a.scale, &e2) * LOG2E, sc = q_scale<F>(max_x32(amax));
         unscale = fmaxf(ldexpf(1.0f / sc, e2), 0x1p-149f);
 #pragma unroll
         for (int k = 0; k < KB; ++k) {
@@ -148,7 +151,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 w[e] = v[k][e] * sc * f;
-            split8<T>(w, out);
+            split8<F>(w, out);
 #pragma unroll
             for (int x = 0; x < NP; ++x)
                 qf[x][k] = out[x];
@@ -160,7 +163,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
     const int32_t *table = c.table + (int64_t)w.b * c.max_pages;
     const int ps_mask = (1 << c.ps_log2) - 1;
     const int last_entry = p.hi > 0 ? (p.hi - 1) >> c.ps_log2 : 0;
-    const int64_t head_off = (int64_t)hkv * D << c.ps_log2;
+    const int64_t head_off = BYTES ? (int64_t)hkv * c.block : (int64_t)hkv * D << c.ps_log2;
     const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
     auto key = [](int row) { return KO == 8 ? row & 15 : KO == 4 ? (row >> 1) & 7 : (row >> 2) & 3; };
     uint32_t ksrc[PASS];
@@ -188,6 +191,63 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
             pt_copy16(vp + ((32 * x) << c.ps_log2), vsrc, __builtin_amdgcn_readfirstlane(dst + HALF + 1024 * x));
         return bad;
     };
+    // 8-bit pages: the same block of a step goes through registers, 16 codes a lane, and to LDS as f16 where
+    // the copies would have put it; lanes 0-15 carry the scales of K, lanes 16-31 those of V
+    constexpr int PASS8 = (D + 63) / 64;
+    struct Codes {
+        au4 k[PASS8], v[PASS8];
+        float d;
+        uint32_t bad;
+    };
+    auto load8 = [&](int s, int ids, Codes &x) {
+        const bool ok = ids >= 0 && ids < c.n_pages;
+        x.bad = (uint32_t)__ballot(!ok) & 15u;
+        const int page = __builtin_amdgcn_readlane(ok ? ids : 0, wave);
+        const int slot = (s * PT_STEP + 16 * wave) & ps_mask;
+        const int64_t at = (int64_t)page * c.page_stride + head_off;
+        const uint8_t *kp = c.k8() + at + slot * D, *vp = c.v8() + at + slot;
+        const uint8_t *dp = (lane & 16 ? c.v8() : c.k8()) + at + ((int64_t)D << c.ps_log2) + 4 * slot;
+        x.d = reinterpret_cast<const float *>(dp)[lane & 15];
+#pragma unroll
+        for (int i = 0; i < PASS8; ++i) {
+            const int idx = min(64 * i + lane, D - 1);
+            x.k[i] = *reinterpret_cast<const au4 *>(kp + 16 * idx);
+            x.v[i] = *reinterpret_cast<const au4 *>(vp + ((int64_t)idx << c.ps_log2));
+        }
+    };
+    auto stage8 = [&](int s, int buf, Codes &x) {
+        uint8_t *kb = lds + buf * 2 * HALF + wave * (HALF / 4), *vb = kb + HALF;
+        const int left = x.bad >> wave & 1 ? 0 : p.hi - s * PT_STEP - 16 * wave;   // positions of the block
+        if (left < 16) {
+            // what a masked position holds must not reach the product: an e4m3 may be NaN
+            if constexpr (T == KV_F8)
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const int m = left - 4 * w;
+                    const uint32_t keep = m >= 4 ? ~0u : m <= 0 ? 0u : (1u << (8 * m)) - 1u;
+#pragma unroll
+                    for (int i = 0; i < PASS8; ++i)
+                        x.v[i][w] &= keep;
+                }
+            x.d = (lane & 15) < left ? x.d : 0.f;
+        }
+        if (lane < 32)
+            s_scale[BYTES ? buf : 0][lane >> 4][16 * wave + (lane & 15)] = x.d;
+#pragma unroll
+        for (int i = 0; i < PASS8; ++i) {
+            const int idx = 64 * i + lane, row = idx / (D / 16), pc = 2 * (idx % (D / 16));
+            if (D % 64 == 0 || idx < D) {
+                au4 lo, hi;
+                halves_of<T>(x.k[i], lo, hi);
+                *reinterpret_cast<au4 *>(kb + row * D * 2 + ((pc ^ key(row)) << 4)) = lo;
+                *reinterpret_cast<au4 *>(kb + row * D * 2 + (((pc + 1) ^ key(row)) << 4)) = hi;
+                halves_of<T>(x.v[i], lo, hi);
+                const int turn = idx >> 4 & 1;
+                *reinterpret_cast<au4 *>(vb + idx * 32 + (turn << 4)) = lo;
+                *reinterpret_cast<au4 *>(vb + idx * 32 + ((turn ^ 1) << 4)) = hi;
+            }
+        }
+    };
 
     // operand reads: K row of score row col, pieces 2 k + hf; V channel col of 32, piece hf of block k
     const int krow = 16 * (col >> 4) + 8 * ((col >> 2) & 1) + 4 * ((col >> 3) & 1) + (col & 3);
@@ -204,6 +264,8 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
         for (int r = 0; r < 16; ++r)
             o[d][r] = 0.f;
     float shift = NO_SHIFT, l = 0.f;
+    // 8-bit: the wave's reference of V's scales, the row's largest scale above it
+    float ref = -200.0f, top = LEAST_TOP;
 
     // raw (unscaled) scores of positions 32 NT sub .. of a step
     auto scores = [&](int buf, int sub, af16 (&sc)[NT]) {
@@ -233,9 +295,28 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
             for (int y = NP - 1; y >= 0; --y)
 #pragma unroll
                 for (int tt = 0; tt < NT; ++tt)
-                    sc[tt] = mm32<T>(kf[k % (AHEAD + 1)][tt], qf[y][k], sc[tt]);
+                    sc[tt] = mm32<F>(kf[k % (AHEAD + 1)][tt], qf[y][k], sc[tt]);
             __builtin_amdgcn_sched_barrier(0);
         }
+    };
+    // 8-bit: position of lane i of each 16 in tile x of a step, so that value r of a row is lane r's
+    auto scale_at = [&](int x) { return 32 * x + 16 * ((lane & 15) >> 3) + 8 * hf + (lane & 7); };
+    // the scales dv of a step's tiles relative to 2^ref, and the largest that the row sees
+    auto follow = [&](float (&dv)[NT], float seen, float most) {
+        if (most > ref + R_SLACK) {                       // (uniform)
+            const float f = __builtin_amdgcn_exp2f(ref - most);
+            top = fmaxf(top + (ref - most), LEAST_TOP);
+            ref = most;
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    o[d][r] *= f;
+        }
+        top = fmaxf(top, exponent_above(seen) - ref);
+#pragma unroll
+        for (int tt = 0; tt < NT; ++tt)
+            dv[tt] = ldexpf(dv[tt], -(int)ref);
     };
     // scores -> probabilities (2^(score + shift)), shift and sum kept up
     auto softmax = [&](af16 (&sc)[NT]) {
@@ -246,8 +327,8 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
             for (int tt = 0; tt < NT; ++tt)
                 mx = fmaxf(mx, sc[tt][r]);
         mx *= unscale;
-        if (__any(mx + shift > TOP<T>)) {
-            const float to = fminf(shift, shift_of<T>(max_x32(mx)));
+        if (__any(BYTES ? mx + shift > TOP8 - top : mx + shift > TOP<F>)) {
+            const float to = fminf(shift, BYTES ? shift8_of(max_x32(mx), top) : shift_of<F>(max_x32(mx)));
             const float f = __builtin_amdgcn_exp2f(to - shift);
             shift = to;
             l *= f;
@@ -273,7 +354,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             pr[e] = sc[k >> 1][8 * (k & 1) + e];
-        split8<T>(pr, pf);
+        split8<F>(pr, pf);
     };
     // O += V^T P
     auto values = [&](const af16 (&sc)[NT], int buf, int sub) {
@@ -294,7 +375,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
                 weights(sc, x / DT, pf);
 #pragma unroll
             for (int y = NP - 1; y >= 0; --y)
-                o[x % DT] = mm32<T>(v[x % (AHEAD + 1)], pf[y], o[x % DT]);
+                o[x % DT] = mm32<F>(v[x % (AHEAD + 1)], pf[y], o[x % DT]);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
@@ -352,25 +433,62 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
     auto compute = [&](int s, int buf, uint32_t bad) {
         const int t0 = s * PT_STEP;
         const bool edge = bad != 0 || t0 + PT_STEP - 1 > tile_min;
-        const bool odd = edge ? scan(buf) : false;
+        const bool odd = !BYTES && edge ? scan(buf) : false;
         const bool active = t0 <= wave_max;            // else nothing of this step is seen by the wave
         const int see = min(pos, p.hi - 1) - t0;
+        auto hidden = [&](int sub, int tt, int r) {
+            const int blk = 2 * (NT * sub + tt) + (r >> 3);
+            return 16 * blk + (r & 7) > see - 8 * hf || (bad >> blk & 1);
+        };
 #pragma unroll
         for (int sub = 0; sub < 2 / NT; ++sub) {
             af16 sc[NT];
             if (active) {
                 scores(buf, sub, sc);
+                float dv[NT];
+                if constexpr (BYTES)
+#pragma unroll
+                    for (int tt = 0; tt < NT; ++tt) {
+                        const int at = scale_at(NT * sub + tt);
+                        dv[tt] = s_scale[buf][1][at];
+                        times_lanes([&](int r) { return Ref<af16>{sc[tt], r}; }, s_scale[buf][0][at]);
+                    }
                 // value r of tile tt is position t0 + 32 (NT sub + tt) + 16 (r / 8) + 8 hf + r % 8
                 if (edge)
 #pragma unroll
                     for (int tt = 0; tt < NT; ++tt)
 #pragma unroll
                         for (int r = 0; r < 16; ++r) {
-                            const int blk = 2 * (NT * sub + tt) + (r >> 3);
-                            if (16 * blk + (r & 7) > see - 8 * hf || (bad >> blk & 1))
+                            if (hidden(sub, tt, r))
                                 sc[tt][r] = -INFINITY;
                         }
+                if constexpr (BYTES) {
+                    float seen = dv[0], most;
+                    if (edge) {
+                        seen = 0.f;
+#pragma unroll
+                        for (int tt = 0; tt < NT; ++tt)
+                            each_lane([&](int r, float d) { seen = hidden(sub, tt, r) ? seen : fmaxf(seen, d); }, dv[tt]);
+                        seen = max_x32(seen);
+                        most = max_x16(max_of_16(exponent_above(seen)));
+                    } else {
+                        if constexpr (NT == 2)
+                            seen = fmaxf(seen, dv[NT - 1]);
+                        seen = max_x32(max_of_16(seen));
+                        most = exponent_above(seen);
+                    }
+                    follow(dv, seen, most);
+                }
                 softmax(sc);
+                if constexpr (BYTES)
+#pragma unroll
+                    for (int tt = 0; tt < NT; ++tt) {
+                        times_lanes([&](int r) { return Ref<af16>{sc[tt], r}; }, dv[tt]);
+                        if (edge)                         // a NaN scale that this row does not see
+#pragma unroll
+                            for (int r = 0; r < 16; ++r)
+                                sc[tt][r] = hidden(sub, tt, r) ? 0.f : sc[tt][r];
+                    }
             }
             if (odd) {
                 if (active)
@@ -384,7 +502,29 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
         }
     };
 
-    if (s1 > s0) {
+    if (BYTES && s1 > s0) {
+        Codes x;
+        load8(s0, ids_of(s0), x);
+        int ids = ids_of(s0 + 1);
+        uint32_t seen_bad = 0;
+        stage8(s0, 0, x);
+        for (int s = s0; s < s1; ++s) {
+            const int buf = (s - s0) & 1;
+            const uint32_t bad = x.bad;
+            seen_bad |= bad;
+            // step s is staged; after the barrier everyone's part is, and everyone is done with step s - 1
+            __syncthreads();
+            if (s + 1 < s1) {
+                load8(s + 1, ids, x);
+                ids = ids_of(s + 2);
+            }
+            compute(s, buf, bad);
+            if (s + 1 < s1)
+                stage8(s + 1, buf ^ 1, x);
+        }
+        if (seen_bad && tid == 0)
+            atomicOr(c.err, 1u);
+    } else if (s1 > s0) {
         uint32_t bad_next = issue(s0, 0, ids_of(s0)), seen_bad = 0;
         int ids = ids_of(s0 + 1);
         for (int s = s0; s < s1; ++s) {
@@ -407,6 +547,14 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
 
     // O^T: lane's row, channels 32 d + 8 (r / 4) + 4 hf + r % 4
     l = sum_x32(l);
+    if constexpr (BYTES) {                             // parts are means
+        const float inv = inverse_sum(l);
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                o[d][r] = ldexpf(o[d][r] * inv, (int)ref);
+    }
     if (!FEW && w.n_chunk > 1) {
         float *part = a.part + (int64_t)(w.slot0 + w.chunk) * prompt_part_floats(D);
         float *row = part + (32 * wave + col) * D + 4 * hf;
@@ -447,6 +595,15 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
             m = fmaxf(m, mk);
         }
         l = 0.f;
+        float inv = 1.f;
+        if constexpr (BYTES) {
+            for (int k = 0; k < w.n_chunk; ++k) {
+                float mk, lk;
+                get2(part, k * stride + ml, mk, lk);
+                l += lk * join_weight(mk, m);
+            }
+            inv = inverse_sum(l);
+        }
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -456,14 +613,15 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
         for (int k = 0; k < w.n_chunk; ++k) {
             float mk, lk;
             get2(part, k * stride + ml, mk, lk);
-            const float f = join_weight(mk, m);
+            const float f = BYTES ? lk * join_weight(mk, m) * inv : join_weight(mk, m);
             af4 x[DT][4];
 #pragma unroll
             for (int d = 0; d < DT; ++d)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
                     x[d][r] = get4(part, k * stride + row + 32 * d + 8 * r);
-            l += lk * f;
+            if constexpr (!BYTES)
+                l += lk * f;
 #pragma unroll
             for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -472,7 +630,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
         }
     }
     if (live) {
-        const float inv = inverse_sum(l);
+        const float inv = BYTES ? 1.f : inverse_sum(l);
         float *row = a.o + ((int64_t)(p.row0 + tok) * a.nq + head) * D + 4 * hf;
 #pragma unroll
         for (int d = 0; d < DT; ++d)
@@ -486,6 +644,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
 // Rows of a split tile from its partial results.  A workgroup takes four rows of a tile and KV head at a
 // time; a thread four channels of a row and every `parts`-th split, in order, then the parts are added
 // in order.
+template <bool MEANS>
 __global__ __launch_bounds__(256) void k_attn_prompt_join(AttnArgs a)
 {
     __shared__ __attribute__((aligned(16))) af4 s_sum[256];
@@ -504,30 +663,55 @@ __global__ __launch_bounds__(256) void k_attn_prompt_join(AttnArgs a)
         const float *ml = part + PT_ROWS * D + 2 * (r0 + row);
         float m = -INFINITY, l = 0.f;
         af4 sum = {0.f, 0.f, 0.f, 0.f};
-        for (int kb = k0; k0 < parts && kb < splits; kb += 8 * parts) {
-            af4 v[8];
-            float2 w[8];
+        if constexpr (MEANS) {
+            // the factors of all parts first, then each mean by its own: threads of a row add them alike
+            for (int k = 0; k < splits; ++k)
+                m = fmaxf(m, ml[k * stride]);
+            for (int k = 0; k < splits; ++k)
+                l += ml[k * stride + 1] * join_weight(ml[k * stride], m);
+            const float inv = inverse_sum(l);
+            for (int kb = k0; k0 < parts && kb < splits; kb += 8 * parts) {
+                af4 v[8];
+                float2 w[8];
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {                      // all loads in flight at once
-                const int64_t at = min(kb + x * parts, splits - 1) * stride;
-                w[x] = *reinterpret_cast<const float2 *>(ml + at);
-                v[x] = *reinterpret_cast<const af4 *>(from + at);
-            }
-            float mb = m;
-#pragma unroll
-            for (int x = 0; x < 8; ++x)
-                mb = fmaxf(mb, w[x].x);
-            const float f0 = join_weight(m, mb);
-            sum *= f0;
-            l *= f0;
-            m = mb;
-#pragma unroll
-            for (int x = 0; x < 8; ++x)
-                if (kb + x * parts < splits) {
-                    const float f = join_weight(w[x].x, m);
-                    sum += v[x] * f;
-                    l += w[x].y * f;
+                for (int x = 0; x < 8; ++x) {
+                    const int64_t at = min(kb + x * parts, splits - 1) * stride;
+                    w[x] = *reinterpret_cast<const float2 *>(ml + at);
+                    v[x] = *reinterpret_cast<const af4 *>(from + at);
                 }
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                    if (kb + x * parts < splits)
+                        sum += v[x] * (w[x].y * join_weight(w[x].x, m) * inv);
+            }
+            l = 1.f / parts;                           // the parts' sums are added as they are
+            m = 0.f;
+        } else {
+            for (int kb = k0; k0 < parts && kb < splits; kb += 8 * parts) {
+                af4 v[8];
+                float2 w[8];
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {                      // all loads in flight at once
+                    const int64_t at = min(kb + x * parts, splits - 1) * stride;
+                    w[x] = *reinterpret_cast<const float2 *>(ml + at);
+                    v[x] = *reinterpret_cast<const af4 *>(from + at);
+                }
+                float mb = m;
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                    mb = fmaxf(mb, w[x].x);
+                const float f0 = join_weight(m, mb);
+                sum *= f0;
+                l *= f0;
+                m = mb;
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                    if (kb + x * parts < splits) {
+                        const float f = join_weight(w[x].x, m);
+                        sum += v[x] * f;
+                        l += w[x].y * f;
+                    }
+            }
         }
         if (parts > 1) {
             s_sum[tid] = sum;
@@ -596,15 +780,19 @@ bool prompt_in_16s(int64_t n_rows, int n_seq, int nq, int nkv, int hd, int64_t p
 int launch_attn_prompt(int kv_type, const AttnArgs &a, void *stream)
 {
     const int64_t table = (int64_t)a.c.max_pages << a.c.ps_log2;
+    const bool bytes = kv_bytes(kv_type);
     if (prompt_in_16s(a.c.n_rows, a.c.n_seq, a.nq, a.c.nkv, a.c.hd, table))
-        return launch_attn_rows(kv_type, a, stream);
+        return bytes ? launch_attn8_rows(kv_type, a, stream) : launch_attn_rows(kv_type, a, stream);
     hipStream_t s = static_cast<hipStream_t>(stream);
     const PromptPlan p = plan_prompt(a.c.n_rows, a.c.n_seq, a.c.nkv, a.group, a.c.hd, table);
     const bool few = p.slots && !p.second;
     void (*k)(AttnArgs, int) = nullptr;
-#define QG_PROMPT_D(DD)                                                                                  \
-    k = kv_type == KV_F16 ? few ? k_attn_prompt<KV_F16, DD, true> : k_attn_prompt<KV_F16, DD, false>     \
-                          : few ? k_attn_prompt<KV_BF16, DD, true> : k_attn_prompt<KV_BF16, DD, false>
+#define QG_PROMPT_T(T, DD) few ? k_attn_prompt<T, DD, true> : k_attn_prompt<T, DD, false>
+#define QG_PROMPT_D(DD)                                \
+    k = kv_type == KV_F16  ? QG_PROMPT_T(KV_F16, DD)   \
+        : kv_type == KV_BF16 ? QG_PROMPT_T(KV_BF16, DD) \
+        : kv_type == KV_I8   ? QG_PROMPT_T(KV_I8, DD)  \
+                             : QG_PROMPT_T(KV_F8, DD)
     switch (a.c.hd) {
     case 64: QG_PROMPT_D(64); break;
     case 96: QG_PROMPT_D(96); break;
@@ -613,6 +801,7 @@ int launch_attn_prompt(int kv_type, const AttnArgs &a, void *stream)
     default: QG_PROMPT_D(256); break;
     }
 #undef QG_PROMPT_D
+#undef QG_PROMPT_T
     hipLaunchKernelGGL(k, dim3((unsigned)p.grid), dim3(256), 0, s, a, p.slots);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !p.second)
@@ -621,7 +810,7 @@ int launch_attn_prompt(int kv_type, const AttnArgs &a, void *stream)
     // behind 4000 positions: 56.3 us, with 2048 61.4; 8192 that find nothing to join cost 1 us more)
     const int64_t share = 4096 / p.pairs;
     const unsigned y = (unsigned)(share > PT_ROWS / 4 ? PT_ROWS / 4 : share > 8 ? share : 8);
-    hipLaunchKernelGGL(k_attn_prompt_join, dim3((unsigned)p.pairs, y), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(bytes ? k_attn_prompt_join<true> : k_attn_prompt_join<false>, dim3((unsigned)p.pairs, y), dim3(256), 0, s, a);
     return (int)hipGetLastError();
 }
 
