@@ -35,13 +35,24 @@ static constexpr int64_t WS_COUNT = 256, WS_PART = WS_COUNT + ATTN_MAX_SLOTS * 4
 // qgemv_attn_prompt's part of it begins with its pair count and its split tiles (32 bytes each).
 static constexpr int64_t WS_SPLITS = 256 + PROMPT_SPLITS * 32;
 
-static int64_t ws_bytes_of(int op, int n_seq, int nq, int nkv, int hd)
+// Partial results of a split.
+static int64_t part_bytes(int op, int nq, int nkv, int hd)
 {
     const int group = nq / nkv;
     if (op == QG_OP_ATTN)
-        return WS_PART + (attn_slots(hd) * attn_part_floats(group < 16 ? group : 16, hd) * 4 + 255) / 256 * 256;
-    if (op == QG_OP_ATTN_PROMPT)
-        return WS_PART + WS_SPLITS + (int64_t)prompt_slots(hd) * 128 * (hd + 2) * 4;   // 128 columns a tile
+        return (attn_slots(hd) * attn_part_floats(group < 16 ? group : 16, hd) * 4 + 255) / 256 * 256;
+    return WS_SPLITS + (int64_t)prompt_slots(hd) * 128 * (hd + 2) * 4;         // 128 columns a tile
+}
+
+// qgemv_attn_shared: an exponent and a sum of each row and head before them.
+static int64_t stats_bytes(int n_seq, int nq) { return ((int64_t)n_seq * nq * 8 + 255) / 256 * 256; }
+
+static int64_t ws_bytes_of(int op, int n_seq, int nq, int nkv, int hd)
+{
+    if (op == QG_OP_ATTN || op == QG_OP_ATTN_PROMPT)
+        return WS_PART + part_bytes(op, nq, nkv, hd);
+    if (op == QG_OP_ATTN_SHARED)
+        return WS_PART + stats_bytes(n_seq, nq) + part_bytes(QG_OP_ATTN_PROMPT, nq, nkv, hd);
     return WS_PART;
 }
 
@@ -178,9 +189,12 @@ static int run_attn(int op, int kv_type, const void *k_pages, const void *v_page
     a.c.err = static_cast<unsigned int *>(ws);
     a.count = reinterpret_cast<unsigned int *>(static_cast<uint8_t *>(ws) + WS_COUNT);
     uint8_t *part = static_cast<uint8_t *>(ws) + WS_PART;
+    a.stats = reinterpret_cast<float *>(part);
+    if (shared)
+        part += stats_bytes(n_seq, nq);
     a.pairs = reinterpret_cast<int *>(part);
     a.splits = reinterpret_cast<PromptSplit *>(part + 256);
-    a.part = reinterpret_cast<float *>(prompt ? part + WS_SPLITS : part);
+    a.part = reinterpret_cast<float *>(prompt || shared ? part + WS_SPLITS : part);
     a.q = q;
     a.q_stride = q_stride;
     a.o = o;
@@ -190,12 +204,11 @@ static int run_attn(int op, int kv_type, const void *k_pages, const void *v_page
     a.group_start = groups.start;
     a.shared_len = groups.shared;
     a.n_group = groups.n;
-    if (op == QG_OP_ATTN && kv_bytes(kv_type))
-        return launch_status(launch_attn8(kv_type, a, stream));
-    if (shared)
-        return launch_status(launch_attn_any(kv_type, a, stream));
-    return launch_status(prompt ? launch_attn_prompt(kv_type, a, stream)
-                                : launch_attn(kv_type, a, stream));
+    const bool bytes = kv_bytes(kv_type);
+    return launch_status(shared   ? launch_attn_shared(kv_type, a, stream)
+                         : prompt ? launch_attn_prompt(kv_type, a, stream)
+                         : bytes  ? launch_attn8(kv_type, a, stream)
+                                  : launch_attn(kv_type, a, stream));
 }
 
 extern "C" {

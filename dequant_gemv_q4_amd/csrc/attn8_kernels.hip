@@ -20,9 +20,10 @@ constexpr int JOIN8_RADIX = 8;
 template <bool SIDE> using Attn8PlanOf = PlanOf<16, 8, 1, 2, 16, JOIN8_RADIX, false, SIDE>;
 typedef Attn8PlanOf<false> Attn8Cols;
 
-template <int T, int D, bool ROWS, bool SIDE>
+template <int T, int D, int FORM, bool SIDE>
 __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn8(AttnArgs a)
 {
+    constexpr bool ROWS = FORM == MANY || FORM == PREFIX;
     constexpr int KB = D / 32, DT = D / 16, NP = 2, KP = D / 64, REST = D % 64 / 32;
     __shared__ __attribute__((aligned(16))) float s_o[4][16][D];
     __shared__ float s_m[4][16], s_l[4][16];
@@ -41,24 +42,30 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn8(AttnArgs a)
         if (id - r + run <= (int)gridDim.x)
             id += r % 8 * a.side + r / 8 - r;
     }
-    if (!attn_plan<Attn8PlanOf<SIDE>, ROWS>(c, a.group, attn_slots(D), id, p,
-                                            reinterpret_cast<AttnSeq *>(&s_o[0][0][0])))
+    if (!attn_plan<Attn8PlanOf<SIDE>, FORM>(a, attn_slots(D), id, p, reinterpret_cast<AttnSeq *>(&s_o[0][0][0])))
         return;
-    const int b = p.b, chunk = p.chunk, n_chunk = p.n_chunk, len = p.len;
+    // (PREFIX: a group's first sequence, whose pages are read)
+    const int b = FORM == PREFIX ? p.row0 : p.b, chunk = p.chunk, n_chunk = p.n_chunk;
+    // SUFFIX: shared positions are in the pages of another; the plan's positions begin at base
+    const int shared = FORM == SUFFIX ? shared_of(a, b) : 0, base = FORM == SUFFIX ? suffix_base(shared) : 0;
+    const int len = FORM == SUFFIX && p.len > 0 ? base + p.len : p.len;
     const int tiles = (p.rows * a.group + 15) / 16, hkv = p.pair / tiles, rho0 = p.pair % tiles * 16;
     const int cols = min(16, p.rows * a.group - rho0);
     auto head_of = [&](int col) { return hkv * a.group + (ROWS ? (rho0 + col) % a.group : rho0 + col); };
     auto row_of = [&](int col) { return p.row0 + (ROWS ? (rho0 + col) / a.group : 0); };
 
     // this chunk's 64-position steps, dealt to the waves in turn
-    const int units = Attn8Cols::units(len);
+    const int units = Attn8Cols::units(p.len);
     const int per = units / n_chunk, more = units % n_chunk;
     const int unit0 = chunk * per + min(chunk, more);
-    const int t_begin = unit0 << Attn8Cols::UNIT_LOG2;
-    const int t_end = min(len, (unit0 + per + (chunk < more ? 1 : 0)) << Attn8Cols::UNIT_LOG2);
+    const int t_begin = base + (unit0 << Attn8Cols::UNIT_LOG2);
+    const int t_end = min(len, base + ((unit0 + per + (chunk < more ? 1 : 0)) << Attn8Cols::UNIT_LOG2));
     // positions this lane's column sees, [0, see), and those that all columns see
     int see = t_end, see_all = t_end;
-    if constexpr (ROWS) {
+    if constexpr (FORM == PREFIX) {
+        see = min(t_end, prefix_seen(a, row_of(min(i, cols - 1)), p.row0, len));
+        see_all = -(int)max_of_16(-(float)see);
+    } else if constexpr (FORM == MANY) {
         const int pos0 = max(c.kv_len[b], -(1 << 30)) - p.rows;
         see = min(t_end, pos0 + (rho0 + min(i, cols - 1)) / a.group + 1);
         see_all = min(t_end, pos0 + rho0 / a.group + 1);
@@ -197,7 +204,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn8(AttnArgs a)
             }
             times_lanes([&](int e) -> float & { return sc[e]; }, x.dk);
             const uint64_t any_bad = __ballot(x.bad);
-            const bool edge = any_bad != 0 || t + 64 > see_all;
+            const bool edge = any_bad != 0 || t + 64 > see_all || (FORM == SUFFIX && t < shared);
             uint32_t hide = 0;                            // of this column's 16 positions
             float dv = x.dv;
             if (edge) {
@@ -205,17 +212,24 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn8(AttnArgs a)
                     atomicOr(c.err, 1u);
                 const int n = x.bad ? 0 : see - t - 16 * g;
                 hide = n >= 16 ? 0u : n <= 0 ? 0xFFFFu : 0xFFFFu & (0xFFFFu << n);
+                const int skip = FORM == SUFFIX ? shared - t - 16 * g : 0;        // < 16
+                if (FORM == SUFFIX && skip > 0)
+                    hide |= (1u << skip) - 1u;
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
                     sc[e] = hide >> e & 1 ? -INFINITY : sc[e];
                 const int left = x.bad ? 0 : t_end - t - 16 * g;      // positions of the group that exist
-                dv = i < left ? dv : 0.f;
+                dv = i < left && (FORM != SUFFIX || i >= skip) ? dv : 0.f;
                 // what a masked position holds must not reach the product: an e4m3 may be NaN
                 if constexpr (T == KV_F8)
 #pragma unroll
                     for (int w = 0; w < 4; ++w) {
                         const int m = left - 4 * w;
-                        const uint32_t keep = m >= 4 ? ~0u : m <= 0 ? 0u : (1u << (8 * m)) - 1u;
+                        uint32_t keep = m >= 4 ? ~0u : m <= 0 ? 0u : (1u << (8 * m)) - 1u;
+                        if constexpr (FORM == SUFFIX) {
+                            const int k = skip - 4 * w;
+                            keep &= k >= 4 ? 0u : k <= 0 ? ~0u : ~0u << (8 * k);
+                        }
 #pragma unroll
                         for (int d = 0; d < DT; ++d)
                             x.v[d][w] &= keep;
@@ -319,9 +333,18 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn8(AttnArgs a)
     const uint32_t stride = (uint32_t)attn_part_floats(width, D);
     const __amdgpu_buffer_rsrc_t part = __builtin_amdgcn_make_buffer_rsrc(
         a.part + (int64_t)p.slot0 * stride, 0, n_chunk * stride * 4, 0x00020000);
-    auto store = [&](int e, af4 mean) {
+    auto store = [&](int e, af4 mean, float m, float ls) {
         const int col = e / (D / 4), d4 = e % (D / 4);
-        *reinterpret_cast<af4 *>(a.o + ((int64_t)row_of(col) * a.nq + head_of(col)) * D + 4 * d4) = mean;
+        const int64_t at = (int64_t)row_of(col) * a.nq + head_of(col);
+        af4 *out = reinterpret_cast<af4 *>(a.o + at * D + 4 * d4);
+        if constexpr (FORM == PREFIX)
+            if (d4 == 0)
+                *reinterpret_cast<float2 *>(a.stats + 2 * at) = make_float2(m, ls);
+        if (FORM == SUFFIX && shared > 0) {
+            const float2 s = *reinterpret_cast<const float2 *>(a.stats + 2 * at);
+            mean = join_means(mean, m, ls, *out, s.x, s.y);
+        }
+        *out = mean;
     };
     auto sums_at = [&](int at, int col) { return at * stride + width * D + 2 * col; };
     auto part_at = [&](int at, int e) { return at * stride + 4 * e; };
@@ -337,7 +360,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn8(AttnArgs a)
         for (int w = 0; w < 4; ++w)
             mean += *reinterpret_cast<const af4 *>(&s_o[w][col][4 * d4]) * f[w];
         if (n_chunk == 1) {
-            store(e, mean);
+            store(e, mean, j.m, j.l);
         } else {
             put4(part, part_at(chunk, e), mean);
             if (d4 == 0)
@@ -370,7 +393,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn8(AttnArgs a)
                 if (k < members)
                     mean += x[k] * f[k];
             if (last) {
-                store(e, mean);
+                store(e, mean, j.m, j.l);
             } else {
                 // the exponent and sum replace what other threads of the column may still have to read
                 put4(part, part_at(g0, e), mean);
@@ -388,14 +411,14 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn8(AttnArgs a)
     }
 }
 
-template <bool ROWS>
+template <int FORM>
 static int launch_k_attn8(int kv_type, const AttnArgs &a, int64_t pairs, void *stream)
 {
     const int slots = attn_slots(a.c.hd);
     void (*k)(AttnArgs) = nullptr;
-#define QG_ATTN8_D(DD)                                                                                     \
-    k = kv_type == KV_I8 ? a.side > 1 ? k_attn8<KV_I8, DD, ROWS, true> : k_attn8<KV_I8, DD, ROWS, false>   \
-                         : a.side > 1 ? k_attn8<KV_F8, DD, ROWS, true> : k_attn8<KV_F8, DD, ROWS, false>
+#define QG_ATTN8_T(T, DD) \
+    a.side > 1 && FORM != SUFFIX ? k_attn8<T, DD, FORM, FORM != SUFFIX> : k_attn8<T, DD, FORM, false>
+#define QG_ATTN8_D(DD) k = kv_type == KV_I8 ? QG_ATTN8_T(KV_I8, DD) : QG_ATTN8_T(KV_F8, DD)
     switch (a.c.hd) {
     case 64: QG_ATTN8_D(64); break;
     case 96: QG_ATTN8_D(96); break;
@@ -404,6 +427,7 @@ static int launch_k_attn8(int kv_type, const AttnArgs &a, int64_t pairs, void *s
     default: QG_ATTN8_D(256); break;
     }
 #undef QG_ATTN8_D
+#undef QG_ATTN8_T
     // as many pairs as slots: those that are much longer than the rest are split all the same
     const int64_t table = (int64_t)a.c.max_pages << a.c.ps_log2;
     const int64_t grid = pairs < slots ? slots : table > Attn8Cols::SOLO << Attn8Cols::UNIT_LOG2 ? pairs + slots : pairs;
@@ -411,18 +435,30 @@ static int launch_k_attn8(int kv_type, const AttnArgs &a, int64_t pairs, void *s
     return (int)hipGetLastError();
 }
 
-int launch_attn8(int kv_type, const AttnArgs &a, void *stream)
+template <int FORM>
+static int launch_one8(int kv_type, const AttnArgs &a, void *stream)
 {
     AttnArgs b = a;
     b.side = (a.group + 15) / 16;
-    return launch_k_attn8<false>(kv_type, b, (int64_t)a.c.n_seq * a.c.nkv * b.side, stream);
+    return launch_k_attn8<FORM>(kv_type, b, (int64_t)a.c.n_seq * a.c.nkv * b.side, stream);
 }
-
-int launch_attn8_rows(int kv_type, const AttnArgs &a, void *stream)
+template <int FORM>
+static int launch_many8(int kv_type, const AttnArgs &a, void *stream)
 {
     AttnArgs b = a;
     b.side = (int)((a.c.n_rows * a.group + 16 * a.c.n_seq - 1) / (16 * a.c.n_seq));   // on average
-    return launch_k_attn8<true>(kv_type, b, a.c.nkv * (a.c.n_rows * a.group / 16 + a.c.n_seq), stream);
+    return launch_k_attn8<FORM>(kv_type, b, a.c.nkv * (a.c.n_rows * a.group / 16 + a.c.n_seq), stream);
+}
+
+int launch_attn8(int kv_type, const AttnArgs &a, void *stream) { return launch_one8<ONE>(kv_type, a, stream); }
+int launch_attn8_rows(int kv_type, const AttnArgs &a, void *stream) { return launch_many8<MANY>(kv_type, a, stream); }
+int launch_attn8_prefix(int kv_type, const AttnArgs &a, void *stream)
+{
+    return launch_many8<PREFIX>(kv_type, a, stream);
+}
+int launch_attn8_suffix(int kv_type, const AttnArgs &a, void *stream)
+{
+    return launch_one8<SUFFIX>(kv_type, a, stream);
 }
 
 }  // namespace qg

@@ -89,19 +89,6 @@ __device__ __forceinline__ void each_lane(X &&x, float v)
     each_lane(x, v, std::make_integer_sequence<int, 16>());
 }
 
-// The largest of a row of 16 lanes, in all of them; NaN is passed over.
-__device__ __forceinline__ float max_of_16(float v)
-{
-    auto turn = [](float x, auto ctrl) {
-        return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x),
-                                                                     decltype(ctrl)::value, 0xF, 0xF, true));
-    };
-    v = fmaxf(v, turn(v, std::integral_constant<int, 0x121>()));      // row_ror 1, 2, 4, 8
-    v = fmaxf(v, turn(v, std::integral_constant<int, 0x122>()));
-    v = fmaxf(v, turn(v, std::integral_constant<int, 0x124>()));
-    return fmaxf(v, turn(v, std::integral_constant<int, 0x128>()));
-}
-
 // The exponent e of the least power of two above v (0: very low).
 __device__ __forceinline__ float exponent_above(float v)
 {

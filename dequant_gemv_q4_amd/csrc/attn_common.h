@@ -3,6 +3,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "attn_internal.h"
 
 namespace qg {
@@ -123,6 +125,19 @@ __device__ __forceinline__ float sum_x16(float v)
     return __builtin_bit_cast(float, s0) + __builtin_bit_cast(float, s1);
 }
 
+// The largest of a row of 16 lanes, in all of them; NaN is passed over.
+__device__ __forceinline__ float max_of_16(float v)
+{
+    auto turn = [](float x, auto ctrl) {
+        return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x),
+                                                                     decltype(ctrl)::value, 0xF, 0xF, true));
+    };
+    v = fmaxf(v, turn(v, std::integral_constant<int, 0x121>()));      // row_ror 1, 2, 4, 8
+    v = fmaxf(v, turn(v, std::integral_constant<int, 0x122>()));
+    v = fmaxf(v, turn(v, std::integral_constant<int, 0x124>()));
+    return fmaxf(v, turn(v, std::integral_constant<int, 0x128>()));
+}
+
 // Power of two that brings a query row's largest |value| to [2^13, 2^14): both f16 pieces of every
 // value then keep their bits (the second one down to 2^-38 of the row's largest).  bf16 has the
 // range of f32 and is not scaled.  A row of zeros, infinities or NaN keeps the factor 1.
@@ -182,6 +197,14 @@ __device__ __forceinline__ float join_weight(float part_m, float largest_m)
 }
 // 1 / sum, or 0 for a row that sees nothing.
 __device__ __forceinline__ float inverse_sum(float l) { return l == 0.f ? 0.f : 1.0f / l; }
+
+// The mean of two parts' means (exponents m, sums l).
+__device__ __forceinline__ af4 join_means(af4 x, float mx, float lx, af4 y, float my, float ly)
+{
+    const float m = fmaxf(mx, my), fx = lx * join_weight(mx, m), fy = ly * join_weight(my, m);
+    const float inv = inverse_sum(fx + fy);
+    return x * (fx * inv) + y * (fy * inv);
+}
 
 // Partial results that pass between workgroups of one launch, which may run on different XCDs: every
 // access carries the agent-scope bit (sc1), so that it neither stays in nor is answered by the L2 of one
@@ -269,13 +292,53 @@ struct AttnSeq {
     int n, pairs, row0, rows;
 };
 
-// Positions of sequence b that have a place in its table.
-__device__ __forceinline__ int seq_len(const KvArgs &c, int b)
+// Of n positions those that have a place in a table.
+__device__ __forceinline__ int placed(const KvArgs &c, int n)
 {
-    const int n = c.kv_len[b], cap = c.max_pages << c.ps_log2;          // cap <= 2^24
+    const int cap = c.max_pages << c.ps_log2;                           // cap <= 2^24
     if (n > cap)
         atomicOr(c.err, 1u);
     return n < 0 ? 0 : n < cap ? n : cap;
+}
+// Positions of sequence b that have a place in its table.
+__device__ __forceinline__ int seq_len(const KvArgs &c, int b) { return placed(c, c.kv_len[b]); }
+
+// What a workgroup of the attention kernels attends to: one new row of each sequence (ONE), several (MANY),
+// or for sequences that begin alike the shared positions for all rows of a group (PREFIX: the plan's
+// sequences are the groups, with q_start their first sequences) and those behind them (SUFFIX).
+enum AttnForm { ONE, MANY, PREFIX, SUFFIX };
+
+// Shared positions of sequence b: none outside the groups.
+__device__ __forceinline__ int shared_of(const AttnArgs &a, int b)
+{
+    if (b < a.group_start[0] || b >= a.group_start[a.n_group])
+        return 0;
+    const int n = a.shared_len[b], cap = a.c.max_pages << a.c.ps_log2;
+    return n < 0 ? 0 : n < cap ? n : cap;
+}
+// SUFFIX: the plan counts from the last multiple of 16 in the shared positions.
+__device__ __forceinline__ int suffix_base(int shared) { return shared & ~15; }
+
+// Positions that the plan counts of its sequence b, whose rows begin with row0.
+template <int FORM>
+__device__ __forceinline__ int plan_len(const AttnArgs &a, int b, int row0, int rows)
+{
+    if constexpr (FORM == PREFIX) {
+        return rows > 0 ? placed(a.c, a.shared_len[row0]) : 0;
+    } else if constexpr (FORM == SUFFIX) {
+        const int n = seq_len(a.c, b), s = shared_of(a, b);
+        return n > s ? n - suffix_base(s) : 0;
+    } else {
+        return seq_len(a.c, b);
+    }
+}
+// PREFIX: of the shared positions `len` of the group's first sequence, those that a row sees.
+__device__ __forceinline__ int prefix_seen(const AttnArgs &a, int row, int first, int len)
+{
+    const int n = a.shared_len[row];
+    if (n > a.shared_len[first])
+        atomicOr(a.c.err, 1u);
+    return max(min(min(n, a.c.kv_len[row]), len), 0);
 }
 
 // First new row of sequence i, cut to the rows there are.
@@ -578,23 +641,25 @@ __device__ __forceinline__ bool attn_plan_of(const KvArgs &c, int n_seq, int gro
 
 // Workgroup id -> its place in the plan; false if the plan has fewer workgroups.  All threads of the
 // workgroup call it; every wave finds the same.  Up to 64 sequences are held a lane each, more in LDS
-// scratch (QG_ATTN_MAX_SEQ entries, free again afterwards).  ROWS: sequence b has the rows between its
-// q_start and the next; else one row, row b.  slots 0: nothing is split.  INDEX: all pairs
+// scratch (QG_ATTN_MAX_SEQ entries, free again afterwards).  Sequence b has the rows between its
+// q_start and the next (MANY, PREFIX); else one row, row b.  slots 0: nothing is split.  INDEX: all pairs
 // or only the longest are split, as `all` says.
-template <class P, bool ROWS>
-__device__ __forceinline__ bool attn_plan(const KvArgs &c, int group, int slots, int id, AttnPlan &p,
-                                          AttnSeq *scratch, bool all = true)
+template <class P, int FORM>
+__device__ __forceinline__ bool attn_plan(const AttnArgs &a, int slots, int id, AttnPlan &p, AttnSeq *scratch,
+                                          bool all = true)
 {
-    const int lane = threadIdx.x & 63;
+    constexpr bool ROWS = FORM == MANY || FORM == PREFIX;
+    const KvArgs &c = a.c;
+    const int lane = threadIdx.x & 63, group = a.group;
     auto load = [&](int b) {
         AttnSeq s = {0, 0, b, 0};
         if (b < c.n_seq) {
-            s.n = seq_len(c, b);
             s.rows = 1;
             if constexpr (ROWS) {
                 s.row0 = row_start(c, b);
                 s.rows = max(row_start(c, b + 1) - s.row0, 0);
             }
+            s.n = plan_len<FORM>(a, b, s.row0, s.rows);
             s.pairs = c.nkv * (int)(((int64_t)s.rows * group + P::COLS - 1) / P::COLS);
         }
         return s;

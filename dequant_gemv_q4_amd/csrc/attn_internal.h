@@ -77,6 +77,7 @@ struct AttnArgs {
     const int32_t *group_start; // groups of sequences that begin alike [n_group + 1], or NULL
     const int32_t *shared_len;  // [n_seq]
     int n_group;
+    float *stats;               // workspace: exponent and sum of each row and head over the shared positions
     unsigned int *count;        // workspace: arrival counters of a split, one per slot, 0 between calls
     int nq, group;              // query heads; query heads per KV head
     int side;                   // set by the launcher: tiles that read the same positions
@@ -107,7 +108,13 @@ int launch_kv_append(int kv_type, const AppendArgs &a, void *stream);
 int launch_qkv_append(int kv_type, bool turn, const QkvArgs &a, void *stream);
 int launch_attn8(int kv_type, const AttnArgs &a, void *stream);
 int launch_attn8_rows(int kv_type, const AttnArgs &a, void *stream);    // few rows per sequence
-int launch_attn_any(int kv_type, const AttnArgs &a, void *stream);
+// Of qgemv_attn_shared: the shared positions of all groups (means to o, exponents and sums to stats), by
+// 16-column or 128-column tiles; then what is behind them, joined with that.
+int launch_attn_prefix(int kv_type, const AttnArgs &a, void *stream);
+int launch_attn8_prefix(int kv_type, const AttnArgs &a, void *stream);
+int launch_attn_suffix(int kv_type, const AttnArgs &a, void *stream);
+int launch_attn8_suffix(int kv_type, const AttnArgs &a, void *stream);
+int launch_attn_shared(int kv_type, const AttnArgs &a, void *stream);
 int launch_attn(int kv_type, const AttnArgs &a, void *stream);
 int launch_attn_rows(int kv_type, const AttnArgs &a, void *stream);     // few rows per sequence
 int launch_attn_prompt(int kv_type, const AttnArgs &a, void *stream);

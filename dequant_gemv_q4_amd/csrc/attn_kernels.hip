@@ -115,9 +115,10 @@ typedef AttnPlanOf<false> AttnCols;
 // (workgroups eight apart), so that one of them finds the other's in the L2: 64 sequences of 7500 positions,
 // 40 / 2 heads of 128: 140.9 us tile by tile, 107 to 111; of 64 75.0 and 58; sixteen of 8 rows x 4000, 24 / 2:
 // 53.3 and 47.6.  (In the code of the others it costs 0.15 of 7 us.)
-template <int T, int D, bool ROWS, bool SIDE>
+template <int T, int D, int FORM, bool SIDE>
 __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn(AttnArgs a)
 {
+    constexpr bool ROWS = FORM == MANY || FORM == PREFIX;
     constexpr int KB = D / 32, DT = D / 16, NP = PIECES<T>;
     __shared__ __attribute__((aligned(16))) float s_o[4][16][D];
     __shared__ float s_m[4][16], s_l[4][16], s_mo[16], s_lo[16];
@@ -136,10 +137,13 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn(AttnArgs a)
         if (id - r + run <= (int)gridDim.x)
             id += r % 8 * a.side + r / 8 - r;
     }
-    if (!attn_plan<AttnPlanOf<SIDE>, ROWS>(c, a.group, attn_slots(D), id, p,
-                                   reinterpret_cast<AttnSeq *>(&s_o[0][0][0])))
+    if (!attn_plan<AttnPlanOf<SIDE>, FORM>(a, attn_slots(D), id, p, reinterpret_cast<AttnSeq *>(&s_o[0][0][0])))
         return;
-    const int b = p.b, chunk = p.chunk, n_chunk = p.n_chunk, len = p.len;
+    // (PREFIX: a group's first sequence, whose pages are read)
+    const int b = FORM == PREFIX ? p.row0 : p.b, chunk = p.chunk, n_chunk = p.n_chunk;
+    // SUFFIX: shared positions are in the pages of another; the plan's positions begin at base
+    const int shared = FORM == SUFFIX ? shared_of(a, b) : 0, base = FORM == SUFFIX ? suffix_base(shared) : 0;
+    const int len = FORM == SUFFIX && p.len > 0 ? base + p.len : p.len;
     const int tiles = (p.rows * a.group + 15) / 16, hkv = p.pair / tiles, rho0 = p.pair % tiles * 16;
     const int cols = min(16, p.rows * a.group - rho0);
     // offset of column col in o, and of its row and head in q
@@ -147,15 +151,18 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn(AttnArgs a)
     auto row_of = [&](int col) { return p.row0 + (ROWS ? (rho0 + col) / a.group : 0); };
 
     // this chunk's 32-position steps, dealt to the waves in turn
-    const int units = AttnCols::units(len);
+    const int units = AttnCols::units(p.len);
     const int per = units / n_chunk, more = units % n_chunk;
     const int unit0 = chunk * per + min(chunk, more);
-    const int t_begin = unit0 << AttnCols::UNIT_LOG2;
-    const int t_end = min(len, (unit0 + per + (chunk < more ? 1 : 0)) << AttnCols::UNIT_LOG2);
+    const int t_begin = base + (unit0 << AttnCols::UNIT_LOG2);
+    const int t_end = min(len, base + ((unit0 + per + (chunk < more ? 1 : 0)) << AttnCols::UNIT_LOG2));
     // positions this lane's column sees, [0, see), and those that all columns see (columns without a
     // row see what the last one does and are not stored)
     int see = t_end, see_all = t_end;
-    if constexpr (ROWS) {
+    if constexpr (FORM == PREFIX) {
+        see = min(t_end, prefix_seen(a, row_of(min(i, cols - 1)), p.row0, len));
+        see_all = -(int)max_of_16(-(float)see);
+    } else if constexpr (FORM == MANY) {
         const int pos0 = max(c.kv_len[b], -(1 << 30)) - p.rows;
         see = min(t_end, pos0 + (rho0 + min(i, cols - 1)) / a.group + 1);
         see_all = min(t_end, pos0 + rho0 / a.group + 1);
@@ -271,17 +278,20 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn(AttnArgs a)
             const uint64_t any_bad = __ballot(x.bad);
             bool odd = false;
             uint16_t *sv = reinterpret_cast<uint16_t *>(&s_o[wave][0][0]);      // [D][32]
-            if (any_bad != 0 || t + 32 > see_all) {
+            if (any_bad != 0 || t + 32 > see_all || (FORM == SUFFIX && t < shared)) {
                 if (any_bad && lane == 0)
                     atomicOr(c.err, 1u);
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    sc[e] = x.bad || t + 8 * g + e >= see ? -INFINITY : sc[e];
+                    sc[e] = x.bad || t + 8 * g + e >= see || (FORM == SUFFIX && t + 8 * g + e < shared) ? -INFINITY
+                                                                                               : sc[e];
                 // what a masked position holds must not reach the product: 0 x NaN is NaN
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
                     const int tw = t + 8 * g + 2 * w;
-                    const uint32_t keep = x.bad || tw >= t_end ? 0u : tw + 1 >= t_end ? 0xFFFFu : ~0u;
+                    uint32_t keep = x.bad || tw >= t_end ? 0u : tw + 1 >= t_end ? 0xFFFFu : ~0u;
+                    if constexpr (FORM == SUFFIX)
+                        keep &= tw + 1 < shared ? 0u : tw < shared ? 0xFFFF0000u : ~0u;
 #pragma unroll
                     for (int d = 0; d < DT; ++d)
                         x.v[d][w] &= keep;
@@ -380,10 +390,19 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn(AttnArgs a)
     const __amdgpu_buffer_rsrc_t part = __builtin_amdgcn_make_buffer_rsrc(
         a.part + (int64_t)p.slot0 * stride, 0, n_chunk * stride * 4, 0x00020000);
     // four channels of a column to o
-    auto store = [&](int e, af4 sum, float ls) {
+    auto store = [&](int e, af4 sum, float m, float ls) {
         const int col = e / (D / 4), d4 = e % (D / 4);
-        *reinterpret_cast<af4 *>(a.o + ((int64_t)row_of(col) * a.nq + head_of(col)) * D + 4 * d4) =
-            sum * inverse_sum(ls);
+        const int64_t at = (int64_t)row_of(col) * a.nq + head_of(col);
+        af4 *out = reinterpret_cast<af4 *>(a.o + at * D + 4 * d4);
+        af4 mean = sum * inverse_sum(ls);
+        if constexpr (FORM == PREFIX)
+            if (d4 == 0)
+                *reinterpret_cast<float2 *>(a.stats + 2 * at) = make_float2(m, ls);
+        if (FORM == SUFFIX && shared > 0) {
+            const float2 s = *reinterpret_cast<const float2 *>(a.stats + 2 * at);
+            mean = join_means(mean, m, ls, *out, s.x, s.y);
+        }
+        *out = mean;
     };
     auto sums_at = [&](int at, int col) { return at * stride + width * D + 2 * col; };
     auto part_at = [&](int at, int e) { return at * stride + 4 * e; };
@@ -400,7 +419,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn(AttnArgs a)
             ls += s_l[w][col] * f;
         }
         if (n_chunk == 1) {
-            store(e, sum, ls);
+            store(e, sum, mm, ls);
         } else {
             put4(part, part_at(chunk, e), sum);
             if (d4 == 0)
@@ -443,7 +462,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn(AttnArgs a)
                     ls += lk[k] * f;
                 }
             if (top) {
-                store(e, sum, ls);
+                store(e, sum, mm, ls);
             } else {
                 // the exponent and sum replace what other threads of the column may still have to read
                 put4(part, part_at(g0, e), sum);
@@ -472,14 +491,14 @@ int launch_kv_append(int kv_type, const AppendArgs &a, void *stream)
     return (int)hipGetLastError();
 }
 
-template <bool ROWS>
+template <int FORM>
 static int launch_k_attn(int kv_type, const AttnArgs &a, int64_t pairs, void *stream)
 {
     const int slots = attn_slots(a.c.hd);
     void (*k)(AttnArgs) = nullptr;
-#define QG_ATTN_D(DD)                                                                                       \
-    k = kv_type == KV_F16 ? a.side > 1 ? k_attn<KV_F16, DD, ROWS, true> : k_attn<KV_F16, DD, ROWS, false>   \
-                          : a.side > 1 ? k_attn<KV_BF16, DD, ROWS, true> : k_attn<KV_BF16, DD, ROWS, false>
+#define QG_ATTN_T(T, DD) \
+    a.side > 1 && FORM != SUFFIX ? k_attn<T, DD, FORM, FORM != SUFFIX> : k_attn<T, DD, FORM, false>
+#define QG_ATTN_D(DD) k = kv_type == KV_F16 ? QG_ATTN_T(KV_F16, DD) : QG_ATTN_T(KV_BF16, DD)
     switch (a.c.hd) {
     case 64: QG_ATTN_D(64); break;
     case 96: QG_ATTN_D(96); break;
@@ -488,26 +507,38 @@ static int launch_k_attn(int kv_type, const AttnArgs &a, int64_t pairs, void *st
     default: QG_ATTN_D(256); break;
     }
 #undef QG_ATTN_D
+#undef QG_ATTN_T
     // as many pairs as slots: those that are much longer than the rest are split all the same
     const int64_t table = (int64_t)a.c.max_pages << a.c.ps_log2;
     const int64_t grid = pairs < slots ? slots : table > AttnCols::SOLO << AttnCols::UNIT_LOG2 ? pairs + slots : pairs;
-    hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(256), 0,
-                       static_cast<hipStream_t>(stream), a);
+    hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(256), 0, static_cast<hipStream_t>(stream), a);
     return (int)hipGetLastError();
 }
 
-int launch_attn(int kv_type, const AttnArgs &a, void *stream)
+template <int FORM>
+static int launch_one(int kv_type, const AttnArgs &a, void *stream)
 {
     AttnArgs b = a;
     b.side = (a.group + 15) / 16;
-    return launch_k_attn<false>(kv_type, b, (int64_t)a.c.n_seq * a.c.nkv * b.side, stream);
+    return launch_k_attn<FORM>(kv_type, b, (int64_t)a.c.n_seq * a.c.nkv * b.side, stream);
 }
-
-int launch_attn_rows(int kv_type, const AttnArgs &a, void *stream)
+template <int FORM>
+static int launch_many(int kv_type, const AttnArgs &a, void *stream)
 {
     AttnArgs b = a;
     b.side = (int)((a.c.n_rows * a.group + 16 * a.c.n_seq - 1) / (16 * a.c.n_seq));   // on average
-    return launch_k_attn<true>(kv_type, b, a.c.nkv * (a.c.n_rows * a.group / 16 + a.c.n_seq), stream);
+    return launch_k_attn<FORM>(kv_type, b, a.c.nkv * (a.c.n_rows * a.group / 16 + a.c.n_seq), stream);
+}
+
+int launch_attn(int kv_type, const AttnArgs &a, void *stream) { return launch_one<ONE>(kv_type, a, stream); }
+int launch_attn_rows(int kv_type, const AttnArgs &a, void *stream) { return launch_many<MANY>(kv_type, a, stream); }
+int launch_attn_prefix(int kv_type, const AttnArgs &a, void *stream)
+{
+    return launch_many<PREFIX>(kv_type, a, stream);
+}
+int launch_attn_suffix(int kv_type, const AttnArgs &a, void *stream)
+{
+    return launch_one<SUFFIX>(kv_type, a, stream);
 }
 
 }  // namespace qg

@@ -66,7 +66,8 @@ __host__ __device__ constexpr int64_t prompt_part_floats(int hd) { return (int64
 // FEW: there are at least as many tiles as slots, and only those behind much longer contexts than the rest
 // are split and joined in this launch (in a kernel of its own: the code of that join costs nine prompts
 // without a split 36.3 -> 38.2 us).  Else, with slots, all are split and a second launch joins.
-template <int T, int D, bool FEW>
+// SHARED: the rows are the sequences of a group, and see its shared positions (PREFIX).
+template <int T, int D, bool FEW, bool SHARED>
 __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs a, int slots)
 {
     constexpr bool BYTES = kv_bytes(T);
@@ -86,8 +87,8 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 31, hf = lane >> 5;
     AttnPlan w;
-    const bool work = attn_plan<PromptCols, true>(c, a.group, slots, blockIdx.x, w,
-                                                  reinterpret_cast<AttnSeq *>(lds), !FEW);
+    const bool work = attn_plan<PromptCols, SHARED ? PREFIX : MANY>(a, slots, blockIdx.x, w,
+                                                                    reinterpret_cast<AttnSeq *>(lds), !FEW);
     if (!FEW && blockIdx.x == 0 && tid == 0 && slots)
         *a.pairs = w.all ? w.pairs : 0;
     if (!work)
@@ -100,8 +101,8 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
     p.row0 = w.row0;
     p.rows = w.rows;
     p.rho0 = w.pair / c.nkv * PT_ROWS;
-    p.pos0 = max(c.kv_len[w.b], -(1 << 30)) - p.rows;      // position of the first new row
-    p.hi = max(0, min(w.len, p.pos0 + min((p.rho0 + PT_ROWS - 1) / a.group, p.rows - 1) + 1));
+    p.pos0 = SHARED ? 0 : max(c.kv_len[w.b], -(1 << 30)) - p.rows;      // position of the first new row
+    p.hi = SHARED ? w.len : max(0, min(w.len, p.pos0 + min((p.rho0 + PT_ROWS - 1) / a.group, p.rows - 1) + 1));
     // this chunk's steps, as far as the tile reads
     const int units = PromptCols::units(w.len), per = units / w.n_chunk, more = units % w.n_chunk;
     const int s0 = w.chunk * per + min(w.chunk, more);
@@ -119,8 +120,22 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
     // with the last one and are not stored
     const int wave_tok0 = (p.rho0 + 32 * wave) / a.group;
     const int wave_tok1 = min((p.rho0 + 32 * wave + 31) / a.group, p.rows - 1);
-    const int wave_max = wave_tok0 < p.rows ? p.pos0 + wave_tok1 : -1;
-    const int pos = live ? p.pos0 + tok : wave_max;    // the row sees positions 0..pos
+    int wave_max = wave_tok0 < p.rows ? p.pos0 + wave_tok1 : -1;
+    int pos = live ? p.pos0 + tok : wave_max;          // the row sees positions 0..pos
+    // the tile's least position; a table that ends before it may end inside a step
+    int tile_min = min(p.pos0 + p.rho0 / a.group, p.hi - 1);
+    if constexpr (SHARED) {
+        // (positions of a table are below 2^24, whole numbers in f32)
+        pos = live ? prefix_seen(a, p.row0 + tok, p.row0, w.len) - 1 : -1;
+        wave_max = (int)max_x16(max_of_16((float)pos));
+        const int least = -(int)max_x16(max_of_16(live ? -(float)pos : -(float)p.hi));
+        s_odd[wave] = __builtin_amdgcn_readfirstlane(least);
+        wave_max = __builtin_amdgcn_readfirstlane(wave_max);
+        __syncthreads();
+        tile_min = min(min(s_odd[0], s_odd[1]), min(s_odd[2], s_odd[3]));
+        tile_min = min(__builtin_amdgcn_readfirstlane(tile_min), p.hi - 1);
+        __syncthreads();
+    }
 
     au4 qf[NP][KB];
     float unscale;
@@ -160,7 +175,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
 
     // copies: wave w's 16-position block w.  K: piece idx = 64 x + lane of the block, row idx / PR,
     // source piece (idx % PR) ^ key(row); V: channel 32 x + lane / 2, source piece lane % 2 ^ its key
-    const int32_t *table = c.table + (int64_t)w.b * c.max_pages;
+    const int32_t *table = c.table + (int64_t)(SHARED ? p.row0 : w.b) * c.max_pages;
     const int ps_mask = (1 << c.ps_log2) - 1;
     const int last_entry = p.hi > 0 ? (p.hi - 1) >> c.ps_log2 : 0;
     const int64_t head_off = BYTES ? (int64_t)hkv * c.block : (int64_t)hkv * D << c.ps_log2;
@@ -428,8 +443,6 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
                 }
         }
     };
-    // the tile's least position; a table that ends before it may end inside a step
-    const int tile_min = min(p.pos0 + p.rho0 / a.group, p.hi - 1);
     auto compute = [&](int s, int buf, uint32_t bad) {
         const int t0 = s * PT_STEP;
         const bool edge = bad != 0 || t0 + PT_STEP - 1 > tile_min;
@@ -631,7 +644,10 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
     }
     if (live) {
         const float inv = BYTES ? 1.f : inverse_sum(l);
-        float *row = a.o + ((int64_t)(p.row0 + tok) * a.nq + head) * D + 4 * hf;
+        const int64_t at = (int64_t)(p.row0 + tok) * a.nq + head;
+        float *row = a.o + at * D + 4 * hf;
+        if (SHARED && hf == 0)
+            *reinterpret_cast<float2 *>(a.stats + 2 * at) = make_float2(-shift, l);
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -644,7 +660,8 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_prompt(AttnArgs 
 // Rows of a split tile from its partial results.  A workgroup takes four rows of a tile and KV head at a
 // time; a thread four channels of a row and every `parts`-th split, in order, then the parts are added
 // in order.
-template <bool MEANS>
+// MEANS: the parts are means.  SHARED: the exponents and sums go to stats.
+template <bool MEANS, bool SHARED>
 __global__ __launch_bounds__(256) void k_attn_prompt_join(AttnArgs a)
 {
     __shared__ __attribute__((aligned(16))) af4 s_sum[256];
@@ -661,7 +678,7 @@ __global__ __launch_bounds__(256) void k_attn_prompt_join(AttnArgs a)
     for (int r0 = 4 * blockIdx.y; r0 < PT_ROWS && (p.rho0 + r0) / a.group < p.rows; r0 += 4 * gridDim.y) {
         const float *part = a.part + p.slot0 * stride, *from = part + (r0 + row) * D + 4 * d4;
         const float *ml = part + PT_ROWS * D + 2 * (r0 + row);
-        float m = -INFINITY, l = 0.f;
+        float m = -INFINITY, l = 0.f, all_m = 0.f, all_l = 0.f;
         af4 sum = {0.f, 0.f, 0.f, 0.f};
         if constexpr (MEANS) {
             // the factors of all parts first, then each mean by its own: threads of a row add them alike
@@ -670,6 +687,8 @@ __global__ __launch_bounds__(256) void k_attn_prompt_join(AttnArgs a)
             for (int k = 0; k < splits; ++k)
                 l += ml[k * stride + 1] * join_weight(ml[k * stride], m);
             const float inv = inverse_sum(l);
+            all_m = m;
+            all_l = l;
             for (int kb = k0; k0 < parts && kb < splits; kb += 8 * parts) {
                 af4 v[8];
                 float2 w[8];
@@ -723,6 +742,7 @@ __global__ __launch_bounds__(256) void k_attn_prompt_join(AttnArgs a)
                 for (int x = 1; x < parts; ++x)
                     all = fmaxf(all, s_m[e + x * items]);
                 const float f0 = join_weight(m, all);
+                m = all;
                 sum *= f0;
                 l *= f0;
                 for (int x = 1; x < parts; ++x) {
@@ -734,9 +754,12 @@ __global__ __launch_bounds__(256) void k_attn_prompt_join(AttnArgs a)
             __syncthreads();
         }
         const int rho = p.rho0 + r0 + row, tok = rho / a.group;
-        if (k0 == 0 && tok < p.rows)
-            *reinterpret_cast<af4 *>(a.o + ((int64_t)(p.row0 + tok) * a.nq + p.hkv * a.group + rho % a.group) * D +
-                                     4 * d4) = sum * inverse_sum(l);
+        if (k0 == 0 && tok < p.rows) {
+            const int64_t at = (int64_t)(p.row0 + tok) * a.nq + p.hkv * a.group + rho % a.group;
+            *reinterpret_cast<af4 *>(a.o + at * D + 4 * d4) = sum * inverse_sum(l);
+            if (SHARED && d4 == 0)
+                *reinterpret_cast<float2 *>(a.stats + 2 * at) = MEANS ? make_float2(all_m, all_l) : make_float2(m, l);
+        }
     }
 }
 
@@ -777,21 +800,20 @@ bool prompt_in_16s(int64_t n_rows, int n_seq, int nq, int nkv, int hd, int64_t p
            columns * nkv * hd * (positions < 16384 ? positions : 16384) <= (int64_t)1 << 31;
 }
 
-int launch_attn_prompt(int kv_type, const AttnArgs &a, void *stream)
+template <bool SHARED>
+static int launch_prompt(int kv_type, const AttnArgs &a, void *stream)
 {
     const int64_t table = (int64_t)a.c.max_pages << a.c.ps_log2;
     const bool bytes = kv_bytes(kv_type);
-    if (prompt_in_16s(a.c.n_rows, a.c.n_seq, a.nq, a.c.nkv, a.c.hd, table))
-        return bytes ? launch_attn8_rows(kv_type, a, stream) : launch_attn_rows(kv_type, a, stream);
     hipStream_t s = static_cast<hipStream_t>(stream);
     const PromptPlan p = plan_prompt(a.c.n_rows, a.c.n_seq, a.c.nkv, a.group, a.c.hd, table);
     const bool few = p.slots && !p.second;
     void (*k)(AttnArgs, int) = nullptr;
-#define QG_PROMPT_T(T, DD) few ? k_attn_prompt<T, DD, true> : k_attn_prompt<T, DD, false>
-#define QG_PROMPT_D(DD)                                \
-    k = kv_type == KV_F16  ? QG_PROMPT_T(KV_F16, DD)   \
+#define QG_PROMPT_T(T, DD) few ? k_attn_prompt<T, DD, true, SHARED> : k_attn_prompt<T, DD, false, SHARED>
+#define QG_PROMPT_D(DD)                                 \
+    k = kv_type == KV_F16    ? QG_PROMPT_T(KV_F16, DD)  \
         : kv_type == KV_BF16 ? QG_PROMPT_T(KV_BF16, DD) \
-        : kv_type == KV_I8   ? QG_PROMPT_T(KV_I8, DD)  \
+        : kv_type == KV_I8   ? QG_PROMPT_T(KV_I8, DD)   \
                              : QG_PROMPT_T(KV_F8, DD)
     switch (a.c.hd) {
     case 64: QG_PROMPT_D(64); break;
@@ -810,8 +832,30 @@ int launch_attn_prompt(int kv_type, const AttnArgs &a, void *stream)
     // behind 4000 positions: 56.3 us, with 2048 61.4; 8192 that find nothing to join cost 1 us more)
     const int64_t share = 4096 / p.pairs;
     const unsigned y = (unsigned)(share > PT_ROWS / 4 ? PT_ROWS / 4 : share > 8 ? share : 8);
-    hipLaunchKernelGGL(bytes ? k_attn_prompt_join<true> : k_attn_prompt_join<false>, dim3((unsigned)p.pairs, y), dim3(256), 0, s, a);
+    auto join = bytes ? k_attn_prompt_join<true, SHARED> : k_attn_prompt_join<false, SHARED>;
+    hipLaunchKernelGGL(join, dim3((unsigned)p.pairs, y), dim3(256), 0, s, a);
     return (int)hipGetLastError();
+}
+
+int launch_attn_prompt(int kv_type, const AttnArgs &a, void *stream)
+{
+    if (prompt_in_16s(a.c.n_rows, a.c.n_seq, a.nq, a.c.nkv, a.c.hd, (int64_t)a.c.max_pages << a.c.ps_log2))
+        return kv_bytes(kv_type) ? launch_attn8_rows(kv_type, a, stream) : launch_attn_rows(kv_type, a, stream);
+    return launch_prompt<false>(kv_type, a, stream);
+}
+
+// The groups as sequences of rows, for the shared positions.
+int launch_attn_shared(int kv_type, const AttnArgs &a, void *stream)
+{
+    AttnArgs g = a;
+    g.c.q_start = a.group_start;
+    g.c.n_seq = a.n_group;
+    const bool bytes = kv_bytes(kv_type);
+    const bool in_16s = prompt_in_16s(g.c.n_rows, g.c.n_seq, g.nq, g.c.nkv, g.c.hd, (int64_t)g.c.max_pages << g.c.ps_log2);
+    const int e = !in_16s ? launch_prompt<true>(kv_type, g, stream)
+                  : bytes ? launch_attn8_prefix(kv_type, g, stream)
+                          : launch_attn_prefix(kv_type, g, stream);
+    return e ? e : bytes ? launch_attn8_suffix(kv_type, a, stream) : launch_attn_suffix(kv_type, a, stream);
 }
 
 }  // namespace qg
