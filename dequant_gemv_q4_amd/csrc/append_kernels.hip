@@ -1,21 +1,24 @@
 // append_kernels.hip -- from the fused QKV output to the cache: norm and rotation of the Q and K heads,
 // and new rows of K and V in pages of any type; and new rows alone in 8-bit pages.
 //
-// A workgroup takes one head of one block of 16 or 32 positions (at most a page) of a sequence: a KV head
-// (its K, then its V) or a Q head.  A row of a head is shared by LPR lanes, four channels each, so a wave
-// holds 64 / LPR rows and reads them in runs of whole heads; the sums and maxima of a row go over those
-// lanes.  The channel that a channel is rotated with is read again instead of exchanged (the line is in the
-// L1).
+// A workgroup takes K or V of a KV head, or four Q heads, of one block of 16 or 32 positions (at most a page)
+// of a sequence.  A row of a head is shared by LPR lanes, four channels each, so a wave holds 64 / LPR rows
+// and reads them in runs of whole heads; the sums and maxima of a row go over those lanes.  The channel that a
+// channel is rotated with is read again instead of exchanged (the line is in the L1; a swap of half rows took
+// as long).
 //
 // K is turned in 64 bits and rounded once: it ends in 3 to 10 bits, and which of two neighbours a value
 // near their middle takes must not depend on the order of the sums (gfx950 runs f64 at the f32 rate).  Codes
-// are those of the exact quotient x / d: the quotient by multiplication is off by one step at most, and its
-// remainder x - n d is exact (f32: n has 7 bits, and the remainder is a multiple of half d's last bit not
-// above d), so it decides, ties included.  V goes through LDS to lie transposed in the page, 16 bytes of a
-// channel at a time; a piece with positions that are not new is written element by element.
+// are those of the exact quotient x / d: the quotient by multiplication is off by one code at most, and the
+// remainder x - n d decides, ties included.  Of an f32 x it is exact (a multiple of half d's last bit not above
+// d); of K it is taken in f32 first and again in f64 where that is too near.  V goes through LDS to lie
+// transposed in the page, 16 bytes of a channel at a time; a piece with positions that are not new is written
+// element by element.
 #include <hip/hip_runtime.h>
 
 #include <float.h>
+
+#include <type_traits>
 
 #include "attn_common.h"
 
@@ -39,24 +42,83 @@ __device__ __forceinline__ float to_odd(float x) { return x; }
 __device__ __forceinline__ float fma_of(float a, float b, float c) { return fmaf(a, b, c); }
 __device__ __forceinline__ double fma_of(double a, double b, double c) { return fma(a, b, c); }
 
-// Combine over the LPR lanes of a row; every lane gets the result.
+// 1 / sqrt(x) to the last place or two, by a step of Newton's method from the instruction's value; f64 by two
+// steps from the instruction's 2^-14 or better (an infinity or a zero stays with its answer).
+__device__ __forceinline__ float inverse_root(float x)
+{
+    if (!(x > 0x1p-100f) || !(x <= FLT_MAX))
+        return 1.0f / sqrtf(x);
+    const float r = __builtin_amdgcn_rsqf(x);
+    return fmaf(r * 0.5f, fmaf(-x * r, r, 1.0f), r);
+}
+__device__ __forceinline__ double inverse_root(double x)
+{
+    double r = __builtin_amdgcn_rsq(x);
+    if (!(x > 0.0) || !(x <= DBL_MAX))
+        return r;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        r = fma(r * 0.5, fma(-x * r, r, 1.0), r);
+    return r;
+}
+
+// A value of the lane that a DPP control names within 16 lanes.
+template <int CTRL, class R>
+__device__ __forceinline__ R moved(R v)
+{
+    if constexpr (sizeof(R) == 4) {
+        return __builtin_bit_cast(R, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+    } else {
+        const uint64_t b = __builtin_bit_cast(uint64_t, v);
+        const uint32_t lo = moved<CTRL>((uint32_t)b), hi = moved<CTRL>((uint32_t)(b >> 32));
+        return __builtin_bit_cast(R, (uint64_t)hi << 32 | lo);
+    }
+}
+// v of lanes l and l ^ 16 (HALF: l ^ 32), combined.
+template <bool HALF, class R, class F>
+__device__ __forceinline__ R crossed(R v, F f)
+{
+    auto swap = [](uint32_t b) {
+        if constexpr (HALF)
+            return __builtin_amdgcn_permlane32_swap(b, b, false, false);
+        else
+            return __builtin_amdgcn_permlane16_swap(b, b, false, false);
+    };
+    if constexpr (sizeof(R) == 4) {
+        const auto s = swap(__builtin_bit_cast(uint32_t, v));
+        const uint32_t s0 = s[0], s1 = s[1];
+        return f(__builtin_bit_cast(R, s0), __builtin_bit_cast(R, s1));
+    } else {
+        const uint64_t b = __builtin_bit_cast(uint64_t, v);
+        const auto lo = swap((uint32_t)b), hi = swap((uint32_t)(b >> 32));
+        const uint32_t l0 = lo[0], l1 = lo[1], h0 = hi[0], h1 = hi[1];
+        return f(__builtin_bit_cast(R, (uint64_t)h0 << 32 | l0), __builtin_bit_cast(R, (uint64_t)h1 << 32 | l1));
+    }
+}
+// Combine over the LPR lanes of a row; every lane gets the result (of sums, up to their order).
 template <int LPR, class R, class F>
 __device__ __forceinline__ R over_row(R v, F f)
 {
-#pragma unroll
-    for (int m = 1; m < LPR; m *= 2)
-        v = f(v, __shfl_xor(v, m, 64));
+    v = f(v, moved<0x121>(v));                             // row_ror 1, 2, 4, 8
+    v = f(v, moved<0x122>(v));
+    v = f(v, moved<0x124>(v));
+    v = f(v, moved<0x128>(v));
+    if constexpr (LPR >= 32)
+        v = crossed<false>(v, f);
+    if constexpr (LPR >= 64)
+        v = crossed<true>(v, f);
     return v;
 }
 
-// The scale of a row from its largest |value| (not finite: NaN).
+// The scale of a row from its largest |value| (not finite: NaN).  The product with f64's 1 / 127 rounds to the
+// same f32 as the quotient of an f32: that is 2^-31 of itself from the middle of two f32 at least.
 template <int T, class R>
 __device__ __forceinline__ float scale_of(R amax)
 {
     if (!(amax <= (R)FLT_MAX))
         return __builtin_nanf("");
     if constexpr (T == KV_I8) {
-        return fmaxf((float)(amax / (R)127), 0x1p-126f);
+        return fmaxf((float)((double)amax * (1.0 / 127)), 0x1p-126f);
     } else {
         // amax = m 2^e, m in [1/2, 1), and 448 = 7/8 2^9
         int e = 0;
@@ -72,25 +134,39 @@ __device__ __forceinline__ uint32_t codes_of(const R (&x)[4], float d)
 {
     if (d != d)
         return 0u;
-    const R dd = (R)d, inv = (R)1 / dd;
+    const float inv = 1.0f / d;
     if constexpr (T == KV_I8) {
-        uint32_t out = 0;
+        int n[4];
+        bool near = false;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const R n = __builtin_elementwise_rint(x[e] * inv), r = fma_of(-n, dd, x[e]), two = r + r;
-            int i = (int)n;
-            if (two > dd || (two == dd && (i & 1)))
-                ++i;
-            if (-two > dd || (-two == dd && (i & 1)))
-                --i;
-            out |= (uint32_t)(i & 0xFF) << (8 * e);
+            const float f = (float)x[e], q = __builtin_rintf(f * inv), r = fmaf(-q, d, f), two = fabsf(r + r);
+            const int up = r > 0.f ? 1 : -1;
+            n[e] = (int)q;
+            if constexpr (sizeof(R) == 4) {
+                if (two > d || (two == d && (n[e] & 1)))
+                    n[e] += up;
+            } else {
+                near |= fabsf(two - d) <= 0x1p-15f * d;   // f is off by 2^-24 |x|, 2^-17 d
+                if (two > d)
+                    n[e] += up;
+            }
         }
-        return out;
+        if constexpr (sizeof(R) == 8)
+            if (__any(near))
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const double r = fma(-(double)n[e], (double)d, x[e]), two = fabs(r + r);
+                    if (two > d || (two == d && (n[e] & 1)))
+                        n[e] += r > 0.0 ? 1 : -1;
+                }
+        return (uint32_t)(n[0] & 0xFF) | (uint32_t)(n[1] & 0xFF) << 8 | (uint32_t)(n[2] & 0xFF) << 16 |
+               (uint32_t)n[3] << 24;
     } else {
         float y[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            y[e] = to_odd(x[e] * inv);                   // d is a power of two
+            y[e] = to_odd(x[e]) * inv;                   // d is a power of two
         int p = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
         p = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], p, true);
         return (uint32_t)p;
@@ -99,6 +175,8 @@ __device__ __forceinline__ uint32_t codes_of(const R (&x)[4], float d)
 
 // Channels of a head, rounded up to a power of two lanes of four.
 constexpr int lanes_per_row(int hd) { return hd <= 64 ? 16 : hd <= 128 ? 32 : 64; }
+
+constexpr int Q_HEADS = 4;                                 // of a workgroup, their loads in flight together
 
 // TURN: norms and rotation (and Q heads); else K and V as they come.  VEC: rope_half is a multiple of four.
 template <int T, int BL, int LPR, bool TURN, bool VEC>
@@ -109,10 +187,12 @@ __global__ __launch_bounds__(256) void k_qkv_append(QkvArgs a)
     constexpr int STRIDE = BLOCK * SIZE + 4;               // bytes of a channel in LDS
     __shared__ __attribute__((aligned(16))) uint8_t s_v[4 * LPR * STRIDE];
     const KvArgs &c = a.c;
-    const int tid = threadIdx.x, role = blockIdx.y, j = tid % LPR, row = tid / LPR, ch = 4 * j;
+    const int tid = threadIdx.x, j = tid % LPR, row = tid / LPR, ch = 4 * j;
+    // roles of a block side by side: the workgroups at work read and write whole rows
+    const int id = blockIdx.x / a.roles, role = blockIdx.x - id * a.roles;
     const bool in = ch < c.hd;
     AppendBlock w;
-    if (!append_block<BL>(c, w))
+    if (!append_block<BL>(c, id, w))
         return;
     int from = w.from, to = w.to;
     if (TURN && a.half > 0 && w.t0 + to > a.rope_rows) {
@@ -127,52 +207,69 @@ __global__ __launch_bounds__(256) void k_qkv_append(QkvArgs a)
         const float4 v = *reinterpret_cast<const float4 *>(p);
         x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
     };
-    // four channels of a head at position t0 + t, normalised and rotated
-    auto turned = [&](const float *x, const float *gamma, int t, auto one) {
-        typedef decltype(one) R;
-        struct Four {
-            R v[4];
-        } r;
-        float y[4] = {0.f, 0.f, 0.f, 0.f}, z[4] = {0.f, 0.f, 0.f, 0.f}, gy[4], gz[4];
-        // channel ch + e is turned with the one `other` away
-        const int h = a.half;
-        float cs[4], sn[4];
-        int other[4];
+    // channel ch + e is turned with the one other(e) away (0: not at all)
+    auto other = [&](int e) {
+        const int k = VEC ? ch : ch + e;
+        return !TURN || !in || k >= 2 * a.half ? 0 : k < a.half ? a.half : -a.half;
+    };
+    // four channels, or those that they are turned with (left as they were where they are not)
+    auto load = [&](const float *p, float (&x)[4]) {
+        if (in)
+            load4(p + ch, x);
+    };
+    auto load_other = [&](const float *p, float (&x)[4]) {
+        if constexpr (VEC) {
+            if (other(0))
+                load4(p + ch + other(0), x);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (other(e))
+                    x[e] = p[ch + e + other(e)];
+        }
+    };
+    const double inv_hd = 1.0 / c.hd;
+    struct Turn {
+        float c[4], s[4], gy[4], gz[4];                    // s with the sign that it has in the channel's sum
+    };
+    auto weights_of = [&](const float *gamma, Turn &u) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            u.gy[e] = u.gz[e] = 1.f;
+        if (gamma) {
+            load(gamma, u.gy);
+            load_other(gamma, u.gz);
+        }
+    };
+    auto angles_of = [&](int t, Turn &u) {
+        const int64_t at = (w.t0 + t) * a.half;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const int k = ch + e, at = VEC ? ch : k;
-            other[e] = in && at < 2 * h ? (at < h ? h : -h) : 0;
-            gy[e] = gz[e] = 1.f;
-            cs[e] = 1.f;
-            sn[e] = 0.f;
+            u.c[e] = 1.f;
+            u.s[e] = 0.f;
         }
-        if (in) {
-            load4(x + ch, y);
-            if (gamma)
-                load4(gamma + ch, gy);
-            const int64_t turn = (w.t0 + t) * h;
-            if constexpr (VEC) {
-                if (other[0]) {
-                    load4(x + ch + other[0], z);
-                    if (gamma)
-                        load4(gamma + ch + other[0], gz);
-                    const int k = other[0] > 0 ? ch : ch - h;
-                    load4(a.cos + turn + k, cs);
-                    load4(a.sin + turn + k, sn);
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (other[e]) {
-                        z[e] = x[ch + e + other[e]];
-                        if (gamma)
-                            gz[e] = gamma[ch + e + other[e]];
-                        const int k = other[e] > 0 ? ch + e : ch + e - h;
-                        cs[e] = a.cos[turn + k];
-                        sn[e] = a.sin[turn + k];
-                    }
+        if constexpr (VEC) {
+            if (other(0)) {
+                const int k = other(0) > 0 ? ch : ch - a.half;
+                load4(a.cos + at + k, u.c);
+                load4(a.sin + at + k, u.s);
             }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (other(e)) {
+                    const int k = ch + e + (other(e) > 0 ? 0 : other(e));
+                    u.c[e] = a.cos[at + k];
+                    u.s[e] = a.sin[at + k];
+                }
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            u.s[e] = other(e) > 0 ? -u.s[e] : u.s[e];
+    };
+    // a head's four channels y (z: those they are turned with), normalised and turned
+    auto turned = [&](const float (&y)[4], const float (&z)[4], const float *gamma, const Turn &u, auto &out) {
+        typedef typename std::remove_reference<decltype(out[0])>::type R;
         R scale = (R)1;
         if (gamma) {
             R ss = (R)0;
@@ -180,31 +277,49 @@ __global__ __launch_bounds__(256) void k_qkv_append(QkvArgs a)
             for (int e = 0; e < 4; ++e)
                 ss = fma_of((R)y[e], (R)y[e], ss);
             ss = over_row<LPR>(ss, [](R u, R v) { return u + v; });
-            const R mean = ss / (R)c.hd + (R)a.eps;
-            scale = (R)1 / (sizeof(R) == 8 ? (R)sqrt((double)mean) : (R)sqrtf((float)mean));
+            scale = inverse_root(fma_of(ss, (R)inv_hd, (R)a.eps));
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const R u = gamma ? (R)y[e] * (R)gy[e] * scale : (R)y[e], v = gamma ? (R)z[e] * (R)gz[e] * scale : (R)z[e];
-            r.v[e] = other[e] ? fma_of(u, (R)cs[e], other[e] > 0 ? -v * (R)sn[e] : v * (R)sn[e]) : u;
+            const R p = gamma ? (R)y[e] * (R)u.gy[e] : (R)y[e], v = gamma ? (R)z[e] * (R)u.gz[e] : (R)z[e];
+            const R r = fma_of(p, (R)u.c[e], v * (R)u.s[e]);
+            out[e] = gamma ? r * scale : r;
         }
-        return r;
     };
 
-    if (role >= c.nkv) {                                   // a Q head
-        const int h = role - c.nkv;
-        for (int t = from + row; t < to; t += ROWS) {
-            const auto r = turned(a.q + (w.row0 + t) * a.stride + (int64_t)h * c.hd, a.q_gamma, t, 1.0f);
-            if (in)
-                *reinterpret_cast<float4 *>(a.qo + (w.row0 + t) * a.qo_stride + (int64_t)h * c.hd + ch) =
-                    make_float4(r.v[0], r.v[1], r.v[2], r.v[3]);
+    if (role >= 2 * c.nkv) {                               // Q heads
+        if constexpr (TURN) {
+            const int h0 = (role - 2 * c.nkv) * Q_HEADS, heads = min(Q_HEADS, a.nq - h0);
+            Turn u;
+            weights_of(a.q_gamma, u);
+            for (int t = from + row; t < to; t += ROWS) {
+                const float *src = a.q + (w.row0 + t) * a.stride + (int64_t)h0 * c.hd;
+                float *dst = a.qo + (w.row0 + t) * a.qo_stride + (int64_t)h0 * c.hd + ch;
+                float y[Q_HEADS][4] = {}, z[Q_HEADS][4] = {};
+                angles_of(t, u);
+#pragma unroll
+                for (int h = 0; h < Q_HEADS; ++h)
+                    if (h < heads) {
+                        load(src + h * c.hd, y[h]);
+                        load_other(src + h * c.hd, z[h]);
+                    }
+#pragma unroll
+                for (int h = 0; h < Q_HEADS; ++h)
+                    if (h < heads) {
+                        float r[4];
+                        turned(y[h], z[h], a.q_gamma, u, r);
+                        if (in)
+                            *reinterpret_cast<float4 *>(dst + h * c.hd) = make_float4(r[0], r[1], r[2], r[3]);
+                    }
+            }
         }
         return;
     }
 
-    const int page = append_page(c, w), h = role;
+    const bool is_v = role >= c.nkv;
+    const int page = append_page(c, w), h = is_v ? role - c.nkv : role;
     if (page < 0) {
-        if (tid == 0 && h == 0)
+        if (tid == 0 && role == 0)
             atomicOr(c.err, 1u);
         return;
     }
@@ -212,55 +327,59 @@ __global__ __launch_bounds__(256) void k_qkv_append(QkvArgs a)
     const int64_t base = (int64_t)page * c.page_stride + (int64_t)h * c.block;
     const int64_t codes = (int64_t)c.hd << c.ps_log2;      // elements before an 8-bit block's scales
 
-    // K: a row's codes lie side by side
-    for (int t = from + row; t < to; t += ROWS) {
-        const float *src = a.k + (w.row0 + t) * a.stride + (int64_t)h * c.hd;
-        RK x[4] = {0, 0, 0, 0};
-        if constexpr (TURN) {
-            const auto r = turned(src, a.k_gamma, t, 1.0);
+    if (!is_v) {                                           // K: a row's codes lie side by side
+        Turn u;
+        if constexpr (TURN)
+            weights_of(a.k_gamma, u);
+        for (int t = from + row; t < to; t += ROWS) {
+            const float *src = a.k + (w.row0 + t) * a.stride + (int64_t)h * c.hd;
+            float y[4] = {};
+            RK x[4];
+            load(src, y);
+            if constexpr (TURN) {
+                float z[4] = {};
+                load_other(src, z);
+                angles_of(t, u);
+                turned(y, z, a.k_gamma, u, x);
+            } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                x[e] = r.v[e];
-        } else if (in) {
-            float y[4];
-            load4(src + ch, y);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                x[e] = y[e];
-        }
-        const int64_t at = base + (int64_t)(slot + t) * c.hd + ch;
-        if constexpr (SIZE == 1) {
-            RK top = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const RK v = x[e] < 0 ? -x[e] : x[e];
-                top = v <= top ? top : v <= (RK)FLT_MAX ? v : (RK)INFINITY;
+                for (int e = 0; e < 4; ++e)
+                    x[e] = y[e];
             }
-            top = over_row<LPR>(top, [](RK u, RK v) { return u > v ? u : v; });
-            const float d = scale_of<T>(top);
-            if (in)
-                *reinterpret_cast<uint32_t *>(c.k8() + at) = codes_of<T>(x, d);
-            if (j == 0)
-                *reinterpret_cast<float *>(c.k8() + base + codes + 4 * (slot + t)) = d;
-        } else if (in) {
-            uint2 v;
-            v.x = pack2<T>(to_odd(x[0]), to_odd(x[1]));
-            v.y = pack2<T>(to_odd(x[2]), to_odd(x[3]));
-            *reinterpret_cast<uint2 *>(c.k + at) = v;
+            const int64_t at = base + (int64_t)(slot + t) * c.hd + ch;
+            if constexpr (SIZE == 1) {
+                RK top = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const RK v = x[e] < 0 ? -x[e] : x[e];
+                    top = v <= top ? top : v <= (RK)FLT_MAX ? v : (RK)INFINITY;
+                }
+                top = over_row<LPR>(top, [](RK u, RK v) { return __builtin_elementwise_max(u, v); });
+                const float d = scale_of<T>(top);
+                if (in)
+                    *reinterpret_cast<uint32_t *>(c.k8() + at) = codes_of<T>(x, d);
+                if (j == 0)
+                    *reinterpret_cast<float *>(c.k8() + base + codes + 4 * (slot + t)) = d;
+            } else if (in) {
+                uint2 v;
+                v.x = pack2<T>(to_odd(x[0]), to_odd(x[1]));
+                v.y = pack2<T>(to_odd(x[2]), to_odd(x[3]));
+                *reinterpret_cast<uint2 *>(c.k + at) = v;
+            }
         }
+        return;
     }
 
     // V: by rows into LDS, by channels out of it
     for (int t = from + row; t < to; t += ROWS) {
-        float x[4] = {0.f, 0.f, 0.f, 0.f};
-        if (in)
-            load4(a.v + (w.row0 + t) * a.stride + (int64_t)h * c.hd + ch, x);
+        float x[4] = {};
+        load(a.v + (w.row0 + t) * a.stride + (int64_t)h * c.hd, x);
         if constexpr (SIZE == 1) {
             float top = 0.f;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 top = fabsf(x[e]) <= top ? top : fabsf(x[e]) <= FLT_MAX ? fabsf(x[e]) : INFINITY;
-            top = over_row<LPR>(top, [](float u, float v) { return u > v ? u : v; });
+            top = over_row<LPR>(top, [](float u, float v) { return fmaxf(u, v); });
             const float d = scale_of<T>(top);
             const uint32_t v = codes_of<T>(x, d);
 #pragma unroll
@@ -299,9 +418,12 @@ __global__ __launch_bounds__(256) void k_qkv_append(QkvArgs a)
 }
 
 template <int T, int BL, bool TURN>
-static void launch_block(const QkvArgs &a, dim3 grid, hipStream_t s)
+static void launch_block(const QkvArgs &a, hipStream_t s)
 {
     const bool vec = a.half % 4 == 0;
+    const int64_t blocks = a.c.q_start ? (a.c.n_rows >> BL) + 2 * (int64_t)a.c.n_seq : a.c.n_seq;
+    QkvArgs b = a;
+    b.roles = 2 * a.c.nkv + (TURN ? (a.nq + Q_HEADS - 1) / Q_HEADS : 0);
     void (*k)(QkvArgs) = nullptr;
 #define QG_APPEND_L(L) k = !TURN || vec ? k_qkv_append<T, BL, L, TURN, true> : k_qkv_append<T, BL, L, TURN, !TURN>
     switch (lanes_per_row(a.c.hd)) {
@@ -310,27 +432,27 @@ static void launch_block(const QkvArgs &a, dim3 grid, hipStream_t s)
     default: QG_APPEND_L(64); break;
     }
 #undef QG_APPEND_L
-    hipLaunchKernelGGL(k, grid, dim3(256), 0, s, a);
+    hipLaunchKernelGGL(k, dim3((unsigned)(blocks * b.roles)), dim3(256), 0, s, b);
+}
+
+template <int T, bool TURN>
+static void launch_type(const QkvArgs &a, hipStream_t s)
+{
+    if (a.c.ps_log2 == 4)
+        launch_block<T, 4, TURN>(a, s);
+    else
+        launch_block<T, 5, TURN>(a, s);
 }
 
 int launch_qkv_append(int kv_type, bool turn, const QkvArgs &a, void *stream)
 {
-    const int bl = a.c.ps_log2 < 5 ? 4 : 5;
-    const int64_t blocks = a.c.q_start ? (a.c.n_rows >> bl) + 2 * (int64_t)a.c.n_seq : a.c.n_seq;
-    const dim3 grid((unsigned)blocks, (unsigned)(a.c.nkv + (turn ? a.nq : 0)));
     hipStream_t s = static_cast<hipStream_t>(stream);
-#define QG_APPEND(T)                                                       \
-    if (turn)                                                              \
-        bl == 4 ? launch_block<T, 4, true>(a, grid, s) : launch_block<T, 5, true>(a, grid, s); \
-    else                                                                   \
-        bl == 4 ? launch_block<T, 4, false>(a, grid, s) : launch_block<T, 5, false>(a, grid, s)
     switch (kv_type) {
-    case KV_I8: QG_APPEND(KV_I8); break;
-    case KV_F8: QG_APPEND(KV_F8); break;
-    case KV_F16: bl == 4 ? launch_block<KV_F16, 4, true>(a, grid, s) : launch_block<KV_F16, 5, true>(a, grid, s); break;
-    default: bl == 4 ? launch_block<KV_BF16, 4, true>(a, grid, s) : launch_block<KV_BF16, 5, true>(a, grid, s); break;
+    case KV_I8: turn ? launch_type<KV_I8, true>(a, s) : launch_type<KV_I8, false>(a, s); break;
+    case KV_F8: turn ? launch_type<KV_F8, true>(a, s) : launch_type<KV_F8, false>(a, s); break;
+    case KV_F16: launch_type<KV_F16, true>(a, s); break;
+    default: launch_type<KV_BF16, true>(a, s); break;
     }
-#undef QG_APPEND
     return (int)hipGetLastError();
 }
 

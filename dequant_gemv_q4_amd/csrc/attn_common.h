@@ -355,32 +355,29 @@ struct AppendBlock {
     int64_t row0;               // row of position t0 (before the sequence's first where from > 0)
 };
 
-// This workgroup's block: those of sequence b begin at block id q_start[b] / size + 2 b, which leaves
+// Block `id`: those of sequence b begin at block id q_start[b] / size + 2 b, which leaves
 // every sequence enough ids wherever its first position lies.
 template <int BL>
-__device__ __forceinline__ bool append_block(const KvArgs &c, AppendBlock &w)
+__device__ __forceinline__ bool append_block(const KvArgs &c, int id, AppendBlock &w)
 {
     const int lane = threadIdx.x & 63;
-    int id = blockIdx.x;
-    if (c.q_start && c.ps_log2 > BL) {
-        // two blocks to an XCD, eight workgroups apart: halves of the same lines of V may meet in its L2
-        // (8000 rows, pages of 64: 24.4 -> 23.4 us)
-        const int r = id % 16;
-        if (id - r + 16 <= (int)gridDim.x)
-            id += r % 8 * 2 + r / 8 - r;
-    }
     int b = id, r0 = id, rows = 1, block = 0;
-    if (c.q_start) {
-        auto start = [&](int i) {
-            const int64_t v = c.q_start[i];
-            return (int)(v < 0 ? 0 : v < c.n_rows ? v : c.n_rows);
-        };
+    int64_t hi;
+    if (c.q_start && c.n_seq < 64) {                     // starts and lengths in one round trip
+        const int first = row_start(c, min(lane, c.n_seq)), len = c.kv_len[min(lane, c.n_seq - 1)];
+        b = __popcll(__ballot(lane < c.n_seq && (first >> BL) + 2 * lane <= id)) - 1;
+        if (b < 0)
+            return false;
+        r0 = __builtin_amdgcn_readlane(first, b);
+        rows = __builtin_amdgcn_readlane(first, b + 1) - r0;
+        hi = __builtin_amdgcn_readlane(len, b);
+    } else if (c.q_start) {
         b = -1;
         for (int b0 = 0; b0 < c.n_seq; b0 += 256) {       // four loads in flight
             int first[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x)
-                first[x] = start(min(b0 + 64 * x + lane, c.n_seq));
+                first[x] = row_start(c, min(b0 + 64 * x + lane, c.n_seq));
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 const int i = b0 + 64 * x + lane;
@@ -390,14 +387,19 @@ __device__ __forceinline__ bool append_block(const KvArgs &c, AppendBlock &w)
         if (b < 0)
             return false;
         b = __builtin_amdgcn_readfirstlane(b);
-        r0 = start(b);
-        rows = start(b + 1) - r0;
+        r0 = row_start(c, b);
+        rows = row_start(c, b + 1) - r0;
+        hi = c.kv_len[b];
+    } else {
+        hi = c.kv_len[b];
+    }
+    if (c.q_start) {
         block = id - ((r0 >> BL) + 2 * b);
         if (rows <= 0 || block < 0)
             return false;
     }
     // positions [lo, hi) of the sequence are new
-    const int64_t hi = c.kv_len[b], first = hi - rows, lo = first > 0 ? first : 0;
+    const int64_t first = hi - rows, lo = first > 0 ? first : 0;
     w.b = b;
     w.t0 = ((lo >> BL) + block) << BL;
     if (w.t0 >= hi)

@@ -61,6 +61,7 @@ struct QkvArgs {
     const float *q_gamma, *k_gamma, *cos, *sin;
     int64_t rope_rows;
     int nq, half;
+    int roles;                  // set by the launcher: workgroups of a block
     float eps;
 };
 
