@@ -9,11 +9,9 @@
 //
 // K is turned in 64 bits and rounded once: it ends in 3 to 10 bits, and which of two neighbours a value
 // near their middle takes must not depend on the order of the sums (gfx950 runs f64 at the f32 rate).  Codes
-// are those of the exact quotient x / d: the quotient by multiplication is off by one code at most, and the
-// remainder x - n d decides, ties included.  Of an f32 x it is exact (a multiple of half d's last bit not above
-// d); of K it is taken in f32 first and again in f64 where that is too near.  V goes through LDS to lie
-// transposed in the page, 16 bytes of a channel at a time; a piece with positions that are not new is written
-// element by element.
+// are those of the exact quotient x / d: taken in f32, and again by the remainder where that is too near to the
+// middle of two.  V goes through LDS to lie transposed in the page, 16 bytes of a channel at a time; a piece with
+// positions that are not new is written element by element.
 #include <hip/hip_runtime.h>
 
 #include <float.h>
@@ -110,8 +108,31 @@ __device__ __forceinline__ R over_row(R v, F f)
     return v;
 }
 
-// The scale of a row from its largest |value| (not finite: NaN).  The product with f64's 1 / 127 rounds to the
-// same f32 as the quotient of an f32: that is 2^-31 of itself from the middle of two f32 at least.
+// The largest of the four |values| that a lane has of a row, over the row; not finite if one of them is not.
+template <int LPR>
+__device__ __forceinline__ float largest_of(const float (&x)[4])
+{
+    uint32_t top = 0;                                      // f32 in the order of their bits, NaN the largest
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        top = max(top, __builtin_bit_cast(uint32_t, x[e]) & 0x7FFFFFFFu);
+    return __builtin_bit_cast(float, over_row<LPR>(top, [](uint32_t u, uint32_t v) { return u > v ? u : v; }));
+}
+template <int LPR>
+__device__ __forceinline__ double largest_of(const double (&x)[4])
+{
+    double top = 0.0, sound = 0.0;                         // 0 times what is not finite is NaN
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        top = fmax(top, fabs(x[e]));
+        sound = fma(x[e], 0.0, sound);
+    }
+    top = sound == sound ? top : (double)INFINITY;
+    return over_row<LPR>(top, [](double u, double v) { return fmax(u, v); });
+}
+
+// The scale of a row from its largest |value| (not finite, or beyond f32: NaN).  The product with f64's 1 / 127
+// rounds to the same f32 as the quotient of an f32: that is 2^-31 of itself from the middle of two f32 at least.
 template <int T, class R>
 __device__ __forceinline__ float scale_of(R amax)
 {
@@ -137,29 +158,25 @@ __device__ __forceinline__ uint32_t codes_of(const R (&x)[4], float d)
     const float inv = 1.0f / d;
     if constexpr (T == KV_I8) {
         int n[4];
-        bool near = false;
+        float off = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const float f = (float)x[e], q = __builtin_rintf(f * inv), r = fmaf(-q, d, f), two = fabsf(r + r);
-            const int up = r > 0.f ? 1 : -1;
+            const float u = (float)x[e] * inv, q = __builtin_rintf(u);
             n[e] = (int)q;
-            if constexpr (sizeof(R) == 4) {
-                if (two > d || (two == d && (n[e] & 1)))
-                    n[e] += up;
-            } else {
-                near |= fabsf(two - d) <= 0x1p-15f * d;   // f is off by 2^-24 |x|, 2^-17 d
-                if (two > d)
-                    n[e] += up;
-            }
+            off = fmaxf(off, fabsf(u - q));
         }
-        if constexpr (sizeof(R) == 8)
-            if (__any(near))
+        // u is off by three roundings, 3 * 2^-24 * 127 < 2^-14: so near to the middle of two codes the remainder
+        // of the nearer one decides, exact for an f32 (a multiple of half d's last bit not above d)
+        if (__any(off > 0.5f - 0x1p-14f))
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const double r = fma(-(double)n[e], (double)d, x[e]), two = fabs(r + r);
-                    if (two > d || (two == d && (n[e] & 1)))
-                        n[e] += r > 0.0 ? 1 : -1;
-                }
+            for (int e = 0; e < 4; ++e) {
+                const R r = fma_of(-(R)n[e], (R)d, x[e]), two = r + r;
+                const bool odd = n[e] & 1;
+                if (two > (R)d || (two == (R)d && odd))
+                    ++n[e];
+                else if (-two > (R)d || (-two == (R)d && odd))
+                    --n[e];
+            }
         return (uint32_t)(n[0] & 0xFF) | (uint32_t)(n[1] & 0xFF) << 8 | (uint32_t)(n[2] & 0xFF) << 16 |
                (uint32_t)n[3] << 24;
     } else {
@@ -229,49 +246,51 @@ __global__ __launch_bounds__(256) void k_qkv_append(QkvArgs a)
         }
     };
     const double inv_hd = 1.0 / c.hd;
-    struct Turn {
-        float c[4], s[4], gy[4], gz[4];                    // s with the sign that it has in the channel's sum
+    // of four channels: the weights of the norm, and the factors of a channel and its other one at a position
+    struct Weights {
+        float y[4], z[4];
     };
-    auto weights_of = [&](const float *gamma, Turn &u) {
+    auto weights_of = [&](const float *gamma) {
+        Weights g;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            u.gy[e] = u.gz[e] = 1.f;
+            g.y[e] = g.z[e] = 1.f;
         if (gamma) {
-            load(gamma, u.gy);
-            load_other(gamma, u.gz);
+            load(gamma, g.y);
+            load_other(gamma, g.z);
         }
+        return g;
     };
-    auto angles_of = [&](int t, Turn &u) {
+    auto factors_of = [&](int t, const Weights &g, auto &fy, auto &fz) {
+        typedef typename std::remove_reference<decltype(fy[0])>::type R;
         const int64_t at = (w.t0 + t) * a.half;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            u.c[e] = 1.f;
-            u.s[e] = 0.f;
-        }
+        float cs[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {};
         if constexpr (VEC) {
             if (other(0)) {
                 const int k = other(0) > 0 ? ch : ch - a.half;
-                load4(a.cos + at + k, u.c);
-                load4(a.sin + at + k, u.s);
+                load4(a.cos + at + k, cs);
+                load4(a.sin + at + k, sn);
             }
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 if (other(e)) {
                     const int k = ch + e + (other(e) > 0 ? 0 : other(e));
-                    u.c[e] = a.cos[at + k];
-                    u.s[e] = a.sin[at + k];
+                    cs[e] = a.cos[at + k];
+                    sn[e] = a.sin[at + k];
                 }
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            u.s[e] = other(e) > 0 ? -u.s[e] : u.s[e];
+        for (int e = 0; e < 4; ++e) {
+            fy[e] = (R)g.y[e] * (R)cs[e];
+            fz[e] = (R)g.z[e] * (R)(other(e) > 0 ? -sn[e] : sn[e]);
+        }
     };
     // a head's four channels y (z: those they are turned with), normalised and turned
-    auto turned = [&](const float (&y)[4], const float (&z)[4], const float *gamma, const Turn &u, auto &out) {
+    auto turned = [&](const float (&y)[4], const float (&z)[4], bool norm, const auto &fy, const auto &fz, auto &out) {
         typedef typename std::remove_reference<decltype(out[0])>::type R;
         R scale = (R)1;
-        if (gamma) {
+        if (norm) {
             R ss = (R)0;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -281,22 +300,20 @@ __global__ __launch_bounds__(256) void k_qkv_append(QkvArgs a)
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const R p = gamma ? (R)y[e] * (R)u.gy[e] : (R)y[e], v = gamma ? (R)z[e] * (R)u.gz[e] : (R)z[e];
-            const R r = fma_of(p, (R)u.c[e], v * (R)u.s[e]);
-            out[e] = gamma ? r * scale : r;
+            const R r = fma_of((R)y[e], fy[e], (R)z[e] * fz[e]);
+            out[e] = norm ? r * scale : r;
         }
     };
 
     if (role >= 2 * c.nkv) {                               // Q heads
         if constexpr (TURN) {
             const int h0 = (role - 2 * c.nkv) * Q_HEADS, heads = min(Q_HEADS, a.nq - h0);
-            Turn u;
-            weights_of(a.q_gamma, u);
+            const Weights g = weights_of(a.q_gamma);
             for (int t = from + row; t < to; t += ROWS) {
                 const float *src = a.q + (w.row0 + t) * a.stride + (int64_t)h0 * c.hd;
                 float *dst = a.qo + (w.row0 + t) * a.qo_stride + (int64_t)h0 * c.hd + ch;
-                float y[Q_HEADS][4] = {}, z[Q_HEADS][4] = {};
-                angles_of(t, u);
+                float y[Q_HEADS][4] = {}, z[Q_HEADS][4] = {}, fy[4], fz[4];
+                factors_of(t, g, fy, fz);
 #pragma unroll
                 for (int h = 0; h < Q_HEADS; ++h)
                     if (h < heads) {
@@ -307,7 +324,7 @@ __global__ __launch_bounds__(256) void k_qkv_append(QkvArgs a)
                 for (int h = 0; h < Q_HEADS; ++h)
                     if (h < heads) {
                         float r[4];
-                        turned(y[h], z[h], a.q_gamma, u, r);
+                        turned(y[h], z[h], a.q_gamma != nullptr, fy, fz, r);
                         if (in)
                             *reinterpret_cast<float4 *>(dst + h * c.hd) = make_float4(r[0], r[1], r[2], r[3]);
                     }
@@ -328,9 +345,7 @@ __global__ __launch_bounds__(256) void k_qkv_append(QkvArgs a)
     const int64_t codes = (int64_t)c.hd << c.ps_log2;      // elements before an 8-bit block's scales
 
     if (!is_v) {                                           // K: a row's codes lie side by side
-        Turn u;
-        if constexpr (TURN)
-            weights_of(a.k_gamma, u);
+        const Weights g = weights_of(TURN ? a.k_gamma : nullptr);
         for (int t = from + row; t < to; t += ROWS) {
             const float *src = a.k + (w.row0 + t) * a.stride + (int64_t)h * c.hd;
             float y[4] = {};
@@ -338,9 +353,10 @@ __global__ __launch_bounds__(256) void k_qkv_append(QkvArgs a)
             load(src, y);
             if constexpr (TURN) {
                 float z[4] = {};
+                RK fy[4], fz[4];
                 load_other(src, z);
-                angles_of(t, u);
-                turned(y, z, a.k_gamma, u, x);
+                factors_of(t, g, fy, fz);
+                turned(y, z, a.k_gamma != nullptr, fy, fz, x);
             } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
@@ -348,14 +364,7 @@ __global__ __launch_bounds__(256) void k_qkv_append(QkvArgs a)
             }
             const int64_t at = base + (int64_t)(slot + t) * c.hd + ch;
             if constexpr (SIZE == 1) {
-                RK top = 0;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const RK v = x[e] < 0 ? -x[e] : x[e];
-                    top = v <= top ? top : v <= (RK)FLT_MAX ? v : (RK)INFINITY;
-                }
-                top = over_row<LPR>(top, [](RK u, RK v) { return __builtin_elementwise_max(u, v); });
-                const float d = scale_of<T>(top);
+                const float d = scale_of<T>(largest_of<LPR>(x));
                 if (in)
                     *reinterpret_cast<uint32_t *>(c.k8() + at) = codes_of<T>(x, d);
                 if (j == 0)
@@ -375,12 +384,7 @@ __global__ __launch_bounds__(256) void k_qkv_append(QkvArgs a)
         float x[4] = {};
         load(a.v + (w.row0 + t) * a.stride + (int64_t)h * c.hd, x);
         if constexpr (SIZE == 1) {
-            float top = 0.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                top = fabsf(x[e]) <= top ? top : fabsf(x[e]) <= FLT_MAX ? fabsf(x[e]) : INFINITY;
-            top = over_row<LPR>(top, [](float u, float v) { return fmaxf(u, v); });
-            const float d = scale_of<T>(top);
+            const float d = scale_of<T>(largest_of<LPR>(x));
             const uint32_t v = codes_of<T>(x, d);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
