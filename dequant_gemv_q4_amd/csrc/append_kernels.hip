@@ -325,8 +325,9 @@ __global__ __launch_bounds__(256) void k_qkv_append(QkvArgs a)
                     if (h < heads) {
                         float r[4];
                         turned(y[h], z[h], a.q_gamma != nullptr, fy, fz, r);
-                        if (in)
-                            *reinterpret_cast<float4 *>(dst + h * c.hd) = make_float4(r[0], r[1], r[2], r[3]);
+                        if (in)                           // (written past the L2: 84.7 -> 81.9 us)
+                            __builtin_nontemporal_store(af4{r[0], r[1], r[2], r[3]},
+                                                        reinterpret_cast<af4 *>(dst + h * c.hd));
                     }
             }
         }
