@@ -28,32 +28,41 @@ static bool heads_ok(int nq, int nkv, int hd)
     return nkv >= 1 && nq >= nkv && nq % nkv == 0 && head_dim_ok(hd) && nq <= 4096;
 }
 
-// Workspace: the sticky flag (256 bytes) and the arrival counters of a split joined in its launch, at the same
-// place for every operation (the counters are 0 between calls and must stay so when operations share
-// a workspace), then the partial results of a split.
-static constexpr int64_t WS_COUNT = 256, WS_PART = WS_COUNT + ATTN_MAX_SLOTS * 4;
+// Workspace: the sticky flag (256 bytes) and the arrival counters (of a split joined in its launch, of one behind
+// a shared prefix, and of a row's halves), at the same place for every operation (the counters are 0 between calls
+// and must stay so when operations share a workspace), then what an operation writes before it reads.
+static constexpr int64_t WS_COUNT = 256, WS_TAIL = WS_COUNT + ATTN_MAX_SLOTS * 4;
+static constexpr int64_t WS_MEET = WS_TAIL + ATTN_MAX_SLOTS * 4, WS_PART = WS_MEET + MEET_MOST * 4;
 // qgemv_attn_prompt's part of it begins with its pair count and its split tiles (32 bytes each).
 static constexpr int64_t WS_SPLITS = 256 + PROMPT_SPLITS * 32;
 
-// Partial results of a split.
-static int64_t part_bytes(int op, int nq, int nkv, int hd)
+static int64_t rounded_up(int64_t bytes) { return (bytes + 255) / 256 * 256; }
+
+// Partial results of a split over 16-column and over 128-column tiles.
+static int64_t parts_16(int nq, int nkv, int hd)
 {
     const int group = nq / nkv;
-    if (op == QG_OP_ATTN)
-        return (attn_slots(hd) * attn_part_floats(group < 16 ? group : 16, hd) * 4 + 255) / 256 * 256;
-    return WS_SPLITS + (int64_t)prompt_slots(hd) * 128 * (hd + 2) * 4;         // 128 columns a tile
+    return rounded_up(attn_slots(hd) * attn_part_floats(group < 16 ? group : 16, hd) * 4);
 }
+static int64_t parts_128(int hd) { return WS_SPLITS + (int64_t)prompt_slots(hd) * 128 * (hd + 2) * 4; }
 
-// qgemv_attn_shared: an exponent and a sum of each row and head before them.
-static int64_t stats_bytes(int n_seq, int nq) { return ((int64_t)n_seq * nq * 8 + 255) / 256 * 256; }
+// qgemv_attn_shared: exponents and sums of both halves, and their means where they meet in one launch.
+static int64_t stats_bytes(int n_seq, int nq) { return rounded_up((int64_t)n_seq * nq * 2 * 8); }
+static int64_t means_bytes(int n_seq, int nq, int hd)
+{
+    const int64_t rows = (int64_t)n_seq * nq;
+    return rows > MEET_MOST ? 0 : rounded_up(rows * hd * 2 * 4);
+}
 
 static int64_t ws_bytes_of(int op, int n_seq, int nq, int nkv, int hd)
 {
-    if (op == QG_OP_ATTN || op == QG_OP_ATTN_PROMPT)
-        return WS_PART + part_bytes(op, nq, nkv, hd);
-    if (op == QG_OP_ATTN_SHARED)
-        return WS_PART + stats_bytes(n_seq, nq) + part_bytes(QG_OP_ATTN_PROMPT, nq, nkv, hd);
-    return WS_PART;
+    switch (op) {
+    case QG_OP_ATTN: return WS_PART + parts_16(nq, nkv, hd);
+    case QG_OP_ATTN_PROMPT: return WS_PART + parts_128(hd);
+    case QG_OP_ATTN_SHARED:
+        return WS_PART + stats_bytes(n_seq, nq) + means_bytes(n_seq, nq, hd) + parts_16(nq, nkv, hd) + parts_128(hd);
+    default: return WS_TAIL;
+    }
 }
 
 struct Span {
@@ -188,13 +197,21 @@ static int run_attn(int op, int kv_type, const void *k_pages, const void *v_page
         return QG_ERR_ALIAS;
     a.c.err = static_cast<unsigned int *>(ws);
     a.count = reinterpret_cast<unsigned int *>(static_cast<uint8_t *>(ws) + WS_COUNT);
-    uint8_t *part = static_cast<uint8_t *>(ws) + WS_PART;
-    a.stats = reinterpret_cast<float *>(part);
-    if (shared)
+    uint8_t *const w = static_cast<uint8_t *>(ws), *part = w + WS_PART;
+    if (shared) {
+        a.meet = reinterpret_cast<unsigned int *>(w + WS_MEET);
+        a.tail_count = reinterpret_cast<unsigned int *>(w + WS_TAIL);
+        a.stats = reinterpret_cast<float *>(part);
         part += stats_bytes(n_seq, nq);
+        a.means = reinterpret_cast<float *>(part);
+        part += means_bytes(n_seq, nq, hd);
+        a.tail_part = reinterpret_cast<float *>(part);
+        part += parts_16(nq, nkv, hd);
+    }
     a.pairs = reinterpret_cast<int *>(part);
     a.splits = reinterpret_cast<PromptSplit *>(part + 256);
     a.part = reinterpret_cast<float *>(prompt || shared ? part + WS_SPLITS : part);
+    a.rows_in_all = n_seq;
     a.q = q;
     a.q_stride = q_stride;
     a.o = o;

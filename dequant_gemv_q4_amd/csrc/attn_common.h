@@ -305,8 +305,10 @@ __device__ __forceinline__ int seq_len(const KvArgs &c, int b) { return placed(c
 
 // What a workgroup of the attention kernels attends to: one new row of each sequence (ONE), several (MANY),
 // or for sequences that begin alike the shared positions for all rows of a group (PREFIX: the plan's
-// sequences are the groups, with q_start their first sequences) and those behind them (SUFFIX).
-enum AttnForm { ONE, MANY, PREFIX, SUFFIX };
+// sequences are the groups, with q_start their first sequences) and those behind them (SUFFIX; TAIL: means to
+// o, exponents and sums to stats, for a later launch to join).
+enum AttnForm { ONE, MANY, PREFIX, SUFFIX, TAIL };
+constexpr bool behind(int form) { return form == SUFFIX || form == TAIL; }
 
 // Shared positions of sequence b: none outside the groups.
 __device__ __forceinline__ int shared_of(const AttnArgs &a, int b)
@@ -316,7 +318,7 @@ __device__ __forceinline__ int shared_of(const AttnArgs &a, int b)
     const int n = a.shared_len[b], cap = a.c.max_pages << a.c.ps_log2;
     return n < 0 ? 0 : n < cap ? n : cap;
 }
-// SUFFIX: the plan counts from the last multiple of 16 in the shared positions.
+// SUFFIX, TAIL: the plan counts from the last multiple of 16 in the shared positions.
 __device__ __forceinline__ int suffix_base(int shared) { return shared & ~15; }
 
 // Positions that the plan counts of its sequence b, whose rows begin with row0.
@@ -325,7 +327,7 @@ __device__ __forceinline__ int plan_len(const AttnArgs &a, int b, int row0, int 
 {
     if constexpr (FORM == PREFIX) {
         return rows > 0 ? placed(a.c, a.shared_len[row0]) : 0;
-    } else if constexpr (FORM == SUFFIX) {
+    } else if constexpr (behind(FORM)) {
         const int n = seq_len(a.c, b), s = shared_of(a, b);
         return n > s ? n - suffix_base(s) : 0;
     } else {

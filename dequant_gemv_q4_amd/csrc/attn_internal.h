@@ -19,6 +19,8 @@ __host__ __device__ constexpr int attn_slots(int hd) { return hd <= 128 ? 512 : 
 __host__ __device__ constexpr int64_t attn_part_floats(int cols, int hd) { return (int64_t)cols * (hd + 2); }
 // The same of qgemv_attn_prompt's 128-column tiles, and the most pairs of a call that may be split.
 #define PROMPT_SLOTS 512
+// Rows times KV heads (and times query heads) of a call whose halves meet in one launch, at most.
+#define MEET_MOST (16 * ATTN_MAX_SLOTS)
 #define PROMPT_SPLITS 1024
 __host__ __device__ constexpr int prompt_slots(int hd) { return hd <= 128 ? PROMPT_SLOTS : 256; }
 
@@ -78,7 +80,11 @@ struct AttnArgs {
     const int32_t *group_start; // groups of sequences that begin alike [n_group + 1], or NULL
     const int32_t *shared_len;  // [n_seq]
     int n_group;
-    float *stats;               // workspace: exponent and sum of each row and head over the shared positions
+    int rows_in_all;            // sequences
+    // workspace of a shared prefix: means [2][rows][nq * hd] and exponents and sums [2][rows][nq][2] of the halves,
+    // arrivals at each row's KV heads (0 between calls), parts and counters of a split behind the prefix
+    float *means, *stats, *tail_part;
+    unsigned int *meet, *tail_count;
     unsigned int *count;        // workspace: arrival counters of a split, one per slot, 0 between calls
     int nq, group;              // query heads; query heads per KV head
     int side;                   // set by the launcher: tiles that read the same positions
@@ -109,12 +115,13 @@ int launch_kv_append(int kv_type, const AppendArgs &a, void *stream);
 int launch_qkv_append(int kv_type, bool turn, const QkvArgs &a, void *stream);
 int launch_attn8(int kv_type, const AttnArgs &a, void *stream);
 int launch_attn8_rows(int kv_type, const AttnArgs &a, void *stream);    // few rows per sequence
-// Of qgemv_attn_shared: the shared positions of all groups (means to o, exponents and sums to stats), by
-// 16-column or 128-column tiles; then what is behind them, joined with that.
-int launch_attn_prefix(int kv_type, const AttnArgs &a, void *stream);
-int launch_attn8_prefix(int kv_type, const AttnArgs &a, void *stream);
-int launch_attn_suffix(int kv_type, const AttnArgs &a, void *stream);
-int launch_attn8_suffix(int kv_type, const AttnArgs &a, void *stream);
+// How a batch with shared prefixes is taken: by 16-column tiles in one launch; the shared positions by 128-column
+// tiles, fewer than slots (beside what is behind them, joined by a second launch) or as many (behind a launch for
+// the others, the longest split if the table holds more than a chunk, or whole).
+enum SharedForm { SHARED_16, SHARED_PARTED, SHARED_FEW, SHARED_WHOLE };
+SharedForm shared_form(int64_t n_seq, int n_group, int nq, int nkv, int hd, int64_t positions);
+int launch_shared_16(int kv_type, const AttnArgs &a, void *stream);
+int launch_shared_128(int kv_type, const AttnArgs &a, void *stream);
 int launch_attn_shared(int kv_type, const AttnArgs &a, void *stream);
 int launch_attn(int kv_type, const AttnArgs &a, void *stream);
 int launch_attn_rows(int kv_type, const AttnArgs &a, void *stream);     // few rows per sequence

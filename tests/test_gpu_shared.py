@@ -1,5 +1,7 @@
 """Attention of a batch whose sequences begin alike, on the GPU, against the definition in 64 bits with each
 sequence's positions spelled out (kv_common)."""
+import ctypes
+
 import numpy as np
 import pytest
 
@@ -94,6 +96,42 @@ def test_shared_small(kv_type, nq, nkv, hd, page):
 ])
 def test_shared_long(kv_type, nq, nkv, hd, page, groups):
     shared(kv_type, nq, nkv, hd, page, groups, len(groups))
+
+
+def form_of(n_seq, n_group, nq, nkv, hd, positions):
+    """Which kernels take the call (the launcher's own choice): 16-column tiles, 128-column tiles with parts, split
+    few among many, or whole."""
+    fn = ctypes.CDLL(q.LIB_PATH)["_ZN2qg11shared_formEliiiil"]
+    fn.restype = ctypes.c_int
+    fn.argtypes = [ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int64]
+    return ["16", "parted", "few", "whole"][fn(n_seq, n_group, nq, nkv, hd, positions)]
+
+
+@pytest.mark.parametrize("kv_type", ALL)
+@pytest.mark.parametrize("form,nq,nkv,hd,page,groups,outside", [
+    ("parted", 12, 2, 128, 16, [[(1003, 30 + i % 9) for i in range(70)], [(77, 900), (70, 3)] * 40], (1, 2)),
+    ("parted", 16, 1, 64, 32, [[(2000, 1 + 7 * i % 40) for i in range(49)]], (0, 0)),
+    ("parted", 5, 1, 96, 16, [[(1500, 20)] * 160], (0, 0)),
+    ("parted", 20, 1, 64, 16, [[(40, 3)] * 30 + [(17, 1500)], [(5, 1)] * 20], (3, 0)),
+    ("parted", 4, 1, 256, 64, [[(1300, 9)] * 99], (0, 1)),
+    ("few", 16, 16, 64, 16, [[(int(20 + 9 * i), i % 5), (int(20 + 9 * i), 2)] for i in range(33)] + [[(3000, 5)] * 3], (1, 1)),
+    ("few", 8, 4, 256, 32, [[(70, 4)] * 2 for _ in range(63)] + [[(1900, 40), (1900, 1)]], (0, 0)),
+    ("whole", 16, 16, 64, 16, [[(int(9 + 5 * i), i % 7)] * 2 for i in range(34)], (2, 0)),
+])
+def test_shared_by_128_columns(kv_type, form, nq, nkv, hd, page, groups, outside):
+    """Groups of more rows than 16-column tiles take, and more groups than workgroup slots."""
+    n = sum(len(g) for g in groups) + sum(outside)
+    lens = [s + a for g in groups for s, a in g] + [17 + 30 * i for i in range(outside[0])] + [41] * outside[1]
+    positions = (-(-max(lens) // page) + 2) * page
+    assert form_of(n, len(groups), nq, nkv, hd, positions) == form
+    shared(kv_type, nq, nkv, hd, page, groups, 11, outside=outside)
+
+
+def test_shared_behind_the_prefix_split_among_many():
+    """As many sequences as slots, one of them long behind its prefix; and few of them, all split."""
+    shared(q.F16, 8, 8, 64, 16, [[(30, 20)] * 65 + [(30, 3000)]], 12)
+    shared(q.I8, 8, 8, 64, 16, [[(30, 20)] * 65 + [(30, 3000)]], 12)
+    shared(q.F8, 16, 1, 64, 16, [[(1200, 3)] * 30 + [(1200, 2500)]], 13)
 
 
 @pytest.mark.parametrize("kv_type", [q.F16, q.F8])
