@@ -19,6 +19,12 @@ __host__ __device__ constexpr int attn_slots(int hd) { return hd <= 128 ? 512 : 
 __host__ __device__ constexpr int64_t attn_part_floats(int cols, int hd) { return (int64_t)cols * (hd + 2); }
 // The same of qgemv_attn_prompt's 128-column tiles, and the most pairs of a call that may be split.
 #define PROMPT_SLOTS 512
+// Workgroups of a shared prefix in parts, one per compute unit: the other half of a unit is for what is behind the
+// prefix.  64 sequences behind 30000 positions, 32 / 8 heads of 128, f16: 105 us, with two per unit 117 to 133 by the
+// order of the workgroups, with 384 111; with hardly anything behind it 89.5 and 90 (fewer parts to join).  8-bit
+// codes are converted on the way, so that there a unit wants more: I8 140, with 384 125, with 512 128.
+#define SHARED_SLOTS 256
+#define SHARED_SLOTS_8 384
 // Rows times KV heads (and times query heads) of a call whose halves meet in one launch, at most.
 #define MEET_MOST (16 * ATTN_MAX_SLOTS)
 #define PROMPT_SPLITS 1024
@@ -119,7 +125,7 @@ int launch_attn8_rows(int kv_type, const AttnArgs &a, void *stream);    // few r
 // tiles, fewer than slots (beside what is behind them, joined by a second launch) or as many (behind a launch for
 // the others, the longest split if the table holds more than a chunk, or whole).
 enum SharedForm { SHARED_16, SHARED_PARTED, SHARED_FEW, SHARED_WHOLE };
-SharedForm shared_form(int64_t n_seq, int n_group, int nq, int nkv, int hd, int64_t positions);
+SharedForm shared_form(int kv_type, int64_t n_seq, int n_group, int nq, int nkv, int hd, int64_t positions);
 int launch_shared_16(int kv_type, const AttnArgs &a, void *stream);
 int launch_shared_128(int kv_type, const AttnArgs &a, void *stream);
 int launch_attn_shared(int kv_type, const AttnArgs &a, void *stream);

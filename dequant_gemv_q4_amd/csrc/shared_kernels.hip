@@ -7,22 +7,22 @@
 
 namespace qg {
 
-// The first `lead` workgroups take the shared positions (g: the groups as sequences of rows), the others what is
-// behind them.
+// The first `lead` workgroups take the shared positions (g: the groups as sequences of rows; `first` slots for a
+// split), the others what is behind them (`slots`).
 template <int T, int D>
-__global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_shared_16(AttnArgs a, AttnArgs g, int lead, int slots)
+__global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_shared_16(AttnArgs a, AttnArgs g, int lead, int first, int slots)
 {
     const int id = blockIdx.x, behind_them = (int)gridDim.x - lead;
     if constexpr (kv_bytes(T)) {
         __shared__ Attn8Lds<T, D> sh;
         if (id < lead)
-            attn8_body<T, D, PREFIX, true>(g, lead, id, lead, sh);
+            attn8_body<T, D, PREFIX, true>(g, first, id, lead, sh);
         else
             attn8_body<T, D, SUFFIX, false>(a, slots, id - lead, behind_them, sh);
     } else {
         __shared__ AttnLds<T, D> sh;
         if (id < lead)
-            attn_body<T, D, PREFIX, true>(g, lead, id, lead, sh);
+            attn_body<T, D, PREFIX, true>(g, first, id, lead, sh);
         else
             attn_body<T, D, SUFFIX, false>(a, slots, id - lead, behind_them, sh);
     }
@@ -37,26 +37,36 @@ static AttnArgs groups_of(const AttnArgs &a)
     return g;
 }
 
-SharedForm shared_form(int64_t n_seq, int n_group, int nq, int nkv, int hd, int64_t positions)
+// The 16-column tiles read a prefix once per 16 columns, the 128-column ones leave parts for a second launch and
+// fill their tiles less.  By the work, columns times positions times channels of all heads, at most: over f16 and
+// bf16 pages 5e8, over 8-bit pages, whose codes the 128-column tiles convert through LDS, 4e9.  16 -> 128 columns,
+// us, 128 channels: f16, 64 sequences, 32 / 8 heads, behind 1500 positions (4e8) 33.9 -> 36.4, behind 4000 (1.1e9)
+// 44.3 -> 37.1, 30000 (7.9e9) 181 -> 90; 12 / 2 heads behind 4000 (4e8) 34.0 -> 33.3, 10000 (1e9) 50.9 -> 36.6;
+// bf16, 150 of 16 / 1 behind 2500 (8e8) 47.9 -> 43.1; I8, 64 of 12 / 2 behind 30000 (3e9) 71.0 -> 74.1, 256 behind
+// 10000 (4e9) 89.2 -> 79.9, 64 of 32 / 8 behind 30000 (7.9e9) 128 -> 124, but 200 behind 10000 (8.3e9) 101 -> 143.
+SharedForm shared_form(int kv_type, int64_t n_seq, int n_group, int nq, int nkv, int hd, int64_t positions)
 {
-    if (n_seq * nq <= MEET_MOST && prompt_in_16s(n_seq, n_group, nq, nkv, hd, positions))
+    const double work = (double)(n_seq * nq) * hd * positions;
+    if (n_seq * nq <= MEET_MOST && work <= (kv_bytes(kv_type) ? 4e9 : 5e8))
         return SHARED_16;
     const PromptPlan p = plan_prompt(n_seq, n_group, nkv, nq / nkv, hd, positions);
-    return p.pairs < prompt_slots(hd) ? SHARED_PARTED : p.slots ? SHARED_FEW : SHARED_WHOLE;
+    return p.pairs < SHARED_SLOTS ? SHARED_PARTED : p.slots ? SHARED_FEW : SHARED_WHOLE;
 }
 
 int launch_shared_16(int kv_type, const AttnArgs &a, void *stream)
 {
-    // slots for either half: what is behind the prefix takes what it can fill, up to a half
+    // slots for either half: what is behind the prefix takes what it can fill, up to a half.  As many pairs as slots:
+    // each has a workgroup, and those that are split as many more as there are slots
     const int all = attn_slots(a.c.hd);
-    const int64_t pairs = (int64_t)a.c.n_seq * a.c.nkv * ((a.group + 15) / 16);
-    const int slots = (int)(pairs < all / 2 ? pairs : all / 2), lead = all - slots;
     const int64_t table = (int64_t)a.c.max_pages << a.c.ps_log2;
     const bool split = table > (kv_bytes(kv_type) ? Attn8Cols::SOLO << Attn8Cols::UNIT_LOG2
                                                   : AttnCols::SOLO << AttnCols::UNIT_LOG2);
-    const int64_t grid = lead + pairs + (split ? slots : 0);
+    auto grid_of = [=](int64_t pairs, int slots) { return pairs < slots ? slots : pairs + (split ? slots : 0); };
+    const int64_t pairs = (int64_t)a.c.n_seq * a.c.nkv * ((a.group + 15) / 16);
+    const int slots = (int)(pairs < all / 2 ? pairs : all / 2), first = all - slots;
+    const int64_t lead = grid_of(a.c.nkv * (a.c.n_rows * a.group / 16 + a.n_group), first);
     const AttnArgs g = groups_of(a);
-    void (*k)(AttnArgs, AttnArgs, int, int) = nullptr;
+    void (*k)(AttnArgs, AttnArgs, int, int, int) = nullptr;
 #define QG_SHARED_D(DD)                               \
     k = kv_type == KV_F16    ? k_shared_16<KV_F16, DD>  \
         : kv_type == KV_BF16 ? k_shared_16<KV_BF16, DD> \
@@ -70,14 +80,15 @@ int launch_shared_16(int kv_type, const AttnArgs &a, void *stream)
     default: QG_SHARED_D(256); break;
     }
 #undef QG_SHARED_D
-    hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(256), 0, static_cast<hipStream_t>(stream), a, g, lead, slots);
+    hipLaunchKernelGGL(k, dim3((unsigned)(lead + grid_of(pairs, slots))), dim3(256), 0, static_cast<hipStream_t>(stream),
+                       a, g, (int)lead, first, slots);
     return (int)hipGetLastError();
 }
 
 int launch_attn_shared(int kv_type, const AttnArgs &a, void *stream)
 {
     const int64_t table = (int64_t)a.c.max_pages << a.c.ps_log2;
-    return shared_form(a.c.n_seq, a.n_group, a.nq, a.c.nkv, a.c.hd, table) == SHARED_16
+    return shared_form(kv_type, a.c.n_seq, a.n_group, a.nq, a.c.nkv, a.c.hd, table) == SHARED_16
                ? launch_shared_16(kv_type, a, stream)
                : launch_shared_128(kv_type, a, stream);
 }

@@ -41,18 +41,17 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_shared_tiles(AttnArgs
     prompt_body<T, D, FEW, JOINED>(g, slots, blockIdx.x, sh);
 }
 
-// Fewer tiles than slots: their parts and what is behind the prefix side by side.  Workgroups [0, lead) and those
-// behind `tails` more take the parts.
+// Fewer tiles than slots: their parts (the first `slots` workgroups) and what is behind the prefix side by side.
 template <int T, int D>
-__global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_shared_128(AttnArgs a, AttnArgs g, int slots, int lead, int tails)
+__global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_shared_128(AttnArgs a, AttnArgs g, int slots)
 {
     constexpr size_t BYTES = sizeof(PromptLds<T, D>) > tail_lds<T, D>() ? sizeof(PromptLds<T, D>) : tail_lds<T, D>();
     __shared__ __attribute__((aligned(1024))) uint8_t lds[BYTES];
     const int id = blockIdx.x;
-    if (id >= lead && id < lead + tails)
-        tail_body<T, D>(a, id - lead, tails, lds);
+    if (id < slots)
+        prompt_body<T, D, false, PARTED>(g, slots, id, *reinterpret_cast<PromptLds<T, D> *>(lds));
     else
-        prompt_body<T, D, false, PARTED>(g, slots, id < lead ? id : id - tails, *reinterpret_cast<PromptLds<T, D> *>(lds));
+        tail_body<T, D>(a, id - slots, (int)gridDim.x - slots, lds);
 }
 
 int launch_shared_128(int kv_type, const AttnArgs &a, void *stream)
@@ -68,10 +67,9 @@ int launch_shared_128(int kv_type, const AttnArgs &a, void *stream)
     const int all = attn_slots(a.c.hd);
     const bool split = table > (bytes ? Attn8Cols::SOLO << Attn8Cols::UNIT_LOG2 : AttnCols::SOLO << AttnCols::UNIT_LOG2);
     const int64_t tails = pairs < all ? (split ? all : pairs) : split ? pairs + all : pairs;
-    const int slots = prompt_slots(a.c.hd);
-    const SharedForm form = shared_form(a.c.n_seq, a.n_group, a.nq, a.c.nkv, a.c.hd, table);
+    const SharedForm form = shared_form(kv_type, a.c.n_seq, a.n_group, a.nq, a.c.nkv, a.c.hd, table);
     if (form == SHARED_PARTED) {
-        void (*k)(AttnArgs, AttnArgs, int, int, int) = nullptr;
+        void (*k)(AttnArgs, AttnArgs, int) = nullptr;
 #define QG_SHARED_D(DD)                                  \
     k = kv_type == KV_F16    ? k_shared_128<KV_F16, DD>  \
         : kv_type == KV_BF16 ? k_shared_128<KV_BF16, DD> \
@@ -85,8 +83,8 @@ int launch_shared_128(int kv_type, const AttnArgs &a, void *stream)
         default: QG_SHARED_D(256); break;
         }
 #undef QG_SHARED_D
-        const int lead = slots / 2;
-        hipLaunchKernelGGL(k, dim3((unsigned)(slots + tails)), dim3(256), 0, s, a, g, slots, lead, (int)tails);
+        const int slots = bytes && a.c.hd <= 128 ? SHARED_SLOTS_8 : SHARED_SLOTS;
+        hipLaunchKernelGGL(k, dim3((unsigned)(slots + tails)), dim3(256), 0, s, a, g, slots);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess)
             return (int)e;

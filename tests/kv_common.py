@@ -14,7 +14,7 @@ from __future__ import annotations
 import numpy as np
 
 from gpu_common import q, torch
-from attn_common import TORCH, U, attention64
+from attn_common import TORCH, U
 
 LEFT = {q.F16: 2.0 ** -22, q.BF16: 2.0 ** -18, q.I8: 2.0 ** -22, q.F8: 2.0 ** -22}
 NAMES = {q.F16: "f16", q.BF16: "bf16", q.I8: "i8", q.F8: "f8"}
@@ -151,21 +151,27 @@ class Cache:
         return x[slot], d
 
 
-def attention_row(qr, K, V, nkv, scale, last):
-    return attention64(qr, K, V, nkv, scale, last)
-
-
-def lost64(qr, K, dV, nkv, scale, last, kv_type):
-    """B of the module's text for one row: [nq][1]; dV [len][nkv] the scales of V."""
-    nq = len(qr)
-    B = np.zeros((nq, 1))
-    if kv_type not in BYTES or last < 0:
-        return B
-    for h in range(nq):
-        s = scale * (K[:last + 1, h // (nq // nkv)].astype(np.float64) @ qr[h].astype(np.float64))
-        total = np.exp(s - s.max()).sum()
-        B[h] = (last + 1) * 2.0 ** -35 * dV[:last + 1, h // (nq // nkv)].max() * CODES[kv_type] / total
-    return B
+def parts64(qr, K, V, dV, nkv, scale, last, kv_type):
+    """One row's attention in f64: qr [nq][hd], K, V [len][nkv][hd] as the cache holds them, dV [len][nkv] the
+    scales of V, positions 0..last.  Returns o and A [nq][hd], S and B [nq][1] of the module's text."""
+    nq, hd = qr.shape
+    o, A, S, B = np.zeros((nq, hd)), np.zeros((nq, hd)), np.zeros((nq, 1)), np.zeros((nq, 1))
+    if last < 0:
+        return o, A, S, B
+    n, g = last + 1, nq // nkv
+    for h in range(nkv):
+        rows = slice(h * g, (h + 1) * g)
+        x = qr[rows].astype(np.float64)
+        k, v = K[:n, h].astype(np.float64), V[:n, h].astype(np.float64)
+        s = scale * (x @ k.T)
+        w = np.exp(s - s.max(axis=1, keepdims=True))
+        total = w.sum(axis=1, keepdims=True)
+        p = w / total
+        o[rows], A[rows] = p @ v, p @ np.abs(v)
+        S[rows] = abs(scale) * (np.abs(x) @ np.abs(k).T).max(axis=1, keepdims=True)
+        if kv_type in BYTES:
+            B[rows] = n * 2.0 ** -35 * dV[:n, h].max() * CODES[kv_type] / total
+    return o, A, S, B
 
 
 def check_rows(got, parts, n, hd, kv_type, what):

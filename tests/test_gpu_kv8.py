@@ -7,7 +7,7 @@ from gpu_common import dev, host, require_gpu, say, torch
 
 import dequant_gemv_q4_amd as q
 from dequant_gemv_q4_amd import device as D
-from kv_common import ALL, BYTES, Cache, attention_row, check_rows, codes64, held, lost64, quantised, scales64
+from kv_common import ALL, BYTES, Cache, as_bytes, check_rows, codes64, held, parts64, quantised, scales64
 
 pytestmark = pytest.mark.gpu
 
@@ -56,7 +56,6 @@ def _expect(before, c, seqs, table, K, V, nkv):
                         body = body[:, slot] if turned else body[slot]
                         if c.kv_type in BYTES:
                             codes, d = quantised(rows[r + i, h], c.kv_type)
-                            from kv_common import as_bytes
                             body[:] = as_bytes(codes, c.kv_type)
                             blk[page * hd + 4 * slot:page * hd + 4 * slot + 4] = np.frombuffer(d.tobytes(), np.uint8)
                         else:
@@ -316,11 +315,6 @@ def _draw(rng, lens, nkv, hd, spread=1.0):
     return out
 
 
-def _parts(qr, K, V, dV, nkv, scale, last, kv_type):
-    o, A, S = attention_row(qr, K, V, nkv, scale, last)
-    return o, A, S, lost64(qr, K, dV, nkv, scale, last, kv_type)
-
-
 def attend(kv_type, nq, nkv, hd, page, seqs, seed=0, prompt=True, scale=None, qmul=1.0, extra_entries=2, tail=0,
            gap=0, bad_entry=-1, spread=1.0, K=None, V=None, ws=None):
     """seqs: (new rows, cached positions with them); not prompt: one row each by qgemv_attn."""
@@ -351,7 +345,7 @@ def attend(kv_type, nq, nkv, hd, page, seqs, seed=0, prompt=True, scale=None, qm
         dv = scales64(V[b], kv_type) if kv_type in BYTES and len(V[b]) else np.ones(V[b].shape[:2])
         for i in range(a):
             last = n - a + i
-            parts.append(_parts(x[start[b] + i, :nq * hd].reshape(nq, hd), hk, hv, dv, nkv, scale, last, kv_type))
+            parts.append(parts64(x[start[b] + i, :nq * hd].reshape(nq, hd), hk, hv, dv, nkv, scale, last, kv_type))
             seen.append(max(0, last + 1))
     if parts:
         check_rows(got[:start[-1]], parts, seen, hd, kv_type, "attention")
@@ -489,8 +483,8 @@ def test_non_finite_rows_reach_only_the_rows_that_see_them(kv_type, where):
             sees = last >= at
             assert np.isnan(got[i, 2:]).all() == sees and np.isfinite(got[i, :2]).all()
             if not sees or i % 16 == 0:
-                o64, A, _ = attention_row(x[i].reshape(nq, hd), held(clean[0], kv_type), held(clean[1], kv_type), nkv,
-                                          0.125, last)
+                o64, A, _, _ = parts64(x[i].reshape(nq, hd), held(clean[0], kv_type), held(clean[1], kv_type),
+                                       scales64(clean[1], kv_type), nkv, 0.125, last, kv_type)
                 good = slice(None) if not sees else slice(0, 2)
                 assert (np.abs(got[i, good] - o64[good]) <= 1e-4 * A[good] + 1e-9).all()
         assert np.isfinite(got[start[1]:]).all()
@@ -516,7 +510,7 @@ def test_attention8_bad_pages_are_left_out(kv_type):
     parts = []
     for b in range(3):
         k, v = K[b][keep[b]], V[b][keep[b]]
-        parts.append(_parts(x[b].reshape(nq, hd), held(k, kv_type), held(v, kv_type), scales64(v, kv_type), nkv, 0.125,
+        parts.append(parts64(x[b].reshape(nq, hd), held(k, kv_type), held(v, kv_type), scales64(v, kv_type), nkv, 0.125,
                             len(k) - 1, kv_type))
     for prompt in (False, True):
         o = torch.full((3, nq * hd), float("nan"), device="cuda")
@@ -545,7 +539,7 @@ def test_pages_beyond_32_bits(kv_type):
                       2 * hd, n, ws)
     K, V = rows[:, None, :hd], rows[:, None, hd:]
     x = rng.standard_normal((1, nq * hd)).astype(np.float32)
-    part = _parts(x.reshape(nq, hd), held(K, kv_type), held(V, kv_type), scales64(V, kv_type), 1, 0.1, n - 1, kv_type)
+    part = parts64(x.reshape(nq, hd), held(K, kv_type), held(V, kv_type), scales64(V, kv_type), 1, 0.1, n - 1, kv_type)
     for prompt in (False, True):
         o = torch.empty((1, nq * hd), device="cuda")
         if prompt:

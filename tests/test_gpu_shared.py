@@ -9,7 +9,7 @@ from gpu_common import dev, host, require_gpu, say, torch
 
 import dequant_gemv_q4_amd as q
 from dequant_gemv_q4_amd import device as D
-from kv_common import ALL, BYTES, Cache, attention_row, check_rows, held, lost64, scales64
+from kv_common import ALL, BYTES, Cache, check_rows, held, parts64, scales64
 from test_gpu_kv8 import _draw, ints
 
 pytestmark = pytest.mark.gpu
@@ -67,8 +67,7 @@ def shared(kv_type, nq, nkv, hd, page, groups, seed=0, outside=(0, 0), scale=Non
         hk, hv = held(K[b], kv_type), held(V[b], kv_type)
         dv = scales64(V[b], kv_type) if kv_type in BYTES and len(V[b]) else np.ones(V[b].shape[:2])
         qr = x[b, :nq * hd].reshape(nq, hd)
-        parts.append((*attention_row(qr, hk, hv, nkv, scale, length[b] - 1),
-                      lost64(qr, hk, dv, nkv, scale, length[b] - 1, kv_type)))
+        parts.append(parts64(qr, hk, hv, dv, nkv, scale, length[b] - 1, kv_type))
     check_rows(host(o), parts, length, hd, kv_type, "shared")
     assert q.qgemv_attn_error(ws) == 0
     return c, x, host(o)
@@ -98,33 +97,59 @@ def test_shared_long(kv_type, nq, nkv, hd, page, groups):
     shared(kv_type, nq, nkv, hd, page, groups, len(groups))
 
 
-def form_of(n_seq, n_group, nq, nkv, hd, positions):
+def form_of(kv_type, n_seq, n_group, nq, nkv, hd, positions):
     """Which kernels take the call (the launcher's own choice): 16-column tiles, 128-column tiles with parts, split
     few among many, or whole."""
-    fn = ctypes.CDLL(q.LIB_PATH)["_ZN2qg11shared_formEliiiil"]
+    fn = ctypes.CDLL(q.LIB_PATH)["_ZN2qg11shared_formEiliiiil"]
     fn.restype = ctypes.c_int
-    fn.argtypes = [ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int64]
-    return ["16", "parted", "few", "whole"][fn(n_seq, n_group, nq, nkv, hd, positions)]
+    fn.argtypes = [ctypes.c_int, ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int64]
+    return ["16", "parted", "few", "whole"][fn(kv_type, n_seq, n_group, nq, nkv, hd, positions)]
 
 
 @pytest.mark.parametrize("kv_type", ALL)
 @pytest.mark.parametrize("form,nq,nkv,hd,page,groups,outside", [
-    ("parted", 12, 2, 128, 16, [[(1003, 30 + i % 9) for i in range(70)], [(77, 900), (70, 3)] * 40], (1, 2)),
-    ("parted", 16, 1, 64, 32, [[(2000, 1 + 7 * i % 40) for i in range(49)]], (0, 0)),
-    ("parted", 5, 1, 96, 16, [[(1500, 20)] * 160], (0, 0)),
-    ("parted", 20, 1, 64, 16, [[(40, 3)] * 30 + [(17, 1500)], [(5, 1)] * 20], (3, 0)),
-    ("parted", 4, 1, 256, 64, [[(1300, 9)] * 99], (0, 1)),
-    ("few", 16, 16, 64, 16, [[(int(20 + 9 * i), i % 5), (int(20 + 9 * i), 2)] for i in range(33)] + [[(3000, 5)] * 3], (1, 1)),
-    ("few", 8, 4, 256, 32, [[(70, 4)] * 2 for _ in range(63)] + [[(1900, 40), (1900, 1)]], (0, 0)),
-    ("whole", 16, 16, 64, 16, [[(int(9 + 5 * i), i % 7)] * 2 for i in range(34)], (2, 0)),
+    ("parted", 64, 2, 128, 16, [[(1003, 3 + i % 9) for i in range(60)], [(77, 40), (70, 3)] * 36], (1, 2)),
+    ("parted", 128, 1, 64, 32, [[(1200, 1 + 7 * i % 40) for i in range(66)]], (0, 0)),
+    ("parted", 60, 3, 96, 16, [[(150, 2)] * 90 + [(17, 900)], [(5, 1)] * 50], (3, 0)),
+    ("parted", 64, 1, 192, 64, [[(130, 9)] * 100, [(700, 3), (0, 7), (700, 2)] * 10], (0, 1)),
+    ("parted", 64, 2, 256, 64, [[(1030, 9)] * 20, [(64, 1), (64, 70)] * 56], (0, 0)),
+    ("few", 64, 16, 64, 16, [[(20 + 4 * i, i % 5), (20 + 4 * i, 2), (9, 1)] for i in range(43)] + [[(1900, 5)] * 3],
+     (1, 1)),
+    ("few", 64, 8, 256, 32, [[(40, 4)] * 2 for _ in range(66)] + [[(1100, 20), (1100, 1)]], (0, 0)),
+    ("whole", 64, 16, 64, 16, [[(9 + 3 * i, i % 7)] * 3 for i in range(45)], (2, 0)),
 ])
 def test_shared_by_128_columns(kv_type, form, nq, nkv, hd, page, groups, outside):
     """Groups of more rows than 16-column tiles take, and more groups than workgroup slots."""
     n = sum(len(g) for g in groups) + sum(outside)
     lens = [s + a for g in groups for s, a in g] + [17 + 30 * i for i in range(outside[0])] + [41] * outside[1]
     positions = (-(-max(lens) // page) + 2) * page
-    assert form_of(n, len(groups), nq, nkv, hd, positions) == form
+    assert form_of(kv_type, n, len(groups), nq, nkv, hd, positions) == form
     shared(kv_type, nq, nkv, hd, page, groups, 11, outside=outside)
+
+
+@pytest.mark.parametrize("kv_type,nq,nkv,hd,n,prefix", [
+    (q.F16, 32, 8, 64, 60, 4500), (q.BF16, 16, 1, 128, 40, 7000), (q.I8, 32, 2, 128, 100, 10000)])
+def test_shared_much_work(kv_type, nq, nkv, hd, n, prefix):
+    """Enough work for the 128-column tiles in a few rows."""
+    groups = [[(prefix, 1 + i % 50) for i in range(n)]]
+    positions = (-(-(prefix + 50) // 32) + 2) * 32
+    assert form_of(kv_type, n, 1, nq, nkv, hd, positions) == "parted"
+    shared(kv_type, nq, nkv, hd, 32, groups, 14)
+
+
+def test_choice_of_form():
+    """By the work, the type and the groups; what the sums of halves meet on is bounded."""
+    assert form_of(q.F16, 64, 1, 32, 8, 128, 30720) == "parted" and form_of(q.F16, 16, 2, 24, 8, 64, 2240) == "16"
+    assert form_of(q.I8, 64, 1, 32, 8, 128, 8000) == "16" and form_of(q.F16, 64, 1, 32, 8, 128, 8000) == "parted"
+    assert form_of(q.F16, 1024, 512, 8, 8, 64, 32) == "16" and form_of(q.F16, 1024, 512, 9, 9, 64, 32) == "whole"
+    assert form_of(q.BF16, 1024, 512, 9, 9, 64, 2000) == "few"
+
+
+def test_shared_as_many_tiles_as_slots():
+    """16-column tiles of the prefixes, more than the slots they have: each has a workgroup, the longest are split."""
+    shared(q.F16, 8, 8, 64, 16, [[(50, 3)] * 2 for _ in range(63)] + [[(2900, 5)] * 2], 15)
+    shared(q.F8, 4, 4, 256, 16, [[(50, 3)] * 2 for _ in range(63)] + [[(2900, 5)] * 2], 16)
+    shared(q.I8, 34, 1, 64, 16, [[(60, 1)] * 30 for _ in range(8)], 17)
 
 
 def test_shared_behind_the_prefix_split_among_many():
@@ -175,9 +200,7 @@ def test_shared_promise_broken_and_bad_pages(kv_type):
             k, v = K[b][keep[b]], V[b][keep[b]]
             dv = scales64(v, kv_type) if kv_type in BYTES else np.ones(v.shape[:2])
             qr = x[b].reshape(nq, hd)
-            hk = held(k, kv_type)
-            parts.append((*attention_row(qr, hk, held(v, kv_type), nkv, 0.125, len(k) - 1),
-                          lost64(qr, hk, dv, nkv, 0.125, len(k) - 1, kv_type)))
+            parts.append(parts64(qr, held(k, kv_type), held(v, kv_type), dv, nkv, 0.125, len(k) - 1, kv_type))
         check_rows(host(o), parts, [80, 100], hd, kv_type, "left out")
         assert q.qgemv_attn_error(ws) == 1 and q.qgemv_attn_error(ws) == 0
 
