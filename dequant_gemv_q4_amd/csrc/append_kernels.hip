@@ -206,10 +206,11 @@ __global__ __launch_bounds__(256) void k_qkv_append(QkvArgs a)
     const KvArgs &c = a.c;
     const int tid = threadIdx.x, j = tid % LPR, row = tid / LPR, ch = 4 * j;
     // roles of a block side by side: the workgroups at work read and write whole rows
-    const int id = blockIdx.x / a.roles, role = blockIdx.x - id * a.roles;
+    const int64_t all = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    const int id = (int)(all / a.roles), role = (int)(all - (int64_t)id * a.roles);
     const bool in = ch < c.hd;
     AppendBlock w;
-    if (!append_block<BL>(c, id, w))
+    if ((!c.q_start && id >= c.n_seq) || !append_block<BL>(c, id, w))
         return;
     int from = w.from, to = w.to;
     if (TURN && a.half > 0 && w.t0 + to > a.rope_rows) {
@@ -437,7 +438,10 @@ static void launch_block(const QkvArgs &a, hipStream_t s)
     default: QG_APPEND_L(64); break;
     }
 #undef QG_APPEND_L
-    hipLaunchKernelGGL(k, dim3((unsigned)(blocks * b.roles)), dim3(256), 0, s, b);
+    // (a grid's row holds fewer than 2^32 threads; ids behind the last find no block)
+    const int64_t all = blocks * b.roles, most = 1 << 23;
+    const dim3 grid((unsigned)(all < most ? all : most), (unsigned)((all + most - 1) / most));
+    hipLaunchKernelGGL(k, grid, dim3(256), 0, s, b);
 }
 
 template <int T, bool TURN>

@@ -376,7 +376,8 @@ int qgemv_attn_prompt(int kv_type, const void *k_pages, const void *v_pages, int
  * pages: its shared_len has to be its group's largest.  Of another's that is larger the positions
  * between are left out, and the flag is set.  The positions from shared_len[b] on, a begun page
  * included, are read from the sequence's own pages.  As everywhere, a sequence sees kv_len[b]
- * positions in all, also where shared_len[b] is larger.  1 <= n_group <= n_seq. */
+ * positions in all, also where shared_len[b] is larger.  1 <= n_group <= n_seq.  (Group starts out of order
+ * leave outputs unwritten and arrival counts behind: the workspace has to be zero-filled again.) */
 int qgemv_attn_shared(int kv_type, const void *k_pages, const void *v_pages, int64_t n_pages,
                       int page_size, int64_t page_stride, int n_kv_heads, int head_dim,
                       const int32_t *table, int max_pages, const int32_t *kv_len, int n_seq,
