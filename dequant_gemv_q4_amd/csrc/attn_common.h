@@ -56,7 +56,10 @@ __device__ __forceinline__ float high_of(uint32_t p)
 template <int T>
 __device__ __forceinline__ void split8(const float (&v)[8], au4 (&out)[PIECES<T>])
 {
-    float r[8];
+    float r[8], minus = -1.0f;
+    // f16: remainder and conversion are one instruction (v_fma_mix), if the compiler does not see a difference
+    if constexpr (T == KV_F16)
+        asm("" : "+s"(minus));
 #pragma unroll
     for (int e = 0; e < 8; ++e)
         r[e] = v[e];
@@ -67,8 +70,8 @@ __device__ __forceinline__ void split8(const float (&v)[8], au4 (&out)[PIECES<T>
             const uint32_t p = pack2<T>(r[2 * e], r[2 * e + 1]);
             out[i][e] = p;
             if (i + 1 < PIECES<T>) {
-                r[2 * e] = fmaf(low_of<T>(p), -1.0f, r[2 * e]);     // f16: one instruction
-                r[2 * e + 1] = fmaf(high_of<T>(p), -1.0f, r[2 * e + 1]);
+                r[2 * e] = fmaf(low_of<T>(p), minus, r[2 * e]);
+                r[2 * e + 1] = fmaf(high_of<T>(p), minus, r[2 * e + 1]);
             }
         }
 }

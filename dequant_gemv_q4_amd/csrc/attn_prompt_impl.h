@@ -483,10 +483,9 @@ __device__ __forceinline__ void prompt_body(const AttnArgs &a, int slots, int id
 #pragma unroll
                     for (int tt = 0; tt < NT; ++tt)
 #pragma unroll
-                        for (int r = 0; r < 16; ++r) {
+                        for (int r = 0; r < 16; ++r)
                             if (hidden(sub, tt, r))
                                 sc[tt][r] = -INFINITY;
-                        }
                 if constexpr (BYTES) {
                     float seen = dv[0], most;
                     if (edge) {
