@@ -454,7 +454,8 @@ __device__ __forceinline__ void prompt_body(const AttnArgs &a, int slots, int id
                 }
         }
     };
-    // between: what is done between the two products
+    // between: what is done between the two products (loads of 8-bit pages there: 8192 rows, 32 / 8 heads of 128, F8
+    // 1104 -> 1050 us against before both)
     auto compute = [&](int s, int buf, uint32_t bad, auto between) {
         const int t0 = s * PT_STEP;
         const bool edge = bad != 0 || t0 + PT_STEP - 1 > tile_min;
@@ -529,27 +530,37 @@ __device__ __forceinline__ void prompt_body(const AttnArgs &a, int slots, int id
     };
 
     if (BYTES && s1 > s0) {
+        // a step's loads are under way while the one before is computed: all of it where there are registers for
+        // that, else between its products
+        constexpr bool AHEAD = D <= 96;
         Codes x;
         load8(s0, ids_of(s0), x);
         int ids = ids_of(s0 + 1);
-        uint32_t seen_bad = 0;
         stage8(s0, 0, x);
+        uint32_t bad = x.bad, seen_bad = 0;
+        auto next = [&](int s) {
+            if (s < s1) {
+                load8(s, ids, x);
+                ids = ids_of(s + 1);
+            }
+        };
+        if (AHEAD)
+            next(s0 + 1);
         for (int s = s0; s < s1; ++s) {
             const int buf = (s - s0) & 1;
-            const uint32_t bad = x.bad;
             seen_bad |= bad;
             // step s is staged; after the barrier everyone's part is, and everyone is done with step s - 1
             __syncthreads();
-            // the loads are not held in registers beside all that the first product holds (8192 rows, 32 / 8 heads of
-            // 128, F8: 1104 -> 1050 us)
             compute(s, buf, bad, [&]() {
-                if (s + 1 < s1) {
-                    load8(s + 1, ids, x);
-                    ids = ids_of(s + 2);
-                }
+                if (!AHEAD)
+                    next(s + 1);
             });
-            if (s + 1 < s1)
+            if (s + 1 < s1) {
                 stage8(s + 1, buf ^ 1, x);
+                bad = x.bad;
+                if (AHEAD)
+                    next(s + 2);
+            }
         }
         if (seen_bad && tid == 0)
             atomicOr(c.err, 1u);
