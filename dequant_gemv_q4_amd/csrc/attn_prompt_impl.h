@@ -716,10 +716,22 @@ __global__ __launch_bounds__(256) void k_attn_prompt_join(AttnArgs a)
         af4 sum = {0.f, 0.f, 0.f, 0.f};
         if constexpr (MEANS) {
             // the factors of all parts first, then each mean by its own: threads of a row add them alike
-            for (int k = 0; k < splits; ++k)
-                m = fmaxf(m, ml[k * stride]);
-            for (int k = 0; k < splits; ++k)
-                l += ml[k * stride + 1] * join_weight(ml[k * stride], m);
+            for (int kb = 0; kb < splits; kb += 8) {
+                float2 w[8];
+#pragma unroll
+                for (int x = 0; x < 8; ++x)                    // all loads in flight at once
+                    w[x] = *reinterpret_cast<const float2 *>(ml + min(kb + x, splits - 1) * stride);
+                float mb = m;
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                    mb = fmaxf(mb, w[x].x);
+                l *= join_weight(m, mb);
+                m = mb;
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                    if (kb + x < splits)
+                        l += w[x].y * join_weight(w[x].x, m);
+            }
             const float inv = inverse_sum(l);
             all_m = m;
             all_l = l;
