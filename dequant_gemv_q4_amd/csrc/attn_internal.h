@@ -115,6 +115,7 @@ struct PromptPlan {
 };
 PromptPlan plan_prompt(int64_t n_rows, int n_seq, int nkv, int group, int hd, int64_t positions);
 bool prompt_in_16s(int64_t n_rows, int n_seq, int nq, int nkv, int hd, int64_t positions);
+bool prompt8_in_16s(int64_t n_rows, int n_seq, int nq, int nkv, int hd, int64_t positions);
 
 // Launchers: a hipError_t value (0 = success).
 int launch_kv_append(int kv_type, const AppendArgs &a, void *stream);

@@ -49,11 +49,22 @@ bool prompt_in_16s(int64_t n_rows, int n_seq, int nq, int nkv, int hd, int64_t p
            columns * nkv * hd * (positions < 16384 ? positions : 16384) <= (int64_t)1 << 31;
 }
 
+// The same over 8-bit pages, where the 16-column kernel reads half the bytes and the 128-row tiles convert the codes
+// on their way through LDS: resident workgroups and bounded work are enough.  128-row tiles -> 16 columns, us, I8:
+// one sequence of 128 rows x 4000, 12 / 2 heads of 128, 45.9 -> 31.5, 32 / 8 heads (2.2e9 channels) 59.3 -> 50.7;
+// 64 rows x 20000, 16 / 1, 63.8 -> 53.4, 24 / 8 of 64 49.1 -> 47.2; 128 rows x 20000, 12 / 2 (3.2e9) 67.4 -> 71.7;
+// 200 rows x 10000, 24 / 8 of 64 (3.1e9) 60.6 -> 89.8.
+bool prompt8_in_16s(int64_t n_rows, int n_seq, int nq, int nkv, int hd, int64_t positions)
+{
+    return nkv * (n_rows * (nq / nkv) / 16 + n_seq) <= attn_slots(hd) &&
+           n_rows * nq * hd * (positions < 16384 ? positions : 16384) <= 2500000000LL;
+}
+
 int launch_attn_prompt(int kv_type, const AttnArgs &a, void *stream)
 {
     const int64_t table = (int64_t)a.c.max_pages << a.c.ps_log2;
     const bool bytes = kv_bytes(kv_type);
-    if (prompt_in_16s(a.c.n_rows, a.c.n_seq, a.nq, a.c.nkv, a.c.hd, table))
+    if ((bytes ? prompt8_in_16s : prompt_in_16s)(a.c.n_rows, a.c.n_seq, a.nq, a.c.nkv, a.c.hd, table))
         return bytes ? launch_attn8_rows(kv_type, a, stream) : launch_attn_rows(kv_type, a, stream);
     hipStream_t s = static_cast<hipStream_t>(stream);
     const PromptPlan p = plan_prompt(a.c.n_rows, a.c.n_seq, a.c.nkv, a.group, a.c.hd, table);

@@ -1,5 +1,7 @@
 """The 8-bit cache on the GPU: quantising rows as they are written, the attentions that read it, and the
 fused norm, rotation and append, against their definitions in 64 bits (kv_common)."""
+import ctypes
+
 import numpy as np
 import pytest
 
@@ -397,30 +399,69 @@ def test_prompt8_small(kv_type, nq, nkv, hd, page):
     attend(kv_type, nq, nkv, hd, page, PROMPTS, hd + page, tail=3)
 
 
+def in_16s(n_rows, n_seq, nq, nkv, hd, positions):
+    """Whether 16-column tiles take a prompt over 8-bit pages (the launcher's own choice)."""
+    fn = ctypes.CDLL(q.LIB_PATH)["_ZN2qg14prompt8_in_16sEliiiil"]
+    fn.restype = ctypes.c_bool
+    fn.argtypes = [ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int64]
+    return fn(n_rows, n_seq, nq, nkv, hd, positions)
+
+
+def _wide(kv_type, nq, nkv, hd, page, seqs, seed, entries, **kw):
+    """By 128-row tiles: a table of so many positions that the smaller ones do not take the call."""
+    rows = sum(a for a, _ in seqs) + kw.get("tail", 0)
+    positions = (max(-(-b // page) for _, b in seqs) + entries) * page
+    assert not in_16s(rows, len(seqs), nq, nkv, hd, positions)
+    attend(kv_type, nq, nkv, hd, page, seqs, seed, extra_entries=entries, **kw)
+
+
+def test_choice_of_tiles():
+    assert in_16s(32, 1, 12, 2, 128, 20000) and in_16s(128, 1, 12, 2, 128, 4160) and in_16s(128, 1, 32, 8, 128, 4160)
+    assert not in_16s(203, 1, 12, 2, 128, 30240) and not in_16s(8192, 1, 32, 8, 128, 8320)
+    assert not in_16s(1200, 2, 8, 8, 64, 632) and not in_16s(1 << 20, 1024, 1024, 1, 256, 1 << 24)
+
+
 @pytest.mark.parametrize("kv_type", BYTES)
 @pytest.mark.parametrize("nq,nkv,hd,page", [(12, 2, 128, 16), (10, 2, 64, 32), (5, 1, 96, 16), (20, 1, 64, 256),
                                             (4, 1, 256, 16), (6, 1, 192, 64)])
 def test_prompt8_wide(kv_type, nq, nkv, hd, page):
     g = nq // nkv
     seqs = [(2100 // g, 2100 // g), (1, 1), (0, 0), (0, 9), (700 // g, 700 // g + 77), (3, 130), (30, 21)]
-    attend(kv_type, nq, nkv, hd, page, seqs, hd + page, tail=3, extra_entries=1024 // page + 1)
+    _wide(kv_type, nq, nkv, hd, page, seqs, hd + page, 16384 // page, tail=3)
+
+
+@pytest.mark.parametrize("kv_type", BYTES)
+@pytest.mark.parametrize("nq,nkv,hd,seqs", [(8, 8, 64, [(600, 600), (600, 611), (3, 2)]), (16, 8, 128, [(600, 900)]),
+                                            (8, 8, 256, [(300, 301), (300, 300)]), (12, 12, 96, [(700, 700)])])
+def test_prompt8_wide_unsplit(kv_type, nq, nkv, hd, seqs):
+    """More tiles than are resident at once, over short tables: none is split."""
+    _wide(kv_type, nq, nkv, hd, 32, seqs, hd, 2, tail=1)
 
 
 @pytest.mark.parametrize("kv_type,nq,nkv,hd,page,seqs", [
-    (q.I8, 8, 1, 128, 16, [(61, 5000)]), (q.F8, 24, 2, 64, 16, [(50, 4000), (50, 64)]),
-    (q.I8, 4, 1, 256, 32, [(100, 2500)]), (q.F8, 9, 1, 96, 16, [(45, 3333)]), (q.F8, 6, 1, 192, 16, [(80, 2100)]),
+    (q.I8, 32, 1, 128, 16, [(61, 5000)]), (q.F8, 48, 2, 64, 16, [(50, 4000), (50, 64)]),
+    (q.I8, 8, 1, 256, 32, [(100, 2500)]), (q.F8, 36, 1, 96, 16, [(45, 3333)]), (q.F8, 12, 1, 192, 16, [(80, 2100)]),
     (q.I8, 64, 4, 64, 32, [(40, 6000), (300, 300), (250, 250), (0, 5000), (400, 420), (9, 3000), (330, 330), (100, 100)]),
     (q.F8, 64, 4, 128, 32, [(10, 2600), (300, 300), (250, 250), (400, 420), (330, 330), (100, 100)]),
-    (q.I8, 8, 1, 128, 16, [(3, 9000)]),
+    (q.F8, 64, 4, 256, 32, [(10, 2600), (300, 300), (250, 250), (12, 5)]),
 ])
 def test_prompt8_long(kv_type, nq, nkv, hd, page, seqs):
-    attend(kv_type, nq, nkv, hd, page, seqs, len(seqs), tail=1, extra_entries=1024 // page + 1)
+    """Tiles split over the cache's length, all of them or a few among many."""
+    _wide(kv_type, nq, nkv, hd, page, seqs, len(seqs), 16384 // page, tail=1)
+
+
+@pytest.mark.parametrize("kv_type", BYTES)
+def test_prompt8_long_by_16_columns(kv_type):
+    assert in_16s(120, 1, 8, 1, 128, 9032)
+    attend(kv_type, 8, 1, 128, 16, [(120, 9000)], 3, tail=1)
+    attend(kv_type, 24, 2, 64, 16, [(17, 5000), (2, 3000)], 4)
 
 
 @pytest.mark.parametrize("kv_type", BYTES)
 def test_attention8_scales_and_sharp_scores(kv_type):
-    for prompt, seqs in ((False, [(1, 300), (1, 77)]), (True, [(110, 300), (100, 131)])):
-        kw = dict(prompt=prompt, extra_entries=70 if prompt else 2)
+    for prompt, seqs in ((False, [(1, 300), (1, 77)]), (True, [(110, 300), (100, 131)]), (True, [(310, 350), (300, 331)])):
+        kw = dict(prompt=prompt, extra_entries=1024 if prompt else 2)
+        assert not prompt or in_16s(sum(a for a, _ in seqs), 2, 4, 1, 64, 17000) == (seqs[0][0] < 200)
         attend(kv_type, 4, 1, 128, 16, seqs, 1, scale=1.0, qmul=2.0, **kw)
         attend(kv_type, 4, 1, 64, 16, seqs, 2, scale=-0.09, **kw)
         attend(kv_type, 4, 1, 64, 16, seqs, 3, scale=0.0, **kw)
@@ -435,13 +476,13 @@ def test_attention8_scales_and_sharp_scores(kv_type):
 def test_attention8_values_near_the_range_ends(kv_type, size):
     """V of any size (the scale is an f32), with rows of zeros among it; K large and small against the scale."""
     rng = np.random.default_rng(11)
-    for prompt, seqs in ((False, [(1, 300), (1, 77)]), (True, [(110, 300), (100, 131)])):
+    for prompt, seqs in ((False, [(1, 300), (1, 77)]), (True, [(110, 300), (100, 131)]), (True, [(310, 350), (300, 331)])):
         K, V = _draw(rng, [b for _, b in seqs], 1, 64, 0.0)
         for v in V:
             v /= np.abs(v).max()
             v *= np.float32(size)
             v[::7] = 0.0
-        kw = dict(prompt=prompt, extra_entries=70 if prompt else 2)
+        kw = dict(prompt=prompt, extra_entries=1024 if prompt else 2)
         attend(kv_type, 4, 1, 64, 16, seqs, 1, K=K, V=V, **kw)
         if 1e-20 < size < 1e20:
             attend(kv_type, 4, 1, 64, 16, seqs, 1, K=[k * np.float32(size) for k in K], V=V, scale=0.1 / size, **kw)
@@ -451,11 +492,11 @@ def test_attention8_values_near_the_range_ends(kv_type, size):
 def test_a_large_value_reaches_only_the_rows_that_see_it(kv_type):
     """V a million times larger at later positions: earlier rows of the tile keep their precision."""
     rng = np.random.default_rng(12)
-    for seqs in ([(40, 40)], [(300, 300)], [(130, 800)]):
+    for seqs in ([(40, 40)], [(300, 300)], [(130, 800)], [(700, 800)]):
         n = seqs[0][1]
         K, V = _draw(rng, [n], 1, 64, 0.0)
         V[0][n - 5:] *= np.float32(1e9)
-        attend(kv_type, 4, 1, 64, 16, seqs, 1, K=K, V=V, extra_entries=70)
+        attend(kv_type, 4, 1, 64, 16, seqs, 1, K=K, V=V, extra_entries=1024)
 
 
 @pytest.mark.parametrize("kv_type", BYTES)
@@ -464,12 +505,12 @@ def test_non_finite_rows_reach_only_the_rows_that_see_them(kv_type, where):
     """A position quantised from a NaN or an infinity: rows and heads that see it are not finite, others exact."""
     rng = np.random.default_rng(13)
     nq, nkv, hd, page = 4, 2, 64, 16
-    for seqs in ([(50, 50), (20, 90)], [(300, 300), (200, 777)]):
+    for seqs in ([(50, 50), (20, 90)], [(600, 600), (200, 777)]):
         K, V = _draw(rng, [b for _, b in seqs], nkv, hd)
         spoilt = (K if where == "k" else V)[0]
         at = seqs[0][1] - 20
         spoilt[at, 1, 3] = np.nan if where == "k" else np.inf
-        c = Cache(kv_type, K, V, page, nkv, hd, rng, extra_entries=70)
+        c = Cache(kv_type, K, V, page, nkv, hd, rng, extra_entries=1024)
         start = np.concatenate([[0], np.cumsum([a for a, _ in seqs])])
         rows = int(start[-1])
         x = rng.standard_normal((rows, nq * hd)).astype(np.float32)

@@ -69,7 +69,7 @@ def _jobs():
     return [
         Job("attn", q.I8, 12, 2, 128, [(1, 9000), (1, 17), (1, 2500), (1, 0)], 1),
         Job("prompt", q.F8, 12, 2, 128, [(3, 6000), (2, 900)], 2),
-        Job("prompt", q.I8, 12, 1, 64, [(200, 3000), (40, 70)], 3, extra=70),
+        Job("prompt", q.I8, 24, 2, 64, [(200, 3000), (40, 70)], 3, extra=1024),
         Job("shared", q.F16, 24, 8, 64, [(1, 700 + i) for i in range(9)], 4, ([0, 4, 9], [640] * 4 + [333] * 5)),
         Job("shared", q.F8, 12, 2, 128, [(1, 3000 + i) for i in range(20)], 5, ([0, 20], [2990] * 20)),
         Job("shared", q.BF16, 64, 1, 64, [(1, 1300 + i % 7) for i in range(130)], 6, ([0, 130], [1299] * 130)),
