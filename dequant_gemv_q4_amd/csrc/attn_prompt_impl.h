@@ -259,18 +259,23 @@ __device__ __forceinline__ void prompt_body(const AttnArgs &a, int slots, int id
         }
         if (lane < 32)
             sh.scale[BYTES ? buf : 0][lane >> 4][16 * wave + (lane & 15)] = x.d;
+        // K and V apart (I8, 8192 rows, 32 / 8 heads of 128, 1072 -> 1027 us, 4096 of 256 822 -> 749 against a loop
+        // body for both, which the compiler orders worse)
 #pragma unroll
-        for (int i = 0; i < PASS8; ++i) {
-            const int idx = 64 * i + lane, row = idx / (D / 16), pc = 2 * (idx % (D / 16));
+        for (int n = 0; n < 2 * PASS8; ++n) {
+            const int idx = 64 * (n / 2) + lane, row = idx / (D / 16), pc = 2 * (idx % (D / 16));
             if (D % 64 == 0 || idx < D) {
                 au4 lo, hi;
-                halves_of<T>(x.k[i], lo, hi);
-                *reinterpret_cast<au4 *>(kb + row * D * 2 + ((pc ^ key(row)) << 4)) = lo;
-                *reinterpret_cast<au4 *>(kb + row * D * 2 + (((pc + 1) ^ key(row)) << 4)) = hi;
-                halves_of<T>(x.v[i], lo, hi);
-                const int turn = idx >> 4 & 1;
-                *reinterpret_cast<au4 *>(vb + idx * 32 + (turn << 4)) = lo;
-                *reinterpret_cast<au4 *>(vb + idx * 32 + ((turn ^ 1) << 4)) = hi;
+                if (n % 2 == 0) {
+                    halves_of<T>(x.k[n / 2], lo, hi);
+                    *reinterpret_cast<au4 *>(kb + row * D * 2 + ((pc ^ key(row)) << 4)) = lo;
+                    *reinterpret_cast<au4 *>(kb + row * D * 2 + (((pc + 1) ^ key(row)) << 4)) = hi;
+                } else {
+                    halves_of<T>(x.v[n / 2], lo, hi);
+                    const int turn = idx >> 4 & 1;
+                    *reinterpret_cast<au4 *>(vb + idx * 32 + (turn << 4)) = lo;
+                    *reinterpret_cast<au4 *>(vb + idx * 32 + ((turn ^ 1) << 4)) = hi;
+                }
             }
         }
     };
