@@ -10,6 +10,11 @@
 //  - lane i of group g loads the scales of position 16 g + i, and a score takes its own by a lane broadcast within
 //    16 lanes (one instruction's operand);
 //  - parts are means (attn_bytes.h).
+//
+// Bound by HBM with long caches: 64 tokens over ~7500 positions each, 24 / 8 heads of 64, I8 (524 MB), 105 us, 5.0
+// TB/s (f16 pages: 1.9 times the bytes); seven, the longest of 60000 positions, 32 / 8 heads of 128, F8 (191 MB),
+// 43 us.  One token over 180 positions 6.6 us, latency.  The conversion of the codes, 2 to 2.5 vector instructions
+// for four, hides behind the loads.
 #pragma once
 
 #include "attn_bytes.h"

@@ -51,9 +51,9 @@ bool prompt_in_16s(int64_t n_rows, int n_seq, int nq, int nkv, int hd, int64_t p
 
 // The same over 8-bit pages, where the 16-column kernel reads half the bytes and the 128-row tiles convert the codes
 // on their way through LDS: resident workgroups and bounded work are enough.  128-row tiles -> 16 columns, us, I8:
-// one sequence of 128 rows x 4000, 12 / 2 heads of 128, 45.9 -> 31.5, 32 / 8 heads (2.2e9 channels) 59.3 -> 50.7;
-// 64 rows x 20000, 16 / 1, 63.8 -> 53.4, 24 / 8 of 64 49.1 -> 47.2; 128 rows x 20000, 12 / 2 (3.2e9) 67.4 -> 71.7;
-// 200 rows x 10000, 24 / 8 of 64 (3.1e9) 60.6 -> 89.8.
+// one sequence of 128 rows x 4000, 12 / 2 heads of 128, 40.7 -> 31.1, 32 / 8 heads (2.2e9 channels) 54.1 -> 47.1;
+// 64 rows x 20000, 16 / 1, 62.0 -> 54.0, 24 / 8 of 64 48.7 -> 47.7; 128 rows x 20000, 12 / 2 (3.2e9) 64.9 -> 69.7;
+// 200 rows x 10000, 24 / 8 of 64 (3.1e9) 58.4 -> 91.1.
 bool prompt8_in_16s(int64_t n_rows, int n_seq, int nq, int nkv, int hd, int64_t positions)
 {
     return nkv * (n_rows * (nq / nkv) / 16 + n_seq) <= attn_slots(hd) &&

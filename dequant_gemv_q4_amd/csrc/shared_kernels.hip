@@ -39,15 +39,17 @@ static AttnArgs groups_of(const AttnArgs &a)
 
 // The 16-column tiles read a prefix once per 16 columns, the 128-column ones leave parts for a second launch and
 // fill their tiles less.  By the work, columns times positions times channels of all heads (of longer tables 16384
-// positions count: a table is sized for the longest cache), at most: over f16 and bf16 pages 5e8, over 8-bit pages, whose codes the 128-column tiles convert through LDS, 4e9.  16 -> 128 columns,
-// us, 128 channels: f16, 64 sequences, 32 / 8 heads, behind 1500 positions (4e8) 33.9 -> 36.4, behind 4000 (1.1e9)
-// 44.3 -> 37.1, 30000 (7.9e9) 181 -> 90; 12 / 2 heads behind 4000 (4e8) 34.0 -> 33.3, 10000 (1e9) 50.9 -> 36.6;
-// bf16, 150 of 16 / 1 behind 2500 (8e8) 47.9 -> 43.1; I8, 64 of 12 / 2 behind 30000 (3e9) 71.0 -> 74.1, 256 behind
-// 10000 (4e9) 89.2 -> 79.9, 64 of 32 / 8 behind 30000 (7.9e9) 128 -> 124, but 200 behind 10000 (8.3e9) 101 -> 143.
+// positions count: a table is sized for the longest cache), at most: over f16 and bf16 pages 5e8, over 8-bit pages,
+// whose codes the 128-column tiles convert through LDS, 1.5e9.  16 -> 128 columns, us, 128 channels: f16, 64
+// sequences, 32 / 8 heads, behind 1500 positions (4e8) 37.4 -> 37.4, behind 4000 (1.1e9) 46.7 -> 38.3, 30000 (4.3e9)
+// 183 -> 93; 12 / 2 heads behind 4000 (4e8) 33.3 -> 34.9, 10000 (1e9) 48.7 -> 37.7; bf16, 150 of 16 / 1 behind 2500
+// (8e8) 47.0 -> 42.5; I8, 64 of 32 / 8 behind 4000 (1.1e9) 35.9 -> 43.4, 8000 (2.1e9) 50.0 -> 48.5, 30000 130 -> 111;
+// 200 of 12 / 2 behind 4000 (1.3e9) 44.4 -> 43.9, 150 of 16 / 1 behind 2500 (8e8) 38.3 -> 43.7, 10000 (3.1e9) 80.7 ->
+// 62.2; heads of 256, 30 of 32 / 8 behind 8000 (2e9) 95.0 -> 78.1; 24 / 8 of 64, 32 behind 20000 (8e8) 36.7 -> 42.7.
 SharedForm shared_form(int kv_type, int64_t n_seq, int n_group, int nq, int nkv, int hd, int64_t positions)
 {
     const double work = (double)(n_seq * nq) * hd * (positions < 16384 ? positions : 16384);
-    if (n_seq * nq <= MEET_MOST && work <= (kv_bytes(kv_type) ? 4e9 : 5e8))
+    if (n_seq * nq <= MEET_MOST && work <= (kv_bytes(kv_type) ? 1.5e9 : 5e8))
         return SHARED_16;
     const PromptPlan p = plan_prompt(n_seq, n_group, nkv, nq / nkv, hd, positions);
     return p.pairs < SHARED_SLOTS ? SHARED_PARTED : p.slots ? SHARED_FEW : SHARED_WHOLE;

@@ -267,7 +267,8 @@ int qgemv_moe_error(const void *ws, int64_t n_exp, int64_t N, int64_t K, int fmt
  *          on, with amax <= 448 d, code = x / d to the nearest-even;
  * amax the largest |x| of the position's head_dim values.  The code is that of the exact quotient.
  * Where one of the values is not finite, d is NaN and the codes are 0: the whole position of the head
- * reads as NaN.  The e4m3 NaN codes are never written, and a cache has to hold none at positions in use.
+ * reads as NaN.  The e4m3 NaN codes are never written, and a cache has to hold none at positions in use, nor a
+ * negative scale.
  * page_stride, at least n_kv_heads * block and a multiple of 8 (8-bit: 16), lets one pool hold several
  * layers or K and V side by side.  table is int32 [n_seq][max_pages]: position t of sequence b lies in slot
  * t % page_size of page table[b][t / page_size].  Entries behind a sequence's last position are
@@ -306,8 +307,8 @@ int qgemv_moe_error(const void *ws, int64_t n_exp, int64_t N, int64_t K, int fmt
 int64_t qgemv_attn_workspace_bytes(int op, int n_seq, int n_q_heads, int n_kv_heads,
                                    int head_dim);
 
-/* Store the new K and V rows in the cache, rounded to nearest-even (8-bit: quantised as above).  k and v point at the first K
- * and V value of row 0, f32, kv_stride floats apart from row to row (the fused QKV output: qkv +
+/* Store the new K and V rows in the cache, rounded to nearest-even (8-bit: quantised as above).  k and
+ * v point at the first K and V value of row 0, f32, kv_stride floats apart from row to row (the fused QKV output: qkv +
  * n_q_heads * head_dim, qkv + (n_q_heads + n_kv_heads) * head_dim, stride (n_q_heads +
  * 2 n_kv_heads) * head_dim), heads back to back. */
 int qgemv_kv_append(int kv_type, void *k_pages, void *v_pages, int64_t n_pages, int page_size,
@@ -356,7 +357,10 @@ int qgemv_attn(int kv_type, const void *k_pages, const void *v_pages, int64_t n_
  * Accuracy of both: scores, softmax statistics and sums in f32; q and the probabilities enter the
  * products with f16 K and V as the sum of two f16 values (22 bits; of q below 2^-16 of the row's
  * largest 2^-38 of that, of probabilities 2^-35 of the row's largest, is lost at most), with bf16 as
- * that of three bf16 values (24 bits); K and V exactly as stored.  A NaN or an infinity in a query makes the
+ * that of three bf16 values (24 bits); K and V exactly as stored.  Over 8-bit pages the codes enter
+ * exactly, as f16, the scales of K multiply f32 scores and those of V f32 weights, and the products are as with f16 (of
+ * a weight times its scale 2^-35 of the row's largest weight times the largest scale that it sees is
+ * lost at most).  A NaN or an infinity in a query makes the
  * outputs of its row and head non-finite, one in K or V those of the rows that see its position (of V
  * its channel's; NaN also where the definition gives an infinity), and touches no other row.  Only an
  * infinity in K whose score comes out as -inf has weight 0; a row all of whose scores are -inf gets 0,

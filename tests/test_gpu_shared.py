@@ -140,7 +140,8 @@ def test_shared_much_work(kv_type, nq, nkv, hd, n, prefix):
 def test_choice_of_form():
     """By the work, the type and the groups; what the sums of halves meet on is bounded."""
     assert form_of(q.F16, 64, 1, 32, 8, 128, 30720) == "parted" and form_of(q.F16, 16, 2, 24, 8, 64, 2240) == "16"
-    assert form_of(q.I8, 64, 1, 32, 8, 128, 8000) == "16" and form_of(q.F16, 64, 1, 32, 8, 128, 8000) == "parted"
+    assert form_of(q.I8, 64, 1, 32, 8, 128, 4000) == "16" and form_of(q.F16, 64, 1, 32, 8, 128, 4000) == "parted"
+    assert form_of(q.I8, 64, 1, 32, 8, 128, 8000) == "parted"
     assert form_of(q.F16, 1024, 512, 8, 8, 64, 32) == "16" and form_of(q.F16, 1024, 512, 9, 9, 64, 32) == "whole"
     assert form_of(q.BF16, 1024, 512, 9, 9, 64, 2000) == "few"
 
