@@ -1,6 +1,6 @@
 // attn8_impl.h -- attention of one or a few new rows per sequence over 8-bit pages.
 //
-// As over f16 pages (attn_kernels.hip): a workgroup takes up to 16 columns rho = token * group + head of a KV
+// As over f16 pages (attn_impl.h): a workgroup takes up to 16 columns rho = token * group + head of a KV
 // head against a chunk of positions, S^T = K Q^T and O^T = V^T P^T on v_mfma_f32_16x16x32_f16, the plan from the
 // lengths on the device, parts joined in the launch.  What the bytes change:
 //  - a step of a wave is 64 positions, so that a lane's loads stay 16 bytes: of K sixteen channels of a position

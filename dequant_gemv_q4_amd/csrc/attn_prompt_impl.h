@@ -22,7 +22,7 @@
 // Bound by the matrix cores: 8192 rows (32 / 8 heads of 128, f16) take 898 to 985 us from box to box, 1.22
 // to 1.12 PFLOP/s with each product's two pieces counted, what a large f16 product reaches on the card; 4500
 // rows of nine prompts (24 / 8 of 64, bf16, three pieces) 36 us.  Over 8-bit pages the vector instructions (scales,
-// conversions, softmax: 500 a step of 64 positions beside 64 products, heads of 128) nearly reach the products' time:
+// conversions, softmax: 500 a step of 64 positions with its 64 products, heads of 128) nearly reach the products' time:
 // I8 1020 to 1050 us for the same rows, F8 1000 to 1020, the nine prompts 39 us.
 #pragma once
 
