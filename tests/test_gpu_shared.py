@@ -217,3 +217,33 @@ def test_shared_is_attention_without_groups():
     ws = D.attn_workspace(q.OP_ATTN, 3, 8, 2, 64)
     q.qgemv_attn(*c.args(), c.kv_len, 3, dev(x), 12 * 64, 8, 64 ** -0.5, one, ws)
     assert np.abs(host(one) - o).max() <= 2e-5 * np.abs(o).max()
+
+
+@pytest.mark.parametrize("kv_type", ALL)
+@pytest.mark.parametrize("form,n,nq", [("16", 3, 4), ("parted", 130, 64)])
+def test_shared_lengths_beyond_the_table(kv_type, form, n, nq):
+    """Lengths and shares past the table's positions, a negative length and a negative share: what has no place is
+    left out and flagged, and the workspace serves the next call."""
+    nkv, hd, page, full = 1, 64, 16, 64
+    assert form_of(kv_type, n, 1, nq, nkv, hd, full) == form
+    rng = np.random.default_rng(21)
+    K, V = _draw(rng, [full] * n, nkv, hd)
+    for b in range(1, n):
+        K[b], V[b] = K[0], V[0]
+    c = Cache(kv_type, K, V, page, nkv, hd, rng, extra_entries=0)
+    x = rng.standard_normal((n, nq * hd)).astype(np.float32)
+    ws = D.attn_workspace(q.OP_ATTN_SHARED, n, nq, nkv, hd)
+    hk, hv = held(K[0], kv_type), held(V[0], kv_type)
+    dv = scales64(V[0], kv_type) if kv_type in BYTES else np.ones(V[0].shape[:2])
+
+    def run(lens, share, flag):
+        o = torch.full((n, nq * hd), float("nan"), device="cuda")
+        q.qgemv_attn_shared(*c.args(), ints(lens), n, ints([0, n]), ints(share), 1, dev(x), nq * hd, nq, 0.125, o, ws)
+        seen = [min(max(a, 0), full) for a in lens]
+        parts = [parts64(x[b].reshape(nq, hd), hk, hv, dv, nkv, 0.125, seen[b] - 1, kv_type) for b in range(n)]
+        check_rows(host(o), parts, seen, hd, kv_type, "beyond the table")
+        assert q.qgemv_attn_error(ws) == flag
+
+    run([2 ** 31 - 1, -5] + [40 + b % 30 for b in range(n - 2)], [2 ** 31 - 1] * n, 1)
+    run([full] * n, [-2 ** 31] * n, 0)
+    run([full] * n, [33] + [b % 34 for b in range(1, n)], 0)
