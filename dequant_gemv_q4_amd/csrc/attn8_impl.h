@@ -257,12 +257,15 @@ __device__ __forceinline__ void attn8_body(const AttnArgs &a, int slots, int id,
             }
             const float most = ROWS && edge ? max_of_16(exponent_above(seen)) : exponent_above(seen);
             if (most > r + R_SLACK) {                     // (uniform)
-                const float f = __builtin_amdgcn_exp2f(r - most);
-                top = fmaxf(top + (r - most), LEAST_TOP);
+                const Moved x = moved_reference(r, most, exponent_above(seen), top, shift,
+                                                exponent_above(max_x32(max_x16(l))));
                 r = most;
+                top = x.top;
+                shift = x.shift;
+                l *= x.l;
 #pragma unroll
                 for (int d = 0; d < DT; ++d)
-                    o[d] *= f;
+                    o[d] *= x.o;
             }
             dv = ldexpf(dv, -(int)r);
             top = fmaxf(top, exponent_above(seen) - r);

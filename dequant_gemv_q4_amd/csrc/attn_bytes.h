@@ -6,11 +6,14 @@
 // over f16 pages.
 //
 // What has to fit f16 is the weight times the scale of V, w = p d^V.  The scales are taken relative to 2^r, r
-// a whole number that follows the largest scale that a wave has met, and a column keeps the exponent `top` of
-// the largest relative scale that it has seen (at least LEAST_TOP): its shift puts the largest p at
-// 2^(LIFT - top), so that w is at most 2^LIFT when the shift moves and under 2^TOP afterwards.  Of w 2^-25 is
-// lost at most: 2^-35 of the largest weight times the largest scale that the column sees.  Sums of p stay in
-// f32.
+// a whole number that follows the largest scale that any column of a wave has met, and a column keeps the exponent
+// `top` of the largest relative scale that it has seen (at least LEAST_TOP): its shift puts the largest p at
+// 2^(LIFT - top), so that w is at most 2^LIFT when the shift moves and under 2^TOP afterwards.  When r moves up,
+// a column's top goes down and its shift up by as much (moved_reference), so that what it weighs from then on is as
+// large as before; left alone, with V 2^29 and then 2^31 times larger than at first, the last weights kept four
+// bits.  Of w 2^-25 is lost at most: 2^-35 of the largest weight times the largest scale that the column sees, as
+// long as that scale is at least 2^LEAST_TOP of the largest that another column of the wave has seen.  Sums of p
+// stay in f32: p is at most 2^(TOP - LEAST_TOP) = 2^96, of 2^24 positions 2^120.
 #pragma once
 
 #include <utility>
@@ -20,8 +23,9 @@
 namespace qg {
 
 constexpr float LIFT8 = LIFT<KV_F16>, TOP8 = TOP<KV_F16>;
-constexpr float LEAST_TOP = -30.0f;            // so far below 2^r, scales lose bits instead
+constexpr float LEAST_TOP = -80.0f;            // so far below 2^r, scales lose bits instead
 constexpr float R_SLACK = 30.0f;               // 2^r moves when a scale is so far above it
+constexpr float MOST_SUM = 114.0f;             // the exponent up to which a move of 2^r may raise a sum of weights
 
 // Sixteen codes as f16, in order.
 template <int T>
@@ -101,6 +105,30 @@ __device__ __forceinline__ float shift8_of(float top_score, float top)
 {
     const float r = LIFT8 - top - top_score;
     return r + top_score > TOP8 - top ? -top_score - top - fabsf(top_score) * 0x1p-23f : r;
+}
+
+// A column as the wave's reference moves from 2^r to 2^to: own is the exponent of the largest scale that it sees
+// in this step, sum that of its sum of weights (over its lanes).  The shift rises by what top falls, but not so
+// far that the sum could reach f32's end: a column whose sum would has weighed positions with small scales by 2^92 or
+// more (2^114 over the 2^22 positions of a wave), and needs no further bits for what comes.  Where scores are so
+// large that the shift is rounded up by more than it has to rise, it stays.
+struct Moved {
+    float top, shift, l, o;                    // top and shift from now on; factors of the sum and of O
+};
+__device__ __forceinline__ Moved moved_reference(float r, float to, float own, float top, float shift, float sum)
+{
+    Moved x;
+    x.top = fmaxf(fmaxf(top + (r - to), own - to), LEAST_TOP);
+    const float rise = fmaxf(fminf(top - x.top, MOST_SUM - sum), 0.f);
+    x.shift = shift + rise;
+    float by = x.shift - shift;
+    if (by > rise + 1.0f) {
+        x.shift = shift;
+        by = 0.f;
+    }
+    x.l = __builtin_amdgcn_exp2f(by);
+    x.o = __builtin_amdgcn_exp2f(by + (r - to));
+    return x;
 }
 
 // A part of a column's positions is held as its mean (weighted by the weights), the exponent m of its weights

@@ -339,14 +339,16 @@ __device__ __forceinline__ void prompt_body(const AttnArgs &a, int slots, int id
     // the scales dv of a step's tiles relative to 2^ref, and the largest that the row sees
     auto follow = [&](float (&dv)[NT], float seen, float most) {
         if (most > ref + R_SLACK) {                       // (uniform)
-            const float f = __builtin_amdgcn_exp2f(ref - most);
-            top = fmaxf(top + (ref - most), LEAST_TOP);
+            const Moved x = moved_reference(ref, most, exponent_above(seen), top, shift, exponent_above(max_x32(l)));
             ref = most;
+            top = x.top;
+            shift = x.shift;
+            l *= x.l;
 #pragma unroll
             for (int d = 0; d < DT; ++d)
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
-                    o[d][r] *= f;
+                    o[d][r] *= x.o;
         }
         top = fmaxf(top, exponent_above(seen) - ref);
 #pragma unroll

@@ -358,9 +358,10 @@ int qgemv_attn(int kv_type, const void *k_pages, const void *v_pages, int64_t n_
  * products with f16 K and V as the sum of two f16 values (22 bits; of q below 2^-16 of the row's
  * largest 2^-38 of that, of probabilities 2^-35 of the row's largest, is lost at most), with bf16 as
  * that of three bf16 values (24 bits); K and V exactly as stored.  Over 8-bit pages the codes enter
- * exactly, as f16, the scales of K multiply f32 scores and those of V f32 weights, and the products are as with f16 (of
- * a weight times its scale 2^-35 of the row's largest weight times the largest scale that it sees is
- * lost at most).  A NaN or an infinity in a query makes the
+ * exactly, as f16, the scales of K multiply f32 scores and those of V f32 weights, and the products
+ * are as with f16 (of a weight times its scale 2^-35 of the row's largest weight times the largest
+ * scale of V that it sees is lost at most; where rows computed beside it see a scale more than 2^80
+ * times as large, a bit more for each factor of two beyond that).  A NaN or an infinity in a query makes the
  * outputs of its row and head non-finite, one in K or V those of the rows that see its position (of V
  * its channel's; NaN also where the definition gives an infinity), and touches no other row.  Only an
  * infinity in K whose score comes out as -inf has weight 0; a row all of whose scores are -inf gets 0,
