@@ -86,7 +86,9 @@ __device__ __forceinline__ void attn8_body(const AttnArgs &a, int slots, int id,
     // queries of column i: scaled, split, in the order of the channels in K's operands
     auto channel = [&](int k) { return k < 2 * KP ? 64 * (k >> 1) + 16 * g + 8 * (k & 1) : 64 * KP + 8 * g; };
     au4 qf[Q_LDS ? 1 : NP][Q_LDS ? 1 : KB];
-    float unscale;
+    // a score is (product * unscale) * d^K * lift: lift, a power of two from 1 on, takes what queries near f32's
+    // end would make of the first product, which K's scale may bring down again
+    float unscale, lift = 1.0f;
     {
         const int col = i < cols ? i : 0;
         const float *qr = a.q + (int64_t)row_of(col) * a.q_stride + (int64_t)head_of(col) * D;
@@ -105,6 +107,12 @@ __device__ __forceinline__ void attn8_body(const AttnArgs &a, int slots, int id,
         }
         const float sc = q_scale<KV_F16>(max_x32(max_x16(amax)));
         unscale = f / sc;
+        int e2 = 0;
+        frexpf(unscale, &e2);
+        if (e2 > 0) {
+            lift = ldexpf(1.0f, e2);
+            unscale = ldexpf(unscale, -e2);
+        }
 #pragma unroll
         for (int k = 0; k < KB; ++k) {
             float w[8];
@@ -273,6 +281,7 @@ __device__ __forceinline__ void attn8_body(const AttnArgs &a, int slots, int id,
 #pragma unroll
             for (int e = 1; e < 16; ++e)
                 mx = fmaxf(mx, sc[e]);
+            mx *= lift;
             if (__any(mx + shift > TOP8 - top)) {
                 const float to = fminf(shift, shift8_of(max_x32(max_x16(mx)), top));
                 const float f = __builtin_amdgcn_exp2f(to - shift);
@@ -284,7 +293,7 @@ __device__ __forceinline__ void attn8_body(const AttnArgs &a, int slots, int id,
             }
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-                sc[e] = __builtin_amdgcn_exp2f(sc[e] + shift);
+                sc[e] = __builtin_amdgcn_exp2f(fmaf(sc[e], lift, shift));
                 l += sc[e];
             }
             times_lanes([&](int e) -> float & { return sc[e]; }, dv);

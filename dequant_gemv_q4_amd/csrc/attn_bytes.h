@@ -26,6 +26,9 @@ constexpr float LIFT8 = LIFT<KV_F16>, TOP8 = TOP<KV_F16>;
 constexpr float LEAST_TOP = -80.0f;            // so far below 2^r, scales lose bits instead
 constexpr float R_SLACK = 30.0f;               // 2^r moves when a scale is so far above it
 constexpr float MOST_SUM = 114.0f;             // the exponent up to which a move of 2^r may raise a sum of weights
+// Raw products are below 2^32 (queries to 2^14 log2 e, codes to 448, 256 channels): times K_ROOM of any scale of K
+// they stay within f32.
+constexpr float K_ROOM = 0x1p-32f;
 
 // Sixteen codes as f16, in order.
 template <int T>

@@ -154,6 +154,7 @@ __device__ __forceinline__ void prompt_body(const AttnArgs &a, int slots, int id
 
     au4 qf[NP][KB];
     float unscale;
+    float k_room = 1.0f;                               // (uniform)
     {
         const float *qr = a.q + (int64_t)(p.row0 + (live ? tok : 0)) * a.q_stride + (int64_t)head * D;
         float v[KB][8], amax = 0.f;
@@ -174,6 +175,14 @@ __device__ __forceinline__ void prompt_body(const AttnArgs &a, int slots, int id
         int e2 = 0;
         const float f = frexpf(a.scale, &e2) * LOG2E, sc = q_scale<F>(max_x32(amax));
         unscale = fmaxf(ldexpf(1.0f / sc, e2), 0x1p-149f);
+        // 8-bit: a product times K's scale must not leave f32 where unscale brings the score back, and with K_ROOM of
+        // the scale it does not.  What that takes from scales below 2^-94 is nothing to a score (2^-26 of its
+        // exponent), unless queries are so near f32's end that it could be: then scales stay as they are.  (8192
+        // rows, 32 / 8 heads of 128, I8, 1016 -> 1021 us; a vote on the scales of each step instead 1027.)
+        if constexpr (BYTES) {
+            k_room = __any(unscale > 0x1p60f) ? 1.0f : K_ROOM;
+            unscale *= 1.0f / k_room;
+        }
 #pragma unroll
         for (int k = 0; k < KB; ++k) {
             float w[8];
@@ -498,7 +507,7 @@ __device__ __forceinline__ void prompt_body(const AttnArgs &a, int slots, int id
                     for (int tt = 0; tt < NT; ++tt) {
                         const int at = scale_at(NT * sub + tt);
                         dv[tt] = sh.scale[buf][1][at];
-                        times_lanes([&](int r) { return Ref<af16>{sc[tt], r}; }, sh.scale[buf][0][at]);
+                        times_lanes([&](int r) { return Ref<af16>{sc[tt], r}; }, sh.scale[buf][0][at] * k_room);
                     }
                 // value r of tile tt is position t0 + 32 (NT sub + tt) + 16 (r / 8) + 8 hf + r % 8
                 if (edge) {

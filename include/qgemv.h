@@ -361,7 +361,9 @@ int qgemv_attn(int kv_type, const void *k_pages, const void *v_pages, int64_t n_
  * exactly, as f16, the scales of K multiply f32 scores and those of V f32 weights, and the products
  * are as with f16 (of a weight times its scale 2^-35 of the row's largest weight times the largest
  * scale of V that it sees is lost at most; where rows computed beside it see a scale more than 2^80
- * times as large, a bit more for each factor of two beyond that).  A NaN or an infinity in a query makes the
+ * times as large, a bit more for each factor of two beyond that).  Scores are right wherever they are
+ * within f32, except in qgemv_attn_prompt and qgemv_attn_shared against scales of K above 2^96 beside a
+ * row with values of scale * q above 2^72.  A NaN or an infinity in a query makes the
  * outputs of its row and head non-finite, one in K or V those of the rows that see its position (of V
  * its channel's; NaN also where the definition gives an infinity), and touches no other row.  Only an
  * infinity in K whose score comes out as -inf has weight 0; a row all of whose scores are -inf gets 0,

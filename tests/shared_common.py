@@ -25,12 +25,13 @@ class Batch:
     """Sequences with dense rows K, V of each ([len][nkv][hd], what is shared written out in all of them), each in
     pages of its own."""
 
-    def __init__(self, kv_type, K, V, nq, nkv, hd, page=16, seed=0, extra_entries=2):
+    def __init__(self, kv_type, K, V, nq, nkv, hd, page=16, seed=0, extra_entries=2, q_size=1.0,
+                 scale=None):
         rng = np.random.default_rng([95, seed])
         self.kv_type, self.K, self.V, self.nq, self.nkv, self.hd = kv_type, K, V, nq, nkv, hd
-        self.n, self.scale = len(K), hd ** -0.5
+        self.n, self.scale = len(K), hd ** -0.5 if scale is None else scale
         self.c = Cache(kv_type, K, V, page, nkv, hd, rng, extra_entries=extra_entries)
-        self.x = rng.standard_normal((self.n, nq * hd)).astype(np.float32)
+        self.x = (rng.standard_normal((self.n, nq * hd)) * q_size).astype(np.float32)
         self.q = dev(self.x)
         self.ws = D.attn_workspace(q.OP_ATTN_SHARED, self.n, nq, nkv, hd)
 

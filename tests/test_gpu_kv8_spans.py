@@ -75,3 +75,46 @@ def test_shares_that_end_before_values_far_larger(kv_type, n, nq, form):
     got, flag = batch.call([0, n], share, lens)
     batch.check(got, lens)
     assert flag == 0
+
+
+@pytest.mark.parametrize("kv_type", BYTES)
+@pytest.mark.parametrize("k_size,q_size", [(1e30, 1.0), (1e33, 1.0), (1e36, 1e-5), (1e-36, 1e37), (1e-30, 1e30), (1e36, 1e-36)])
+@pytest.mark.parametrize("rows,n,prompt,hd", [(1, 900, False, 64), (1, 700, False, 256), (40, 300, True, 128),
+                                              (700, 800, True, 64), (500, 700, True, 256)])
+def test_scores_of_keys_and_queries_of_any_size(kv_type, k_size, q_size, rows, n, prompt, hd):
+    """Ordinary scores of K near either end of f32's range, where the products on the way are not."""
+    rng = np.random.default_rng([34, hd])
+    K, V = _draw(rng, [n], 1, hd, 0.0)
+    K[0] *= np.float32(k_size)
+    assert not prompt or in_16s(rows, 1, 4, 1, hd, n + 16384) == (rows < 300)
+    attend(kv_type, 4, 1, hd, 16, [(rows, n)], 1, K=K, V=V, prompt=prompt, extra_entries=1024 if prompt else 2,
+           scale=hd ** -0.5 / (k_size * q_size), qmul=q_size)
+
+
+@pytest.mark.parametrize("kv_type", BYTES)
+@pytest.mark.parametrize("rows,n", [(40, 300), (700, 800)])
+def test_scores_of_keys_of_all_sizes_in_one_step(kv_type, rows, n):
+    """Keys from 1e-35 to 1e35 side by side, and queries from 1e-30 to 1e2: a large one's score is the row's
+    maximum or its minimum, the small ones' are near zero."""
+    rng = np.random.default_rng(35)
+    K, V = _draw(rng, [n], 1, 64, 0.0)
+    K[0] *= (10.0 ** rng.integers(-35, 36, (n, 1, 1))).astype(np.float32)
+    assert in_16s(rows, 1, 4, 1, 64, n + 16384) == (rows < 300)
+    for qmul in (1e-30, 1e-10, 1e2):
+        attend(kv_type, 4, 1, 64, 16, [(rows, n)], 2, K=K, V=V, extra_entries=1024, scale=1e-3, qmul=qmul)
+
+
+@pytest.mark.parametrize("kv_type", BYTES)
+@pytest.mark.parametrize("n,nq,form", [(6, 4, "16"), (520, 16, "parted")])
+@pytest.mark.parametrize("k_size,q_size", [(1e33, 1.0), (1e-36, 1e37)])
+def test_scores_behind_a_prefix_of_keys_of_any_size(kv_type, n, nq, form, k_size, q_size):
+    rng = np.random.default_rng(36)
+    K, V = _draw(rng, [150] * n, 1, 64, 0.0)
+    for b in range(1, n):
+        K[b][:130], V[b][:130] = K[0][:130], V[0][:130]
+    K = [k * np.float32(k_size) for k in K]
+    batch = Batch(kv_type, K, V, nq, 1, 64, q_size=q_size, scale=0.125 / (k_size * q_size))
+    assert batch.form(1) == form
+    got, flag = batch.call([0, n], [130] * n, [150] * n)
+    batch.check(got, [150] * n)
+    assert flag == 0
