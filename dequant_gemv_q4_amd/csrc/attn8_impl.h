@@ -59,7 +59,7 @@ __device__ __forceinline__ void attn8_body(const AttnArgs &a, int slots, int id,
     const int b = FORM == PREFIX ? p.row0 : p.b, chunk = p.chunk, n_chunk = p.n_chunk;
     // behind a prefix: the shared positions are in the pages of another, the plan's begin at base
     const int shared = behind(FORM) ? shared_of(a, b) : 0, base = behind(FORM) ? suffix_base(shared) : 0;
-    const int len = behind(FORM) && p.len > 0 ? base + p.len : p.len;
+    int len = behind(FORM) && p.len > 0 ? base + p.len : p.len;
     const int tiles = (p.rows * a.group + 15) / 16, hkv = p.pair / tiles, rho0 = p.pair % tiles * 16;
     const int cols = min(16, p.rows * a.group - rho0);
     auto head_of = [&](int col) { return hkv * a.group + (ROWS ? (rho0 + col) % a.group : rho0 + col); };
@@ -70,11 +70,15 @@ __device__ __forceinline__ void attn8_body(const AttnArgs &a, int slots, int id,
     const int per = units / n_chunk, more = units % n_chunk;
     const int unit0 = chunk * per + min(chunk, more);
     const int t_begin = base + (unit0 << Attn8Cols::UNIT_LOG2);
-    const int t_end = min(len, base + ((unit0 + per + (chunk < more ? 1 : 0)) << Attn8Cols::UNIT_LOG2));
+    int t_end = min(len, base + ((unit0 + per + (chunk < more ? 1 : 0)) << Attn8Cols::UNIT_LOG2));
     // positions this lane's column sees, [0, see), and those that all columns see
     int see = t_end, see_all = t_end;
     if constexpr (FORM == PREFIX) {
-        see = min(t_end, prefix_seen(a, row_of(min(i, cols - 1)), p.row0, len));
+        // what none of these rows sees is not read (positions are below 2^24, whole numbers in f32)
+        const int seen = prefix_seen(a, row_of(min(i, cols - 1)), len);
+        len = __builtin_amdgcn_readfirstlane((int)max_of_16((float)seen));
+        t_end = min(t_end, len);
+        see = min(t_end, seen);
         see_all = -(int)max_of_16(-(float)see);
     } else if constexpr (FORM == MANY) {
         const int pos0 = max(c.kv_len[b], -(1 << 30)) - p.rows;

@@ -295,16 +295,14 @@ struct AttnSeq {
     int n, pairs, row0, rows;
 };
 
-// Of n positions those that have a place in a table.
-__device__ __forceinline__ int placed(const KvArgs &c, int n)
+// Positions of sequence b that have a place in its table.
+__device__ __forceinline__ int seq_len(const KvArgs &c, int b)
 {
-    const int cap = c.max_pages << c.ps_log2;                           // cap <= 2^24
+    const int n = c.kv_len[b], cap = c.max_pages << c.ps_log2;          // cap <= 2^24
     if (n > cap)
         atomicOr(c.err, 1u);
     return n < 0 ? 0 : n < cap ? n : cap;
 }
-// Positions of sequence b that have a place in its table.
-__device__ __forceinline__ int seq_len(const KvArgs &c, int b) { return placed(c, c.kv_len[b]); }
 
 // What a workgroup of the attention kernels attends to: one new row of each sequence (ONE), several (MANY),
 // or for sequences that begin alike the shared positions for all rows of a group (PREFIX: the plan's
@@ -324,12 +322,13 @@ __device__ __forceinline__ int shared_of(const AttnArgs &a, int b)
 // SUFFIX, TAIL: the plan counts from the last multiple of 16 in the shared positions.
 __device__ __forceinline__ int suffix_base(int shared) { return shared & ~15; }
 
-// Positions that the plan counts of its sequence b, whose rows begin with row0.
+// Positions that the plan counts of its sequence b, whose rows begin with row0.  (PREFIX: what the first sequence
+// shares, though no row may see all of it.)
 template <int FORM>
 __device__ __forceinline__ int plan_len(const AttnArgs &a, int b, int row0, int rows)
 {
     if constexpr (FORM == PREFIX) {
-        return rows > 0 ? placed(a.c, a.shared_len[row0]) : 0;
+        return rows > 0 ? min(max(a.shared_len[row0], 0), a.c.max_pages << a.c.ps_log2) : 0;
     } else if constexpr (behind(FORM)) {
         const int n = seq_len(a.c, b), s = shared_of(a, b);
         return n > s ? n - suffix_base(s) : 0;
@@ -338,12 +337,12 @@ __device__ __forceinline__ int plan_len(const AttnArgs &a, int b, int row0, int 
     }
 }
 // PREFIX: of the shared positions `len` of the group's first sequence, those that a row sees.
-__device__ __forceinline__ int prefix_seen(const AttnArgs &a, int row, int first, int len)
+__device__ __forceinline__ int prefix_seen(const AttnArgs &a, int row, int len)
 {
-    const int n = a.shared_len[row];
-    if (n > a.shared_len[first])
+    const int n = min(a.shared_len[row], a.c.kv_len[row]);
+    if (n > len)                                           // it shares more, and has more
         atomicOr(a.c.err, 1u);
-    return max(min(min(n, a.c.kv_len[row]), len), 0);
+    return max(min(n, len), 0);
 }
 
 // First new row of sequence i, cut to the rows there are.

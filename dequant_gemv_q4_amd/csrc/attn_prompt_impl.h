@@ -73,7 +73,7 @@ struct PromptLds {
     static constexpr int HALF = PT_STEP * D * 2;
     __attribute__((aligned(1024))) uint8_t kv[4 * HALF];               // K0 V0 K1 V1
     float scale[kv_bytes(T) ? 2 : 1][2][PT_STEP];                      // 8-bit: of K and V
-    int odd[4], last;
+    int odd[4], most[4], last;
 };
 
 // FEW: there are at least as many tiles as slots, and only those behind much longer contexts than the rest
@@ -121,7 +121,6 @@ __device__ __forceinline__ void prompt_body(const AttnArgs &a, int slots, int id
     // this chunk's steps, as far as the tile reads
     const int units = PromptCols::units(w.len), per = units / w.n_chunk, more = units % w.n_chunk;
     const int s0 = w.chunk * per + min(w.chunk, more);
-    const int s1 = min(s0 + per + (w.chunk < more ? 1 : 0), PromptCols::units(p.hi));
     if (w.all && (w.n_chunk > 1 || SHARED == PARTED) && w.chunk == 0 && tid == 0)
         a.splits[w.first_pair + w.pair] = PromptSplit{w.slot0, w.n_chunk, p.row0, p.rows, p.rho0, hkv, {0, 0}};
     if (w.all && w.n_chunk == 1 && SHARED != PARTED && tid == 0)
@@ -141,16 +140,20 @@ __device__ __forceinline__ void prompt_body(const AttnArgs &a, int slots, int id
     int tile_min = min(p.pos0 + p.rho0 / a.group, p.hi - 1);
     if constexpr (SHARED) {
         // (positions of a table are below 2^24, whole numbers in f32)
-        pos = live ? prefix_seen(a, p.row0 + tok, p.row0, w.len) - 1 : -1;
-        wave_max = (int)max_x16(max_of_16((float)pos));
+        pos = live ? prefix_seen(a, p.row0 + tok, w.len) - 1 : -1;
+        wave_max = __builtin_amdgcn_readfirstlane((int)max_x16(max_of_16((float)pos)));
         const int least = -(int)max_x16(max_of_16(live ? -(float)pos : -(float)p.hi));
         sh.odd[wave] = __builtin_amdgcn_readfirstlane(least);
-        wave_max = __builtin_amdgcn_readfirstlane(wave_max);
+        sh.most[wave] = wave_max;
         __syncthreads();
+        // what none of the tile's rows sees is not read
+        const int most = max(max(sh.most[0], sh.most[1]), max(sh.most[2], sh.most[3]));
+        p.hi = min(p.hi, __builtin_amdgcn_readfirstlane(most) + 1);
         tile_min = min(min(sh.odd[0], sh.odd[1]), min(sh.odd[2], sh.odd[3]));
         tile_min = min(__builtin_amdgcn_readfirstlane(tile_min), p.hi - 1);
         __syncthreads();
     }
+    const int s1 = min(s0 + per + (w.chunk < more ? 1 : 0), PromptCols::units(p.hi));
 
     au4 qf[NP][KB];
     float unscale;

@@ -380,8 +380,9 @@ int qgemv_attn_prompt(int kv_type, const void *k_pages, const void *v_pages, int
  * group_start[g + 1] - 1 (int32 [n_group + 1], not decreasing, within [0, n_seq]); a sequence before
  * the first or behind the last group shares nothing.  The first shared_len[b] positions of sequence b
  * (int32 [n_seq]; below 1: none) are those of its group's first sequence, and are read from that one's
- * pages: its shared_len has to be its group's largest.  Of another's that is larger the positions
- * between are left out, and the flag is set.  The positions from shared_len[b] on, a begun page
+ * pages, as far as any of the group sees them: its shared_len has to be its group's largest.  Of
+ * another's that is larger the positions between that it sees are left out, and the flag is set.  The
+ * positions from shared_len[b] on, a begun page
  * included, are read from the sequence's own pages.  As everywhere, a sequence sees kv_len[b]
  * positions in all, also where shared_len[b] is larger.  1 <= n_group <= n_seq.  (Group starts out of order
  * leave outputs unwritten and arrival counts behind: the workspace has to be zero-filled again.) */

@@ -1,0 +1,78 @@
+"""Shared prefixes with shares, lengths and groups at the ends of what the device may find, on the GPU against the
+definition in 64 bits: every form of the kernels, and what the sticky flag says."""
+import numpy as np
+import pytest
+
+from gpu_common import require_gpu
+
+import dequant_gemv_q4_amd as q
+from kv_common import ALL
+from shared_common import Batch
+from test_gpu_kv8 import _draw
+
+pytestmark = pytest.mark.gpu
+
+# rows, query heads, KV heads, channels, groups: forms of the kernels
+FORMS = [(5, 4, 1, 64, 1, "16"), (520, 16, 1, 64, 1, "parted"), (140, 64, 1, 192, 2, "parted")]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    require_gpu()
+
+
+def alike(kv_type, n, nq, nkv, hd, form, prefix=150, own=20, n_group=1, seed=0, **kw):
+    """n sequences of prefix + own positions; the same prefix in all of them."""
+    rng = np.random.default_rng([41, seed])
+    K, V = _draw(rng, [prefix + own] * n, nkv, hd)
+    for b in range(1, n):
+        K[b][:prefix], V[b][:prefix] = K[0][:prefix], V[0][:prefix]
+    batch = Batch(kv_type, K, V, nq, nkv, hd, **kw)
+    assert batch.form(n_group) == form
+    return batch
+
+
+@pytest.mark.parametrize("kv_type", ALL)
+@pytest.mark.parametrize("n,nq,nkv,hd,n_group,form", FORMS)
+def test_positions_that_no_row_sees_are_not_read(kv_type, n, nq, nkv, hd, n_group, form):
+    """A share that is longer than every sequence of the group (a stale one of padded slots, say): entries behind the
+    longest are not read, whatever they hold, and set no flag."""
+    batch = alike(kv_type, n, nq, nkv, hd, form, n_group=n_group)
+    starts = [0, n] if n_group == 1 else [0, n // 2, n]
+    lens = [(7 * b) % 41 for b in range(n)]                  # at most 40 positions: three pages of 16
+    batch.c.table[:, 3:] = -1
+    got, flag = batch.call(starts, [150] * n, lens)
+    batch.check(got, lens)
+    assert flag == 0
+    lens = [10] + [100 - b % 60 for b in range(1, n)]        # the first is short, others see what its pages hold
+    batch = alike(kv_type, n, nq, nkv, hd, form, n_group=n_group, seed=1)
+    batch.c.table[:, 7:] = 2 ** 30
+    got, flag = batch.call(starts, [150] * n, lens)
+    batch.check(got, lens)
+    assert flag == 0
+
+
+@pytest.mark.parametrize("kv_type", ALL)
+@pytest.mark.parametrize("n,nq,nkv,hd,n_group,form", FORMS)
+def test_flag_only_for_what_is_left_out(kv_type, n, nq, nkv, hd, n_group, form):
+    """No flag for shares below zero or beyond the table where no sequence is, nor for a share larger than the
+    first's of a sequence that ends before; one for positions between that are seen, which are left out."""
+    batch = alike(kv_type, n, nq, nkv, hd, form, n_group=n_group)
+    starts = [0, n] if n_group == 1 else [0, n // 2, n]
+    lens = [160 - b % 90 for b in range(n)]
+    for share in ([-7 if b in starts else -(b % 2) for b in range(n)], [2 ** 31 - 1] * n):
+        batch = alike(kv_type, n, nq, nkv, hd, form, n_group=n_group, own=10 if share[0] > 0 else 20)
+        if share[0] > 0:                                     # only what the first sequences hold is shared
+            lens = [min(x, 150) for x in lens]
+        got, flag = batch.call(starts, share, lens)
+        batch.check(got, lens)
+        assert flag == 0
+    share = [40 if b in starts else 64 for b in range(n)]
+    lens = [90 if b in starts else 40 - b % 3 for b in range(n)]
+    got, flag = batch.call(starts, share, lens)
+    batch.check(got, lens)
+    assert flag == 0
+    lens[n - 1] = 80
+    got, flag = batch.call(starts, share, lens)
+    batch.check(got, [np.r_[0:40, 64:80] if b == n - 1 else lens[b] for b in range(n)])
+    assert flag == 1
