@@ -58,7 +58,7 @@ __device__ __forceinline__ void attn8_body(const AttnArgs &a, int slots, int id,
     // (PREFIX: a group's first sequence, whose pages are read)
     const int b = FORM == PREFIX ? p.row0 : p.b, chunk = p.chunk, n_chunk = p.n_chunk;
     // behind a prefix: the shared positions are in the pages of another, the plan's begin at base
-    const int shared = behind(FORM) ? shared_of(a, b) : 0, base = behind(FORM) ? suffix_base(shared) : 0;
+    const int shared = behind(FORM) && p.sound ? shared_of(a, b) : 0, base = behind(FORM) ? suffix_base(shared) : 0;
     int len = behind(FORM) && p.len > 0 ? base + p.len : p.len;
     const int tiles = (p.rows * a.group + 15) / 16, hkv = p.pair / tiles, rho0 = p.pair % tiles * 16;
     const int cols = min(16, p.rows * a.group - rho0);

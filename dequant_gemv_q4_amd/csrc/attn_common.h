@@ -288,6 +288,7 @@ struct AttnPlan {
     bool all;                      // fewer pairs than slots: all of them share the slots
     int len;                       // the sequence's positions
     int row0, rows;                // its new rows
+    bool sound;                    // groups' starts are in order; if not, nothing is shared
 };
 
 // What the plan has to know of a sequence.
@@ -311,7 +312,7 @@ __device__ __forceinline__ int seq_len(const KvArgs &c, int b)
 enum AttnForm { ONE, MANY, PREFIX, SUFFIX, TAIL };
 constexpr bool behind(int form) { return form == SUFFIX || form == TAIL; }
 
-// Shared positions of sequence b: none outside the groups.
+// Shared positions of sequence b, if the groups' starts are in order: none outside the groups.
 __device__ __forceinline__ int shared_of(const AttnArgs &a, int b)
 {
     if (b < a.group_start[0] || b >= a.group_start[a.n_group])
@@ -325,12 +326,12 @@ __device__ __forceinline__ int suffix_base(int shared) { return shared & ~15; }
 // Positions that the plan counts of its sequence b, whose rows begin with row0.  (PREFIX: what the first sequence
 // shares, though no row may see all of it.)
 template <int FORM>
-__device__ __forceinline__ int plan_len(const AttnArgs &a, int b, int row0, int rows)
+__device__ __forceinline__ int plan_len(const AttnArgs &a, int b, int row0, int rows, bool sound)
 {
     if constexpr (FORM == PREFIX) {
         return rows > 0 ? min(max(a.shared_len[row0], 0), a.c.max_pages << a.c.ps_log2) : 0;
     } else if constexpr (behind(FORM)) {
-        const int n = seq_len(a.c, b), s = shared_of(a, b);
+        const int n = seq_len(a.c, b), s = sound ? shared_of(a, b) : 0;
         return n > s ? n - suffix_base(s) : 0;
     } else {
         return seq_len(a.c, b);
@@ -650,14 +651,18 @@ __device__ __forceinline__ bool attn_plan_of(const KvArgs &c, int n_seq, int gro
 // scratch (QG_ATTN_MAX_SEQ entries, free again afterwards).  Sequence b has the rows between its
 // q_start and the next (MANY, PREFIX); else one row, row b.  slots 0: nothing is split.  INDEX: all pairs
 // or only the longest are split, as `all` says.
+// Groups whose starts are out of order or range would leave rows to no workgroup or to two, and counts of arrivals
+// behind: then the flag is set, there is no prefix, and what is behind it is all of a sequence.  The starts are
+// loaded beside the lengths, which are taken as if in order and again if not.
 template <class P, int FORM>
 __device__ __forceinline__ bool attn_plan(const AttnArgs &a, int slots, int id, AttnPlan &p, AttnSeq *scratch,
                                           bool all = true)
 {
-    constexpr bool ROWS = FORM == MANY || FORM == PREFIX;
+    constexpr bool ROWS = FORM == MANY || FORM == PREFIX, GROUPS = FORM == PREFIX || behind(FORM);
     const KvArgs &c = a.c;
     const int lane = threadIdx.x & 63, group = a.group;
-    auto load = [&](int b) {
+    p.sound = true;
+    auto load = [&](int b, bool sound) {
         AttnSeq s = {0, 0, b, 0};
         if (b < c.n_seq) {
             s.rows = 1;
@@ -665,13 +670,34 @@ __device__ __forceinline__ bool attn_plan(const AttnArgs &a, int slots, int id, 
                 s.row0 = row_start(c, b);
                 s.rows = max(row_start(c, b + 1) - s.row0, 0);
             }
-            s.n = plan_len<FORM>(a, b, s.row0, s.rows);
+            s.n = plan_len<FORM>(a, b, s.row0, s.rows, sound);
             s.pairs = c.nkv * (int)(((int64_t)s.rows * group + P::COLS - 1) / P::COLS);
         }
         return s;
     };
+    auto broken = [&](int from, int to) { return from < 0 || from > to || to > a.rows_in_all; };
+    // no plan of groups out of order
+    auto none = [&]() {
+        if (threadIdx.x == 0)
+            atomicOr(c.err, 1u);
+        p.all = false;
+        p.pairs = 0;
+        return FORM == PREFIX;
+    };
     if (c.n_seq <= 64) {
-        const AttnSeq s = load(lane);
+        int from = 0, to = 0;
+        if constexpr (GROUPS) {                           // (no more groups than sequences)
+            const int g = min(lane, a.n_group - 1);
+            from = a.group_start[g];
+            to = a.group_start[g + 1];
+        }
+        AttnSeq s = load(lane, true);
+        if (GROUPS && __any(broken(from, to))) {
+            p.sound = false;
+            if (none())
+                return false;
+            s = load(lane, false);
+        }
         return attn_plan_of<P, ROWS>(c, 1, group, slots, all, id, p, [&](int) { return s; }, [&]() {
             AttnTotals t = {0, 0, 0};
             t.add<P>(s);
@@ -679,16 +705,34 @@ __device__ __forceinline__ bool attn_plan(const AttnArgs &a, int slots, int id, 
         });
     }
     __shared__ AttnTotals s_tot[4];
-    AttnTotals t = {0, 0, 0};
-    for (int b = threadIdx.x; b < (c.n_seq + 63) / 64 * 64; b += 256) {
-        const AttnSeq s = load(b);
-        scratch[b] = s;
-        t.add<P>(s);
+    __shared__ int s_broken[4];
+    auto fill = [&](bool sound) {
+        AttnTotals t = {0, 0, 0};
+        for (int b = threadIdx.x; b < (c.n_seq + 63) / 64 * 64; b += 256) {
+            const AttnSeq s = load(b, sound);
+            scratch[b] = s;
+            t.add<P>(s);
+        }
+        t = t.of_wave();
+        if (lane == 0)
+            s_tot[threadIdx.x >> 6] = t;
+    };
+    if constexpr (GROUPS) {
+        bool bad = false;
+        for (int g = threadIdx.x; g < a.n_group; g += 256)
+            bad |= broken(a.group_start[g], a.group_start[g + 1]);
+        s_broken[threadIdx.x >> 6] = __any(bad);
     }
-    t = t.of_wave();
-    if (lane == 0)
-        s_tot[threadIdx.x >> 6] = t;
+    fill(true);
     __syncthreads();
+    if (GROUPS && (s_broken[0] | s_broken[1] | s_broken[2] | s_broken[3])) {
+        p.sound = false;
+        if (none())
+            return false;
+        __syncthreads();
+        fill(false);
+        __syncthreads();
+    }
     const bool found = attn_plan_of<P, ROWS>(
         c, c.n_seq, group, slots, all, id, p, [&](int b0) { return scratch[b0 + lane]; }, [&]() {
             AttnTotals v = {0, 0, 0};

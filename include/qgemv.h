@@ -382,10 +382,10 @@ int qgemv_attn_prompt(int kv_type, const void *k_pages, const void *v_pages, int
  * (int32 [n_seq]; below 1: none) are those of its group's first sequence, and are read from that one's
  * pages, as far as any of the group sees them: its shared_len has to be its group's largest.  Of
  * another's that is larger the positions between that it sees are left out, and the flag is set.  The
- * positions from shared_len[b] on, a begun page
- * included, are read from the sequence's own pages.  As everywhere, a sequence sees kv_len[b]
- * positions in all, also where shared_len[b] is larger.  1 <= n_group <= n_seq.  (Group starts out of order
- * leave outputs unwritten and arrival counts behind: the workspace has to be zero-filled again.) */
+ * positions from shared_len[b] on, a begun page included, are read from the sequence's own pages.  As
+ * everywhere, a sequence sees kv_len[b] positions in all, also where shared_len[b] is larger.  Group
+ * starts out of order or range set the flag, and no sequence of the call shares anything: each reads all
+ * of its positions from its own pages.  1 <= n_group <= n_seq. */
 int qgemv_attn_shared(int kv_type, const void *k_pages, const void *v_pages, int64_t n_pages,
                       int page_size, int64_t page_stride, int n_kv_heads, int head_dim,
                       const int32_t *table, int max_pages, const int32_t *kv_len, int n_seq,
@@ -394,8 +394,8 @@ int qgemv_attn_shared(int kv_type, const void *k_pages, const void *v_pages, int
                       size_t ws_bytes, void *stream);
 
 /* Reads and clears the flag that the calls above leave in their workspace (*flag = 1 if any
- * position of an earlier call on this workspace had no valid page).  Like qgemv_moe_error it
- * SYNCHRONIZES `stream`. */
+ * position of an earlier call on this workspace had no valid page, or was left out as said above).  Like
+ * qgemv_moe_error it SYNCHRONIZES `stream`. */
 int qgemv_attn_error(const void *ws, int *flag, void *stream);
 
 /* Routing of rows to experts: the ids and weights qgemv_moe takes.  logits f32 [n_rows][n_exp].

@@ -76,3 +76,46 @@ def test_flag_only_for_what_is_left_out(kv_type, n, nq, nkv, hd, n_group, form):
     got, flag = batch.call(starts, share, lens)
     batch.check(got, [np.r_[0:40, 64:80] if b == n - 1 else lens[b] for b in range(n)])
     assert flag == 1
+
+
+def broken_starts(n, n_group):
+    """Starts in order, then such as are not, or leave the sequences."""
+    good = [i * n // n_group for i in range(n_group)] + [n]
+    swapped = list(good)
+    if n_group > 2:
+        swapped[n_group // 2], swapped[n_group // 2 + 1] = swapped[n_group // 2 + 1], swapped[n_group // 2]
+    else:
+        swapped[0], swapped[1] = 3, 1
+    overlap = list(good)
+    overlap[n_group // 2] = n - 1
+    overlap[-1] = n - 2
+    return good, [swapped, good[::-1], [-1] + good[1:], good[:-1] + [n + 1], [-2 ** 31] + good[1:], overlap,
+                  good[:-1] + [2 ** 31 - 1]]
+
+
+@pytest.mark.parametrize("kv_type", ALL)
+@pytest.mark.parametrize("n,nq,nkv,hd,n_group,form,extra", [
+    (5, 4, 1, 64, 1, "16", 2), (9, 40, 1, 128, 4, "16", 2), (300, 4, 2, 64, 90, "16", 2), (520, 16, 1, 64, 1, "parted", 2),
+    (140, 64, 1, 192, 2, "parted", 2), (60, 160, 1, 64, 20, "parted", 2), (134, 64, 16, 64, 44, "few", 70),
+    (134, 64, 16, 64, 44, "whole", 2)])
+def test_group_starts_out_of_order(kv_type, n, nq, nkv, hd, n_group, form, extra):
+    """The flag, every sequence by itself from its own pages, and a workspace that serves the next call."""
+    prefix, own = 30, 12
+    batch = alike(kv_type, n, nq, nkv, hd, form, prefix=prefix, own=own, n_group=n_group, extra_entries=extra)
+    good, bad = broken_starts(n, n_group)
+    lens = [prefix + own - b % 25 for b in range(n)]
+    share = [prefix] * n
+    first, flag = batch.call(good, share, lens)
+    batch.check(first, lens)
+    assert flag == 0
+    for starts in bad:
+        got, flag = batch.call(starts, share, lens)
+        batch.check(got, lens)
+        assert flag == 1
+        again, flag = batch.call(good, share, lens)
+        assert flag == 0 and (again == first).all()
+    if n <= 9:                                              # not from the first one's pages
+        batch.c.table[1, 0] = -1
+        got, flag = batch.call(bad[0], share, lens)
+        batch.check(got, [np.r_[16:x] if b == 1 else x for b, x in enumerate(lens)])
+        assert flag == 1
