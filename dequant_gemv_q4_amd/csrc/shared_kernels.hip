@@ -57,15 +57,18 @@ SharedForm shared_form(int kv_type, int64_t n_seq, int n_group, int nq, int nkv,
 
 int launch_shared_16(int kv_type, const AttnArgs &a, void *stream)
 {
-    // slots for either half: what is behind the prefix takes what it can fill, up to a half.  As many pairs as slots:
-    // each has a workgroup, and those that are split as many more as there are slots
+    // Slots for either half.  The prefix leaves to what is behind it a workgroup a pair, up to a half of those that
+    // are resident; that half has its slots too, so that long ones are split: two sequences of up to 15000 positions
+    // behind 500 (12 / 2 heads of 128, f16) 94 -> 22.5 us in a graph, qgemv_attn 17.7; 16 of 3000 behind 400 (24 / 8 of
+    // 64) 26.2 -> 23.4; a prefix of 8000 before 300 of 4 each 23.2 and 23.2 (with half of the slots for it alone 24.4).
+    // As many pairs as slots: each has a workgroup, and those that are split as many more as there are slots.
     const int all = attn_slots(a.c.hd);
     const int64_t table = (int64_t)a.c.max_pages << a.c.ps_log2;
     const bool split = table > (kv_bytes(kv_type) ? Attn8Cols::SOLO << Attn8Cols::UNIT_LOG2
                                                   : AttnCols::SOLO << AttnCols::UNIT_LOG2);
     auto grid_of = [=](int64_t pairs, int slots) { return pairs < slots ? slots : pairs + (split ? slots : 0); };
     const int64_t pairs = (int64_t)a.c.n_seq * a.c.nkv * ((a.group + 15) / 16);
-    const int slots = (int)(pairs < all / 2 ? pairs : all / 2), first = all - slots;
+    const int few = (int)(pairs < all / 2 ? pairs : all / 2), first = all - few, slots = split ? all / 2 : few;
     const int64_t lead = grid_of(a.c.nkv * (a.c.n_rows * a.group / 16 + a.n_group), first);
     const AttnArgs g = groups_of(a);
     void (*k)(AttnArgs, AttnArgs, int, int, int) = nullptr;

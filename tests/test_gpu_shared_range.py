@@ -119,3 +119,16 @@ def test_group_starts_out_of_order(kv_type, n, nq, nkv, hd, n_group, form, extra
         got, flag = batch.call(bad[0], share, lens)
         batch.check(got, [np.r_[16:x] if b == 1 else x for b, x in enumerate(lens)])
         assert flag == 1
+
+
+@pytest.mark.parametrize("kv_type", ALL)
+@pytest.mark.parametrize("n,nq,nkv,hd,prefix,own", [(2, 12, 2, 128, 100, 9000), (5, 8, 4, 64, 37, 3000),
+                                                    (3, 40, 2, 96, 500, 2500), (3, 4, 1, 256, 64, 4000)])
+def test_equally_long_positions_behind_a_short_prefix(kv_type, n, nq, nkv, hd, prefix, own):
+    """Fewer sequences than slots, all of them split behind the prefix; and once more on the same workspace."""
+    batch = alike(kv_type, n, nq, nkv, hd, "16", prefix=prefix, own=own, n_group=1)
+    lens = [prefix + own - b for b in range(n)]
+    first, flag = batch.call([0, n], [prefix] * n, lens)
+    batch.check(first, lens)
+    again, again_flag = batch.call([0, n], [prefix] * n, lens)
+    assert flag == again_flag == 0 and (again == first).all()
