@@ -3,7 +3,7 @@ definition in 64 bits: every form of the kernels, and what the sticky flag says.
 import numpy as np
 import pytest
 
-from gpu_common import require_gpu
+from gpu_common import require_gpu, torch
 
 import dequant_gemv_q4_amd as q
 from kv_common import ALL
@@ -132,3 +132,26 @@ def test_equally_long_positions_behind_a_short_prefix(kv_type, n, nq, nkv, hd, p
     batch.check(first, lens)
     again, again_flag = batch.call([0, n], [prefix] * n, lens)
     assert flag == again_flag == 0 and (again == first).all()
+
+
+@pytest.mark.parametrize("kv_type", ALL)
+@pytest.mark.parametrize("n,nq,nkv,hd,n_group,form,prefix,own,extra", [
+    (3, 4, 1, 64, 1, "16", 2000, 1200, 2), (7, 40, 2, 256, 2, "16", 300, 700, 2), (512, 16, 1, 64, 1, "16", 30, 12, 2),
+    (513, 16, 1, 64, 1, "parted", 30, 12, 2), (140, 64, 1, 256, 2, "parted", 150, 9, 60),
+    (129, 64, 16, 64, 44, "few", 30, 12, 130), (129, 64, 16, 64, 44, "whole", 30, 12, 2)])
+def test_nothing_behind_the_workspace_is_written(kv_type, n, nq, nkv, hd, n_group, form, prefix, own, extra):
+    """A workspace of just the size that is asked for, with a pattern behind it, on both sides of the number of rows
+    whose halves meet in one launch."""
+    batch = alike(kv_type, n, nq, nkv, hd, form, prefix=prefix, own=own, n_group=n_group, extra_entries=extra)
+    starts = [i * n // n_group for i in range(n_group)] + [n]
+    lens = [prefix + own - b % 7 for b in range(n)]
+    size = q.qgemv_attn_workspace_bytes(q.OP_ATTN_SHARED, n, nq, nkv, hd)
+    guarded = torch.full((size + (1 << 20),), 0xA5, dtype=torch.uint8, device="cuda")
+    guarded[:size] = 0
+    for _ in range(2):
+        got, flag = batch.call(starts, [prefix] * n, lens, ws=guarded[:size])
+        batch.check(got, lens)
+        assert flag == 0
+    assert bool((guarded[size:] == 0xA5).all())
+    counters = guarded[256:256 + (2 * 512 + 8192) * 4]       # arrivals are 0 between calls
+    assert not bool(counters.any())
