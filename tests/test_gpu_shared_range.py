@@ -6,7 +6,7 @@ import pytest
 from gpu_common import require_gpu, torch
 
 import dequant_gemv_q4_amd as q
-from kv_common import ALL
+from kv_common import ALL, BYTES
 from shared_common import Batch
 from test_gpu_kv8 import _draw
 
@@ -155,3 +155,82 @@ def test_nothing_behind_the_workspace_is_written(kv_type, n, nq, nkv, hd, n_grou
     assert bool((guarded[size:] == 0xA5).all())
     counters = guarded[256:256 + (2 * 512 + 8192) * 4]       # arrivals are 0 between calls
     assert not bool(counters.any())
+
+
+def spoil(batch, b, page_entry, slots, kv_type, code=0x7F):
+    """Positions `slots` of a sequence's page hold NaN in K and V (8-bit: NaN scales; of f8 0x7F is a NaN as well)."""
+    page = int(batch.c.table[b, page_entry])
+    hd, ps = batch.hd, batch.c.page
+    for pool, turned in ((batch.c.k, False), (batch.c.v, True)):
+        for h in range(batch.nkv):
+            block = pool[page, h * batch.c.block:(h + 1) * batch.c.block]
+            data = block[:ps * hd]
+            data = data.view(hd, ps).T if turned else data.view(ps, hd)
+            data[slots] = code if kv_type in BYTES else float("nan")
+            if kv_type in BYTES:
+                block[ps * hd:].view(torch.float32)[slots] = float("nan")
+
+
+@pytest.mark.parametrize("kv_type", ALL)
+@pytest.mark.parametrize("n,nq,nkv,hd,n_group,form", FORMS)
+def test_a_begun_page_holds_anything_before_the_share_ends(kv_type, n, nq, nkv, hd, n_group, form):
+    batch = alike(kv_type, n, nq, nkv, hd, form, prefix=150, own=20, n_group=n_group)
+    starts = [0, n] if n_group == 1 else [0, n // 2, n]
+    for b in set(range(n)) - set(starts):
+        spoil(batch, b, 150 // 16, slice(0, 150 % 16), kv_type)
+        batch.c.table[b, 150 // 16 - 1] = -1
+    lens = [170 - b % 15 for b in range(n)]
+    got, flag = batch.call(starts, [150] * n, lens)
+    batch.check(got, lens)
+    assert flag == 0
+
+
+@pytest.mark.parametrize("kv_type", ALL)
+@pytest.mark.parametrize("n,nq,nkv,hd,n_group,form", FORMS)
+def test_non_finite_queries_and_positions_reach_their_rows_alone(kv_type, n, nq, nkv, hd, n_group, form):
+    """A query with a NaN or an infinity, and a position of the prefix that only some sequences share (or see) and
+    that is not finite: other rows and heads are as without them."""
+    starts = [0, n] if n_group == 1 else [0, n // 2, n]
+    batch = alike(kv_type, n, nq, nkv, hd, form, prefix=150, own=20, n_group=n_group)
+    share = [150 if b in starts or b % 3 else 100 for b in range(n)]
+    lens = [s + 9 - b % 7 for b, s in enumerate(share)]
+    lens[3] = 90
+    bad = {1: np.nan, n // 2 + 1: np.inf, n - 1: -np.inf}
+    batch.q = batch.q.clone()
+    for b, x in bad.items():
+        batch.q[b, 5] = float(x)                             # of head 0
+    clean = [b for b in range(n) if b not in bad]
+    got, flag = batch.call(starts, share, lens)
+    assert flag == 0
+    got = got.reshape(n, nq, hd)
+    for b in bad:
+        finite = int(np.isfinite(got[b, 0]).sum())
+        assert finite == 0
+        got[b, 0] = 0.0
+    finite = bool(np.isfinite(got).all())
+    assert finite
+    plain = alike(kv_type, n, nq, nkv, hd, form, prefix=150, own=20, n_group=n_group)
+    want, _ = plain.call(starts, share, lens)
+    want = want.reshape(n, nq, hd)
+    far = np.abs(got[clean] - want[clean]).max()
+    assert far <= 1e-6 * np.abs(want).max()
+    for b in starts[:-1]:                                   # positions 112 .. 115 of the shared pages
+        spoil(plain, b, 7, slice(0, 4), kv_type, code=0)     # (as the append leaves them)
+    got, flag = plain.call(starts, share, lens)
+    sees = np.array([min(s, x) > 112 for s, x in zip(share, lens)])
+    assert flag == 0 and sees.any() and not sees.all()
+    nans = int(np.isnan(got[sees]).sum())
+    assert nans == got[sees].size
+    far = np.abs(got.reshape(n, nq, hd)[~sees] - want[~sees]).max()
+    assert far <= 1e-6 * np.abs(want).max()
+
+
+@pytest.mark.parametrize("kv_type", ALL)
+@pytest.mark.parametrize("scale", [0.0, -0.2, 1e-30, 40.0])
+def test_scales_of_any_sign_and_size(kv_type, scale):
+    for n, nq, nkv, hd, n_group, form in FORMS[:2]:
+        batch = alike(kv_type, n, nq, nkv, hd, form, scale=scale, seed=2)
+        lens = [170 - b % 90 for b in range(n)]
+        got, flag = batch.call([0, n], [150] * n, lens)
+        batch.check(got, lens)
+        assert flag == 0
