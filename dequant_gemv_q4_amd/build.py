@@ -23,8 +23,9 @@ BW_LIB = os.path.join(PKG, "libqgbw.so")       # the benchmark's bandwidth refer
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["gemv_kernels.hip", "gemv_kernels_x.hip", "stream_kernels.hip", "stream_kernels_x.hip",
            "stream_kernels_g.hip",
-           "mfma_kernels.hip", "gemm_kernels.hip", "append_kernels.hip", "attn8_kernels.hip", "shared_kernels.hip", "shared_prompt_kernels.hip", "attn_kernels.hip", "attn_prompt_kernels.hip",
-           "route_kernels.hip", "abi.cpp", "abi_attn.cpp"]
+           "mfma_kernels.hip", "gemm_kernels.hip", "append_kernels.hip", "attn_kernels.hip",
+           "attn8_kernels.hip", "attn_prompt_kernels.hip", "shared_kernels.hip",
+           "shared_prompt_kernels.hip", "route_kernels.hip", "abi.cpp", "abi_attn.cpp"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

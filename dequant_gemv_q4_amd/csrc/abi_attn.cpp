@@ -70,8 +70,8 @@ struct Span {
     int64_t n;
 };
 
-// Checks of the cache and the metadata shared by the three calls; fills c and the byte span of
-// either page array.
+// Checks of the cache and the metadata shared by the five calls that take a cache; fills c and the
+// byte span of either page array.
 static int check_cache(int kv_type, const void *k_pages, const void *v_pages, int64_t n_pages,
                        int page_size, int64_t page_stride, int nq, int nkv, int hd,
                        const int32_t *table, int max_pages, const int32_t *q_start,

@@ -44,11 +44,6 @@ constexpr int JOIN_RADIX = 8;
 template <bool SIDE> using AttnPlanOf = PlanOf<16, 7, 2, 4, 32, JOIN_RADIX, false, SIDE>;
 typedef AttnPlanOf<false> AttnCols;
 
-// Partial results of a slot: the tile's O (unnormalised) [cols][hd], then (exponent, sum) [cols].
-// SIDE: several tiles of a KV head read the same positions.  They come next to each other and on one XCD
-// (workgroups eight apart), so that one of them finds the other's in the L2: 64 sequences of 7500 positions,
-// 40 / 2 heads of 128: 140.9 us tile by tile, 107 to 111; of 64 75.0 and 58; sixteen of 8 rows x 4000, 24 / 2:
-// 53.3 and 47.6.  (In the code of the others it costs 0.15 of 7 us.)
 // LDS of a workgroup.
 template <int T, int D>
 struct AttnLds {
@@ -61,6 +56,11 @@ struct AttnLds {
     int last, done[16];
 };
 
+// Partial results of a slot: the tile's O (unnormalised) [cols][hd], then (exponent, sum) [cols].
+// SIDE: several tiles of a KV head read the same positions.  They come next to each other and on one XCD
+// (workgroups eight apart), so that one of them finds the other's in the L2: 64 sequences of 7500 positions,
+// 40 / 2 heads of 128: 140.9 us tile by tile, 107 to 111; of 64 75.0 and 58; sixteen of 8 rows x 4000, 24 / 2:
+// 53.3 and 47.6.  (In the code of the others it costs 0.15 of 7 us.)
 template <int T, int D, int FORM, bool SIDE>
 __device__ __forceinline__ void attn_body(const AttnArgs &a, int slots, int id, int grid, AttnLds<T, D> &sh)
 {
@@ -332,7 +332,6 @@ __device__ __forceinline__ void attn_body(const AttnArgs &a, int slots, int id, 
     const uint32_t stride = (uint32_t)attn_part_floats(width, D);
     const __amdgpu_buffer_rsrc_t part = __builtin_amdgcn_make_buffer_rsrc(
         (behind(FORM) ? a.tail_part : a.part) + (int64_t)p.slot0 * stride, 0, n_chunk * stride * 4, 0x00020000);
-    // four channels of a column to o
     // four channels of a column to o, or to where the halves meet
     auto store = [&](int e, af4 sum, float m, float ls) {
         const af4 mean = sum * inverse_sum(ls);

@@ -22,7 +22,8 @@ __host__ __device__ constexpr int64_t attn_part_floats(int cols, int hd) { retur
 // Workgroups of a shared prefix in parts, one per compute unit: the other half of a unit is for what is behind the
 // prefix.  64 sequences behind 30000 positions, 32 / 8 heads of 128, f16: 105 us, with two per unit 117 to 133 by the
 // order of the workgroups, with 384 111; with hardly anything behind it 89.5 and 90 (fewer parts to join).  8-bit
-// codes are converted on the way, so that there a unit wants more: I8 140, with 384 125, with 512 128.
+// codes are converted on the way, so that there a unit wants more: I8 140, with 384 125, with 512 128.  (Both from
+// this one batch; bf16 and F8, other heads and shorter prefixes take the same.  Heads above 128 have 256 resident.)
 #define SHARED_SLOTS 256
 #define SHARED_SLOTS_8 384
 // Rows times KV heads (and times query heads) of a call whose halves meet in one launch, at most.
@@ -73,7 +74,7 @@ struct QkvArgs {
     float eps;
 };
 
-struct PromptSplit;             // a split tile (attn_prompt_kernels.hip)
+struct PromptSplit;             // a split tile (attn_prompt_impl.h)
 
 struct AttnArgs {
     KvArgs c;

@@ -46,6 +46,8 @@ static AttnArgs groups_of(const AttnArgs &a)
 // (8e8) 47.0 -> 42.5; I8, 64 of 32 / 8 behind 4000 (1.1e9) 35.9 -> 43.4, 8000 (2.1e9) 50.0 -> 48.5, 30000 130 -> 111;
 // 200 of 12 / 2 behind 4000 (1.3e9) 44.4 -> 43.9, 150 of 16 / 1 behind 2500 (8e8) 38.3 -> 43.7, 10000 (3.1e9) 80.7 ->
 // 62.2; heads of 256, 30 of 32 / 8 behind 8000 (2e9) 95.0 -> 78.1; 24 / 8 of 64, 32 behind 20000 (8e8) 36.7 -> 42.7.
+// (All with tables as long as the caches; lengths are on the device, so a short prefix in a long table is taken for a
+// long one.  Over f16 and bf16 only heads of 128 were timed.)
 SharedForm shared_form(int kv_type, int64_t n_seq, int n_group, int nq, int nkv, int hd, int64_t positions)
 {
     const double work = (double)(n_seq * nq) * hd * (positions < 16384 ? positions : 16384);

@@ -265,15 +265,14 @@ int qgemv_moe_error(const void *ws, int64_t n_exp, int64_t N, int64_t K, int fmt
  *   QG_I8: code a signed byte, d = max(amax / 127, 2^-126), code = x / d to the nearest, ties to even;
  *   QG_F8: code an e4m3 (bias 7, largest 448, no infinities), d the least power of two, from 2^-126
  *          on, with amax <= 448 d, code = x / d to the nearest-even;
- * amax the largest |x| of the position's head_dim values.  The code is that of the exact quotient.
- * Where one of the values is not finite, d is NaN and the codes are 0: the whole position of the head
- * reads as NaN.  The e4m3 NaN codes are never written, and a cache has to hold none at positions in use, nor a
- * negative scale.
- * page_stride, at least n_kv_heads * block and a multiple of 8 (8-bit: 16), lets one pool hold several
- * layers or K and V side by side.  table is int32 [n_seq][max_pages]: position t of sequence b lies in slot
- * t % page_size of page table[b][t / page_size].  Entries behind a sequence's last position are
- * never read.  kv_len, int32 [n_seq], counts a sequence's cached positions WITH the new ones of
- * this step.
+ * amax the largest |x| of the position's head_dim values.  The code is that of the exact
+ * quotient.  Where one of the values is not finite, d is NaN and the codes are 0: the whole
+ * position of the head reads as NaN.  The e4m3 NaN codes are never written, and a cache has to
+ * hold none at positions in use, nor a negative scale.  page_stride, at least n_kv_heads * block
+ * and a multiple of 8 (8-bit: 16), lets one pool hold several layers or K and V side by side.
+ * table is int32 [n_seq][max_pages]: position t of sequence b lies in slot t % page_size of
+ * page table[b][t / page_size].  Entries behind a sequence's last position are never read.
+ * kv_len, int32 [n_seq], counts a sequence's cached positions WITH the new ones of this step.
  *
  * New rows (of K and V for qgemv_kv_append, of queries for qgemv_attn_prompt) are packed:
  * sequence b owns rows q_start[b] .. q_start[b + 1] - 1 (int32 [n_seq + 1], not decreasing,
@@ -293,43 +292,45 @@ int qgemv_moe_error(const void *ws, int64_t n_exp, int64_t N, int64_t K, int fmt
  * Order: append the step's K and V first, then attend, on one stream.  Two sequences may share
  * pages that neither appends to; appending to one page position from two rows is a race.
  * page_size is 16, 32, 64, 128 or 256; head_dim 64, 96, 128, 192 or 256; n_kv_heads divides
- * n_q_heads (query head h reads KV head h / (n_q_heads / n_kv_heads)), which is at most 4096 (for
- * qgemv_kv_append n_kv_heads is); n_seq in [1, QG_ATTN_MAX_SEQ]; max_pages * page_size <= 2^24; n_rows in
- * [1, QG_GEMM_MAX_M]; n_pages in [1, 2^28]; page_stride < 2^32; q_stride (kv_stride) from n_q_heads *
- * head_dim (n_kv_heads * head_dim) to 2^31 floats; scale finite.  All float pointers and both page arrays are
- * 16-byte aligned, row strides are multiples of 4 floats.  Calls that share a workspace are ordered on
- * one stream, as above; calls with workspaces of their own may run side by side. */
+ * n_q_heads (query head h reads KV head h / (n_q_heads / n_kv_heads)), which is at most 4096
+ * (for qgemv_kv_append n_kv_heads is); n_seq in [1, QG_ATTN_MAX_SEQ]; max_pages * page_size <=
+ * 2^24; n_rows in [1, QG_GEMM_MAX_M]; n_pages in [1, 2^28]; page_stride < 2^32; q_stride
+ * (kv_stride) from n_q_heads * head_dim (n_kv_heads * head_dim) to 2^31 floats; scale finite.
+ * All float pointers and both page arrays are 16-byte aligned, row strides are multiples of 4
+ * floats.  Calls that share a workspace are ordered on one stream, as above; calls with
+ * workspaces of their own may run side by side. */
 
-/* Workspace bytes of an attention-side operation (QG_OP_KV_APPEND, QG_OP_QKV_APPEND, QG_OP_ATTN,
- * QG_OP_ATTN_PROMPT, QG_OP_ATTN_SHARED), or -1 on invalid sizes.  It holds the sticky flag and the partial results of
- * a split over the cache's length, so, like qgemv_moe's, it must be zero-filled once after
- * allocation; a larger one also serves.  Host-only. */
+/* Workspace bytes of an attention-side operation (QG_OP_KV_APPEND, QG_OP_QKV_APPEND,
+ * QG_OP_ATTN, QG_OP_ATTN_PROMPT, QG_OP_ATTN_SHARED), or -1 on invalid sizes.  It holds the
+ * sticky flag and the partial results of a split over the cache's length, so, like qgemv_moe's,
+ * it must be zero-filled once after allocation; a larger one also serves.  Host-only. */
 int64_t qgemv_attn_workspace_bytes(int op, int n_seq, int n_q_heads, int n_kv_heads,
                                    int head_dim);
 
-/* Store the new K and V rows in the cache, rounded to nearest-even (8-bit: quantised as above).  k and
- * v point at the first K and V value of row 0, f32, kv_stride floats apart from row to row (the fused QKV output: qkv +
- * n_q_heads * head_dim, qkv + (n_q_heads + n_kv_heads) * head_dim, stride (n_q_heads +
- * 2 n_kv_heads) * head_dim), heads back to back. */
+/* Store the new K and V rows in the cache, rounded to nearest-even (8-bit: quantised as
+ * above).  k and v point at the first K and V value of row 0, f32, kv_stride floats apart from
+ * row to row (the fused QKV output: qkv + n_q_heads * head_dim, qkv + (n_q_heads + n_kv_heads)
+ * * head_dim, stride (n_q_heads + 2 n_kv_heads) * head_dim), heads back to back. */
 int qgemv_kv_append(int kv_type, void *k_pages, void *v_pages, int64_t n_pages, int page_size,
                     int64_t page_stride, int n_kv_heads, int head_dim, const int32_t *table,
                     int max_pages, const int32_t *q_start, const int32_t *kv_len, int n_seq,
                     const float *k, const float *v, int64_t kv_stride, int64_t n_rows, void *ws,
                     size_t ws_bytes, void *stream);
 
-/* From the fused QKV output to the cache in one pass: what qgemv_qk_norm_rope and qgemv_kv_append do
- * one after the other, for any number of packed rows.  qkv is f32, row r at qkv + r * qkv_stride: Q
- * heads, K heads, V heads.  Each Q (K) head is normalised with q_gamma (k_gamma; NULL skips that) and
- * rotated as in qgemv_qk_norm_rope, but with row t of the tables rope_cos and rope_sin, f32
- * [rope_rows][rope_half], for a row at position t.  Q goes to q, row r at q + r * q_stride
- * ([n_rows][n_q_heads * head_dim], what the attentions take), K and V to the cache; K is computed in
- * 64 bits and rounded once.  q may be qkv itself with q_stride = qkv_stride (in place), else it
- * overlaps nothing.  K and V of qkv stay as they are.  A row at a negative position, or at or behind
- * rope_rows where rope_half > 0 (that sets the flag of qgemv_attn_error), is left out: nothing is
- * stored and its q is not written.  A position without a valid page is not stored; its q is written.
- * q_start NULL as in qgemv_kv_append.  Limits: 0 <= rope_half <= head_dim / 2, eps >= 0 finite,
- * rope_rows in [1, 2^24] (rope_half 0: no tables are read and they may be NULL), gammas and tables
- * 16-byte aligned, n_rows * n_q_heads <= 2^30. */
+/* From the fused QKV output to the cache in one pass: what qgemv_qk_norm_rope and
+ * qgemv_kv_append do one after the other, for any number of packed rows.  qkv is f32, row r at
+ * qkv + r * qkv_stride: Q heads, K heads, V heads.  Each Q (K) head is normalised with q_gamma
+ * (k_gamma; NULL skips that) and rotated as in qgemv_qk_norm_rope, but with row t of the tables
+ * rope_cos and rope_sin, f32 [rope_rows][rope_half], for a row at position t.  Q goes to q, row
+ * r at q + r * q_stride ([n_rows][n_q_heads * head_dim], what the attentions take), K and V to
+ * the cache; K is computed in 64 bits and rounded once.  q may be qkv itself with q_stride =
+ * qkv_stride (in place), else it overlaps nothing.  K and V of qkv stay as they are.  A row at
+ * a negative position, or at or behind rope_rows where rope_half > 0 (that sets the flag of
+ * qgemv_attn_error), is left out: nothing is stored and its q is not written.  A position
+ * without a valid page is not stored; its q is written. q_start NULL as in qgemv_kv_append.
+ * Limits: 0 <= rope_half <= head_dim / 2, eps >= 0 finite, rope_rows in [1, 2^24] (rope_half 0:
+ * no tables are read and they may be NULL), gammas and tables 16-byte aligned, n_rows *
+ * n_q_heads <= 2^30. */
 int qgemv_qkv_append(int kv_type, void *k_pages, void *v_pages, int64_t n_pages, int page_size,
                      int64_t page_stride, int n_kv_heads, int head_dim, const int32_t *table,
                      int max_pages, const int32_t *q_start, const int32_t *kv_len, int n_seq,
@@ -352,22 +353,23 @@ int qgemv_attn(int kv_type, const void *k_pages, const void *v_pages, int64_t n_
 /* Causal attention of packed sequences of new rows (a prompt, a prefill chunk behind cached
  * positions, or several tokens to verify): row r at position t attends to the positions <= t of
  * its sequence.  q as in qgemv_attn, one row per new row; o is f32 [n_rows][n_q_heads *
- * head_dim], rows outside every sequence left as they were.  n_rows * n_q_heads <= 2^30.  Few rows
- * over a long cache are split over its length and joined, within the launch or by a second one.
- * Accuracy of both: scores, softmax statistics and sums in f32; q and the probabilities enter the
- * products with f16 K and V as the sum of two f16 values (22 bits; of q below 2^-16 of the row's
- * largest 2^-38 of that, of probabilities 2^-35 of the row's largest, is lost at most), with bf16 as
- * that of three bf16 values (24 bits); K and V exactly as stored.  Over 8-bit pages the codes enter
- * exactly, as f16, the scales of K multiply f32 scores and those of V f32 weights, and the products
- * are as with f16 (of a weight times its scale 2^-35 of the row's largest weight times the largest
- * scale of V that it sees is lost at most; where rows computed beside it see a scale more than 2^80
- * times as large, a bit more for each factor of two beyond that).  Scores are right wherever they are
- * within f32, except in qgemv_attn_prompt and qgemv_attn_shared against scales of K above 2^96 beside a
- * row with values of scale * q above 2^72.  A NaN or an infinity in a query makes the
- * outputs of its row and head non-finite, one in K or V those of the rows that see its position (of V
- * its channel's; NaN also where the definition gives an infinity), and touches no other row.  Only an
- * infinity in K whose score comes out as -inf has weight 0; a row all of whose scores are -inf gets 0,
- * as one that sees no position. */
+ * head_dim], rows outside every sequence left as they were.  n_rows * n_q_heads <= 2^30.  Few
+ * rows over a long cache are split over its length and joined, within the launch or by a second
+ * one.  Accuracy of both: scores, softmax statistics and sums in f32; q and the probabilities
+ * enter the products with f16 K and V as the sum of two f16 values (22 bits; of q below 2^-16
+ * of the row's largest 2^-38 of that, of probabilities 2^-35 of the row's largest, is lost at
+ * most), with bf16 as that of three bf16 values (24 bits); K and V exactly as stored.  Over
+ * 8-bit pages the codes enter exactly, as f16, the scales of K multiply f32 scores and those of
+ * V f32 weights, and the products are as with f16 (of a weight times its scale 2^-35 of the
+ * row's largest weight times the largest scale of V that it sees is lost at most; where rows
+ * computed beside it see a scale more than 2^80 times as large, a bit more for each factor of
+ * two beyond that).  Scores are right wherever they are within f32, except in qgemv_attn_prompt
+ * and qgemv_attn_shared against scales of K above 2^96 beside a row with values of scale * q
+ * above 2^72.  A NaN or an infinity in a query makes the outputs of its row and head
+ * non-finite, one in K or V those of the rows that see its position (of V its channel's; NaN
+ * also where the definition gives an infinity), and touches no other row.  Only an infinity in
+ * K whose score comes out as -inf has weight 0; a row all of whose scores are -inf gets 0, as
+ * one that sees no position. */
 int qgemv_attn_prompt(int kv_type, const void *k_pages, const void *v_pages, int64_t n_pages,
                       int page_size, int64_t page_stride, int n_kv_heads, int head_dim,
                       const int32_t *table, int max_pages, const int32_t *q_start,
@@ -375,17 +377,18 @@ int qgemv_attn_prompt(int kv_type, const void *k_pages, const void *v_pages, int
                       int64_t n_rows, int n_q_heads, float scale, float *o, void *ws,
                       size_t ws_bytes, void *stream);
 
-/* qgemv_attn for a batch whose sequences begin alike: the shared positions are read once for a group,
- * by tiles of all its sequences' query heads.  Group g is the sequences group_start[g] ..
- * group_start[g + 1] - 1 (int32 [n_group + 1], not decreasing, within [0, n_seq]); a sequence before
- * the first or behind the last group shares nothing.  The first shared_len[b] positions of sequence b
- * (int32 [n_seq]; below 1: none) are those of its group's first sequence, and are read from that one's
- * pages, as far as any of the group sees them: its shared_len has to be its group's largest.  Of
- * another's that is larger the positions between that it sees are left out, and the flag is set.  The
- * positions from shared_len[b] on, a begun page included, are read from the sequence's own pages.  As
- * everywhere, a sequence sees kv_len[b] positions in all, also where shared_len[b] is larger.  Group
- * starts out of order or range set the flag, and no sequence of the call shares anything: each reads all
- * of its positions from its own pages.  1 <= n_group <= n_seq. */
+/* qgemv_attn for a batch whose sequences begin alike: the shared positions are read once for a
+ * group, by tiles of all its sequences' query heads.  Group g is the sequences group_start[g]
+ * .. group_start[g + 1] - 1 (int32 [n_group + 1], not decreasing, within [0, n_seq]); a
+ * sequence before the first or behind the last group shares nothing.  The first shared_len[b]
+ * positions of sequence b (int32 [n_seq]; below 1: none) are those of its group's first
+ * sequence, and are read from that one's pages, as far as any of the group sees them: its
+ * shared_len has to be its group's largest.  Of another's that is larger the positions between
+ * that it sees are left out, and the flag is set.  The positions from shared_len[b] on, a begun
+ * page included, are read from the sequence's own pages.  As everywhere, a sequence sees
+ * kv_len[b] positions in all, also where shared_len[b] is larger.  Group starts out of order or
+ * range set the flag, and no sequence of the call shares anything: each reads all of its
+ * positions from its own pages.  1 <= n_group <= n_seq. */
 int qgemv_attn_shared(int kv_type, const void *k_pages, const void *v_pages, int64_t n_pages,
                       int page_size, int64_t page_stride, int n_kv_heads, int head_dim,
                       const int32_t *table, int max_pages, const int32_t *kv_len, int n_seq,
@@ -394,8 +397,8 @@ int qgemv_attn_shared(int kv_type, const void *k_pages, const void *v_pages, int
                       size_t ws_bytes, void *stream);
 
 /* Reads and clears the flag that the calls above leave in their workspace (*flag = 1 if any
- * position of an earlier call on this workspace had no valid page, or was left out as said above).  Like
- * qgemv_moe_error it SYNCHRONIZES `stream`. */
+ * position of an earlier call on this workspace had no valid page, or was left out as said
+ * above).  Like qgemv_moe_error it SYNCHRONIZES `stream`. */
 int qgemv_attn_error(const void *ws, int *flag, void *stream);
 
 /* Routing of rows to experts: the ids and weights qgemv_moe takes.  logits f32 [n_rows][n_exp].
