@@ -266,7 +266,7 @@ int qgemv_moe_error(const void *ws, int64_t n_exp, int64_t N, int64_t K, int fmt
  *   QG_F8: code an e4m3 (bias 7, largest 448, no infinities), d the least power of two, from 2^-126
  *          on, with amax <= 448 d, code = x / d to the nearest-even;
  * amax the largest |x| of the position's head_dim values.  The code is that of the exact
- * quotient.  Where one of the values is not finite, d is NaN and the codes are 0: the whole
+ * quotient.  Where one of the values is not finite in f32, d is NaN and the codes are 0: the whole
  * position of the head reads as NaN.  The e4m3 NaN codes are never written, and a cache has to
  * hold none at positions in use, nor a negative scale.  page_stride, at least n_kv_heads * block
  * and a multiple of 8 (8-bit: 16), lets one pool hold several layers or K and V side by side.
@@ -323,7 +323,7 @@ int qgemv_kv_append(int kv_type, void *k_pages, void *v_pages, int64_t n_pages, 
  * (k_gamma; NULL skips that) and rotated as in qgemv_qk_norm_rope, but with row t of the tables
  * rope_cos and rope_sin, f32 [rope_rows][rope_half], for a row at position t.  Q goes to q, row
  * r at q + r * q_stride ([n_rows][n_q_heads * head_dim], what the attentions take), K and V to
- * the cache; K is computed in 64 bits and rounded once.  q may be qkv itself with q_stride =
+ * the cache; Q is computed in f32, K in 64 bits and rounded once.  q may be qkv itself with q_stride =
  * qkv_stride (in place), else it overlaps nothing.  K and V of qkv stay as they are.  A row at
  * a negative position, or at or behind rope_rows where rope_half > 0 (that sets the flag of
  * qgemv_attn_error), is left out: nothing is stored and its q is not written.  A position

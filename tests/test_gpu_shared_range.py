@@ -234,3 +234,17 @@ def test_scales_of_any_sign_and_size(kv_type, scale):
         got, flag = batch.call([0, n], [150] * n, lens)
         batch.check(got, lens)
         assert flag == 0
+
+
+@pytest.mark.parametrize("kv_type", ALL)
+@pytest.mark.parametrize("form,extra", [("few", 70), ("whole", 2)])
+def test_stale_shares_of_many_groups(kv_type, form, extra):
+    """More groups than workgroup slots: each group's rows see less than its share, some of them nothing."""
+    n, n_group = 134, 44
+    batch = alike(kv_type, n, 64, 16, 64, form, prefix=90, own=6, n_group=n_group, extra_entries=extra)
+    starts = [i * n // n_group for i in range(n_group)] + [n]
+    lens = [max(0, (11 * b) % 53 - 5) for b in range(n)]    # at most 47: three pages of 16
+    batch.c.table[:, 3:] = -1
+    got, flag = batch.call(starts, [2 ** 31 - 1 if b in starts else 90 for b in range(n)], lens)
+    batch.check(got, lens)
+    assert flag == 0
