@@ -74,18 +74,12 @@ __device__ __forceinline__ void attn8_body(const AttnArgs &a, int slots, int id,
     // positions this lane's column sees, [0, see), and those that all columns see
     int see = t_end, see_all = t_end;
     if constexpr (FORM == PREFIX) {
-        // what none of these rows sees is not read (positions are below 2^24, whole numbers in f32)
-        const int seen = prefix_seen(a, row_of(min(i, cols - 1)), len);
-        len = __builtin_amdgcn_readfirstlane((int)max_of_16((float)seen));
-        t_end = min(t_end, len);
-        see = min(t_end, seen);
-        see_all = -(int)max_of_16(-(float)see);
+        see = min(t_end, prefix_seen(a, row_of(min(i, cols - 1)), len));
     } else if constexpr (FORM == MANY) {
         const int pos0 = max(c.kv_len[b], -(1 << 30)) - p.rows;
         see = min(t_end, pos0 + (rho0 + min(i, cols - 1)) / a.group + 1);
         see_all = min(t_end, pos0 + rho0 / a.group + 1);
     }
-    const int n_steps = t_end > t_begin + 64 * wave ? (t_end - t_begin - 64 * wave + 255) / 256 : 0;
 
     // queries of column i: scaled, split, in the order of the channels in K's operands
     auto channel = [&](int k) { return k < 2 * KP ? 64 * (k >> 1) + 16 * g + 8 * (k & 1) : 64 * KP + 8 * g; };
@@ -133,6 +127,14 @@ __device__ __forceinline__ void attn8_body(const AttnArgs &a, int slots, int id,
                     sh.q[(x * KB + k) * 64 + lane] = out[x];
         }
     }
+    if constexpr (FORM == PREFIX) {
+        // what none of these rows sees is not read (positions are below 2^24, whole numbers in f32); the rows' lengths
+        // have arrived by now
+        t_end = __builtin_amdgcn_readfirstlane((int)max_of_16((float)see));
+        len = min(len, t_end);
+        see_all = -(int)max_of_16(-(float)see);
+    }
+    const int n_steps = t_end > t_begin + 64 * wave ? (t_end - t_begin - 64 * wave + 255) / 256 : 0;
     if constexpr (Q_LDS)
         __syncthreads();
 
@@ -268,10 +270,17 @@ __device__ __forceinline__ void attn8_body(const AttnArgs &a, int slots, int id,
                 seen = max_x32(max_x16(max_of_16(seen)));
             }
             const float most = ROWS && edge ? max_of_16(exponent_above(seen)) : exponent_above(seen);
-            if (most > r + R_SLACK) {                     // (uniform)
-                const Moved x = moved_reference(r, most, exponent_above(seen), top, shift,
-                                                exponent_above(max_x32(max_x16(l))));
-                r = most;
+            top = fmaxf(top, exponent_above(seen) - r);
+            float mx = sc[0];
+#pragma unroll
+            for (int e = 1; e < 16; ++e)
+                mx = fmaxf(mx, sc[e]);
+            mx *= lift;
+            const bool moved = __builtin_amdgcn_readfirstlane(most > r + R_SLACK);
+            if (moved || __any(mx + shift > TOP8 - top)) {
+                const float to = moved ? most : r;
+                const Rescaled x = rescaled(r, to, top, shift, max_x32(max_x16(mx)), exponent_above(max_x32(max_x16(l))));
+                r = to;
                 top = x.top;
                 shift = x.shift;
                 l *= x.l;
@@ -280,21 +289,6 @@ __device__ __forceinline__ void attn8_body(const AttnArgs &a, int slots, int id,
                     o[d] *= x.o;
             }
             dv = ldexpf(dv, -(int)r);
-            top = fmaxf(top, exponent_above(seen) - r);
-            float mx = sc[0];
-#pragma unroll
-            for (int e = 1; e < 16; ++e)
-                mx = fmaxf(mx, sc[e]);
-            mx *= lift;
-            if (__any(mx + shift > TOP8 - top)) {
-                const float to = fminf(shift, shift8_of(max_x32(max_x16(mx)), top));
-                const float f = __builtin_amdgcn_exp2f(to - shift);
-                shift = to;
-                l *= f;
-#pragma unroll
-                for (int d = 0; d < DT; ++d)
-                    o[d] *= f;
-            }
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
                 sc[e] = __builtin_amdgcn_exp2f(fmaf(sc[e], lift, shift));

@@ -9,7 +9,7 @@
 // a whole number that follows the largest scale that any column of a wave has met, and a column keeps the exponent
 // `top` of the largest relative scale that it has seen (at least LEAST_TOP): its shift puts the largest p at
 // 2^(LIFT - top), so that w is at most 2^LIFT when the shift moves and under 2^TOP afterwards.  When r moves up,
-// a column's top goes down and its shift up by as much (moved_reference), so that what it weighs from then on is as
+// a column's top goes down and its shift up by as much (rescaled), so that what it weighs from then on is as
 // large as before; left alone, with V 2^29 and then 2^31 times larger than at first, the last weights kept four
 // bits.  Of w 2^-25 is lost at most: 2^-35 of the largest weight times the largest scale that the column sees, as
 // long as that scale is at least 2^LEAST_TOP of the largest that another column of the wave has seen.  Sums of p
@@ -110,25 +110,23 @@ __device__ __forceinline__ float shift8_of(float top_score, float top)
     return r + top_score > TOP8 - top ? -top_score - top - fabsf(top_score) * 0x1p-23f : r;
 }
 
-// A column as the wave's reference moves from 2^r to 2^to: own is the exponent of the largest scale that it sees
-// in this step, sum that of its sum of weights (over its lanes).  The shift rises by what top falls, but not so
-// far that the sum could reach f32's end: a column whose sum would has weighed positions with small scales by 2^92 or
-// more (2^114 over the 2^22 positions of a wave), and needs no further bits for what comes.  Where scores are so
-// large that the shift is rounded up by more than it has to rise, it stays.
-struct Moved {
+// A column when its wave rescales: because a score would bring a weight above 2^TOP, or because the reference moves
+// from 2^r up to 2^to (else to = r).  top includes the scales of this step; score is the largest of its
+// scores, sum the exponent of its sum of weights, over its lanes.  As the reference moves, the shift rises by what
+// top falls, but not so far that the sum could reach f32's end: a column whose sum would has weighed positions with
+// small scales by 2^92 or more (2^114 over the 2^22 positions of a wave), and needs no further bits for what comes.
+// Where scores are so large that the shift would be rounded by more than a quarter, it stays.  (One branch for both
+// reasons: with one each, heads of 256 spilled, 4000 rows, 16 / 8 heads, I8, 436 us against 368.)
+struct Rescaled {
     float top, shift, l, o;                    // top and shift from now on; factors of the sum and of O
 };
-__device__ __forceinline__ Moved moved_reference(float r, float to, float own, float top, float shift, float sum)
+__device__ __forceinline__ Rescaled rescaled(float r, float to, float top, float shift, float score, float sum)
 {
-    Moved x;
-    x.top = fmaxf(fmaxf(top + (r - to), own - to), LEAST_TOP);
-    const float rise = fmaxf(fminf(top - x.top, MOST_SUM - sum), 0.f);
-    x.shift = shift + rise;
-    float by = x.shift - shift;
-    if (by > rise + 1.0f) {
-        x.shift = shift;
-        by = 0.f;
-    }
+    Rescaled x;
+    x.top = r == to ? top : fmaxf(top + (r - to), LEAST_TOP);
+    const float rise = fmaxf(fminf(fminf(top, R_SLACK) - x.top, MOST_SUM - sum), 0.f);
+    x.shift = fminf(fabsf(shift) < 0x1p22f ? shift + rise : shift, shift8_of(score, x.top));
+    const float by = x.shift - shift;
     x.l = __builtin_amdgcn_exp2f(by);
     x.o = __builtin_amdgcn_exp2f(by + (r - to));
     return x;

@@ -128,6 +128,12 @@ __device__ __forceinline__ float sum_x16(float v)
     return __builtin_bit_cast(float, s0) + __builtin_bit_cast(float, s1);
 }
 
+// A value that is the same in all lanes, in a scalar register.
+__device__ __forceinline__ float scalar(float v)
+{
+    return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, v)));
+}
+
 // The largest of a row of 16 lanes, in all of them; NaN is passed over.
 __device__ __forceinline__ float max_of_16(float v)
 {

@@ -99,18 +99,12 @@ __device__ __forceinline__ void attn_body(const AttnArgs &a, int slots, int id, 
     // row see what the last one does and are not stored)
     int see = t_end, see_all = t_end;
     if constexpr (FORM == PREFIX) {
-        // what none of these rows sees is not read (positions are below 2^24, whole numbers in f32)
-        const int seen = prefix_seen(a, row_of(min(i, cols - 1)), len);
-        len = __builtin_amdgcn_readfirstlane((int)max_of_16((float)seen));
-        t_end = min(t_end, len);
-        see = min(t_end, seen);
-        see_all = -(int)max_of_16(-(float)see);
+        see = min(t_end, prefix_seen(a, row_of(min(i, cols - 1)), len));
     } else if constexpr (FORM == MANY) {
         const int pos0 = max(c.kv_len[b], -(1 << 30)) - p.rows;
         see = min(t_end, pos0 + (rho0 + min(i, cols - 1)) / a.group + 1);
         see_all = min(t_end, pos0 + rho0 / a.group + 1);
     }
-    const int n_steps = t_end > t_begin + 32 * wave ? (t_end - t_begin - 32 * wave + 127) / 128 : 0;
 
     // queries of column i: scaled, split
     au4 qf[Q_LDS ? 1 : NP][Q_LDS ? 1 : KB];
@@ -149,6 +143,14 @@ __device__ __forceinline__ void attn_body(const AttnArgs &a, int slots, int id, 
                     sh.q[(x * KB + k) * 64 + lane] = out[x];
         }
     }
+    if constexpr (FORM == PREFIX) {
+        // what none of these rows sees is not read (positions are below 2^24, whole numbers in f32); the rows' lengths
+        // have arrived by now
+        t_end = __builtin_amdgcn_readfirstlane((int)max_of_16((float)see));
+        len = min(len, t_end);
+        see_all = -(int)max_of_16(-(float)see);
+    }
+    const int n_steps = t_end > t_begin + 32 * wave ? (t_end - t_begin - 32 * wave + 127) / 128 : 0;
     if constexpr (Q_LDS)
         __syncthreads();
 

@@ -183,7 +183,7 @@ __device__ __forceinline__ void prompt_body(const AttnArgs &a, int slots, int id
         // exponent), unless queries are so near f32's end that it could be: then scales stay as they are.  (8192
         // rows, 32 / 8 heads of 128, I8, 1016 -> 1021 us; a vote on the scales of each step instead 1027.)
         if constexpr (BYTES) {
-            k_room = __any(unscale > 0x1p60f) ? 1.0f : K_ROOM;
+            k_room = scalar(__any(unscale > 0x1p60f) ? 1.0f : K_ROOM);
             unscale *= 1.0f / k_room;
         }
 #pragma unroll
@@ -348,27 +348,9 @@ __device__ __forceinline__ void prompt_body(const AttnArgs &a, int slots, int id
     };
     // 8-bit: position of lane i of each 16 in tile x of a step, so that value r of a row is lane r's
     auto scale_at = [&](int x) { return 32 * x + 16 * ((lane & 15) >> 3) + 8 * hf + (lane & 7); };
-    // the scales dv of a step's tiles relative to 2^ref, and the largest that the row sees
-    auto follow = [&](float (&dv)[NT], float seen, float most) {
-        if (most > ref + R_SLACK) {                       // (uniform)
-            const Moved x = moved_reference(ref, most, exponent_above(seen), top, shift, exponent_above(max_x32(l)));
-            ref = most;
-            top = x.top;
-            shift = x.shift;
-            l *= x.l;
-#pragma unroll
-            for (int d = 0; d < DT; ++d)
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    o[d][r] *= x.o;
-        }
-        top = fmaxf(top, exponent_above(seen) - ref);
-#pragma unroll
-        for (int tt = 0; tt < NT; ++tt)
-            dv[tt] = ldexpf(dv[tt], -(int)ref);
-    };
-    // scores -> probabilities (2^(score + shift)), shift and sum kept up
-    auto softmax = [&](af16 (&sc)[NT]) {
+    // scores -> probabilities (2^(score + shift)), shift and sum kept up.  most: 8-bit, the largest exponent of V's
+    // scales that a row of the wave sees
+    auto softmax = [&](af16 (&sc)[NT], float most) {
         float mx = sc[0][0];
 #pragma unroll
         for (int r = 0; r < 16; ++r)
@@ -376,11 +358,23 @@ __device__ __forceinline__ void prompt_body(const AttnArgs &a, int slots, int id
             for (int tt = 0; tt < NT; ++tt)
                 mx = fmaxf(mx, sc[tt][r]);
         mx *= unscale;
-        if (__any(BYTES ? mx + shift > TOP8 - top : mx + shift > TOP<F>)) {
-            const float to = fminf(shift, BYTES ? shift8_of(max_x32(mx), top) : shift_of<F>(max_x32(mx)));
-            const float f = __builtin_amdgcn_exp2f(to - shift);
-            shift = to;
-            l *= f;
+        const bool moved = BYTES && __builtin_amdgcn_readfirstlane(most > ref + R_SLACK);
+        if (__any(moved || (BYTES ? mx + shift > TOP8 - top : mx + shift > TOP<F>))) {
+            float f;
+            if constexpr (BYTES) {
+                const float to = moved ? scalar(most) : ref;
+                const Rescaled x = rescaled(ref, to, top, shift, max_x32(mx), exponent_above(max_x32(l)));
+                ref = to;
+                top = x.top;
+                shift = x.shift;
+                l *= x.l;
+                f = x.o;
+            } else {
+                const float to = fminf(shift, shift_of<F>(max_x32(mx)));
+                f = __builtin_amdgcn_exp2f(to - shift);
+                shift = to;
+                l *= f;
+            }
 #pragma unroll
             for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -522,12 +516,13 @@ __device__ __forceinline__ void prompt_body(const AttnArgs &a, int slots, int id
                             if (hidden(last, sub, tt, r))
                                 sc[tt][r] = -INFINITY;
                 }
+                float most = 0.f;
                 if constexpr (BYTES) {
                     float seen = dv[0];
                     if constexpr (NT == 2)
                         seen = fmaxf(seen, dv[NT - 1]);
                     seen = max_x32(max_of_16(seen));
-                    float most = exponent_above(seen);
+                    most = exponent_above(seen);
                     // scales that some rows do not see matter where they pass what a row has seen
                     if (edge && __any(most > ref + top)) {
                         const int last = last_seen();
@@ -539,12 +534,13 @@ __device__ __forceinline__ void prompt_body(const AttnArgs &a, int slots, int id
                         seen = max_x32(seen);
                         most = max_x16(max_of_16(exponent_above(seen)));
                     }
-                    follow(dv, seen, most);
+                    top = fmaxf(top, exponent_above(seen) - ref);
                 }
-                softmax(sc);
+                softmax(sc, most);
                 if constexpr (BYTES)
 #pragma unroll
                     for (int tt = 0; tt < NT; ++tt) {
+                        dv[tt] = ldexpf(dv[tt], -(int)ref);
                         times_lanes([&](int r) { return Ref<af16>{sc[tt], r}; }, dv[tt]);
                         if (edge && __any(!(dv[tt] <= FLT_MAX))) {       // a NaN scale that this row does not see
                             const int last = last_seen();
